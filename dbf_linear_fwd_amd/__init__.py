@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional
+from typing import Dict, NamedTuple, Optional
 
 import numpy as np
 
@@ -32,6 +32,8 @@ __all__ = [
     "dbf_timing_enable", "dbf_timing_read", "Layer", "dbf_linear_forward_group", "forward_group",
     "dbf_pack_ex", "dbf_linear_backward_data", "dbf_linear_backward", "DBF_PACK_BACKWARD", "dbf_bqq_pack",
     "dbf_factorize", "factorize", "dbf_linear_forward_noalloc", "dbf_bqq_pack_grouped",
+    "DBF_TYPE_F16", "DBF_TYPE_BF16", "DBF_TYPE_F32", "DBF_TYPE_E4M3", "DBF_TYPE_E2M1", "MxTensor", "mx_quantize",
+    "dbf_mx_pack", "rms_norm", "RmsNormOutput", "rms_norm_backward",
 ]
 
 DBF_OK = 0
@@ -49,6 +51,12 @@ DBF_PATH_DECODE_EXACT = 4
 
 DBF_PACK_BACKWARD = 1
 
+DBF_TYPE_F16 = 0
+DBF_TYPE_BF16 = 1
+DBF_TYPE_F32 = 2
+DBF_TYPE_E4M3 = 3
+DBF_TYPE_E2M1 = 4
+
 DECODE_MAX_BATCH = 16
 
 EXPORTED_SYMBOLS = (
@@ -56,7 +64,9 @@ EXPORTED_SYMBOLS = (
     "dbf_linear_backward_data", "dbf_linear_backward", "dbf_free", "dbf_get_info", "dbf_status_string",
     "dbf_pack_signs", "dbf_layout_signs", "dbf_layout_words", "dbf_layout_signs_dec", "dbf_layout_words_dec",
     "dbf_timing_enable", "dbf_timing_read", "dbf_bqq_pack", "dbf_factorize", "dbf_linear_forward_noalloc",
-    "dbf_bqq_pack_grouped",
+    "dbf_bqq_pack_grouped", "dbf_mx_code_bytes", "dbf_mx_scale_bytes", "dbf_mx_quantize", "dbf_mx_dequantize",
+    "dbf_mx_pack", "dbf_mx_forward", "dbf_mx_backward_data", "dbf_rms_norm", "dbf_rms_norm_backward_workspace",
+    "dbf_rms_norm_backward",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -122,6 +132,26 @@ def lib() -> ctypes.CDLL:
     L.dbf_linear_backward.restype = ctypes.c_int
     L.dbf_linear_forward_group.argtypes = [ctypes.POINTER(vp), i32, vp, ctypes.POINTER(vp), i32, vp]
     L.dbf_linear_forward_group.restype = ctypes.c_int
+    L.dbf_mx_code_bytes.argtypes = [i32, i32]
+    L.dbf_mx_code_bytes.restype = sz
+    L.dbf_mx_scale_bytes.argtypes = [i32]
+    L.dbf_mx_scale_bytes.restype = sz
+    L.dbf_mx_quantize.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+    L.dbf_mx_quantize.restype = ctypes.c_int
+    L.dbf_mx_dequantize.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp]
+    L.dbf_mx_dequantize.restype = ctypes.c_int
+    L.dbf_mx_pack.argtypes = [i32, i32, vp, vp, i32, i32, vp, ctypes.POINTER(vp)]
+    L.dbf_mx_pack.restype = ctypes.c_int
+    L.dbf_mx_forward.argtypes = [vp, vp, i32, vp, vp, i32, i32, vp]
+    L.dbf_mx_forward.restype = ctypes.c_int
+    L.dbf_mx_backward_data.argtypes = [vp, vp, vp, i32, i32, vp]
+    L.dbf_mx_backward_data.restype = ctypes.c_int
+    L.dbf_rms_norm.argtypes = [vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp, i32, vp, vp, vp]
+    L.dbf_rms_norm.restype = ctypes.c_int
+    L.dbf_rms_norm_backward_workspace.argtypes = [i32, i32]
+    L.dbf_rms_norm_backward_workspace.restype = sz
+    L.dbf_rms_norm_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+    L.dbf_rms_norm_backward.restype = ctypes.c_int
     L.dbf_free.argtypes = [vp]
     L.dbf_free.restype = None
     L.dbf_get_info.argtypes = [vp, ctypes.POINTER(_Info)]
@@ -385,6 +415,192 @@ def dbf_timing_read(h: int) -> Dict[str, Dict[str, float]]:
             for i in range(min(cnt.value, cap))}
 
 
+_TYPE_NAMES = {"e4m3": DBF_TYPE_E4M3, "e2m1": DBF_TYPE_E2M1}
+
+
+def _type_of(dtype) -> int:
+    """The library's code of a torch dtype (-1: none)."""
+    import torch
+    return {torch.float16: DBF_TYPE_F16, torch.bfloat16: DBF_TYPE_BF16, torch.float32: DBF_TYPE_F32}.get(dtype, -1)
+
+
+def _block_type(fmt: str) -> int:
+    if fmt not in _TYPE_NAMES:
+        raise ValueError("the block format is 'e4m3' or 'e2m1'")
+    return _TYPE_NAMES[fmt]
+
+
+def _current_stream(t) -> int:
+    import torch
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _on_device(t):
+    """Context in which t's device is the current one."""
+    import torch
+    return torch.cuda.device(t.device)
+
+
+class MxTensor:
+    """A matrix in blocks of 32 columns with one power-of-two scale each (see
+    "Block formats" in include/dbf.h).
+
+    ``codes`` (uint8, rows x row bytes) and ``scales`` (uint8, rows x blocks)
+    are contiguous CUDA tensors in the padded row layout; ``cols`` is the
+    matrix's width and ``fmt`` is 'e4m3' (a byte per column) or 'e2m1' (half a
+    byte).
+    """
+
+    __slots__ = ("codes", "scales", "cols", "fmt")
+
+    def __init__(self, codes, scales, cols: int, fmt: str):
+        import torch
+        cols = int(cols)
+        t = _block_type(fmt)
+        if cols < 1:
+            raise ValueError("cols must be positive")
+        wide = -(-cols // 128) * 128
+        row = wide if t == DBF_TYPE_E4M3 else wide // 2
+        for a, width, what in ((codes, row, "codes"), (scales, wide // 32, "scales")):
+            if a.dtype != torch.uint8 or not a.is_cuda or a.dim() != 2 or a.shape[1] != width or not a.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous CUDA uint8 tensor of shape (rows, {width})")
+        if codes.shape[0] != scales.shape[0] or codes.device != scales.device:
+            raise ValueError("codes and scales must have the same rows and device")
+        self.codes, self.scales, self.cols, self.fmt = codes, scales, cols, fmt
+
+    @property
+    def shape(self):
+        return (self.codes.shape[0], self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def dequantize(self, dtype=None):
+        """The values, as a tensor of `dtype` (float32, float16 or bfloat16; default float32)."""
+        import torch
+        dtype = torch.float32 if dtype is None else dtype
+        t = _type_of(dtype)
+        if t < 0:
+            raise ValueError("dtype must be float32, float16 or bfloat16")
+        out = torch.empty(self.shape, dtype=dtype, device=self.device)
+        with _on_device(out):
+            _check(lib().dbf_mx_dequantize(self.codes.data_ptr(), self.scales.data_ptr(), _TYPE_NAMES[self.fmt],
+                                           out.shape[0], self.cols, out.data_ptr(), t, _current_stream(out)),
+                   "dbf_mx_dequantize")
+        return out
+
+
+def _empty_blocks(rows: int, cols: int, fmt: str, device) -> MxTensor:
+    import torch
+    wide = -(-cols // 128) * 128
+    codes = torch.empty((rows, wide if fmt == "e4m3" else wide // 2), dtype=torch.uint8, device=device)
+    scales = torch.empty((rows, wide // 32), dtype=torch.uint8, device=device)
+    return MxTensor(codes, scales, cols, fmt)
+
+
+def mx_quantize(x, fmt: str = "e4m3") -> MxTensor:
+    """x (contiguous 2-D CUDA tensor, float16, bfloat16 or float32) in blocks of 32 columns."""
+    t = _type_of(x.dtype)
+    ft = _block_type(fmt)
+    if t < 0 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous() or x.shape[1] < 1:
+        raise ValueError("x must be a contiguous 2-D CUDA tensor of float16, bfloat16 or float32")
+    q = _empty_blocks(x.shape[0], x.shape[1], fmt, x.device)
+    with _on_device(x):
+        _check(lib().dbf_mx_quantize(x.data_ptr(), t, x.shape[0], x.shape[1], ft, q.codes.data_ptr(),
+                                     q.scales.data_ptr(), _current_stream(x)), "dbf_mx_quantize")
+    return q
+
+
+def dbf_mx_pack(n: int, m: int, codes_ptr: int, scales_ptr: int, act_type: int, max_batch: int,
+                stream: int = 0) -> int:
+    """Handle of a layer with an e2m1 block weight (see dbf_mx_pack in include/dbf.h)."""
+    h = ctypes.c_void_p()
+    _check(lib().dbf_mx_pack(n, m, codes_ptr, scales_ptr, act_type, max_batch, stream, ctypes.byref(h)),
+           "dbf_mx_pack")
+    return h.value
+
+
+class RmsNormOutput(NamedTuple):
+    """y: the normalised rows (a tensor, or an e4m3 MxTensor); h: x + residual (x itself without a residual);
+    rstd: 1 / rms of each row, float32."""
+    y: object
+    h: object
+    rstd: object
+
+
+def _check_rows(t, what, like=None):
+    import torch
+    if t.dtype not in (torch.float16, torch.bfloat16) or not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous 2-D CUDA tensor of float16 or bfloat16")
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape or t.device != like.device):
+        raise ValueError(f"{what} must match the other rows in shape, type and device")
+
+
+def _check_norm_weight(weight, x) -> int:
+    import torch
+    if weight is None:
+        return _type_of(x.dtype)
+    if (weight.dtype not in (x.dtype, torch.float32) or tuple(weight.shape) != (x.shape[1],)
+            or not weight.is_contiguous() or weight.device != x.device):
+        raise ValueError("weight must be a contiguous vector of x's width and device, in x's type or float32")
+    return _type_of(weight.dtype)
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, mx: bool = False) -> RmsNormOutput:
+    """Root-mean-square norm of the rows of x (+ residual): see dbf_rms_norm in include/dbf.h.
+
+    x and residual are contiguous 2-D CUDA tensors (float16 or bfloat16).
+    With ``mx`` the normalised rows come in e4m3 blocks, the input of
+    ``Layer.mx`` layers; otherwise in x's type, the input of any layer.
+    """
+    import torch
+    _check_rows(x, "x")
+    if residual is not None:
+        _check_rows(residual, "residual", x)
+    wt = _check_norm_weight(weight, x)
+    rows, cols = x.shape
+    t = _type_of(x.dtype)
+    h = torch.empty_like(x) if residual is not None else x
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if mx:
+        y = _empty_blocks(rows, cols, "e4m3", x.device)
+        y_ptr, s_ptr, yt = y.codes.data_ptr(), y.scales.data_ptr(), DBF_TYPE_E4M3
+    else:
+        y = torch.empty_like(x)
+        y_ptr, s_ptr, yt = y.data_ptr(), None, t
+    with _on_device(x):
+        _check(lib().dbf_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(),
+                                  None if weight is None else weight.data_ptr(), t, wt, rows, cols, eps,
+                                  None if residual is None else h.data_ptr(), y_ptr, yt, s_ptr, rstd.data_ptr(),
+                                  _current_stream(x)), "dbf_rms_norm")
+    return RmsNormOutput(y, h, rstd)
+
+
+def rms_norm_backward(dy, h, weight, rstd, dh=None):
+    """(dx, dweight) of rms_norm at its h and rstd: dx is the gradient of x and of the residual, with dh, the
+    gradient that reaches h past the norm, added; dweight is float32 (also for weight=None)."""
+    import torch
+    _check_rows(dy, "dy")
+    _check_rows(h, "h", dy)
+    if dh is not None:
+        _check_rows(dh, "dh", dy)
+    wt = _check_norm_weight(weight, dy)
+    rows, cols = dy.shape
+    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (rows,) or not rstd.is_contiguous() or rstd.device != dy.device:
+        raise ValueError("rstd must be a contiguous float32 vector with one entry per row, on dy's device")
+    dx = torch.empty_like(dy)
+    dw = torch.empty(cols, dtype=torch.float32, device=dy.device)
+    nbytes = lib().dbf_rms_norm_backward_workspace(rows, cols)
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dy.device)
+    with _on_device(dy):
+        _check(lib().dbf_rms_norm_backward(dy.data_ptr(), h.data_ptr(), None if weight is None else weight.data_ptr(),
+                                           rstd.data_ptr(), None if dh is None else dh.data_ptr(), _type_of(dy.dtype),
+                                           wt, rows, cols, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes,
+                                           _current_stream(dy)), "dbf_rms_norm_backward")
+    return dx, dw
+
+
 class Layer:
     """A DBF linear layer on the current GPU: ``y = layer(x)``.
 
@@ -393,6 +609,8 @@ class Layer:
     batch <= max_batch; the result is a new fp16 tensor of shape (batch, n)
     computed on the current stream.
     """
+
+    act: Optional[str] = None  # input blocks of a 4-bit layer (Layer.mx); None: a sign-factor layer
 
     def __init__(self, A, B, a, mid, b, max_batch: int = 2048, backward: bool = False):
         A = np.asarray(A)
@@ -437,11 +655,69 @@ class Layer:
         self.handle = dbf_bqq_pack_grouped(self.n, self.m, d, p, int(group), Y, Z, r, s, t, u, self.max_batch)
         return self
 
+    @classmethod
+    def mx(cls, W: MxTensor, max_batch: int = 2048, act: str = "e4m3") -> "Layer":
+        """A layer with a 4-bit weight W (n x m, an e2m1 MxTensor: `mx_quantize(w, "e2m1")`).
+
+        Its forward takes float16 or bfloat16 rows, which are quantised into
+        `act` blocks ('e4m3' or 'e2m1') by the call, or an MxTensor of either
+        format; `backward_data` takes float16 or bfloat16.
+        """
+        if not isinstance(W, MxTensor) or W.fmt != "e2m1":
+            raise ValueError("W must be an e2m1 MxTensor")
+        at = _block_type(act)
+        self = cls.__new__(cls)
+        self.n, self.m = W.shape
+        self.k = 0
+        self.max_batch = int(max_batch)
+        self.act = act
+        with _on_device(W.codes):
+            self.handle = dbf_mx_pack(self.n, self.m, W.codes.data_ptr(), W.scales.data_ptr(), at, self.max_batch,
+                                      _current_stream(W.codes))
+        return self
+
+    def _forward_mx(self, x, out, path, out_dtype):
+        import torch
+        if path not in (DBF_PATH_AUTO, DBF_PATH_DECODE, DBF_PATH_PREFILL):
+            raise DbfError(DBF_ERR_UNSUPPORTED, "Layer.forward")
+        if isinstance(x, MxTensor):
+            if x.cols != self.m:
+                raise ValueError(f"x must have {self.m} columns")
+            ptr, scales, xt, batch, default = x.codes.data_ptr(), x.scales.data_ptr(), _TYPE_NAMES[x.fmt], \
+                x.codes.shape[0], torch.float16
+        else:
+            if (x.dtype not in (torch.float16, torch.bfloat16) or not x.is_cuda or x.dim() != 2
+                    or x.shape[1] != self.m or not x.is_contiguous()):
+                raise ValueError(f"x must be an MxTensor or a contiguous CUDA float16 or bfloat16 tensor of shape "
+                                 f"(batch, {self.m})")
+            ptr, scales, xt, batch, default = x.data_ptr(), None, _type_of(x.dtype), x.shape[0], x.dtype
+        if path == DBF_PATH_DECODE and batch > DECODE_MAX_BATCH:
+            raise DbfError(DBF_ERR_INVALID_ARG, "Layer.forward")
+        if out is not None:
+            default = out.dtype
+        if out_dtype is None:
+            out_dtype = default
+        if out_dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("the output is float16 or bfloat16")
+        if out is None:
+            out = torch.empty((batch, self.n), dtype=out_dtype, device=x.device)
+        elif (out.shape != (batch, self.n) or out.dtype != out_dtype or not out.is_contiguous()
+              or out.device != x.device):
+            raise ValueError("out must be a contiguous tensor of shape (batch, n) on x's device")
+        with _on_device(out):
+            _check(lib().dbf_mx_forward(self.handle, ptr, xt, scales, out.data_ptr(), _type_of(out_dtype), batch,
+                                        _current_stream(out)), "dbf_mx_forward")
+        return out
+
     def info(self) -> Dict[str, int]:
         return dbf_get_info(self.handle)
 
-    def forward(self, x, out=None, path: int = DBF_PATH_AUTO):
+    def forward(self, x, out=None, path: int = DBF_PATH_AUTO, out_dtype=None):
         import torch
+        if self.act is not None:
+            return self._forward_mx(x, out, path, out_dtype)
+        if out_dtype not in (None, torch.float16):
+            raise ValueError("the output is float16")
         if x.dtype != torch.float16 or not x.is_cuda or x.dim() != 2 or x.shape[1] != self.m:
             raise ValueError(f"x must be a CUDA float16 tensor of shape (batch, {self.m})")
         dev = getattr(self, "_device", None)
@@ -470,8 +746,21 @@ class Layer:
             raise ValueError(f"{what} must be a contiguous CUDA float16 tensor of shape (batch, {width})")
 
     def backward_data(self, dy, out=None):
-        """dX = dY W for dY of shape (batch, n); needs backward=True."""
+        """dX = dY W for dY of shape (batch, n); needs backward=True (Layer.mx: nothing, and dY may be bfloat16)."""
         import torch
+        if self.act is not None:
+            _check_rows(dy, "dy")
+            if dy.shape[1] != self.n:
+                raise ValueError(f"dy must have {self.n} columns")
+            if out is None:
+                out = torch.empty((dy.shape[0], self.m), dtype=dy.dtype, device=dy.device)
+            elif (tuple(out.shape) != (dy.shape[0], self.m) or out.dtype != dy.dtype or not out.is_contiguous()
+                  or out.device != dy.device):
+                raise ValueError("out must be a contiguous tensor of shape (batch, m) in dy's type on its device")
+            with _on_device(dy):
+                _check(lib().dbf_mx_backward_data(self.handle, dy.data_ptr(), out.data_ptr(), _type_of(dy.dtype),
+                                                  dy.shape[0], _current_stream(dy)), "dbf_mx_backward_data")
+            return out
         self._check_act(dy, self.n, "dy")
         if out is None:
             out = torch.empty((dy.shape[0], self.m), dtype=torch.float16, device=dy.device)

@@ -260,6 +260,42 @@ int launch_bqq_rowstats(const void *x, int batch, int m, const float *gamma, flo
 constexpr int kMaxStatQ = 9;
 int launch_bqq_rowstats_q(const void *x, int batch, int m, const float *w, int Q, float *stats, void *stream);
 
+// ---- 4-bit weights in blocks of 32 columns (mx_quant.hip, mx_gemm.hip)
+
+// Device layout of an e2m1 weight of n x m: rows in tiles of 32 (n_pad rows),
+// `blocks` = round_up(m, 128) / 32 blocks per row.  Block kb of row 32 t + r
+// has its 16 bytes of codes (columns in order, the even one in the low half)
+// at codes[((t * blocks + kb) * 32 + r) * 16] and its scale byte at
+// scales[((t * blocks / 4 + kb / 4) * 32 + r) * 4 + kb % 4]: 512 contiguous
+// bytes hold one block of 32 rows, in the order in which the 32 lanes of a
+// matrix-core operand take them.  colmax[kb] is the largest scale byte (255
+// aside) of block column kb.
+struct MxWeight {
+    const uint8_t *codes = nullptr, *scales = nullptr, *colmax = nullptr;
+    int n = 0, m = 0, n_pad = 0, blocks = 0;
+};
+
+int launch_mx_quantize(const void *x, int x_type, int rows, int cols, int fmt, void *codes, uint8_t *scales,
+                       void *stream);
+int launch_mx_dequantize(const void *codes, const uint8_t *scales, int fmt, int rows, int cols, void *out,
+                         int out_type, void *stream);
+int launch_mx_layout(const void *codes, const uint8_t *scales, int n, int m, uint8_t *out_codes, uint8_t *out_scales,
+                     uint8_t *colmax, void *stream);
+
+// y (M x n, y_type f16 / bf16) = x wᵀ with x in blocks (x_type e4m3 / e2m1,
+// padded rows of w.blocks blocks).
+struct MxProduct {
+    const void *xcodes = nullptr;
+    const uint8_t *xscales = nullptr;
+    int x_type = 0, M = 0;
+    MxWeight w;
+    void *y = nullptr;
+    int y_type = 0;
+};
+int launch_mx_product(const MxProduct &p, void *stream);
+// dx (M x m) = dy (M x n) w, both f16 or bf16.
+int launch_mx_backward(const void *dy, int type, int M, const MxWeight &w, void *dx, void *stream);
+
 }  // namespace dbf
 
 #endif  // DBF_INTERNAL_H_

@@ -59,6 +59,12 @@ struct dbf_layer {
     // bqq_stats [max_batch][p + 1] (bqq_Q = p + 1)
     int32_t bqq_groups = 0, bqq_p = 0, bqq_d = 0, bqq_Q = 2;
     uint16_t *bqq_b = nullptr;
+    // layer with a 4-bit block weight (dbf_mx_pack): the weight's device
+    // layout, and the quantised input [max_batch] of the forwards
+    bool mx = false;
+    int32_t mx_act = DBF_TYPE_E4M3;
+    uint8_t *mx_codes = nullptr, *mx_scales = nullptr, *mx_colmax = nullptr;
+    uint8_t *mx_xcodes = nullptr, *mx_xscales = nullptr;
     size_t packed_bytes = 0, scale_bytes = 0, workspace_bytes = 0;
     // backward (dbf_pack_ex with DBF_PACK_BACKWARD): the transposed layer
     // Wᵀ = diag(b) Bᵀ diag(mid) Aᵀ diag(a), and fp32 intermediates of the
@@ -124,6 +130,11 @@ void release(dbf_layer *h) {
     (void)hipFree(h->bqq_b);
     (void)hipFree(h->t32);
     (void)hipFree(h->red);
+    (void)hipFree(h->mx_codes);
+    (void)hipFree(h->mx_scales);
+    (void)hipFree(h->mx_colmax);
+    (void)hipFree(h->mx_xcodes);
+    (void)hipFree(h->mx_xscales);
     release(h->bwd);
     for (auto &p : h->pending) {
         (void)hipEventDestroy(p.start);
@@ -861,6 +872,141 @@ static dbf_status_t forward_bqq_grouped(dbf_layer *h, const void *x, void *y, in
     return st;
 }
 
+// ---------------------------------------------------------------------------
+// Layers with a 4-bit block weight (dbf_mx_pack).
+
+static dbf::MxWeight mx_weight(const dbf_layer *h) {
+    dbf::MxWeight w;
+    w.codes = h->mx_codes;
+    w.scales = h->mx_scales;
+    w.colmax = h->mx_colmax;
+    w.n = h->n;
+    w.m = h->m;
+    w.n_pad = h->n_pad;
+    w.blocks = h->m_pad / 32;
+    return w;
+}
+
+// x of x_type (16 bits: quantised into the handle's workspace first; blocks:
+// codes at x, scales at x_scales) times the weight; arguments are checked.
+static dbf_status_t forward_mx(dbf_layer *h, const void *x, int32_t x_type, const uint8_t *x_scales, void *y,
+                               int32_t y_type, int32_t batch, hipStream_t stream) {
+    dbf::MxProduct p;
+    p.xcodes = x;
+    p.xscales = x_scales;
+    p.x_type = x_type;
+    if (x_type == DBF_TYPE_F16 || x_type == DBF_TYPE_BF16) {
+        const dbf_status_t st = timed_launch(h, "mx_quantize", stream, [&] {
+            return dbf::launch_mx_quantize(x, x_type, batch, h->m, h->mx_act, h->mx_xcodes, h->mx_xscales, stream);
+        });
+        if (st != DBF_OK) return st;
+        p.xcodes = h->mx_xcodes;
+        p.xscales = h->mx_xscales;
+        p.x_type = h->mx_act;
+    }
+    p.M = batch;
+    p.w = mx_weight(h);
+    p.y = y;
+    p.y_type = y_type;
+    return timed_launch(h, "mx_product", stream, [&] { return dbf::launch_mx_product(p, stream); });
+}
+
+// Layers that share the f16 input: it is quantised once for the layers of
+// one activation format.
+static dbf_status_t forward_mx_group(const dbf_handle_t *hs, int32_t count, const void *x, void *const *ys,
+                                     int32_t batch, hipStream_t stream) {
+    for (int i = 0; i < count; ++i) {
+        const dbf_layer *q = nullptr;  // an earlier layer of the same format: its quantised x
+        for (int j = 0; j < i && !q; ++j)
+            if (hs[j]->mx_act == hs[i]->mx_act) q = hs[j];
+        const dbf_status_t st =
+            q ? forward_mx(hs[i], q->mx_xcodes, q->mx_act, q->mx_xscales, ys[i], DBF_TYPE_F16, batch, stream)
+              : forward_mx(hs[i], x, DBF_TYPE_F16, nullptr, ys[i], DBF_TYPE_F16, batch, stream);
+        if (st != DBF_OK) return st;
+    }
+    return DBF_OK;
+}
+
+extern "C" dbf_status_t dbf_mx_pack(int32_t n, int32_t m, const void *codes, const uint8_t *scales, int32_t act_type,
+                                    int32_t max_batch, hipStream_t stream, dbf_handle_t *out) {
+    if (out) *out = nullptr;
+    if (!out || !codes || !scales || !aligned16(codes) || !aligned16(scales)) return DBF_ERR_INVALID_ARG;
+    if (n < 1 || m < 1 || max_batch < 1) return DBF_ERR_INVALID_ARG;
+    if (act_type != DBF_TYPE_E4M3 && act_type != DBF_TYPE_E2M1) return DBF_ERR_INVALID_ARG;
+    const int64_t lim = int64_t(1) << 30;
+    if (n > lim || m > lim) return DBF_ERR_SHAPE;
+    const int32_t n_pad = round_up(n, 32), m_pad = round_up(m, 128);
+    if (int64_t(n_pad) * m_pad > (int64_t(1) << 36) || int64_t(max_batch) * m_pad > (int64_t(1) << 31) ||
+        int64_t(max_batch) * n > (int64_t(1) << 31))
+        return DBF_ERR_SHAPE;
+    g_alloc_calls = 0;
+    dbf_layer *h = new (std::nothrow) dbf_layer();
+    if (!h) return DBF_ERR_OOM;
+    h->mx = true;
+    h->mx_act = act_type;
+    h->n = n;
+    h->m = m;
+    h->n_pad = n_pad;
+    h->m_pad = m_pad;
+    h->max_batch = max_batch;
+    const size_t blocks = static_cast<size_t>(m_pad) / 32;
+    const size_t code_bytes = static_cast<size_t>(n_pad) * blocks * 16, scale_bytes = static_cast<size_t>(n_pad) * blocks;
+    const size_t xc_bytes = static_cast<size_t>(max_batch) * dbf_mx_code_bytes(m, act_type);
+    const size_t xs_bytes = static_cast<size_t>(max_batch) * blocks;
+    dbf_status_t st = hipGetDevice(&h->device) == hipSuccess ? DBF_OK : DBF_ERR_HIP;
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_codes), code_bytes);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_scales), scale_bytes);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_colmax), blocks);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xcodes), xc_bytes);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xscales), xs_bytes);
+    if (st == DBF_OK && dbf::launch_mx_layout(codes, scales, n, m, h->mx_codes, h->mx_scales, h->mx_colmax, stream) != 0)
+        st = DBF_ERR_HIP;
+    // the weight is in place when the call returns, for any stream
+    if (st == DBF_OK && hipStreamSynchronize(stream) != hipSuccess) st = DBF_ERR_HIP;
+    if (st != DBF_OK) {
+        release(h);
+        return st;
+    }
+    h->packed_bytes = code_bytes;
+    h->scale_bytes = scale_bytes + blocks;
+    h->workspace_bytes = xc_bytes + xs_bytes;
+    *out = h;
+    return DBF_OK;
+}
+
+extern "C" dbf_status_t dbf_mx_forward(dbf_handle_t h, const void *x, int32_t x_type, const uint8_t *x_scales,
+                                       void *y, int32_t y_type, int32_t batch, hipStream_t stream) {
+    if (!h) return DBF_ERR_INVALID_ARG;
+    if (!h->mx) return DBF_ERR_UNSUPPORTED;
+    if (batch < 0 || batch > h->max_batch) return DBF_ERR_INVALID_ARG;
+    const bool real = x_type == DBF_TYPE_F16 || x_type == DBF_TYPE_BF16;
+    if (!real && x_type != DBF_TYPE_E4M3 && x_type != DBF_TYPE_E2M1) return DBF_ERR_INVALID_ARG;
+    if (y_type != DBF_TYPE_F16 && y_type != DBF_TYPE_BF16) return DBF_ERR_INVALID_ARG;
+    if (batch == 0) return DBF_OK;
+    if (!x || !y || !aligned16(x) || !aligned16(y)) return DBF_ERR_INVALID_ARG;
+    if (real ? x_scales != nullptr : (!x_scales || (reinterpret_cast<uintptr_t>(x_scales) & 3u)))
+        return DBF_ERR_INVALID_ARG;
+    int cur = -1;
+    if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
+    if (cur != h->device) return DBF_ERR_INVALID_ARG;
+    return forward_mx(h, x, x_type, x_scales, y, y_type, batch, stream);
+}
+
+extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, void *dx, int32_t type, int32_t batch,
+                                             hipStream_t stream) {
+    if (!h) return DBF_ERR_INVALID_ARG;
+    if (!h->mx) return DBF_ERR_UNSUPPORTED;
+    if (batch < 0 || batch > h->max_batch) return DBF_ERR_INVALID_ARG;
+    if (type != DBF_TYPE_F16 && type != DBF_TYPE_BF16) return DBF_ERR_INVALID_ARG;
+    if (batch == 0) return DBF_OK;
+    if (!dy || !dx || !aligned16(dy) || !aligned16(dx)) return DBF_ERR_INVALID_ARG;
+    int cur = -1;
+    if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
+    if (cur != h->device) return DBF_ERR_INVALID_ARG;
+    return timed_launch(h, "mx_backward", stream,
+                        [&] { return dbf::launch_mx_backward(dy, type, batch, mx_weight(h), dx, stream); });
+}
+
 extern "C" dbf_status_t dbf_linear_forward_ex(dbf_handle_t h, const void *x, void *y, int32_t batch, int32_t path,
                                               hipStream_t stream) {
     if (!h) return DBF_ERR_INVALID_ARG;
@@ -876,6 +1022,10 @@ extern "C" dbf_status_t dbf_linear_forward_ex(dbf_handle_t h, const void *x, voi
     if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
     if (cur != h->device) return DBF_ERR_INVALID_ARG;
     if (path == DBF_PATH_DECODE_TABLE) return DBF_ERR_UNSUPPORTED;  // (removed: slower than the matrix cores)
+    if (h->mx) {
+        if (path == DBF_PATH_DECODE_EXACT) return DBF_ERR_UNSUPPORTED;
+        return forward_mx(h, x, DBF_TYPE_F16, nullptr, y, DBF_TYPE_F16, batch, stream);
+    }
     if (path == DBF_PATH_DECODE_EXACT) {
         // the exact int8 sums at batch 1..4, every row the bits of its batch-1 forward
         if (!i8_rows_ok(h, batch) || h->binary || h->bqq_groups > 0) return DBF_ERR_UNSUPPORTED;
@@ -910,6 +1060,17 @@ extern "C" dbf_status_t dbf_linear_forward_group(const dbf_handle_t *hs, int32_t
     int cur = -1;
     if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
     if (cur != hs[0]->device) return DBF_ERR_INVALID_ARG;
+    int mx_layers = 0;
+    for (int i = 0; i < count; ++i) mx_layers += hs[i]->mx ? 1 : 0;
+    if (mx_layers == count) return forward_mx_group(hs, count, x, ys, batch, stream);
+    if (mx_layers > 0) {
+        // layers of both kinds: each layer's own forward
+        for (int i = 0; i < count; ++i) {
+            const dbf_status_t st = dbf_linear_forward_ex(hs[i], x, ys[i], batch, DBF_PATH_AUTO, stream);
+            if (st != DBF_OK) return st;
+        }
+        return DBF_OK;
+    }
     if (batch > dbf::kDecodeMaxBatch) {
         // one launch per product for all the layers (their tiles in one
         // grid), where every product has the deep-pipelined form (m a
@@ -998,6 +1159,7 @@ extern "C" dbf_status_t dbf_linear_forward_group(const dbf_handle_t *hs, int32_t
 extern "C" dbf_status_t dbf_linear_backward_data(dbf_handle_t h, const void *dy, void *dx, int32_t batch,
                                                  hipStream_t stream) {
     if (!h) return DBF_ERR_INVALID_ARG;
+    if (h->mx) return dbf_mx_backward_data(h, dy, dx, DBF_TYPE_F16, batch, stream);
     if (!h->bwd) return DBF_ERR_UNSUPPORTED;
     return dbf_linear_forward_ex(h->bwd, dy, dx, batch, DBF_PATH_AUTO, stream);
 }
@@ -1150,6 +1312,7 @@ __global__ void zero_u32_kernel(unsigned *p, int n) {
 // workspace would give them for this batch.
 struct ScratchPlan {
     size_t v32 = 0, v16 = 0, tpart = 0, tickets = 0, T = 0, split = 0, stats = 0, total = 0;
+    size_t xcodes = 0, xscales = 0;  // 4-bit block weights: the quantised input
     size_t tpart_cap = 0, split_cap = 0;
     bool i8 = false, decode = false, parts = false;
 };
@@ -1162,6 +1325,12 @@ ScratchPlan plan_scratch(const dbf_layer *h, int32_t batch) {
         off += (bytes + 255) & ~size_t(255);
         return at;
     };
+    if (h->mx) {
+        p.xcodes = take(size_t(batch) * dbf_mx_code_bytes(h->m, h->mx_act));
+        p.xscales = take(size_t(batch) * dbf_mx_scale_bytes(h->m));
+        p.total = off;
+        return p;
+    }
     p.decode = batch <= dbf::kDecodeMaxBatch;
     if (p.decode && batch == 1 && h->i8_ok) {
         p.i8 = true;
@@ -1219,6 +1388,11 @@ extern "C" dbf_status_t dbf_linear_forward_noalloc(dbf_handle_t h, const void *x
     unsigned *const o_tickets = h->tickets;
     const size_t o_tpart_cap = h->tpart_cap, o_split_cap = h->split_cap;
     const bool o_timing = h->timing;
+    uint8_t *const o_xcodes = h->mx_xcodes, *const o_xscales = h->mx_xscales;
+    if (h->mx) {
+        h->mx_xcodes = reinterpret_cast<uint8_t *>(base + p.xcodes);
+        h->mx_xscales = reinterpret_cast<uint8_t *>(base + p.xscales);
+    }
     if (p.i8) h->v32 = reinterpret_cast<float *>(base + p.v32);
     if (p.decode && !p.i8) h->v16 = reinterpret_cast<uint16_t *>(base + p.v16);
     if (p.parts) {
@@ -1226,7 +1400,7 @@ extern "C" dbf_status_t dbf_linear_forward_noalloc(dbf_handle_t h, const void *x
         h->tpart_cap = p.tpart_cap;
         h->tickets = reinterpret_cast<unsigned *>(base + p.tickets);
     }
-    if (!p.decode) {
+    if (!p.decode && !h->mx) {
         h->T = reinterpret_cast<uint16_t *>(base + p.T);
         h->split = reinterpret_cast<float *>(base + p.split);
         h->split_cap = p.split_cap;
@@ -1244,5 +1418,7 @@ extern "C" dbf_status_t dbf_linear_forward_noalloc(dbf_handle_t h, const void *x
     h->tpart_cap = o_tpart_cap;
     h->split_cap = o_split_cap;
     h->timing = o_timing;
+    h->mx_xcodes = o_xcodes;
+    h->mx_xscales = o_xscales;
     return st;
 }

@@ -1,0 +1,214 @@
+"""GPU: root-mean-square norm with the residual's addition, and its gradient, against the fp64 oracle.
+
+Tolerances, in units of the compared value: a row's sum of squares is a sum of
+non-negative fp32 terms, at most 32 of a lane in a row, 6 over the wave and 16
+over the waves: relative error at most 56 * 2^-24 < 2^-18, halved by the root;
+with the root, the division and two products: below 2^-18.  Then half a step
+of the output's type.
+
+Every case prints its name before it touches the GPU.
+"""
+
+import sys
+
+import numpy as np
+import pytest
+
+import dbf_linear_fwd_amd as dbf
+from oracle import mx_oracle as O
+from tests.test_mx_gpu import T, half_step, rows_of, same_bits, tiny, to_dev
+
+pytestmark = pytest.mark.gpu
+
+REL = 2.0 ** -18
+
+
+def _say(msg):
+    print(f"[case] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+# widths of every kernel variant (one wave to sixteen per row), odd ones, block tails
+SIZES = [(1, 1), (3, 7), (5, 32), (2, 100), (9, 512), (4, 513), (1, 1000), (33, 1024), (6, 1032), (3, 2048),
+         (2, 3001), (1, 4096), (17, 4097), (2, 8192), (3, 8200), (2, 16384), (2, 16385), (1, 32768), (700, 264)]
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_forward(gpu, rows, cols, name):
+    import torch
+    _say(f"norm {rows}x{cols} {name}")
+    rng = np.random.default_rng(rows * 31 + cols)
+    x, xv = to_dev(rows_of(rng, rows, cols), name)
+    r, rv = to_dev(rows_of(rng, rows, cols, 0.5), name)
+    eps = 1e-5
+    # the fp32 epsilon that the call takes
+    e32 = float(np.float32(eps))
+    for residual in (None, r):
+        for wname in (None, name, "f32"):
+            w, wv = (None, np.ones(cols)) if wname is None else to_dev(1 + 0.2 * rng.standard_normal(cols), wname)
+            out = dbf.rms_norm(x, w, residual=residual, eps=eps)
+            if residual is None:
+                assert out.h is x
+                h = xv
+            else:
+                h = torch.from_numpy(xv + rv).to(T(name)).double().numpy()
+                assert np.array_equal(out.h.double().cpu().numpy(), h)
+            ref, rstd = O.rms_norm(h, wv, e32)
+            assert np.all(np.abs(out.rstd.double().cpu().numpy() - rstd) <= REL * rstd)
+            d = np.abs(out.y.double().cpu().numpy() - ref)
+            assert np.all(d <= (half_step(name) * (1 + REL) + REL) * np.abs(ref) + tiny(name))
+            # in blocks: the codes of the fp32 values
+            q = dbf.rms_norm(x, w, residual=residual, eps=eps, mx=True)
+            assert q.y.shape == (rows, cols) and q.y.fmt == "e4m3"
+            codes, s = O.unpad_rows(q.y.codes.cpu().numpy(), q.y.scales.cpu().numpy(), cols, "e4m3")
+            pc, ps = O.pad_rows(codes, s, "e4m3")
+            assert np.array_equal(pc, q.y.codes.cpu().numpy()) and np.array_equal(ps, q.y.scales.cpu().numpy())
+            check_blocks(codes, s, ref)
+
+
+def check_blocks(codes, s, ref):
+    """Each block's scale is right for some value within REL of its largest, and each code for some value within
+    REL of its own."""
+    rows, cols = ref.shape
+    lo_s = O.quantize(ref * (1 - REL), "e4m3")[1].astype(int)
+    hi_s = O.quantize(ref * (1 + REL), "e4m3")[1].astype(int)
+    s = s.astype(int)
+    assert np.all((s >= lo_s) & (s <= hi_s))
+    inv = np.exp2(127.0 - np.repeat(s, 32, axis=1)[:, :cols])
+    a = np.abs(ref) * inv
+    got = np.abs(O.code_values("e4m3")[codes])
+    lo = O.code_values("e4m3")[O.nearest_code(a * (1 - REL), "e4m3")]
+    hi = O.code_values("e4m3")[O.nearest_code(a * (1 + REL), "e4m3")]
+    assert np.all((got >= lo) & (got <= hi))
+    assert np.all((np.sign(ref) * O.code_values("e4m3")[codes] >= 0))
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,cols", SIZES + [(1500, 96), (2100, 40)])
+def test_backward(gpu, rows, cols, name):
+    """dx: the row's mean is a sum of fp32 terms of either sign: its error is REL times the mean of their
+    magnitudes.  dweight: fp32 sums over the rows, at most 16 + parts / 16 + rows / parts additions in a row."""
+    import torch
+    _say(f"norm backward {rows}x{cols} {name}")
+    rng = np.random.default_rng(rows * 17 + cols)
+    h, hv = to_dev(rows_of(rng, rows, cols), name)
+    dy, dyv = to_dev(rows_of(rng, rows, cols, 0.1), name)
+    dh, dhv = to_dev(rows_of(rng, rows, cols, 0.1), name)
+    rstd = (1 / np.sqrt((hv * hv).mean(axis=1) + 1e-5)).astype(np.float32)
+    rd = torch.from_numpy(rstd).cuda()
+    rv = rstd.astype(np.float64)
+    for wname in (None, name, "f32"):
+        w, wv = (None, np.ones(cols)) if wname is None else to_dev(1 + 0.2 * rng.standard_normal(cols), wname)
+        ref, dw = O.rms_norm_backward(dyv, hv, wv, rv)
+        xh = hv * rv[:, None]
+        g = np.abs(dyv * wv)
+        part = rv[:, None] * (g + np.abs(xh) * (g * np.abs(xh)).mean(axis=1, keepdims=True))
+        for up in (None, dh):
+            want = ref if up is None else ref + dhv
+            dx, dwg = dbf.rms_norm_backward(dy, h, w, rd, dh=up)
+            err = REL * part + 2.0 ** -23 * np.abs(want)
+            d = np.abs(dx.double().cpu().numpy() - want)
+            assert np.all(d <= half_step(name) * (np.abs(want) + err) + err + tiny(name))
+            mag = np.abs(dyv * xh).sum(axis=0)
+            assert dwg.dtype == torch.float32
+            n_add = 16 + 128 + rows / 256
+            assert np.all(np.abs(dwg.double().cpu().numpy() - dw) <= (n_add + 3) * 2.0 ** -24 * mag + 1e-45)
+        again = dbf.rms_norm_backward(dy, h, w, rd, dh=dh)
+        assert same_bits(again[0], dx) and same_bits(again[1], dwg)
+
+
+def test_gradient_against_differences(gpu):
+    """Directional differences of the forward itself (bf16 rows of few bits, fp32 statistics)."""
+    _say("norm differences")
+    rng = np.random.default_rng(3)
+    rows, cols = 4, 96
+    h = rng.integers(-8, 9, size=(rows, cols)) / 4.0
+    hd, hv = to_dev(h, "bf16")
+    w, wv = to_dev(1 + rng.integers(-4, 5, size=cols) / 16.0, "bf16")
+    dy, dyv = to_dev(rng.integers(-8, 9, size=(rows, cols)) / 8.0, "bf16")
+    out = dbf.rms_norm(hd, w, eps=1e-5)
+    dx, dw = dbf.rms_norm_backward(dy, hd, w, out.rstd)
+    v = rng.standard_normal((rows, cols))
+    d = 1e-4
+    f = lambda s: (O.rms_norm(hv + s * v, wv, 1e-5)[0] * dyv).sum()  # noqa: E731
+    num = (f(d) - f(-d)) / (2 * d)
+    got = (dx.double().cpu().numpy() * v).sum()
+    # bf16 rounding of dx: half a step per term
+    assert abs(num - got) <= half_step("bf16") * (np.abs(dx.double().cpu().numpy()) * np.abs(v)).sum() * 1.01 + 1e-4
+    u = rng.standard_normal(cols)
+    num = ((O.rms_norm(hv, wv + u, 1e-5)[0] - O.rms_norm(hv, wv, 1e-5)[0]) * dyv).sum()
+    assert abs(num - (dw.double().cpu().numpy() * u).sum()) <= 1e-4
+
+
+def test_special_rows(gpu):
+    """Rows of zeros, of the type's largest values, with a NaN, with an infinity; the rows beside them unchanged."""
+    import torch
+    _say("norm special rows")
+    for name in ("f16", "bf16"):
+        for cols in (40, 2048, 5000):
+            rng = np.random.default_rng(cols)
+            x, _ = to_dev(rng.standard_normal((6, cols)), name)
+            plain = dbf.rms_norm(x, None, eps=1e-6)
+            plain_q = dbf.rms_norm(x, None, eps=1e-6, mx=True)
+            x[1] = 0
+            x[2] = torch.finfo(T(name)).max
+            x[3, cols // 2] = float("nan")
+            x[4, cols - 1] = float("inf")
+            out = dbf.rms_norm(x, None, eps=1e-6)
+            q = dbf.rms_norm(x, None, eps=1e-6, mx=True)
+            for i in (0, 5):
+                assert torch.equal(out.y[i], plain.y[i])
+                assert torch.equal(q.y.codes[i], plain_q.y.codes[i]) and torch.equal(q.y.scales[i], plain_q.y.scales[i])
+            v = q.y.dequantize()
+            assert bool((out.y[1] == 0).all()) and bool((v[1] == 0).all())
+            if name == "f16":
+                # 65504² * 5000 is inside fp32: every value 1; in blocks 1, or where fp32 has it just below a
+                # power of two, and so the scale one lower, 448 * 2^-9
+                assert bool((out.y[2] == 1).all()) and bool(((v[2] == 1) | (v[2] == 0.875)).all())
+            else:              # the squares overflow: rstd 0
+                assert bool((out.y[2] == 0).all()) and bool((v[2] == 0).all())
+            assert bool(torch.isnan(out.y[3]).all()) and bool(torch.isnan(v[3]).all())
+            assert bool(torch.isnan(out.y[4, cols - 1])) and bool((out.y[4, :cols - 1] == 0).all())
+            last = (cols - 1) // 32 * 32
+            assert bool(torch.isnan(v[4, last:]).all()) and bool((v[4, :last] == 0).all())
+
+
+def test_in_place_and_no_rows(gpu):
+    import torch
+    _say("norm in place")
+    rng = np.random.default_rng(4)
+    x, _ = to_dev(rng.standard_normal((5, 1032)), "bf16")
+    r, _ = to_dev(rng.standard_normal((5, 1032)), "bf16")
+    want = dbf.rms_norm(x, None, residual=r)
+    st = torch.cuda.current_stream().cuda_stream
+    x2, r2 = x.clone(), r.clone()
+    code = dbf.lib().dbf_rms_norm(x2.data_ptr(), r2.data_ptr(), None, 1, 1, 5, 1032, 1e-6, r2.data_ptr(),
+                                  x2.data_ptr(), 1, None, None, st)
+    assert code == dbf.DBF_OK
+    assert same_bits(x2, want.y) and same_bits(r2, want.h)
+    e = torch.empty((0, 64), dtype=torch.float16, device="cuda")
+    out = dbf.rms_norm(e, None, residual=e, mx=True)
+    assert out.y.shape == (0, 64)
+    dx, dw = dbf.rms_norm_backward(e, e, None, torch.empty(0, device="cuda"))
+    assert dx.shape == (0, 64) and bool((dw == 0).all())
+
+
+def test_feeds_a_sign_layer(gpu):
+    """The 16-bit output in front of a sign-factor layer, as a decoder block runs it."""
+    import torch
+    from oracle import dbf_oracle
+    from tests import inputs
+    _say("norm into a sign layer")
+    R = inputs.random_layer("norm feed", 128, 256, 192, 0, 0.05, 0.05, 0.05, (3,))
+    L = dbf.Layer(R.A, R.B, R.a, R.mid, R.b, max_batch=3)
+    try:
+        x, _ = to_dev(np.random.default_rng(0).standard_normal((3, 256)), "f16")
+        out = dbf.rms_norm(x, None, residual=x)
+        y = L(out.y)
+        torch.cuda.synchronize()
+        ref = dbf_oracle.dense_forward(out.y.cpu().numpy(), R.A, R.B, R.a, R.mid, R.b)
+        err = np.abs(y.double().cpu().numpy() - ref).max(axis=1) / np.abs(ref).max(axis=1)
+        assert err.max() <= 2e-3
+    finally:
+        L.close()
