@@ -275,15 +275,35 @@ struct MxWeight {
     int n = 0, m = 0, n_pad = 0, blocks = 0;
 };
 
+// Few rows (batch <= kMxDecodeBatch): y[i] (batch x n_i, y_type) = x w[i]ᵀ for
+// layers that share x, one launch.  x: batch rows of x_type f16 / bf16
+// (batch <= 16, m a multiple of 8; quantised into `act` blocks), or padded
+// rows of `act` codes (x_type = act) with scales xs.  `first` is filled by
+// the launch.
+constexpr int kMxDecodeBatch = 64;
+struct MxDecodeArgs {
+    const void *x = nullptr;
+    const uint8_t *xs = nullptr;
+    int x_type = 0, act = 0, batch = 0, y_type = 0;
+    int count = 0;
+    MxWeight w[kMaxGroup];
+    void *y[kMaxGroup] = {};
+    int first[kMaxGroup] = {};  // first workgroup of each layer
+};
+int launch_mx_decode(MxDecodeArgs &a, void *stream);
+
+// tiled: scales in 32-row tiles (see MxWeight) instead of rows.
 int launch_mx_quantize(const void *x, int x_type, int rows, int cols, int fmt, void *codes, uint8_t *scales,
-                       void *stream);
+                       bool tiled, void *stream);
 int launch_mx_dequantize(const void *codes, const uint8_t *scales, int fmt, int rows, int cols, void *out,
                          int out_type, void *stream);
 int launch_mx_layout(const void *codes, const uint8_t *scales, int n, int m, uint8_t *out_codes, uint8_t *out_scales,
                      uint8_t *colmax, void *stream);
 
-// y (M x n, y_type f16 / bf16) = x wᵀ with x in blocks (x_type e4m3 / e2m1,
-// padded rows of w.blocks blocks).
+// y (M x n, y_type f16 / bf16) = x wᵀ with x in blocks: codes in padded rows
+// of w.blocks blocks (x_type e4m3 / e2m1), scales in 32-row tiles like the
+// weight's (launch_mx_tile_scales, or launch_mx_quantize with tiled).  part:
+// at least mx_product_parts() floats for the sums of K parts.
 struct MxProduct {
     const void *xcodes = nullptr;
     const uint8_t *xscales = nullptr;
@@ -291,7 +311,13 @@ struct MxProduct {
     MxWeight w;
     void *y = nullptr;
     int y_type = 0;
+    float *part = nullptr;
+    size_t part_cap = 0;
 };
+// Floats of K-part sums that the product of this shape uses (0: K whole).
+size_t mx_product_parts(int M, int n, int blocks, int x_type);
+// Padded scale rows into 32-row tiles: round_up(M, 32) * blocks bytes.
+int launch_mx_tile_scales(const uint8_t *xs, int M, int blocks, uint8_t *out, void *stream);
 int launch_mx_product(const MxProduct &p, void *stream);
 // dx (M x m) = dy (M x n) w, both f16 or bf16.
 int launch_mx_backward(const void *dy, int type, int M, const MxWeight &w, void *dx, void *stream);

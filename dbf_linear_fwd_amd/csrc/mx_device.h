@@ -131,28 +131,30 @@ __device__ __forceinline__ float mx_scale_value(uint32_t s) {
     return __builtin_bit_cast(float, bits);
 }
 
+// Turn saturation of e4m3 conversions on or off for this wave (the mode bit
+// FP16_OVFL; it also keeps overflowing f16 results finite, so it is on only
+// around the conversions).
+__device__ __forceinline__ void mx_saturate(bool on) {
+    // hwreg(MODE, offset 23, size 1)
+    if (on) __builtin_amdgcn_s_setreg(1 | (23 << 6), 1);
+    else __builtin_amdgcn_s_setreg(1 | (23 << 6), 0);
+}
+
 // Codes of eight values of a block with scale byte s: e4m3 in two words,
 // e2m1 in one.  The conversion instruction divides by the power of two and
-// rounds to nearest even; e2m1 saturates in it, e4m3 does not, so the values
-// are brought into +-448 * 2^(s-127) first.  A block with a non-finite
-// value (s = 255) has zero codes.
+// rounds to nearest even; e2m1 saturates in it, e4m3 under mx_saturate.  A
+// block with a non-finite value (s = 255) has zero codes.
 template <int FMT>
 __device__ __forceinline__ u32v2 mx_codes8(const float (&v)[8], uint32_t s) {
     u32v2 r = {0u, 0u};
     if (s == 255u) return r;
     const float sc = mx_scale_value(s);
     if constexpr (FMT == DBF_TYPE_E4M3) {
-        // 448 * 2^(s-127) = 1.75 * 2^(s+8-127)
-        const float top = __builtin_bit_cast(float, ((s + 8u) << 23) | 0x00600000u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             s16x2 w = {0, 0};
-            const float a = __builtin_amdgcn_fmed3f(v[4 * h], -top, top);
-            const float b = __builtin_amdgcn_fmed3f(v[4 * h + 1], -top, top);
-            const float c = __builtin_amdgcn_fmed3f(v[4 * h + 2], -top, top);
-            const float d = __builtin_amdgcn_fmed3f(v[4 * h + 3], -top, top);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, sc, false);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, sc, true);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[4 * h], v[4 * h + 1], sc, false);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, v[4 * h + 2], v[4 * h + 3], sc, true);
             r[h] = __builtin_bit_cast(uint32_t, w);
         }
     } else {
@@ -167,10 +169,10 @@ __device__ __forceinline__ u32v2 mx_codes8(const float (&v)[8], uint32_t s) {
 }
 
 // Quantise the eight columns of this lane (lanes 4q..4q+3 hold one block's 32
-// columns in order) and store codes and scale of column `col` (a multiple of
-// 8) of a row.
+// columns in order) and store the codes of column `col` (a multiple of 8) of
+// a row, and the block's scale byte at `scale`.
 template <int FMT>
-__device__ __forceinline__ void mx_store8(const float (&v)[8], int col, uint8_t *crow, uint8_t *srow) {
+__device__ __forceinline__ void mx_store8(const float (&v)[8], int col, uint8_t *crow, uint8_t *scale) {
     uint32_t a = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -182,7 +184,7 @@ __device__ __forceinline__ void mx_store8(const float (&v)[8], int col, uint8_t 
     const u32v2 c = mx_codes8<FMT>(v, s);
     if constexpr (FMT == DBF_TYPE_E4M3) *reinterpret_cast<u32v2 *>(crow + col) = c;
     else *reinterpret_cast<uint32_t *>(crow + col / 2) = c[0];
-    if ((col & 31) == 0) srow[col >> 5] = static_cast<uint8_t>(s);
+    if ((col & 31) == 0) *scale = static_cast<uint8_t>(s);
 }
 
 }  // namespace dbf

@@ -11,10 +11,14 @@
 
 #include "mx_device.h"
 
+#include <algorithm>
+#include <atomic>
+
 namespace dbf {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -24,47 +28,432 @@ __device__ __forceinline__ i32x8 operand(u32v4 a, u32v4 b) {
                  static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
 }
 
-// One wave per 32 x 32 output tile.
-template <int FMT, typename E>
-__global__ __launch_bounds__(256) void mx_product_kernel(const uint8_t *__restrict__ xc,
-                                                         const uint8_t *__restrict__ xs, int M, MxWeight w,
-                                                         typename E::T *__restrict__ y) {
-    const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
-    const int nt = w.n_pad / 32;
-    const int64_t tile = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    const int64_t mt64 = tile / nt;
-    if (mt64 * 32 >= M) return;
-    const int mt = static_cast<int>(mt64), t = static_cast<int>(tile - mt64 * nt);
-    const int row = mt * 32 + r < M ? mt * 32 + r : M - 1;  // rows past M: multiplied, not written
-    const int kb = w.blocks;
-    constexpr int kBytes = FMT == DBF_TYPE_E4M3 ? 32 : 16;  // of a block
-    const uint8_t *xr = xc + static_cast<size_t>(row) * kb * kBytes;
-    const uint8_t *xsr = xs + static_cast<size_t>(row) * kb;
-    const uint8_t *wt = w.codes + (static_cast<size_t>(t) * kb * 32 + r) * 16;
-    const uint8_t *wst = w.scales + (static_cast<size_t>(t) * (kb >> 2) * 32 + r) * 4;
-    f32x16 acc = {};
-    for (int b = 0; b < kb; b += 2) {
-        u32v4 a0, a1 = {0u, 0u, 0u, 0u};
-        if constexpr (FMT == DBF_TYPE_E4M3) {
-            a0 = *reinterpret_cast<const u32v4 *>(xr + b * 32 + 16 * g);
-            a1 = *reinterpret_cast<const u32v4 *>(xr + b * 32 + 32 + 16 * g);
-        } else {
-            a0 = *reinterpret_cast<const u32v4 *>(xr + (b + g) * 16);
-        }
-        const u32v4 z = {0u, 0u, 0u, 0u};
-        const u32v4 c = *reinterpret_cast<const u32v4 *>(wt + static_cast<size_t>(b + g) * 512);
-        const int sx = xsr[b + g];
-        const int sw = wst[static_cast<size_t>((b + g) >> 2) * 128 + ((b + g) & 3)];
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a0, a1), operand(c, z), acc,
-                                                              FMT == DBF_TYPE_E4M3 ? 0 : 4, 4, 0, sx, 0, sw);
+// ---------------------------------------------------------------------------
+// Tiled product: a BM x BN output tile per workgroup; K goes through a ring of
+// LDS stages that global_load_lds fills several stages ahead.
+//
+// A stage holds 64 bytes of each of the tile's rows of x (64 columns of e4m3,
+// 128 of e2m1) and the weight's blocks of the same columns; scale words (four
+// bytes: 128 columns) sit in stages of their own kind, one per 128 columns.
+// The 16-byte chunks of a row of x are permuted so that eight rows which one
+// operand read touches fall on different banks; the weight's and the scales'
+// device order is the order in which the lanes read them.
+//
+// The unit of work is a half: 64 columns, MI x NI matrix-core instructions
+// per wave.  While a half is multiplied, the operands of the next one are
+// read from LDS and loads of a later stage are started, one or two between
+// each two products: bunched in front of them they leave the matrix cores
+// idle (2048 x 4096, K 14336, e4m3, 128 x 256 tiles: 104 instead of 95 us).
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ void dma16(const void *g, char *l) {
+    __builtin_amdgcn_global_load_lds(g, (lds_void *)(l), 16, 0, 0);
+}
+__device__ __forceinline__ void dma4(const void *g, char *l) {
+    __builtin_amdgcn_global_load_lds(g, (lds_void *)(l), 4, 0, 0);
+}
+
+// Wait until at most N of this wave's loads are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    // vmcnt bits [3:0] and [15:14]; expcnt [6:4] and lgkmcnt [11:8] left at "no wait"
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+// This wave's LDS reads have returned.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14)); }
+
+// Nothing moves across in the compiler's schedule.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+__device__ __forceinline__ void block_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int V>
+using Const = std::integral_constant<int, V>;
+
+// A product tile: waves WM x WN, each MI x NI fragments of 32 x 32.
+template <int FMT_, int MI_, int NI_, int WM_, int WN_, int S_>
+struct MxTile {
+    static constexpr int FMT = FMT_, MI = MI_, NI = NI_, WM = WM_, WN = WN_, S = S_;
+    static constexpr bool X8 = FMT == DBF_TYPE_E4M3;
+    static constexpr int Waves = WM * WN, Threads = 64 * Waves;
+    static constexpr int BM = 32 * MI * WM, BN = 32 * NI * WN;
+    static constexpr int Parts = X8 ? 2 : 1;               // stages per 128 columns
+    static constexpr int WTile = 2048 / Parts;             // bytes of 32 weight rows in a stage
+    static constexpr int XBytes = BM * 64, WBytes = BN / 32 * WTile;
+    static constexpr int StageBytes = XBytes + WBytes;
+    static constexpr int SBytes = (BM + BN + 63) / 64 * 256;  // scale words of x, then of w
+    static constexpr int ScaleAt = S * StageBytes;            // S / Parts scale stages
+    static constexpr size_t Lds = static_cast<size_t>(S) * StageBytes + static_cast<size_t>(S / Parts) * SBytes;
+    static constexpr int Units16 = StageBytes / 1024;         // 1 KiB loads
+    static constexpr int Units4 = SBytes / 256;               // 256-byte loads
+    static constexpr int D16 = (Units16 + Waves - 1) / Waves, D4 = (Units4 + Waves - 1) / Waves;
+    // loads per wave of the stage at part p of its 128 columns
+    static constexpr int loads(int p) { return p == 0 ? D16 + D4 : D16; }
+    // loads of the y stages after one at part p
+    static constexpr int younger(int p, int y) {
+        int n = 0;
+        for (int i = 1; i <= y; ++i) n += loads((p + i) % Parts);
+        return n;
     }
-    const int col = t * 32 + r;
-    if (col >= w.n) return;
+    static constexpr int XR = X8 ? 2 : 1;                     // 16-byte reads of an x fragment
+    static constexpr int Reads = MI * XR + NI;
+    static_assert(S % Parts == 0 && S >= 3, "whole 128 columns; a stage lands while one is read");
+    static_assert(StageBytes % 1024 == 0, "whole loads");
+    static_assert(Lds <= 160 * 1024, "LDS of a CU");
+    static_assert(younger(0, S - 1) < 64, "vmcnt range");
+};
+
+// The operands of a half in registers.
+template <typename C>
+struct MxFrags {
+    u32v4 x[C::MI][C::XR], w[C::NI];
+};
+// Scale words of 128 columns, one of four blocks for each row.
+template <typename C>
+struct MxScales {
+    int x[C::MI], w[C::NI];
+};
+
+// Read `i` of the operands of half T from its stage.  xrow / wrow: this
+// lane's place in the stage's rows of x and in its weight.
+template <typename C, int T>
+__device__ __forceinline__ void read_operand(const char *__restrict__ stage, MxFrags<C> &r, int i, int xrow, int wrow,
+                                             int swz, int g) {
+    if (i < C::MI * C::XR) {
+        const int f = i / C::XR, h = i % C::XR;
+        const int c = C::X8 ? 2 * h + g : 2 * T + g;
+        r.x[f][h] = *reinterpret_cast<const u32v4 *>(stage + xrow + f * 2048 + ((c ^ swz) << 4));
+    } else {
+        const int f = i - C::MI * C::XR;
+        r.w[f] = *reinterpret_cast<const u32v4 *>(stage + wrow + f * C::WTile + (C::X8 ? 0 : T * 1024));
+    }
+}
+
+template <typename C>
+__device__ __forceinline__ void read_scales(const char *__restrict__ stage, MxScales<C> &s, int wm, int wn, int l32) {
+    const uint32_t *sc = reinterpret_cast<const uint32_t *>(stage) + l32;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int o = mt * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
-        if (o < M) y[static_cast<size_t>(o) * w.n + col] = E::put(acc[v]);
+    for (int i = 0; i < C::MI; ++i) s.x[i] = static_cast<int>(sc[(wm * C::MI + i) * 32]);
+#pragma unroll
+    for (int f = 0; f < C::NI; ++f) s.w[f] = static_cast<int>(sc[C::BM + (wn * C::NI + f) * 32]);
+}
+
+// Bytes 0 and 2 become this lane's blocks (of lane group g) of the two halves.
+template <typename C>
+__device__ __forceinline__ void shift_scales(MxScales<C> &d, const MxScales<C> &s, int g) {
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) d.x[i] = s.x[i] >> (8 * g);
+#pragma unroll
+    for (int f = 0; f < C::NI; ++f) d.w[f] = s.w[f] >> (8 * g);
+}
+
+// The products of half T, with between(j) after each.
+template <typename C, int T, typename F>
+__device__ __forceinline__ void multiply(const MxFrags<C> &r, const MxScales<C> &s, f32x16 (&acc)[C::MI][C::NI],
+                                         F between) {
+    constexpr int FX = C::X8 ? 0 : 4;
+    const u32v4 z = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+        for (int f = 0; f < C::NI; ++f) {
+            acc[i][f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                operand(r.w[f], z), operand(r.x[i][0], C::X8 ? r.x[i][C::XR - 1] : z), acc[i][f], 4, FX, 2 * T, s.w[f],
+                2 * T, s.x[i]);
+            between(i * C::NI + f);
+            keep_order();
+        }
+}
+
+// Scale rows of x (padded row layout) into 32-row tiles like the weight's: a
+// step's scale words of 32 rows are 128 contiguous bytes.  Read as rows, the
+// 256 words of a tile's 128 columns come from 256 cache lines (2048 x 14336,
+// K 4096, e2m1: 88 instead of 83 us).
+__global__ __launch_bounds__(256) void mx_tile_scales_kernel(const uint32_t *__restrict__ xs, int M, int steps,
+                                                             uint32_t *__restrict__ out) {
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t q = idx >> 5;
+    const int64_t t = q / steps;
+    if (t * 32 >= M) return;
+    const int k = static_cast<int>(q - t * steps);
+    const int64_t row = t * 32 + (idx & 31);
+    out[idx] = row < M ? xs[row * steps + k] : 0u;
+}
+
+// XCD-aware position of workgroup b among G: the workgroups of one XCD
+// (b mod 8) take consecutive indexes, so that they share operands in its L2.
+__device__ __forceinline__ int xcd_index(int b, int G) {
+    constexpr int kXcds = 8;
+    const int xcd = b % kXcds, slot = b / kXcds, q = G / kXcds, rem = G % kXcds;
+    return xcd * q + min(xcd, rem) + slot;
+}
+
+struct MxGemmArgs {
+    const uint8_t *xc, *xs;  // codes in padded rows; scales in 32-row tiles
+    int M;
+    MxWeight w;
+    void *y;
+    int nbm, nbn, nsplit;
+    float *part;             // null: whole sums to y
+    int group;               // tile rows that consecutive workgroups go through first
+};
+
+// Output tile of position `tile`: bands of `group` tile rows, column by
+// column within a band, so that the tiles which run on one XCD at a time
+// form a block that shares its rows of x and of the weight in that XCD's L2.
+__device__ __forceinline__ void tile_at(const MxGemmArgs &a, int tile, int &bm, int &bn) {
+    const int band = tile / (a.group * a.nbn);
+    const int rows = min(a.group, a.nbm - band * a.group);
+    const int at = tile - band * a.group * a.nbn;
+    bn = at / rows;
+    bm = band * a.group + at - bn * rows;
+}
+
+// A wave's results to y.  A 32 x 32 result has one row of y per lane, its
+// columns 8 (v / 4) + 4 g + v % 4 in register v; each wave takes them through
+// its own part of LDS into rows of 16-byte stores.  (Stored from the
+// registers, two bytes a lane: 106 instead of 101 us, 256 x 256 tiles of
+// 2048 x 14336, K 4096.)
+template <typename C, typename E>
+__device__ __forceinline__ void store_tile(char *lds, const f32x16 (&acc)[C::MI][C::NI], const MxGemmArgs &a, int m0,
+                                           int n0, int wave, int lane) {
+    const int wm = wave / C::WN, wn = wave % C::WN, l32 = lane & 31, g = lane >> 5;
+    constexpr int Cols = 32 * C::NI, Pitch = Cols * 2 + 16;  // 16-bit values of a wave's row, bytes
+    static_assert(static_cast<size_t>(C::Waves) * 32 * Pitch <= C::Lds, "a result fits the ring");
+    char *mine = lds + wave * (32 * Pitch);
+    uint16_t *y = static_cast<uint16_t *>(a.y);
+    const int c0 = n0 + wn * Cols;
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) {
+        const int r0 = m0 + (wm * C::MI + i) * 32;
+#pragma unroll
+        for (int f = 0; f < C::NI; ++f)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t p[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float lo = acc[i][f][4 * q + 2 * h], hi = acc[i][f][4 * q + 2 * h + 1];
+                    p[h] = static_cast<uint32_t>(E::put(lo)) | static_cast<uint32_t>(E::put(hi)) << 16;
+                }
+                *reinterpret_cast<u32v2 *>(mine + l32 * Pitch + (f * 32 + 8 * q + 4 * g) * 2) = u32v2{p[0], p[1]};
+            }
+        if (a.w.n % 8 == 0) {
+            constexpr int Per = Cols / 8, Rows = 64 / Per;  // lanes per row, rows per store
+            const int c = lane % Per * 8;
+#pragma unroll
+            for (int j = 0; j < 32; j += Rows) {
+                const int r = j + lane / Per;
+                const u32v4 v = *reinterpret_cast<const u32v4 *>(mine + r * Pitch + c * 2);
+                if (r0 + r < a.M && c0 + c < a.w.n)
+                    *reinterpret_cast<u32v4 *>(y + static_cast<size_t>(r0 + r) * a.w.n + c0 + c) = v;
+            }
+        } else {
+            for (int j = lane; j < 32 * Cols; j += 64) {
+                const int r = j / Cols, c = j % Cols;
+                if (r0 + r < a.M && c0 + c < a.w.n)
+                    y[static_cast<size_t>(r0 + r) * a.w.n + c0 + c] =
+                        *reinterpret_cast<const uint16_t *>(mine + r * Pitch + c * 2);
+            }
+        }
     }
+}
+
+template <typename C, typename E>
+__global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int T = a.nbm * a.nbn;
+    const int idx = xcd_index(blockIdx.x, T * a.nsplit);
+    const int split = idx / T, tile = idx - split * T;
+    int bm, bn;
+    tile_at(a, tile, bm, bn);
+    const int m0 = bm * C::BM, n0 = bn * C::BN;
+    const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const int steps = a.w.blocks >> 2;  // of 128 columns
+    const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / a.nsplit);
+    const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * steps / a.nsplit) - k0;
+
+    // sources of this wave's loads; a stage moves them by inc bytes
+    const uint8_t *src[C::D16 + C::D4];
+    int inc[C::D16], at[C::D16 + C::D4];
+#pragma unroll
+    for (int q = 0; q < C::D16; ++q) {
+        const int u = min(wave * C::D16 + q, C::Units16 - 1);  // (a unit too many: loaded twice, the same bytes)
+        at[q] = u * 1024;
+        constexpr int XU = C::XBytes / 1024;
+        if (u < XU) {
+            const int c = u * 64 + lane, r = c >> 2, lc = (c & 3) ^ ((r >> 1) & 3);
+            const int row = min(m0 + r, a.M - 1);  // rows past M: multiplied, not written
+            src[q] = a.xc + (static_cast<size_t>(row) * steps + k0) * (64 * C::Parts) + lc * 16;
+            inc[q] = 64;
+        } else {
+            const int v = (u - XU) * 1024 + lane * 16;  // byte of the stage's weight
+            const int t = min(n0 / 32 + v / C::WTile, a.w.n_pad / 32 - 1);
+            src[q] = a.w.codes + (static_cast<size_t>(t) * steps + k0) * 2048 + v % C::WTile;
+            inc[q] = C::WTile;
+        }
+    }
+#pragma unroll
+    for (int q = C::D16; q < C::D16 + C::D4; ++q) {
+        const int u = min(wave * C::D4 + q - C::D16, C::Units4 - 1);
+        at[q] = C::ScaleAt + u * 256;
+        const int r = u * 64 + lane;
+        const bool x = r < C::BM;
+        // 32-row tiles; those past the end (and the padding of the last load): any valid one
+        const int t = x ? min((m0 + r) / 32, (a.M + 31) / 32 - 1) : min((n0 + r - C::BM) / 32, a.w.n_pad / 32 - 1);
+        src[q] = (x ? a.xs : a.w.scales) + (static_cast<size_t>(t) * steps + k0) * 128 + (r & 31) * 4;
+    }
+    // load q of the stage in slot `slot`
+    auto issue_one = [&](int slot, int q) {
+        if (q < C::D16) {
+            dma16(src[q], lds + slot * C::StageBytes + at[q]);
+            src[q] += inc[q];
+        } else {
+            dma4(src[q], lds + (slot / C::Parts) * C::SBytes + at[q]);
+            src[q] += 128;
+        }
+    };
+
+    f32x16 acc[C::MI][C::NI];
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+        for (int f = 0; f < C::NI; ++f)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.0f;
+
+    const int xrow = (wm * C::MI * 32 + l32) * 64, swz = (l32 >> 1) & 3;
+    const int wrow = C::XBytes + wn * C::NI * C::WTile + g * 512 + l32 * 16;
+    MxFrags<C> f0, f1;
+    MxScales<C> sc, sn;
+    auto stage_at = [&](int slot) { return lds + slot * C::StageBytes; };
+    auto scales_at = [&](int slot) { return lds + C::ScaleAt + (slot / C::Parts) * C::SBytes; };
+    auto next = [](int slot) { return slot + 1 == C::S ? 0 : slot + 1; };
+
+    // One half: multiply `cur` while `nxt` (half 1 - T of the stage in slot
+    // nslot) is read and the loads of part P's stage into slot fslot start
+    // (P < 0: none).  No branch inside: the compiler would move the products
+    // behind it.
+    constexpr int NM = C::MI * C::NI;
+    auto half = [&](auto t, auto part, const MxFrags<C> &cur, MxFrags<C> &nxt, int nslot, int fslot) {
+        constexpr int TC = decltype(t)::value, TN = 1 - TC, P = decltype(part)::value;
+        constexpr int NL = P >= 0 ? C::loads(P) : 0;
+        const char *st = stage_at(nslot);
+        multiply<C, TC>(cur, sc, acc, [&](int j) {
+#pragma unroll
+            for (int i = C::Reads * j / NM; i < C::Reads * (j + 1) / NM; ++i)
+                read_operand<C, TN>(st, nxt, i, xrow, wrow, swz, g);
+            if constexpr (TN == 0)
+                if (j == 0) read_scales<C>(scales_at(nslot), sn, wm, wn, l32);
+#pragma unroll
+            for (int q = NL * j / NM; q < NL * (j + 1) / NM; ++q) issue_one(fslot, q);
+        });
+        if constexpr (TN == 0) shift_scales<C>(sc, sn, g);
+    };
+
+    const int stages = nk * C::Parts;
+    constexpr int Chunks = C::S / C::Parts;  // of 128 columns that the ring holds
+#pragma unroll
+    for (int st = 0; st < C::S; ++st)
+        if (st < stages) {
+#pragma unroll
+            for (int q = 0; q < C::loads(st % C::Parts); ++q) issue_one(st, q);
+        }
+    if (nk >= Chunks) wait_vm<C::younger(0, C::S - 1)>();
+    else wait_vm<0>();
+    block_barrier();
+#pragma unroll
+    for (int i = 0; i < C::Reads; ++i) read_operand<C, 0>(stage_at(0), f0, i, xrow, wrow, swz, g);
+    read_scales<C>(scales_at(0), sn, wm, wn, l32);
+    shift_scales<C>(sc, sn, g);
+
+    // Before a stage's first read: this wave's loads of it have landed, then
+    // the barrier: every wave's have, and every wave's reads of the stage
+    // before it have returned, so that one's slot is free for the next loads.
+    // The last half reads past the last stage, in LDS and to no use.
+    int slot = 0;
+    auto chunk = [&](auto go) {
+        constexpr bool GO = decltype(go)::value != 0;
+        constexpr int W0 = GO ? C::younger(0, C::S - 2) : 0, W1 = GO ? C::younger(1, C::S - 2) : 0;
+        if constexpr (C::Parts == 2) {
+            const int s1 = slot + 1, s2 = next(s1);
+            wait_vm<W1>();
+            wait_lds();
+            block_barrier();
+            half(Const<0>{}, Const<GO ? 0 : -1>{}, f0, f1, s1, slot);
+            wait_vm<W0>();
+            wait_lds();
+            block_barrier();
+            half(Const<1>{}, Const<GO ? 1 : -1>{}, f1, f0, s2, s1);
+            slot = s2;
+        } else {
+            const int s1 = next(slot);
+            half(Const<0>{}, Const<-1>{}, f0, f1, slot, 0);
+            wait_vm<W0>();
+            wait_lds();
+            block_barrier();
+            half(Const<1>{}, Const<GO ? 0 : -1>{}, f1, f0, s1, slot);
+            slot = s1;
+        }
+    };
+    int left = nk;
+    for (; left > Chunks; --left) chunk(Const<1>{});
+    for (; left > 0; --left) chunk(Const<0>{});
+
+    if (a.part) {
+        // a K part of a tile: the sums as they are, for mx_finish_kernel
+        float *p = a.part + ((static_cast<size_t>(split) * T + tile) * C::Waves + wave) * (C::MI * C::NI * 1024) + lane * 4;
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+            for (int f = 0; f < C::NI; ++f)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<f32x4 *>(p + ((i * C::NI + f) * 4 + q) * 256) =
+                        f32x4{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
+        return;
+    }
+    __syncthreads();  // every wave's last operands have been read
+    store_tile<C, E>(lds, acc, a, m0, n0, wave, lane);
+}
+
+// The K parts of a tile, added in order and stored.
+template <typename C, typename E>
+__global__ __launch_bounds__(C::Threads) void mx_finish_kernel(const MxGemmArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int T = a.nbm * a.nbn, tile = blockIdx.x;
+    int bm, bn;
+    tile_at(a, tile, bm, bn);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const float *p = a.part + (static_cast<size_t>(tile) * C::Waves + wave) * (C::MI * C::NI * 1024) + lane * 4;
+    const size_t plane = static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024);
+    f32x16 acc[C::MI][C::NI];
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+        for (int f = 0; f < C::NI; ++f)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.0f;
+    for (int s = 0; s < a.nsplit; ++s, p += plane)
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+            for (int f = 0; f < C::NI; ++f)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(p + ((i * C::NI + f) * 4 + q) * 256);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][f][4 * q + e] += v[e];
+                }
+    store_tile<C, E>(lds, acc, a, bm * C::BM, bn * C::BN, wave, lane);
 }
 
 // One wave per 32 rows x 32 columns (one block) of dX.  The weight's values
@@ -120,22 +509,152 @@ __global__ __launch_bounds__(256) void mx_backward_kernel(const typename E::T *_
 
 }  // namespace
 
+namespace {
+
+// ---- choice of the tile and of the K parts
+
+// A tile's cost: microseconds per 128 columns of K with a workgroup alone on
+// its CU's neighbourhood (few tiles) and with all CUs busy (the matrix cores'
+// clock and the L2s are shared), measured at K 4096 and 14336.
+struct TileCost {
+    int bm, bn;
+    float light[2], full[2];  // e4m3, e2m1
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, {1.05f, 0.66f}, {1.48f, 0.98f}},
+    {128, 256, {0.55f, 0.41f}, {0.78f, 0.53f}},
+    {128, 128, {0.36f, 0.27f}, {0.52f, 0.38f}},
+    {64, 128, {0.24f, 0.21f}, {0.34f, 0.27f}},
+    {64, 64, {0.19f, 0.145f}, {0.28f, 0.19f}},
+};
+constexpr int kTileCount = sizeof(kTiles) / sizeof(kTiles[0]);
+constexpr int kCus = 256;
+
+struct MxPlan {
+    int tile = 0, nsplit = 1;
+};
+
+// The tile and K parts of least estimated time: rounds of workgroups over the
+// CUs, each a start of 3 us and its steps; K parts add a launch and the
+// traffic of their fp32 sums.  (2048 x 14336, K 4096, e4m3: 256 x 256 tiles
+// 101 us, 128 x 256 116; 2048 x 4096, K 14336: 130 and 87; 64 x 4096,
+// K 14336: four parts 13, one 25.)
+MxPlan mx_plan(int M, int n, int steps, bool x8) {
+    MxPlan best;
+    float least = 0.0f;
+    const int f = x8 ? 0 : 1;
+    for (int t = 0; t < kTileCount; ++t) {
+        const TileCost &c = kTiles[t];
+        const int64_t tiles = static_cast<int64_t>((M + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
+        for (int sp : {1, 2, 3, 4, 6, 8}) {
+            if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
+            const float wgs = static_cast<float>(tiles) * sp;
+            const float load = wgs < kCus ? wgs / kCus : 1.0f;
+            // small tiles share a CU, so their last round is only as long as it is full
+            const float rounds = wgs <= kCus ? 1.0f : t < 2 ? static_cast<float>((tiles * sp + kCus - 1) / kCus) : wgs / kCus;
+            const float step = c.light[f] + (c.full[f] - c.light[f]) * load;
+            float us = rounds * (3.0f + static_cast<float>((steps + sp - 1) / sp) * step);
+            if (sp > 1) us += 3.5f + wgs * c.bm * c.bn * 8.0f * 3e-7f;
+            if (least == 0.0f || us < least) {
+                least = us;
+                best.tile = t;
+                best.nsplit = sp;
+            }
+        }
+    }
+    return best;
+}
+
+template <int FMT, int T>
+struct TileOf;
+template <int FMT>
+struct TileOf<FMT, 0> { using C = MxTile<FMT, 2, 4, 4, 2, FMT == DBF_TYPE_E4M3 ? 6 : 4>; };
+template <int FMT>
+struct TileOf<FMT, 1> { using C = MxTile<FMT, 2, 4, 2, 2, FMT == DBF_TYPE_E4M3 ? 4 : 3>; };
+template <int FMT>
+struct TileOf<FMT, 2> { using C = MxTile<FMT, 2, 2, 2, 2, FMT == DBF_TYPE_E4M3 ? 4 : 3>; };
+template <int FMT>
+struct TileOf<FMT, 3> { using C = MxTile<FMT, 2, 1, 1, 4, FMT == DBF_TYPE_E4M3 ? 8 : 6>; };
+template <int FMT>
+struct TileOf<FMT, 4> { using C = MxTile<FMT, 1, 1, 2, 2, FMT == DBF_TYPE_E4M3 ? 8 : 6>; };
+
+// More than 64 KiB of LDS has to be asked for, once per kernel and device.
+template <typename K>
+void allow_lds(K kernel, size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    (void)hipGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return;
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes));
+    done.fetch_or(bit, std::memory_order_relaxed);
+}
+
+template <typename C, typename E>
+void launch_gemm(MxGemmArgs &a, hipStream_t s) {
+    constexpr size_t kFinishLds = static_cast<size_t>(C::Waves) * 32 * (64 * C::NI + 16);
+    auto product = mx_gemm_kernel<C, E>;
+    auto finish = mx_finish_kernel<C, E>;
+    a.nbm = (a.M + C::BM - 1) / C::BM;
+    a.nbn = (a.w.n + C::BN - 1) / C::BN;
+    a.group = a.nbm < 4 ? a.nbm : 4;
+    if constexpr (C::Lds > 65536) allow_lds(product, C::Lds);
+    launch_kernel(product, dim3(a.nbm * a.nbn * a.nsplit), dim3(C::Threads), C::Lds, s, a);
+    if (a.part) {
+        if constexpr (kFinishLds > 65536) allow_lds(finish, kFinishLds);
+        launch_kernel(finish, dim3(a.nbm * a.nbn), dim3(C::Threads), kFinishLds, s, a);
+    }
+}
+
+template <int FMT, typename E, int T = 0>
+void launch_tile(int tile, MxGemmArgs &a, hipStream_t s) {
+    if constexpr (T < kTileCount) {
+        using C = typename TileOf<FMT, T>::C;
+        static_assert(C::BM == kTiles[T].bm && C::BN == kTiles[T].bn, "the table's tile");
+        if (tile == T) launch_gemm<C, E>(a, s);
+        else launch_tile<FMT, E, T + 1>(tile, a, s);
+    }
+}
+
+}  // namespace
+
+size_t mx_product_parts(int M, int n, int blocks, int x_type) {
+    const MxPlan p = mx_plan(M, n, blocks / 4, x_type == DBF_TYPE_E4M3);
+    if (p.nsplit == 1) return 0;
+    const TileCost &c = kTiles[p.tile];
+    return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((n + c.bn - 1) / c.bn * c.bn);
+}
+
+int launch_mx_tile_scales(const uint8_t *xs, int M, int blocks, uint8_t *out, void *stream) {
+    const int steps = blocks / 4;
+    const int64_t threads = static_cast<int64_t>((M + 31) / 32) * 32 * steps;
+    launch_kernel(mx_tile_scales_kernel, dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0,
+                  static_cast<hipStream_t>(stream), reinterpret_cast<const uint32_t *>(xs), M, steps,
+                  reinterpret_cast<uint32_t *>(out));
+    return static_cast<int>(hipGetLastError());
+}
+
 int launch_mx_product(const MxProduct &p, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t tiles = static_cast<int64_t>((p.M + 31) / 32) * (p.w.n_pad / 32);
-    const dim3 grid(static_cast<uint32_t>((tiles + 3) / 4));
-    auto go = [&](auto f, auto e) {
-        using E = decltype(e);
-        launch_kernel(mx_product_kernel<decltype(f)::value, E>, grid, dim3(256), 0, s,
-                      static_cast<const uint8_t *>(p.xcodes), p.xscales, p.M, p.w, static_cast<typename E::T *>(p.y));
-    };
+    MxGemmArgs a{};
+    a.xc = static_cast<const uint8_t *>(p.xcodes);
+    a.xs = p.xscales;
+    a.M = p.M;
+    a.w = p.w;
+    a.y = p.y;
+    const MxPlan plan = mx_plan(p.M, p.w.n, p.w.blocks / 4, p.x_type == DBF_TYPE_E4M3);
+    a.nsplit = plan.nsplit;
+    a.part = plan.nsplit > 1 ? p.part : nullptr;
+    if (plan.nsplit > 1 && (!p.part || p.part_cap < mx_product_parts(p.M, p.w.n, p.w.blocks, p.x_type)))
+        return static_cast<int>(hipErrorInvalidValue);
     auto pick = [&](auto f) {
-        if (p.y_type == DBF_TYPE_F16) go(f, F16{});
-        else if (p.y_type == DBF_TYPE_BF16) go(f, BF16{});
-        else go(f, F32{});
+        constexpr int FMT = decltype(f)::value;
+        if (p.y_type == DBF_TYPE_F16) launch_tile<FMT, F16>(plan.tile, a, s);
+        else launch_tile<FMT, BF16>(plan.tile, a, s);
     };
-    if (p.x_type == DBF_TYPE_E4M3) pick(std::integral_constant<int, DBF_TYPE_E4M3>{});
-    else pick(std::integral_constant<int, DBF_TYPE_E2M1>{});
+    if (p.x_type == DBF_TYPE_E4M3) pick(Const<DBF_TYPE_E4M3>{});
+    else pick(Const<DBF_TYPE_E2M1>{});
     return static_cast<int>(hipGetLastError());
 }
 

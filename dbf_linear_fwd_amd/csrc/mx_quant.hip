@@ -18,7 +18,7 @@ namespace {
 template <typename E, int FMT, bool VEC>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const typename E::T *__restrict__ x, uint32_t rows,
                                                           int cols, int wide, uint8_t *__restrict__ codes,
-                                                          uint8_t *__restrict__ scales) {
+                                                          uint8_t *__restrict__ scales, int tiled) {
     const uint32_t per_row = static_cast<uint32_t>(wide) / 8;
     const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
     const uint32_t row = idx / per_row;
@@ -27,8 +27,12 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const typename E::T *_
     float v[8];
     load8<E, VEC>(x + static_cast<size_t>(row) * cols + col, cols - col, v);
     constexpr int kPer = FMT == DBF_TYPE_E4M3 ? 1 : 2;  // columns per byte
-    mx_store8<FMT>(v, col, codes + static_cast<size_t>(row) * (wide / kPer),
-                   scales + static_cast<size_t>(row) * (wide / 32));
+    if constexpr (FMT == DBF_TYPE_E4M3) mx_saturate(true);
+    // tiled: four scale bytes of a row, then the next row of the 32-row tile
+    const int kb = col >> 5;
+    uint8_t *at = tiled ? scales + (static_cast<size_t>(row >> 5) * (wide / 128) + (kb >> 2)) * 128 + (row & 31) * 4 + (kb & 3)
+                        : scales + static_cast<size_t>(row) * (wide / 32) + kb;
+    mx_store8<FMT>(v, col, codes + static_cast<size_t>(row) * (wide / kPer), at);
 }
 
 // Values of eight columns per lane.  The conversion instructions multiply by
@@ -148,7 +152,7 @@ uint32_t grid_for(uint64_t threads) { return static_cast<uint32_t>((threads + 25
 }  // namespace
 
 int launch_mx_quantize(const void *x, int x_type, int rows, int cols, int fmt, void *codes, uint8_t *scales,
-                       void *stream) {
+                       bool tiled, void *stream) {
     const int wide = round_up_int(cols, 128);
     const dim3 grid(grid_for(static_cast<uint64_t>(rows) * (wide / 8)));
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -158,8 +162,8 @@ int launch_mx_quantize(const void *x, int x_type, int rows, int cols, int fmt, v
         constexpr int FMT = decltype(f)::value;
         const auto *p = static_cast<const typename E::T *>(x);
         auto *c = static_cast<uint8_t *>(codes);
-        if (vec) launch_kernel(mx_quantize_kernel<E, FMT, true>, grid, dim3(256), 0, s, p, uint32_t(rows), cols, wide, c, scales);
-        else launch_kernel(mx_quantize_kernel<E, FMT, false>, grid, dim3(256), 0, s, p, uint32_t(rows), cols, wide, c, scales);
+        if (vec) launch_kernel(mx_quantize_kernel<E, FMT, true>, grid, dim3(256), 0, s, p, uint32_t(rows), cols, wide, c, scales, int(tiled));
+        else launch_kernel(mx_quantize_kernel<E, FMT, false>, grid, dim3(256), 0, s, p, uint32_t(rows), cols, wide, c, scales, int(tiled));
     };
     auto pick = [&](auto f) {
         if (x_type == DBF_TYPE_F16) go(F16{}, f);
@@ -243,7 +247,7 @@ extern "C" dbf_status_t dbf_mx_quantize(const void *x, int32_t x_type, int32_t r
                                         void *codes, uint8_t *scales, hipStream_t stream) {
     const dbf_status_t st = check(x, x_type, rows, cols, type, codes, scales);
     if (st != DBF_OK || rows == 0) return st;
-    return dbf::launch_mx_quantize(x, x_type, rows, cols, type, codes, scales, stream) == 0 ? DBF_OK : DBF_ERR_HIP;
+    return dbf::launch_mx_quantize(x, x_type, rows, cols, type, codes, scales, false, stream) == 0 ? DBF_OK : DBF_ERR_HIP;
 }
 
 extern "C" dbf_status_t dbf_mx_dequantize(const void *codes, const uint8_t *scales, int32_t type, int32_t rows,

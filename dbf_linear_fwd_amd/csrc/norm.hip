@@ -92,6 +92,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rms_norm_kernel(cons
     const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     const int wide = (a.cols + 127) / 128 * 128;
+    if constexpr (MX) mx_saturate(true);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int col = (c * 64 * WPR + t) * 8;
@@ -109,7 +110,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rms_norm_kernel(cons
                     for (int i = 0; i < 8; ++i) y[i] = col + i < a.cols ? y[i] : 0.0f;
                 }
                 mx_store8<DBF_TYPE_E4M3>(y, col, static_cast<uint8_t *>(a.y) + static_cast<size_t>(row) * wide,
-                                         a.ys + static_cast<size_t>(row) * (wide / 32));
+                                         a.ys + static_cast<size_t>(row) * (wide / 32) + (col >> 5));
             }
         } else {
             store8<E, VEC>(static_cast<T *>(a.y) + base + col, a.cols - col, y);

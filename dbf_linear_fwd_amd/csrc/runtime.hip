@@ -887,44 +887,95 @@ static dbf::MxWeight mx_weight(const dbf_layer *h) {
     return w;
 }
 
-// x of x_type (16 bits: quantised into the handle's workspace first; blocks:
-// codes at x, scales at x_scales) times the weight; arguments are checked.
-static dbf_status_t forward_mx(dbf_layer *h, const void *x, int32_t x_type, const uint8_t *x_scales, void *y,
-                               int32_t y_type, int32_t batch, hipStream_t stream) {
+// One or several layers (same m, same activation format) on the input x of
+// x_type (f16 / bf16 rows, or blocks with x_scales); arguments are checked.
+// Few rows: one launch for all the layers, the 16-bit rows quantised by it
+// where it can; otherwise x is quantised once into the first handle's
+// workspace and each layer's product is a launch (two with K parts).
+static dbf_status_t forward_mx(dbf_layer *const *hs, int count, const void *x, int32_t x_type,
+                               const uint8_t *x_scales, void *const *ys, int32_t y_type, int32_t batch,
+                               hipStream_t stream) {
+    dbf_layer *h = hs[0];  // kernel timing follows the first handle
+    const bool real = x_type == DBF_TYPE_F16 || x_type == DBF_TYPE_BF16;
+    const int act = real ? h->mx_act : x_type;
+    const int blocks = h->m_pad / 32;
+    const bool few = batch <= dbf::kMxDecodeBatch;
+    const bool direct = real && batch <= dbf::kDecodeMaxBatch && h->m % 8 == 0;
+    dbf_status_t st = DBF_OK;
+    if (real && !direct) {
+        st = timed_launch(h, "mx_quantize", stream, [&] {
+            return dbf::launch_mx_quantize(x, x_type, batch, h->m, act, h->mx_xcodes, h->mx_xscales, !few, stream);
+        });
+        x = h->mx_xcodes;
+        x_scales = h->mx_xscales;
+        x_type = act;
+    } else if (!real && !few) {
+        st = timed_launch(h, "mx_tile_scales", stream,
+                          [&] { return dbf::launch_mx_tile_scales(x_scales, batch, blocks, h->mx_xscales, stream); });
+        x_scales = h->mx_xscales;
+    }
+    if (st != DBF_OK) return st;
+    if (few) {
+        dbf::MxDecodeArgs d;
+        d.x = x;
+        d.xs = x_scales;
+        d.x_type = x_type;
+        d.act = act;
+        d.batch = batch;
+        d.y_type = y_type;
+        d.count = count;
+        for (int i = 0; i < count; ++i) {
+            d.w[i] = mx_weight(hs[i]);
+            d.y[i] = ys[i];
+        }
+        return timed_launch(h, "mx_decode", stream, [&] { return dbf::launch_mx_decode(d, stream); });
+    }
     dbf::MxProduct p;
     p.xcodes = x;
     p.xscales = x_scales;
-    p.x_type = x_type;
-    if (x_type == DBF_TYPE_F16 || x_type == DBF_TYPE_BF16) {
-        const dbf_status_t st = timed_launch(h, "mx_quantize", stream, [&] {
-            return dbf::launch_mx_quantize(x, x_type, batch, h->m, h->mx_act, h->mx_xcodes, h->mx_xscales, stream);
-        });
-        if (st != DBF_OK) return st;
-        p.xcodes = h->mx_xcodes;
-        p.xscales = h->mx_xscales;
-        p.x_type = h->mx_act;
-    }
+    p.x_type = act;
     p.M = batch;
-    p.w = mx_weight(h);
-    p.y = y;
     p.y_type = y_type;
-    return timed_launch(h, "mx_product", stream, [&] { return dbf::launch_mx_product(p, stream); });
+    for (int i = 0; i < count && st == DBF_OK; ++i) {
+        p.w = mx_weight(hs[i]);
+        p.y = ys[i];
+        p.part = hs[i]->split;
+        p.part_cap = hs[i]->split_cap;
+        st = timed_launch(h, "mx_product", stream, [&] { return dbf::launch_mx_product(p, stream); });
+    }
+    return st;
 }
 
-// Layers that share the f16 input: it is quantised once for the layers of
-// one activation format.
+// Layers that share the f16 input, those of one activation format together.
 static dbf_status_t forward_mx_group(const dbf_handle_t *hs, int32_t count, const void *x, void *const *ys,
                                      int32_t batch, hipStream_t stream) {
-    for (int i = 0; i < count; ++i) {
-        const dbf_layer *q = nullptr;  // an earlier layer of the same format: its quantised x
-        for (int j = 0; j < i && !q; ++j)
-            if (hs[j]->mx_act == hs[i]->mx_act) q = hs[j];
-        const dbf_status_t st =
-            q ? forward_mx(hs[i], q->mx_xcodes, q->mx_act, q->mx_xscales, ys[i], DBF_TYPE_F16, batch, stream)
-              : forward_mx(hs[i], x, DBF_TYPE_F16, nullptr, ys[i], DBF_TYPE_F16, batch, stream);
+    for (int32_t act : {DBF_TYPE_E4M3, DBF_TYPE_E2M1}) {
+        dbf_layer *sel[dbf::kMaxGroup];
+        void *out[dbf::kMaxGroup];
+        int n = 0;
+        for (int i = 0; i < count; ++i)
+            if (hs[i]->mx_act == act) {
+                sel[n] = hs[i];
+                out[n++] = ys[i];
+            }
+        if (n == 0) continue;
+        const dbf_status_t st = forward_mx(sel, n, x, DBF_TYPE_F16, nullptr, out, DBF_TYPE_F16, batch, stream);
         if (st != DBF_OK) return st;
     }
     return DBF_OK;
+}
+
+// Floats of K-part sums of any forward up to max_batch (the tile grid changes
+// every 64 rows; either activation format may come in ready blocks).
+static size_t mx_part_floats(int32_t n, int32_t blocks, int32_t max_batch) {
+    size_t most = 0;
+    for (int64_t top = dbf::kMxDecodeBatch + 1;; top += 64) {
+        const int32_t M = static_cast<int32_t>(std::min<int64_t>(top, max_batch));
+        if (M <= dbf::kMxDecodeBatch) break;
+        for (int32_t t : {DBF_TYPE_E4M3, DBF_TYPE_E2M1}) most = std::max(most, dbf::mx_product_parts(M, n, blocks, t));
+        if (M == max_batch || top > 65536) break;
+    }
+    return most;
 }
 
 extern "C" dbf_status_t dbf_mx_pack(int32_t n, int32_t m, const void *codes, const uint8_t *scales, int32_t act_type,
@@ -952,13 +1003,16 @@ extern "C" dbf_status_t dbf_mx_pack(int32_t n, int32_t m, const void *codes, con
     const size_t blocks = static_cast<size_t>(m_pad) / 32;
     const size_t code_bytes = static_cast<size_t>(n_pad) * blocks * 16, scale_bytes = static_cast<size_t>(n_pad) * blocks;
     const size_t xc_bytes = static_cast<size_t>(max_batch) * dbf_mx_code_bytes(m, act_type);
-    const size_t xs_bytes = static_cast<size_t>(max_batch) * blocks;
+    const size_t xs_bytes = static_cast<size_t>(round_up(max_batch, 32)) * blocks;
+    const size_t parts = mx_part_floats(n, static_cast<int32_t>(blocks), max_batch);
     dbf_status_t st = hipGetDevice(&h->device) == hipSuccess ? DBF_OK : DBF_ERR_HIP;
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_codes), code_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_scales), scale_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_colmax), blocks);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xcodes), xc_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xscales), xs_bytes);
+    if (st == DBF_OK && parts > 0) st = dev_alloc(reinterpret_cast<void **>(&h->split), sizeof(float) * parts);
+    if (st == DBF_OK) h->split_cap = parts;
     if (st == DBF_OK && dbf::launch_mx_layout(codes, scales, n, m, h->mx_codes, h->mx_scales, h->mx_colmax, stream) != 0)
         st = DBF_ERR_HIP;
     // the weight is in place when the call returns, for any stream
@@ -969,7 +1023,7 @@ extern "C" dbf_status_t dbf_mx_pack(int32_t n, int32_t m, const void *codes, con
     }
     h->packed_bytes = code_bytes;
     h->scale_bytes = scale_bytes + blocks;
-    h->workspace_bytes = xc_bytes + xs_bytes;
+    h->workspace_bytes = xc_bytes + xs_bytes + sizeof(float) * parts;
     *out = h;
     return DBF_OK;
 }
@@ -989,7 +1043,7 @@ extern "C" dbf_status_t dbf_mx_forward(dbf_handle_t h, const void *x, int32_t x_
     int cur = -1;
     if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
     if (cur != h->device) return DBF_ERR_INVALID_ARG;
-    return forward_mx(h, x, x_type, x_scales, y, y_type, batch, stream);
+    return forward_mx(&h, 1, x, x_type, x_scales, &y, y_type, batch, stream);
 }
 
 extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, void *dx, int32_t type, int32_t batch,
@@ -1024,7 +1078,7 @@ extern "C" dbf_status_t dbf_linear_forward_ex(dbf_handle_t h, const void *x, voi
     if (path == DBF_PATH_DECODE_TABLE) return DBF_ERR_UNSUPPORTED;  // (removed: slower than the matrix cores)
     if (h->mx) {
         if (path == DBF_PATH_DECODE_EXACT) return DBF_ERR_UNSUPPORTED;
-        return forward_mx(h, x, DBF_TYPE_F16, nullptr, y, DBF_TYPE_F16, batch, stream);
+        return forward_mx(&h, 1, x, DBF_TYPE_F16, nullptr, &y, DBF_TYPE_F16, batch, stream);
     }
     if (path == DBF_PATH_DECODE_EXACT) {
         // the exact int8 sums at batch 1..4, every row the bits of its batch-1 forward
@@ -1327,7 +1381,9 @@ ScratchPlan plan_scratch(const dbf_layer *h, int32_t batch) {
     };
     if (h->mx) {
         p.xcodes = take(size_t(batch) * dbf_mx_code_bytes(h->m, h->mx_act));
-        p.xscales = take(size_t(batch) * dbf_mx_scale_bytes(h->m));
+        p.xscales = take(size_t(round_up(batch, 32)) * dbf_mx_scale_bytes(h->m));
+        if (batch > dbf::kMxDecodeBatch) p.split_cap = dbf::mx_product_parts(batch, h->n, h->m_pad / 32, h->mx_act);
+        p.split = take(sizeof(float) * p.split_cap);
         p.total = off;
         return p;
     }
@@ -1392,6 +1448,8 @@ extern "C" dbf_status_t dbf_linear_forward_noalloc(dbf_handle_t h, const void *x
     if (h->mx) {
         h->mx_xcodes = reinterpret_cast<uint8_t *>(base + p.xcodes);
         h->mx_xscales = reinterpret_cast<uint8_t *>(base + p.xscales);
+        h->split = reinterpret_cast<float *>(base + p.split);
+        h->split_cap = p.split_cap;
     }
     if (p.i8) h->v32 = reinterpret_cast<float *>(base + p.v32);
     if (p.decode && !p.i8) h->v16 = reinterpret_cast<uint16_t *>(base + p.v16);
