@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdbf.so")
 
 HIP_SOURCES = ["runtime.hip", "decode_mfma.hip", "decode_i8.hip", "prefill.hip", "grad.hip", "bqq.hip", "factor.hip",
-               "mx_quant.hip", "mx_gemm.hip", "mx_decode.hip", "norm.hip"]
+               "mx_quant.hip", "mx_gemm.hip", "mx_decode.hip", "mx_grad.hip", "norm.hip"]
 CXX_SOURCES = ["pack.cpp"]
 
 ARCH = "gfx950"

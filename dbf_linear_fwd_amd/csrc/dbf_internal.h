@@ -319,8 +319,18 @@ size_t mx_product_parts(int M, int n, int blocks, int x_type);
 // Padded scale rows into 32-row tiles: round_up(M, 32) * blocks bytes.
 int launch_mx_tile_scales(const uint8_t *xs, int M, int blocks, uint8_t *out, void *stream);
 int launch_mx_product(const MxProduct &p, void *stream);
-// dx (M x m) = dy (M x n) w, both f16 or bf16.
-int launch_mx_backward(const void *dy, int type, int M, const MxWeight &w, void *dx, void *stream);
+// dx (M x m) = dy (M x n) w, both f16 or bf16 (type).  zeros: 16 zero bytes
+// on the device; part: at least mx_backward_parts() floats.
+struct MxBackward {
+    const void *dy = nullptr, *zeros = nullptr;
+    int type = 0, M = 0;
+    MxWeight w;
+    void *dx = nullptr;
+    float *part = nullptr;
+    size_t part_cap = 0;
+};
+size_t mx_backward_parts(int M, int n, int m);
+int launch_mx_backward(const MxBackward &b, void *stream);
 
 }  // namespace dbf
 

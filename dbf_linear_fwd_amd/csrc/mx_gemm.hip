@@ -1,7 +1,6 @@
-// Products with a 4-bit weight in blocks of 32 with power-of-two scales
+// Product with a 4-bit weight in blocks of 32 with power-of-two scales
 // (include/dbf.h, "Block formats") on the scaled matrix-core instructions:
 //   Y[b][o]  = Σ_l xq[b][l] wq[o][l]      x in e4m3 or e2m1 blocks
-//   dX[b][l] = Σ_o dy[b][o] wq[o][l]      dy in f16 or bf16
 //
 // The 32x32x64 instruction multiplies 64 columns of K per step and applies
 // both operands' block scales itself.  A lane (r = lane % 32, g = lane / 32)
@@ -9,19 +8,10 @@
 // operand bytes 16g..16g+15 of block 0 and of block 1; its scale byte is
 // always that of block g.
 
-#include "mx_device.h"
-
-#include <algorithm>
-#include <atomic>
+#include "mx_tile.h"
 
 namespace dbf {
 namespace {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ i32x8 operand(u32v4 a, u32v4 b) {
     return i32x8{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
@@ -44,37 +34,6 @@ __device__ __forceinline__ i32x8 operand(u32v4 a, u32v4 b) {
 // read from LDS and loads of a later stage are started, one or two between
 // each two products: bunched in front of them they leave the matrix cores
 // idle (2048 x 4096, K 14336, e4m3, 128 x 256 tiles: 104 instead of 95 us).
-
-typedef __attribute__((address_space(3))) void lds_void;
-
-__device__ __forceinline__ void dma16(const void *g, char *l) {
-    __builtin_amdgcn_global_load_lds(g, (lds_void *)(l), 16, 0, 0);
-}
-__device__ __forceinline__ void dma4(const void *g, char *l) {
-    __builtin_amdgcn_global_load_lds(g, (lds_void *)(l), 4, 0, 0);
-}
-
-// Wait until at most N of this wave's loads are outstanding.
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    // vmcnt bits [3:0] and [15:14]; expcnt [6:4] and lgkmcnt [11:8] left at "no wait"
-    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-// This wave's LDS reads have returned.
-__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14)); }
-
-// Nothing moves across in the compiler's schedule.
-__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
-
-__device__ __forceinline__ void block_barrier() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
-template <int V>
-using Const = std::integral_constant<int, V>;
 
 // A product tile: waves WM x WN, each MI x NI fragments of 32 x 32.
 template <int FMT_, int MI_, int NI_, int WM_, int WN_, int S_>
@@ -186,100 +145,30 @@ __global__ __launch_bounds__(256) void mx_tile_scales_kernel(const uint32_t *__r
     out[idx] = row < M ? xs[row * steps + k] : 0u;
 }
 
-// XCD-aware position of workgroup b among G: the workgroups of one XCD
-// (b mod 8) take consecutive indexes, so that they share operands in its L2.
-__device__ __forceinline__ int xcd_index(int b, int G) {
-    constexpr int kXcds = 8;
-    const int xcd = b % kXcds, slot = b / kXcds, q = G / kXcds, rem = G % kXcds;
-    return xcd * q + min(xcd, rem) + slot;
-}
-
 struct MxGemmArgs {
     const uint8_t *xc, *xs;  // codes in padded rows; scales in 32-row tiles
     int M;
     MxWeight w;
     void *y;
-    int nbm, nbn, nsplit;
+    TileGrid grid;
     float *part;             // null: whole sums to y
-    int group;               // tile rows that consecutive workgroups go through first
 };
-
-// Output tile of position `tile`: bands of `group` tile rows, column by
-// column within a band, so that the tiles which run on one XCD at a time
-// form a block that shares its rows of x and of the weight in that XCD's L2.
-__device__ __forceinline__ void tile_at(const MxGemmArgs &a, int tile, int &bm, int &bn) {
-    const int band = tile / (a.group * a.nbn);
-    const int rows = min(a.group, a.nbm - band * a.group);
-    const int at = tile - band * a.group * a.nbn;
-    bn = at / rows;
-    bm = band * a.group + at - bn * rows;
-}
-
-// A wave's results to y.  A 32 x 32 result has one row of y per lane, its
-// columns 8 (v / 4) + 4 g + v % 4 in register v; each wave takes them through
-// its own part of LDS into rows of 16-byte stores.  (Stored from the
-// registers, two bytes a lane: 106 instead of 101 us, 256 x 256 tiles of
-// 2048 x 14336, K 4096.)
-template <typename C, typename E>
-__device__ __forceinline__ void store_tile(char *lds, const f32x16 (&acc)[C::MI][C::NI], const MxGemmArgs &a, int m0,
-                                           int n0, int wave, int lane) {
-    const int wm = wave / C::WN, wn = wave % C::WN, l32 = lane & 31, g = lane >> 5;
-    constexpr int Cols = 32 * C::NI, Pitch = Cols * 2 + 16;  // 16-bit values of a wave's row, bytes
-    static_assert(static_cast<size_t>(C::Waves) * 32 * Pitch <= C::Lds, "a result fits the ring");
-    char *mine = lds + wave * (32 * Pitch);
-    uint16_t *y = static_cast<uint16_t *>(a.y);
-    const int c0 = n0 + wn * Cols;
-#pragma unroll
-    for (int i = 0; i < C::MI; ++i) {
-        const int r0 = m0 + (wm * C::MI + i) * 32;
-#pragma unroll
-        for (int f = 0; f < C::NI; ++f)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t p[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float lo = acc[i][f][4 * q + 2 * h], hi = acc[i][f][4 * q + 2 * h + 1];
-                    p[h] = static_cast<uint32_t>(E::put(lo)) | static_cast<uint32_t>(E::put(hi)) << 16;
-                }
-                *reinterpret_cast<u32v2 *>(mine + l32 * Pitch + (f * 32 + 8 * q + 4 * g) * 2) = u32v2{p[0], p[1]};
-            }
-        if (a.w.n % 8 == 0) {
-            constexpr int Per = Cols / 8, Rows = 64 / Per;  // lanes per row, rows per store
-            const int c = lane % Per * 8;
-#pragma unroll
-            for (int j = 0; j < 32; j += Rows) {
-                const int r = j + lane / Per;
-                const u32v4 v = *reinterpret_cast<const u32v4 *>(mine + r * Pitch + c * 2);
-                if (r0 + r < a.M && c0 + c < a.w.n)
-                    *reinterpret_cast<u32v4 *>(y + static_cast<size_t>(r0 + r) * a.w.n + c0 + c) = v;
-            }
-        } else {
-            for (int j = lane; j < 32 * Cols; j += 64) {
-                const int r = j / Cols, c = j % Cols;
-                if (r0 + r < a.M && c0 + c < a.w.n)
-                    y[static_cast<size_t>(r0 + r) * a.w.n + c0 + c] =
-                        *reinterpret_cast<const uint16_t *>(mine + r * Pitch + c * 2);
-            }
-        }
-    }
-}
 
 template <typename C, typename E>
 __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int T = a.nbm * a.nbn;
-    const int idx = xcd_index(blockIdx.x, T * a.nsplit);
+    const int T = a.grid.nbm * a.grid.nbn;
+    const int idx = xcd_index(blockIdx.x, T * a.grid.nsplit);
     const int split = idx / T, tile = idx - split * T;
     int bm, bn;
-    tile_at(a, tile, bm, bn);
+    tile_at(a.grid, tile, bm, bn);
     const int m0 = bm * C::BM, n0 = bn * C::BN;
     const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
     const int steps = a.w.blocks >> 2;  // of 128 columns
-    const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / a.nsplit);
-    const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * steps / a.nsplit) - k0;
+    const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / a.grid.nsplit);
+    const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * steps / a.grid.nsplit) - k0;
 
     // sources of this wave's loads; a stage moves them by inc bytes
     const uint8_t *src[C::D16 + C::D4];
@@ -409,102 +298,26 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a)
     for (; left > 0; --left) chunk(Const<0>{});
 
     if (a.part) {
-        // a K part of a tile: the sums as they are, for mx_finish_kernel
-        float *p = a.part + ((static_cast<size_t>(split) * T + tile) * C::Waves + wave) * (C::MI * C::NI * 1024) + lane * 4;
-#pragma unroll
-        for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-            for (int f = 0; f < C::NI; ++f)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<f32x4 *>(p + ((i * C::NI + f) * 4 + q) * 256) =
-                        f32x4{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
+        store_part<C>(part_at<C>(a.part, split, T, tile, wave, lane), acc);
         return;
     }
+    static_assert(static_cast<size_t>(C::Waves) * 32 * (64 * C::NI + 16) <= C::Lds, "a result fits the ring");
     __syncthreads();  // every wave's last operands have been read
-    store_tile<C, E>(lds, acc, a, m0, n0, wave, lane);
+    store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, m0, n0, wave, lane);
 }
 
 // The K parts of a tile, added in order and stored.
 template <typename C, typename E>
 __global__ __launch_bounds__(C::Threads) void mx_finish_kernel(const MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int T = a.nbm * a.nbn, tile = blockIdx.x;
+    const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x;
     int bm, bn;
-    tile_at(a, tile, bm, bn);
+    tile_at(a.grid, tile, bm, bn);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const float *p = a.part + (static_cast<size_t>(tile) * C::Waves + wave) * (C::MI * C::NI * 1024) + lane * 4;
-    const size_t plane = static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024);
     f32x16 acc[C::MI][C::NI];
-#pragma unroll
-    for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-        for (int f = 0; f < C::NI; ++f)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.0f;
-    for (int s = 0; s < a.nsplit; ++s, p += plane)
-#pragma unroll
-        for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-            for (int f = 0; f < C::NI; ++f)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4 v = *reinterpret_cast<const f32x4 *>(p + ((i * C::NI + f) * 4 + q) * 256);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][f][4 * q + e] += v[e];
-                }
-    store_tile<C, E>(lds, acc, a, bm * C::BM, bn * C::BN, wave, lane);
-}
-
-// One wave per 32 rows x 32 columns (one block) of dX.  The weight's values
-// enter as code * 2^(s - smax + 13) with smax the largest scale of the block
-// column, so that they are exact in f16 unless 2^-37 or less of the largest
-// one; the sum is multiplied by 2^(smax - 13) at the end.
-template <typename E>
-__global__ __launch_bounds__(256) void mx_backward_kernel(const typename E::T *__restrict__ dy, int M, MxWeight w,
-                                                          typename E::T *__restrict__ dx) {
-    const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
-    const int nb = (w.m + 31) / 32;
-    const int64_t tile = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    const int64_t mt64 = tile / nb;
-    if (mt64 * 32 >= M) return;
-    const int mt = static_cast<int>(mt64), kb = static_cast<int>(tile - mt64 * nb);
-    const int row = mt * 32 + r < M ? mt * 32 + r : M - 1;
-    const typename E::T *dyr = dy + static_cast<size_t>(row) * w.n;
-    const int smax = w.colmax[kb];
-    f32x16 acc = {};
-    for (int o0 = 0; o0 < w.n; o0 += 16) {
-        uint16_t a[8], b[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int o = o0 + 8 * g + i, t = o >> 5;
-            const bool in = o < w.n;  // (n_pad is a multiple of 32: the weight's rows exist)
-            a[i] = in ? dyr[o] : 0;
-            const size_t at = (static_cast<size_t>(t) * w.blocks + kb) * 32 + (o & 31);
-            const uint32_t byte = w.codes[at * 16 + r / 2];
-            const int s = w.scales[((static_cast<size_t>(t) * (w.blocks >> 2) + (kb >> 2)) * 32 + (o & 31)) * 4 + (kb & 3)];
-            const int e = s - smax + 13 + 127;
-            const float sc = s == 255 ? __builtin_bit_cast(float, 0x7fc00000u)
-                                      : __builtin_bit_cast(float, static_cast<uint32_t>(e < 1 ? 1 : e) << 23);
-            uint32_t p;
-            if constexpr (E::code == DBF_TYPE_BF16)
-                p = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(byte, sc, 0));
-            else
-                p = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(byte, sc, 0));
-            b[i] = static_cast<uint16_t>(r & 1 ? p >> 16 : p & 0xffffu);
-        }
-        if constexpr (E::code == DBF_TYPE_BF16)
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<bf16x8 *>(a), *reinterpret_cast<bf16x8 *>(b), acc, 0, 0, 0);
-        else
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<f16x8 *>(a), *reinterpret_cast<f16x8 *>(b), acc, 0, 0, 0);
-    }
-    const int col = kb * 32 + r;
-    if (col >= w.m) return;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int o = mt * 32 + 8 * (v >> 2) + 4 * g + (v & 3);
-        if (o < M) dx[static_cast<size_t>(o) * w.m + col] = E::put(ldexpf(acc[v], smax - 127 - 13));
-    }
+    add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
+                 a.grid.nsplit, acc);
+    store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, bm * C::BM, bn * C::BN, wave, lane);
 }
 
 }  // namespace
@@ -578,32 +391,21 @@ struct TileOf<FMT, 3> { using C = MxTile<FMT, 2, 1, 1, 4, FMT == DBF_TYPE_E4M3 ?
 template <int FMT>
 struct TileOf<FMT, 4> { using C = MxTile<FMT, 1, 1, 2, 2, FMT == DBF_TYPE_E4M3 ? 8 : 6>; };
 
-// More than 64 KiB of LDS has to be asked for, once per kernel and device.
-template <typename K>
-void allow_lds(K kernel, size_t bytes) {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    (void)hipGetDevice(&dev);
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (done.load(std::memory_order_relaxed) & bit) return;
-    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes));
-    done.fetch_or(bit, std::memory_order_relaxed);
-}
-
 template <typename C, typename E>
 void launch_gemm(MxGemmArgs &a, hipStream_t s) {
     constexpr size_t kFinishLds = static_cast<size_t>(C::Waves) * 32 * (64 * C::NI + 16);
     auto product = mx_gemm_kernel<C, E>;
     auto finish = mx_finish_kernel<C, E>;
-    a.nbm = (a.M + C::BM - 1) / C::BM;
-    a.nbn = (a.w.n + C::BN - 1) / C::BN;
-    a.group = a.nbm < 4 ? a.nbm : 4;
-    if constexpr (C::Lds > 65536) allow_lds(product, C::Lds);
-    launch_kernel(product, dim3(a.nbm * a.nbn * a.nsplit), dim3(C::Threads), C::Lds, s, a);
+    static std::atomic<uint64_t> lds_product{0}, lds_finish{0};
+    TileGrid &t = a.grid;
+    t.nbm = (a.M + C::BM - 1) / C::BM;
+    t.nbn = (a.w.n + C::BN - 1) / C::BN;
+    t.group = t.nbm < 4 ? t.nbm : 4;
+    if constexpr (C::Lds > 65536) allow_lds(product, C::Lds, lds_product);
+    launch_kernel(product, dim3(t.nbm * t.nbn * t.nsplit), dim3(C::Threads), C::Lds, s, a);
     if (a.part) {
-        if constexpr (kFinishLds > 65536) allow_lds(finish, kFinishLds);
-        launch_kernel(finish, dim3(a.nbm * a.nbn), dim3(C::Threads), kFinishLds, s, a);
+        if constexpr (kFinishLds > 65536) allow_lds(finish, kFinishLds, lds_finish);
+        launch_kernel(finish, dim3(t.nbm * t.nbn), dim3(C::Threads), kFinishLds, s, a);
     }
 }
 
@@ -644,7 +446,7 @@ int launch_mx_product(const MxProduct &p, void *stream) {
     a.w = p.w;
     a.y = p.y;
     const MxPlan plan = mx_plan(p.M, p.w.n, p.w.blocks / 4, p.x_type == DBF_TYPE_E4M3);
-    a.nsplit = plan.nsplit;
+    a.grid.nsplit = plan.nsplit;
     a.part = plan.nsplit > 1 ? p.part : nullptr;
     if (plan.nsplit > 1 && (!p.part || p.part_cap < mx_product_parts(p.M, p.w.n, p.w.blocks, p.x_type)))
         return static_cast<int>(hipErrorInvalidValue);
@@ -655,17 +457,6 @@ int launch_mx_product(const MxProduct &p, void *stream) {
     };
     if (p.x_type == DBF_TYPE_E4M3) pick(Const<DBF_TYPE_E4M3>{});
     else pick(Const<DBF_TYPE_E2M1>{});
-    return static_cast<int>(hipGetLastError());
-}
-
-int launch_mx_backward(const void *dy, int type, int M, const MxWeight &w, void *dx, void *stream) {
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t tiles = static_cast<int64_t>((M + 31) / 32) * ((w.m + 31) / 32);
-    const dim3 grid(static_cast<uint32_t>((tiles + 3) / 4));
-    if (type == DBF_TYPE_BF16)
-        launch_kernel(mx_backward_kernel<BF16>, grid, dim3(256), 0, s, static_cast<const uint16_t *>(dy), M, w, static_cast<uint16_t *>(dx));
-    else
-        launch_kernel(mx_backward_kernel<F16>, grid, dim3(256), 0, s, static_cast<const uint16_t *>(dy), M, w, static_cast<uint16_t *>(dx));
     return static_cast<int>(hipGetLastError());
 }
 

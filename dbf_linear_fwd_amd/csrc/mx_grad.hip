@@ -1,0 +1,388 @@
+// Gradient of the input through a 4-bit block weight:
+//   dX[b][l] = Σ_o dy[b][o] w[o][l],   dy and dX in f16 or bf16.
+//
+// The sum runs over the weight's rows, across its blocks, so every term of a
+// sum has another scale and the scaled matrix-core instructions do not apply:
+// the weight becomes 16-bit values on the way, on the 32x32x16 instructions
+// (2.5 PFLOP/s).  Per 64 rows of the weight a thread takes one block (one row,
+// 32 columns): its codes become e5m2 values relative to the largest scale of
+// their block column, code * 2^(s - smax + 13), one byte each in LDS; the
+// transposing LDS read hands a lane the eight rows of its column, which four
+// conversions turn into the 16-bit operand.  (As 16-bit values in LDS the
+// weight's share of the LDS traffic doubles, and the LDS is then what bounds
+// a 256 x 256 tile: 2300 of its cycles for 2048 of the matrix cores.)  e5m2
+// holds the codes exactly down to scales of 2^-28 of the largest; the sums
+// are multiplied by 2^(smax - 13) at the end.
+
+#include "mx_tile.h"
+
+namespace dbf {
+namespace {
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kShift = 13;  // 6 * 2^13 is e5m2's top binade
+
+// Waves WM x WN, each MI x NI fragments of 32 x 32; one weight block per
+// thread and step.
+template <int MI_, int NI_, int WM_, int WN_>
+struct GradTile {
+    static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_;
+    static constexpr int Waves = WM * WN, Threads = 64 * Waves;
+    static constexpr int BM = 32 * MI * WM, BN = 32 * NI * WN, BK = 64;
+    static constexpr int ABytes = BM * BK * 2;
+    static constexpr int BPitch = BN + 32;            // bytes of a weight row: eight rows on different banks
+    static constexpr int BBytes = BK * BPitch;
+    static constexpr int AStages = 3, BStages = 2;
+    static constexpr size_t Lds = static_cast<size_t>(AStages) * ABytes + static_cast<size_t>(BStages) * BBytes;
+    static constexpr int DA = ABytes / 1024 / Waves;  // 1 KiB loads per wave and step
+    static_assert(BN / 32 * BK == Threads, "one block per thread");
+    static_assert(DA * Waves * 1024 == ABytes, "whole loads");
+    static_assert(Lds <= 160 * 1024, "LDS of a CU");
+    static_assert(static_cast<size_t>(Waves) * 32 * (64 * NI + 16) <= Lds, "a result fits");
+};
+
+struct MxGradArgs {
+    const void *dy;
+    const void *zeros;  // 16 zero bytes
+    int M;
+    MxWeight w;
+    void *dx;
+    TileGrid grid;
+    float *part;
+};
+
+// The e5m2 bytes of a block's 32 columns.
+__device__ __forceinline__ void block_values(u32v4 codes, int s, int smax, u32v4 &lo, u32v4 &hi) {
+    // the conversion divides by its scale: 2^-(s - smax + 13)
+    const int e = 127 - kShift + smax - s;
+    const uint32_t bits = s == 255 ? 0x7fc00000u : static_cast<uint32_t>(e < 254 ? e : 254) << 23;
+    const float sc = __builtin_bit_cast(float, bits);
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = codes[i >> 1];
+        s16x2 o = {0, 0};
+        if (i & 1) {
+            o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2), sc, false);
+            o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3), sc, true);
+        } else {
+            o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0), sc, false);
+            o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1), sc, true);
+        }
+        out[i] = __builtin_bit_cast(uint32_t, o);
+    }
+    lo = u32v4{out[0], out[1], out[2], out[3]};
+    hi = u32v4{out[4], out[5], out[6], out[7]};
+}
+
+// Eight e5m2 bytes as 16-bit values.
+template <typename E>
+__device__ __forceinline__ u32v4 widen(i32x2 b) {
+    u32v4 r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t w = static_cast<uint32_t>(b[i]);
+        if constexpr (E::code == DBF_TYPE_BF16) {
+            r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, false));
+            r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, true));
+        } else {
+            r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(w, 1.0f, false));
+            r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(w, 1.0f, true));
+        }
+    }
+    return r;
+}
+
+template <typename E>
+__device__ __forceinline__ f32x16 product(u32v4 w, u32v4 d, f32x16 acc) {
+    if constexpr (E::code == DBF_TYPE_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, d), acc, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, d), acc, 0, 0, 0);
+}
+
+// The sums times 2^(smax - 13) of their block column.
+template <typename C>
+__device__ __forceinline__ void scale_columns(f32x16 (&acc)[C::MI][C::NI], const MxWeight &w, int n0, int wn) {
+#pragma unroll
+    for (int f = 0; f < C::NI; ++f) {
+        const int kb = min(n0 / 32 + wn * C::NI + f, w.blocks - 1);
+        const int e = static_cast<int>(w.colmax[kb]) - 127 - kShift;
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][f][v] = ldexpf(acc[i][f][v], e);
+    }
+}
+
+// ROWS16: dy's rows are 16-byte aligned (n a multiple of 8) and go straight
+// into LDS; otherwise by elements through registers.
+template <typename C, typename E, bool ROWS16>
+__global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int T = a.grid.nbm * a.grid.nbn;
+    const int idx = xcd_index(blockIdx.x, T * a.grid.nsplit);
+    const int split = idx / T, tile = idx - split * T;
+    int bm, bn;
+    tile_at(a.grid, tile, bm, bn);
+    const int m0 = bm * C::BM, n0 = bn * C::BN;
+    const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const int steps = (a.w.n + C::BK - 1) / C::BK;
+    const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / a.grid.nsplit);
+    const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * steps / a.grid.nsplit) - k0;
+    const uint16_t *dy = static_cast<const uint16_t *>(a.dy);
+
+    // dy: chunk c of eight columns of row r sits at position c ^ (r & 7)
+    const uint16_t *src[C::DA];
+    int col[C::DA];
+#pragma unroll
+    for (int q = 0; q < C::DA; ++q) {
+        const int c = (wave * C::DA + q) * 64 + lane, r = c >> 3;
+        col[q] = k0 * C::BK + ((c & 7) ^ (r & 7)) * 8;
+        src[q] = dy + static_cast<size_t>(min(m0 + r, a.M - 1)) * a.w.n + col[q];  // rows past M: not written
+    }
+    auto load_dy = [&](int slot) {  // the next step's, each call
+        char *st = lds + slot * C::ABytes;
+#pragma unroll
+        for (int q = 0; q < C::DA; ++q) {
+            if constexpr (ROWS16) {
+                // columns past n: zeros, whatever stands in the next row
+                dma16(col[q] < a.w.n ? static_cast<const void *>(src[q]) : a.zeros, st + (wave * C::DA + q) * 1024);
+            } else {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x = col[q] + 2 * i < a.w.n ? src[q][2 * i] : 0;
+                    const uint32_t y = col[q] + 2 * i + 1 < a.w.n ? src[q][2 * i + 1] : 0;
+                    v[i] = x | y << 16;
+                }
+                *reinterpret_cast<u32v4 *>(st + (wave * C::DA + q) * 1024 + lane * 16) = u32v4{v[0], v[1], v[2], v[3]};
+            }
+            src[q] += C::BK;
+            col[q] += C::BK;
+        }
+    };
+    // weight: this thread's block is row `lane` of the step, block column n0 / 32 + wave
+    const int kb = min(n0 / 32 + wave, a.w.blocks - 1);  // block columns past the end: not written
+    const int smax = a.w.colmax[kb];
+    int wrow = k0 * C::BK + lane;
+    u32v4 raw;
+    int rs;
+    bool past = false;  // raw is a row past n
+    auto load_w = [&]() {  // the next step's, each call
+        const int row = min(wrow, a.w.n_pad - 1);
+        const size_t t = static_cast<size_t>(row >> 5);
+        raw = *reinterpret_cast<const u32v4 *>(a.w.codes + ((t * a.w.blocks + kb) * 32 + (row & 31)) * 16);
+        rs = a.w.scales[((t * (a.w.blocks >> 2) + (kb >> 2)) * 32 + (row & 31)) * 4 + (kb & 3)];
+        past = wrow >= a.w.n;
+        wrow += C::BK;
+    };
+    constexpr int BAt = C::AStages * C::ABytes;
+    auto store_w = [&](int slot) {
+        u32v4 lo, hi;
+        // rows past n are zeros (here, where the loads are awaited anyway)
+        block_values(past ? u32v4{0u, 0u, 0u, 0u} : raw, past ? 0 : rs, smax, lo, hi);
+        char *p = lds + BAt + slot * C::BBytes + lane * C::BPitch + wave * 32;
+        *reinterpret_cast<u32v4 *>(p) = lo;
+        *reinterpret_cast<u32v4 *>(p + 16) = hi;
+    };
+
+    f32x16 acc[C::MI][C::NI];
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+        for (int f = 0; f < C::NI; ++f)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.0f;
+
+    // operands of 16 rows of the weight
+    struct Frags {
+        u32v4 d[C::MI];
+        i32x2 w[C::NI];
+    };
+    const int arow = (wm * C::MI * 32 + l32) * 128;
+    // transposing read: lane i of 16 gives row i / 2, eight columns; gets column i % 16
+    const int brow = BAt + (8 * g + (lane & 15) / 2) * C::BPitch + wn * C::NI * 32 + ((lane >> 4) & 1) * 16 + (lane & 1) * 8;
+    auto load_frags = [&](int ks, int aslot, int bslot, Frags &f) {
+        typedef __attribute__((address_space(3))) i32x2 lds_i2;
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i)
+            f.d[i] = *reinterpret_cast<const u32v4 *>(lds + aslot * C::ABytes + arow + i * 4096 + (((2 * ks + g) ^ (l32 & 7)) << 4));
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j)
+            f.w[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (lds_i2 *)(lds + brow + bslot * C::BBytes + ks * 16 * C::BPitch + j * 32));
+    };
+
+    // step kt: dy in slot kt % 3, weight in slot kt % 2; dy of the next two
+    // steps and the next step's weight (in registers) are under way.  The
+    // loads run on past the last step (zeros, or rows of the next part, to no
+    // use): a branch here would have the compiler move the products behind it.
+    load_dy(0);
+    load_dy(1);
+    load_w();
+    store_w(0);
+    load_w();
+    if constexpr (ROWS16) wait_vm<C::DA + 2>();
+    wait_lds();
+    block_barrier();
+    int as = 0, bs = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+        const int a2 = as == 0 ? 2 : as - 1;  // slot of step kt + 2: the barrier has freed it
+        store_w(bs ^ 1);                      // the next step's weight
+        load_dy(a2);
+        load_w();
+        Frags f[2];
+        load_frags(0, as, bs, f[0]);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            if (ks < 3) load_frags(ks + 1, as, bs, f[(ks + 1) & 1]);
+            keep_order();
+            u32v4 wv[C::NI];
+#pragma unroll
+            for (int j = 0; j < C::NI; ++j) wv[j] = widen<E>(f[ks & 1].w[j]);
+#pragma unroll
+            for (int j = 0; j < C::NI; ++j)
+#pragma unroll
+                for (int i = 0; i < C::MI; ++i) acc[i][j] = product<E>(wv[j], f[ks & 1].d[i], acc[i][j]);
+            keep_order();
+        }
+        // the next step's dy has landed; that of the one after it, and the
+        // weight's two loads, may be in flight
+        if constexpr (ROWS16) wait_vm<C::DA + 2>();
+        wait_lds();
+        block_barrier();
+        as = as == 2 ? 0 : as + 1;
+        bs ^= 1;
+    }
+    wait_vm<0>();  // nothing more lands in the LDS that the result goes through
+    block_barrier();
+
+    if (a.part) {
+        store_part<C>(part_at<C>(a.part, split, T, tile, wave, lane), acc);
+        return;
+    }
+    scale_columns<C>(acc, a.w, n0, wn);
+    store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, m0, n0, wave, lane);
+}
+
+template <typename C, typename E>
+__global__ __launch_bounds__(C::Threads) void mx_grad_finish_kernel(const MxGradArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x;
+    int bm, bn;
+    tile_at(a.grid, tile, bm, bn);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    f32x16 acc[C::MI][C::NI];
+    add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
+                 a.grid.nsplit, acc);
+    scale_columns<C>(acc, a.w, bn * C::BN, wave % C::WN);
+    store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, bm * C::BM, bn * C::BN, wave, lane);
+}
+
+// ---- choice of the tile and of the K parts (as the product's, mx_gemm.hip)
+
+struct GradCost {
+    int bm, bn;
+    float light, full;  // us per 64 rows of the weight
+};
+constexpr GradCost kGrad[] = {
+    {256, 256, 1.0f, 1.4f},
+    {128, 128, 0.45f, 0.6f},
+    {32, 128, 0.25f, 0.35f},
+};
+constexpr int kGradCount = sizeof(kGrad) / sizeof(kGrad[0]);
+constexpr int kCus = 256;
+
+struct GradPlan {
+    int tile = 0, nsplit = 1;
+};
+
+GradPlan grad_plan(int M, int n, int m) {
+    GradPlan best;
+    float least = 0.0f;
+    const int steps = (n + 63) / 64;
+    for (int t = 0; t < kGradCount; ++t) {
+        const GradCost &c = kGrad[t];
+        const int64_t tiles = static_cast<int64_t>((M + c.bm - 1) / c.bm) * ((m + c.bn - 1) / c.bn);
+        for (int sp : {1, 2, 3, 4, 6, 8, 12}) {
+            if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
+            const float wgs = static_cast<float>(tiles) * sp;
+            const float load = wgs < kCus ? wgs / kCus : 1.0f;
+            const float rounds = wgs <= kCus ? 1.0f : t < 1 ? static_cast<float>((tiles * sp + kCus - 1) / kCus) : wgs / kCus;
+            float us = rounds * (3.0f + static_cast<float>((steps + sp - 1) / sp) * (c.light + (c.full - c.light) * load));
+            if (sp > 1) us += 3.5f + wgs * c.bm * c.bn * 8.0f * 3e-7f;
+            if (least == 0.0f || us < least) {
+                least = us;
+                best.tile = t;
+                best.nsplit = sp;
+            }
+        }
+    }
+    return best;
+}
+
+template <typename C, typename E>
+void launch_grad(MxGradArgs &a, hipStream_t s) {
+    static std::atomic<uint64_t> lds0{0}, lds1{0}, lds2{0};
+    constexpr size_t kFinishLds = static_cast<size_t>(C::Waves) * 32 * (64 * C::NI + 16);
+    TileGrid &t = a.grid;
+    t.nbm = (a.M + C::BM - 1) / C::BM;
+    t.nbn = (a.w.m + C::BN - 1) / C::BN;
+    t.group = t.nbm < 4 ? t.nbm : 4;
+    const dim3 grid(t.nbm * t.nbn * t.nsplit);
+    if (a.w.n % 8 == 0) {
+        auto k = mx_grad_kernel<C, E, true>;
+        if constexpr (C::Lds > 65536) allow_lds(k, C::Lds, lds0);
+        launch_kernel(k, grid, dim3(C::Threads), C::Lds, s, a);
+    } else {
+        auto k = mx_grad_kernel<C, E, false>;
+        if constexpr (C::Lds > 65536) allow_lds(k, C::Lds, lds1);
+        launch_kernel(k, grid, dim3(C::Threads), C::Lds, s, a);
+    }
+    if (a.part) {
+        auto k = mx_grad_finish_kernel<C, E>;
+        if constexpr (kFinishLds > 65536) allow_lds(k, kFinishLds, lds2);
+        launch_kernel(k, dim3(t.nbm * t.nbn), dim3(C::Threads), kFinishLds, s, a);
+    }
+}
+
+}  // namespace
+
+size_t mx_backward_parts(int M, int n, int m) {
+    const GradPlan p = grad_plan(M, n, m);
+    if (p.nsplit == 1) return 0;
+    const GradCost &c = kGrad[p.tile];
+    return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((m + c.bn - 1) / c.bn * c.bn);
+}
+
+int launch_mx_backward(const MxBackward &b, void *stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const GradPlan plan = grad_plan(b.M, b.w.n, b.w.m);
+    MxGradArgs a{};
+    a.dy = b.dy;
+    a.zeros = b.zeros;
+    a.M = b.M;
+    a.w = b.w;
+    a.dx = b.dx;
+    a.grid.nsplit = plan.nsplit;
+    a.part = plan.nsplit > 1 ? b.part : nullptr;
+    if (plan.nsplit > 1 && (!b.part || b.part_cap < mx_backward_parts(b.M, b.w.n, b.w.m)))
+        return static_cast<int>(hipErrorInvalidValue);
+    auto go = [&](auto e) {
+        using E = decltype(e);
+        if (plan.tile == 0) launch_grad<GradTile<2, 4, 4, 2>, E>(a, s);
+        else if (plan.tile == 1) launch_grad<GradTile<2, 2, 2, 2>, E>(a, s);
+        else launch_grad<GradTile<1, 1, 1, 4>, E>(a, s);
+    };
+    if (b.type == DBF_TYPE_BF16) go(BF16{});
+    else go(F16{});
+    return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace dbf

@@ -128,7 +128,8 @@ __global__ __launch_bounds__(256) void mx_layout_kernel(const uint8_t *__restric
     out_scales[((static_cast<int64_t>(tile) * (blocks >> 2) + (kb >> 2)) * 32 + r) * 4 + (kb & 3)] = s;
 }
 
-// Largest scale byte (NaN bytes aside) of each block of columns over all rows.
+// Largest scale byte (NaN bytes aside) of each block of columns over all rows,
+// and 16 zero bytes after the last (what the gradient reads past a row's end).
 __global__ __launch_bounds__(256) void mx_colmax_kernel(const uint8_t *__restrict__ scales, int n, int blocks,
                                                         uint8_t *__restrict__ out) {
     const int kb = blockIdx.x;
@@ -145,6 +146,7 @@ __global__ __launch_bounds__(256) void mx_colmax_kernel(const uint8_t *__restric
         __syncthreads();
     }
     if (threadIdx.x == 0) out[kb] = static_cast<uint8_t>(red[0]);
+    if (kb == 0 && threadIdx.x < 16) out[blocks + threadIdx.x] = 0;
 }
 
 uint32_t grid_for(uint64_t threads) { return static_cast<uint32_t>((threads + 255) / 256); }

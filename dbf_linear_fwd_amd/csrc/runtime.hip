@@ -60,7 +60,8 @@ struct dbf_layer {
     int32_t bqq_groups = 0, bqq_p = 0, bqq_d = 0, bqq_Q = 2;
     uint16_t *bqq_b = nullptr;
     // layer with a 4-bit block weight (dbf_mx_pack): the weight's device
-    // layout, and the quantised input [max_batch] of the forwards
+    // layout (colmax: with 16 zero bytes behind it), and the quantised input
+    // [max_batch] of the forwards
     bool mx = false;
     int32_t mx_act = DBF_TYPE_E4M3;
     uint8_t *mx_codes = nullptr, *mx_scales = nullptr, *mx_colmax = nullptr;
@@ -965,15 +966,17 @@ static dbf_status_t forward_mx_group(const dbf_handle_t *hs, int32_t count, cons
     return DBF_OK;
 }
 
-// Floats of K-part sums of any forward up to max_batch (the tile grid changes
-// every 64 rows; either activation format may come in ready blocks).
-static size_t mx_part_floats(int32_t n, int32_t blocks, int32_t max_batch) {
+// Floats of K-part sums of any call up to max_batch: the tile grids change
+// every 32 rows; either activation format may come in ready blocks.
+static size_t mx_part_floats(int32_t n, int32_t m, int32_t max_batch) {
+    const int32_t blocks = round_up(m, 128) / 32;
     size_t most = 0;
-    for (int64_t top = dbf::kMxDecodeBatch + 1;; top += 64) {
+    for (int64_t top = 32; top < 65536 + 32; top += 32) {  // (no K parts beyond: the grids are full)
         const int32_t M = static_cast<int32_t>(std::min<int64_t>(top, max_batch));
-        if (M <= dbf::kMxDecodeBatch) break;
-        for (int32_t t : {DBF_TYPE_E4M3, DBF_TYPE_E2M1}) most = std::max(most, dbf::mx_product_parts(M, n, blocks, t));
-        if (M == max_batch || top > 65536) break;
+        most = std::max(most, dbf::mx_backward_parts(M, n, m));
+        if (M > dbf::kMxDecodeBatch)
+            for (int32_t t : {DBF_TYPE_E4M3, DBF_TYPE_E2M1}) most = std::max(most, dbf::mx_product_parts(M, n, blocks, t));
+        if (M == max_batch) break;
     }
     return most;
 }
@@ -1004,11 +1007,11 @@ extern "C" dbf_status_t dbf_mx_pack(int32_t n, int32_t m, const void *codes, con
     const size_t code_bytes = static_cast<size_t>(n_pad) * blocks * 16, scale_bytes = static_cast<size_t>(n_pad) * blocks;
     const size_t xc_bytes = static_cast<size_t>(max_batch) * dbf_mx_code_bytes(m, act_type);
     const size_t xs_bytes = static_cast<size_t>(round_up(max_batch, 32)) * blocks;
-    const size_t parts = mx_part_floats(n, static_cast<int32_t>(blocks), max_batch);
+    const size_t parts = mx_part_floats(n, m, max_batch);
     dbf_status_t st = hipGetDevice(&h->device) == hipSuccess ? DBF_OK : DBF_ERR_HIP;
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_codes), code_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_scales), scale_bytes);
-    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_colmax), blocks);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_colmax), blocks + 16);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xcodes), xc_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xscales), xs_bytes);
     if (st == DBF_OK && parts > 0) st = dev_alloc(reinterpret_cast<void **>(&h->split), sizeof(float) * parts);
@@ -1022,7 +1025,7 @@ extern "C" dbf_status_t dbf_mx_pack(int32_t n, int32_t m, const void *codes, con
         return st;
     }
     h->packed_bytes = code_bytes;
-    h->scale_bytes = scale_bytes + blocks;
+    h->scale_bytes = scale_bytes + blocks + 16;
     h->workspace_bytes = xc_bytes + xs_bytes + sizeof(float) * parts;
     *out = h;
     return DBF_OK;
@@ -1057,8 +1060,16 @@ extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, voi
     int cur = -1;
     if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
     if (cur != h->device) return DBF_ERR_INVALID_ARG;
-    return timed_launch(h, "mx_backward", stream,
-                        [&] { return dbf::launch_mx_backward(dy, type, batch, mx_weight(h), dx, stream); });
+    dbf::MxBackward b;
+    b.dy = dy;
+    b.zeros = h->mx_colmax + h->m_pad / 32;
+    b.type = type;
+    b.M = batch;
+    b.w = mx_weight(h);
+    b.dx = dx;
+    b.part = h->split;
+    b.part_cap = h->split_cap;
+    return timed_launch(h, "mx_backward", stream, [&] { return dbf::launch_mx_backward(b, stream); });
 }
 
 extern "C" dbf_status_t dbf_linear_forward_ex(dbf_handle_t h, const void *x, void *y, int32_t batch, int32_t path,

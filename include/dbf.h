@@ -446,8 +446,8 @@ dbf_status_t dbf_mx_forward(dbf_handle_t h, const void *x, int32_t x_type, const
  * of the input through a frozen weight (and straight through the input's
  * quantisation).  dy batch x n and dx batch x m, both of `type` (f16 or
  * bf16).  The weight's values enter the 16-bit matrix cores relative to the
- * largest scale of their block of columns: exact in f16 down to 2^-37 of
- * it (smaller ones lose bits or vanish) and in bf16 wherever they count.
+ * largest scale of their block of 32 columns (over all rows): exact where
+ * their scale is at least 2^-28 of it; smaller ones lose bits or vanish.
  * Products accumulate in fp32.  Pointer, batch and ordering rules as
  * dbf_linear_forward.
  */
