@@ -9,10 +9,17 @@
 // their block column, code * 2^(s - smax + 13), one byte each in LDS; the
 // transposing LDS read hands a lane the eight rows of its column, which four
 // conversions turn into the 16-bit operand.  (As 16-bit values in LDS the
-// weight's share of the LDS traffic doubles, and the LDS is then what bounds
+// weight's share of the LDS traffic would double, and the LDS be what bounds
 // a 256 x 256 tile: 2300 of its cycles for 2048 of the matrix cores.)  e5m2
 // holds the codes exactly down to scales of 2^-28 of the largest; the sums
 // are multiplied by 2^(smax - 13) at the end.
+//
+// 2048 rows, n 14336, m 4096, bf16: 247 us, 0.98 PFLOP/s.  A step of 64 rows
+// of a 256 x 256 tile takes 1.33 us alone and 1.9 with all CUs at work, where
+// its products take 0.91: reading the operands and converting the weight
+// (190 vector instructions a wave and step beside 32 products) fill the rest
+// as far as they do not overlap.  Placed one by one between the products
+// instead of in front of them: 247 instead of 272 us.
 
 #include "mx_tile.h"
 
@@ -25,8 +32,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kShift = 13;  // 6 * 2^13 is e5m2's top binade
 
-// Waves WM x WN, each MI x NI fragments of 32 x 32; one weight block per
-// thread and step.
+// Waves WM x WN, each MI x NI fragments of 32 x 32.
 template <int MI_, int NI_, int WM_, int WN_>
 struct GradTile {
     static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_;
@@ -35,10 +41,13 @@ struct GradTile {
     static constexpr int ABytes = BM * BK * 2;
     static constexpr int BPitch = BN + 32;            // bytes of a weight row: eight rows on different banks
     static constexpr int BBytes = BK * BPitch;
-    static constexpr int AStages = 3, BStages = 2;
-    static constexpr size_t Lds = static_cast<size_t>(AStages) * ABytes + static_cast<size_t>(BStages) * BBytes;
+    static constexpr int AStages = 3, BStages = 2, RStages = 2;
+    static constexpr int NB = BN / 32 * BK / Threads;  // weight blocks per thread and step
+    static constexpr int RBytes = NB * 1280;           // a wave's codes and scale words of a step
+    static constexpr int BAt = AStages * ABytes, RAt = BAt + BStages * BBytes;
+    static constexpr size_t Lds = static_cast<size_t>(RAt) + static_cast<size_t>(RStages) * Waves * RBytes;
     static constexpr int DA = ABytes / 1024 / Waves;  // 1 KiB loads per wave and step
-    static_assert(BN / 32 * BK == Threads, "one block per thread");
+    static_assert(NB * Threads == BN / 32 * BK, "whole blocks per thread");
     static_assert(DA * Waves * 1024 == ABytes, "whole loads");
     static_assert(Lds <= 160 * 1024, "LDS of a CU");
     static_assert(static_cast<size_t>(Waves) * 32 * (64 * NI + 16) <= Lds, "a result fits");
@@ -76,6 +85,19 @@ __device__ __forceinline__ void block_values(u32v4 codes, int s, int smax, u32v4
     }
     lo = u32v4{out[0], out[1], out[2], out[3]};
     hi = u32v4{out[4], out[5], out[6], out[7]};
+}
+
+// Transposing read of 8 x 16 bytes by 16 lanes.  (The restrict-qualified
+// argument keeps the compiler from waiting for every load into LDS first.)
+__device__ __forceinline__ i32x2 read_columns(const char *__restrict__ p) {
+    typedef __attribute__((address_space(3))) i32x2 lds_i2;
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i2 *)p);
+}
+
+// A lane's codes and scale word of a block.
+__device__ __forceinline__ void read_raw(const char *__restrict__ p, int lane, u32v4 &codes, uint32_t &scales) {
+    codes = *reinterpret_cast<const u32v4 *>(p + lane * 16);
+    scales = *reinterpret_cast<const uint32_t *>(p + 1024 + lane * 4);
 }
 
 // Eight e5m2 bytes as 16-bit values.
@@ -167,29 +189,45 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
             col[q] += C::BK;
         }
     };
-    // weight: this thread's block is row `lane` of the step, block column n0 / 32 + wave
-    const int kb = min(n0 / 32 + wave, a.w.blocks - 1);  // block columns past the end: not written
-    const int smax = a.w.colmax[kb];
-    int wrow = k0 * C::BK + lane;
-    u32v4 raw;
-    int rs;
-    bool past = false;  // raw is a row past n
-    auto load_w = [&]() {  // the next step's, each call
-        const int row = min(wrow, a.w.n_pad - 1);
+    // weight: this thread's blocks are row `lane` of the step, block columns
+    // n0 / 32 + NB wave + i
+    int kb[C::NB], smax[C::NB];
+#pragma unroll
+    for (int i = 0; i < C::NB; ++i) {
+        kb[i] = min(n0 / 32 + wave * C::NB + i, a.w.blocks - 1);  // block columns past the end: not written
+        smax[i] = a.w.colmax[kb[i]];
+    }
+    int wrow = k0 * C::BK + lane;  // of the step that store_w takes next
+    int lrow = wrow;               // of the step that load_w takes next
+    // Through LDS too, each wave its own (loaded into registers, they would
+    // have the compiler wait for every load that is under way).
+    auto load_w = [&](int slot) {
+        const int row = min(lrow, a.w.n_pad - 1);
         const size_t t = static_cast<size_t>(row >> 5);
-        raw = *reinterpret_cast<const u32v4 *>(a.w.codes + ((t * a.w.blocks + kb) * 32 + (row & 31)) * 16);
-        rs = a.w.scales[((t * (a.w.blocks >> 2) + (kb >> 2)) * 32 + (row & 31)) * 4 + (kb & 3)];
-        past = wrow >= a.w.n;
-        wrow += C::BK;
+        char *p = lds + C::RAt + (slot * C::Waves + wave) * C::RBytes;
+#pragma unroll
+        for (int i = 0; i < C::NB; ++i) {
+            dma16(a.w.codes + ((t * a.w.blocks + kb[i]) * 32 + (row & 31)) * 16, p + i * 1280);
+            dma4(a.w.scales + ((t * (a.w.blocks >> 2) + (kb[i] >> 2)) * 32 + (row & 31)) * 4, p + i * 1280 + 1024);
+        }
+        lrow += C::BK;
     };
-    constexpr int BAt = C::AStages * C::ABytes;
-    auto store_w = [&](int slot) {
-        u32v4 lo, hi;
-        // rows past n are zeros (here, where the loads are awaited anyway)
-        block_values(past ? u32v4{0u, 0u, 0u, 0u} : raw, past ? 0 : rs, smax, lo, hi);
-        char *p = lds + BAt + slot * C::BBytes + lane * C::BPitch + wave * 32;
-        *reinterpret_cast<u32v4 *>(p) = lo;
-        *reinterpret_cast<u32v4 *>(p + 16) = hi;
+    constexpr int DW = 2 * C::NB;  // loads of a step's weight
+    auto store_w = [&](int slot, int bslot) {
+        const char *p = lds + C::RAt + (slot * C::Waves + wave) * C::RBytes;
+        const bool past = wrow >= a.w.n;  // rows past n are zeros
+#pragma unroll
+        for (int i = 0; i < C::NB; ++i) {
+            u32v4 codes, lo, hi;
+            uint32_t sw;
+            read_raw(p + i * 1280, lane, codes, sw);
+            const int sb = static_cast<int>(sw >> (8 * (kb[i] & 3)) & 255u);
+            block_values(past ? u32v4{0u, 0u, 0u, 0u} : codes, past ? 0 : sb, smax[i], lo, hi);
+            char *q = lds + C::BAt + bslot * C::BBytes + lane * C::BPitch + (wave * C::NB + i) * 32;
+            *reinterpret_cast<u32v4 *>(q) = lo;
+            *reinterpret_cast<u32v4 *>(q + 16) = hi;
+        }
+        wrow += C::BK;
     };
 
     f32x16 acc[C::MI][C::NI];
@@ -200,67 +238,113 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.0f;
 
-    // operands of 16 rows of the weight
+    // operands of 16 rows of the weight as they come from LDS
     struct Frags {
         u32v4 d[C::MI];
         i32x2 w[C::NI];
     };
     const int arow = (wm * C::MI * 32 + l32) * 128;
     // transposing read: lane i of 16 gives row i / 2, eight columns; gets column i % 16
-    const int brow = BAt + (8 * g + (lane & 15) / 2) * C::BPitch + wn * C::NI * 32 + ((lane >> 4) & 1) * 16 + (lane & 1) * 8;
+    const int brow = C::BAt + (8 * g + (lane & 15) / 2) * C::BPitch + wn * C::NI * 32 + ((lane >> 4) & 1) * 16 + (lane & 1) * 8;
     auto load_frags = [&](int ks, int aslot, int bslot, Frags &f) {
-        typedef __attribute__((address_space(3))) i32x2 lds_i2;
 #pragma unroll
         for (int i = 0; i < C::MI; ++i)
             f.d[i] = *reinterpret_cast<const u32v4 *>(lds + aslot * C::ABytes + arow + i * 4096 + (((2 * ks + g) ^ (l32 & 7)) << 4));
 #pragma unroll
         for (int j = 0; j < C::NI; ++j)
-            f.w[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                (lds_i2 *)(lds + brow + bslot * C::BBytes + ks * 16 * C::BPitch + j * 32));
+            f.w[j] = read_columns(lds + brow + bslot * C::BBytes + ks * 16 * C::BPitch + j * 32);
+    };
+    struct Wide {
+        u32v4 w[C::NI];
+    };
+    auto widen_all = [&](const Frags &f, Wide &v) {
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j) v.w[j] = widen<E>(f.w[j]);
+    };
+    auto multiply = [&](const Frags &f, const Wide &v) {
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j)
+#pragma unroll
+            for (int i = 0; i < C::MI; ++i) acc[i][j] = product<E>(v.w[j], f.d[i], acc[i][j]);
+    };
+    // Order of a region: V vector instructions and one LDS read after each product.
+    auto interleave = [&](auto v) {
+#pragma unroll
+        for (int i = 0; i < C::MI * C::NI; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, decltype(v)::value, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        keep_order();
     };
 
-    // step kt: dy in slot kt % 3, weight in slot kt % 2; dy of the next two
-    // steps and the next step's weight (in registers) are under way.  The
-    // loads run on past the last step (zeros, or rows of the next part, to no
-    // use): a branch here would have the compiler move the products behind it.
+    // Step kt: dy in slot kt % 3, the weight's values in slot kt % 2.  Under
+    // way: dy of steps kt + 1 and kt + 2, the weight's codes of steps kt + 1 and
+    // kt + 2 (slots kt % 2 again).  Its four times 16 rows are a pipeline: read
+    // from LDS two before, widened one before its products; the next step's
+    // weight is converted beside the first two.  The loads run on past the last
+    // step, to no use: a branch around them would have the compiler move the
+    // products behind it.
+    Frags f0, f1, f2;
+    Wide v0, v1;
+    load_w(0);
     load_dy(0);
+    load_w(1);
     load_dy(1);
-    load_w();
-    store_w(0);
-    load_w();
-    if constexpr (ROWS16) wait_vm<C::DA + 2>();
+    wait_vm<2 * C::DA + DW>();
+    store_w(0, 0);
+    load_w(0);
+    load_dy(2);
+    if constexpr (ROWS16) wait_vm<2 * C::DA + 2 * DW>();
     wait_lds();
     block_barrier();
+    load_frags(0, 0, 0, f0);
+    load_frags(1, 0, 0, f1);
+    widen_all(f0, v0);
     int as = 0, bs = 0;
     for (int kt = 0; kt < nk; ++kt) {
-        const int a2 = as == 0 ? 2 : as - 1;  // slot of step kt + 2: the barrier has freed it
-        store_w(bs ^ 1);                      // the next step's weight
-        load_dy(a2);
-        load_w();
-        Frags f[2];
-        load_frags(0, as, bs, f[0]);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            if (ks < 3) load_frags(ks + 1, as, bs, f[(ks + 1) & 1]);
-            keep_order();
-            u32v4 wv[C::NI];
-#pragma unroll
-            for (int j = 0; j < C::NI; ++j) wv[j] = widen<E>(f[ks & 1].w[j]);
-#pragma unroll
-            for (int j = 0; j < C::NI; ++j)
-#pragma unroll
-                for (int i = 0; i < C::MI; ++i) acc[i][j] = product<E>(wv[j], f[ks & 1].d[i], acc[i][j]);
-            keep_order();
-        }
-        // the next step's dy has landed; that of the one after it, and the
-        // weight's two loads, may be in flight
-        if constexpr (ROWS16) wait_vm<C::DA + 2>();
+        const int a1 = as == 2 ? 0 : as + 1;
+        if constexpr (ROWS16) wait_vm<2 * C::DA + DW>();
+        else wait_vm<DW>();
+        keep_order();
+        // 0: reads of 2, widening of 1, conversion of the next step's weight
+        load_frags(2, as, bs, f2);
+        multiply(f0, v0);
+        widen_all(f1, v1);
+        store_w(bs ^ 1, bs ^ 1);
+        interleave(Const<12>{});
+        load_w(bs ^ 1);
+        keep_order();
+        // 1: reads of 3, widening of 2
+        load_frags(3, as, bs, f0);
+        multiply(f1, v1);
+        widen_all(f2, v0);
+        interleave(Const<2>{});
+        // The next step's dy has landed (younger: its successor's, and two
+        // steps' weight).  Past the barrier that holds for every wave, the
+        // next step's weight is in LDS, and this step's operands have been read.
+        if constexpr (ROWS16) wait_vm<C::DA + 2 * DW>();
         wait_lds();
         block_barrier();
-        as = as == 2 ? 0 : as + 1;
+        // 2: reads of the next step's 0, widening of 3
+        load_frags(0, a1, bs ^ 1, f1);
+        multiply(f2, v0);
+        widen_all(f0, v1);
+        interleave(Const<2>{});
+        load_dy(as);
+        keep_order();
+        // 3: reads of the next step's 1, widening of its 0
+        load_frags(1, a1, bs ^ 1, f2);
+        multiply(f0, v1);
+        widen_all(f1, v0);
+        interleave(Const<2>{});
+        f0 = f1;
+        f1 = f2;
+        as = a1;
         bs ^= 1;
     }
     wait_vm<0>();  // nothing more lands in the LDS that the result goes through
+    wait_lds();
     block_barrier();
 
     if (a.part) {
@@ -285,16 +369,19 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_finish_kernel(const MxGrad
     store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, bm * C::BM, bn * C::BN, wave, lane);
 }
 
-// ---- choice of the tile and of the K parts (as the product's, mx_gemm.hip)
+// ---- choice of the tile and of the K parts
 
+// A tile's cost in microseconds per 64 rows of the weight: with few
+// workgroups (a step's latency), and per workgroup of a full CU.  Measured at
+// n 14336, m 4096 and n 4096, m 14336.
 struct GradCost {
     int bm, bn;
-    float light, full;  // us per 64 rows of the weight
+    float light, full;
 };
 constexpr GradCost kGrad[] = {
-    {256, 256, 1.0f, 1.4f},
-    {128, 128, 0.45f, 0.6f},
-    {32, 128, 0.25f, 0.35f},
+    {256, 256, 1.33f, 1.90f},
+    {128, 128, 0.64f, 0.66f},
+    {32, 128, 0.46f, 0.29f},
 };
 constexpr int kGradCount = sizeof(kGrad) / sizeof(kGrad[0]);
 constexpr int kCus = 256;
@@ -303,6 +390,10 @@ struct GradPlan {
     int tile = 0, nsplit = 1;
 };
 
+// The tile and K parts of least estimated time; K parts add a launch and the
+// traffic of their fp32 sums.  (2048 rows, n 14336, m 4096, bf16: 256 x 256
+// tiles in two parts 247 us, whole 328, 128 x 128 tiles 296; 512 rows: 128 x
+// 128 in four parts 84, whole 180; 16 rows: 32 x 128 in eight parts 23, whole 105.)
 GradPlan grad_plan(int M, int n, int m) {
     GradPlan best;
     float least = 0.0f;
@@ -313,9 +404,10 @@ GradPlan grad_plan(int M, int n, int m) {
         for (int sp : {1, 2, 3, 4, 6, 8, 12}) {
             if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
             const float wgs = static_cast<float>(tiles) * sp;
-            const float load = wgs < kCus ? wgs / kCus : 1.0f;
-            const float rounds = wgs <= kCus ? 1.0f : t < 1 ? static_cast<float>((tiles * sp + kCus - 1) / kCus) : wgs / kCus;
-            float us = rounds * (3.0f + static_cast<float>((steps + sp - 1) / sp) * (c.light + (c.full - c.light) * load));
+            // the largest tile has a CU to itself; smaller ones share
+            const float per_cu = t == 0 ? static_cast<float>((tiles * sp + kCus - 1) / kCus) : wgs / kCus;
+            const float step = c.full * per_cu > c.light ? c.full * per_cu : c.light;
+            float us = 3.0f + static_cast<float>((steps + sp - 1) / sp) * step;
             if (sp > 1) us += 3.5f + wgs * c.bm * c.bn * 8.0f * 3e-7f;
             if (least == 0.0f || us < least) {
                 least = us;
@@ -376,7 +468,7 @@ int launch_mx_backward(const MxBackward &b, void *stream) {
         return static_cast<int>(hipErrorInvalidValue);
     auto go = [&](auto e) {
         using E = decltype(e);
-        if (plan.tile == 0) launch_grad<GradTile<2, 4, 4, 2>, E>(a, s);
+        if (plan.tile == 0) launch_grad<GradTile<4, 2, 2, 4>, E>(a, s);
         else if (plan.tile == 1) launch_grad<GradTile<2, 2, 2, 2>, E>(a, s);
         else launch_grad<GradTile<1, 1, 1, 4>, E>(a, s);
     };

@@ -228,6 +228,39 @@ def test_forward_whole_numbers(gpu, b, n, m, act):
         L.close()
 
 
+def _device_products(a, b):
+    """a @ bᵀ and |a| @ |b|ᵀ of fp64 numpy values, on the GPU in fp64 (sizes that take the CPU too long)."""
+    torch = _torch()
+    x, y = torch.from_numpy(a).cuda(), torch.from_numpy(np.ascontiguousarray(b.T)).cuda()
+    return (x @ y).cpu().numpy(), (x.abs() @ y.abs()).cpu().numpy()
+
+
+# every tile size, ragged in rows and columns, whole K and K in parts, K short of the pipeline's depth
+LARGE = [(1900, 8100, 1030, "f16", "e4m3"), (1900, 8100, 1030, "bf16", "e2m1"), (1900, 4000, 1540, "bf16", "e4m3"),
+         (1901, 4003, 1540, "f16", "e2m1"), (1000, 3990, 700, "f16", "e4m3"), (1000, 3990, 700, "bf16", "e2m1"),
+         (300, 1000, 4100, "bf16", "e4m3"), (300, 1001, 4100, "f16", "e2m1"), (130, 500, 9000, "f16", "e4m3"),
+         (1900, 8100, 100, "bf16", "e4m3"), (1900, 8100, 200, "f16", "e2m1"), (70, 60, 4096, "f16", "e2m1")]
+
+
+@pytest.mark.parametrize("b,n,m,name,act", LARGE)
+def test_forward_large(gpu, b, n, m, name, act):
+    _say(f"mx forward large b={b} n={n} m={m} {name} {act}")
+    rng = np.random.default_rng(b + n + m)
+    W, wv = weight(rng, n, m)
+    xd, xv = to_dev(rows_of(rng, b, m), name)
+    codes, s = O.quantize(xv, act)
+    ref, mag = _device_products(O.values(codes, s, act), wv)
+    L = dbf.Layer.mx(W, max_batch=b, act=act)
+    try:
+        y = L(xd)
+        check(y, ref, mag, m, name, act == "e2m1")
+        for _ in range(3):
+            assert same_bits(L(xd), y)
+        assert same_bits(L.forward(blocks_to_dev(codes, s, m, act), out_dtype=T(name)), y)
+    finally:
+        L.close()
+
+
 def test_forward_batches_of_one_handle(gpu):
     """Every batch up to max_batch on one handle; a row's neighbours do not change it beyond the tolerance, and
     rows behind the batch stay as they were."""
@@ -443,6 +476,51 @@ def test_backward_data(gpu, b, n, m, name):
             dx2 = _torch().empty_like(dx)
             dbf.dbf_linear_backward_data(L.handle, dyd.data_ptr(), dx2.data_ptr(), b, st)
             assert same_bits(dx, dx2)
+    finally:
+        L.close()
+
+
+@pytest.mark.parametrize("b,n,m,name", [(1900, 1032, 8100, "bf16"), (1900, 1030, 8100, "f16"), (700, 2008, 2050, "f16"),
+                                        (700, 2001, 2050, "bf16"), (300, 4104, 1000, "bf16"), (33, 4099, 900, "f16"),
+                                        (1900, 40, 8100, "f16"), (1900, 100, 8100, "bf16")])
+def test_backward_large(gpu, b, n, m, name):
+    """Every tile, whole and in K parts, fewer steps than the pipeline holds, rows that are not 16-byte aligned."""
+    _say(f"mx backward large b={b} n={n} m={m} {name}")
+    rng = np.random.default_rng(b + n + m)
+    W, wv = weight(rng, n, m)
+    dyd, dyv = to_dev(rows_of(rng, b, n, 0.1), name)
+    ref, mag = _device_products(dyv, wv.T)
+    L = dbf.Layer.mx(W, max_batch=b)
+    try:
+        dx = L.backward_data(dyd)
+        acc = (n / 8 + 4) * 2.0 ** -24
+        tol = half_step(name) * (np.abs(ref) + acc * mag) + acc * mag + tiny(name)
+        d = np.abs(dx.double().cpu().numpy() - ref)
+        assert np.all(d <= tol), float((d / tol).max())
+        for _ in range(3):
+            assert same_bits(L.backward_data(dyd), dx)
+    finally:
+        L.close()
+
+
+def test_backward_non_finite_rows(gpu):
+    """An infinity or a NaN of dy stays in its row, also beside the end of the rows."""
+    _say("mx backward non-finite")
+    torch = _torch()
+    rng = np.random.default_rng(9)
+    n, m, b = 72, 96, 70
+    W, _ = weight(rng, n, m)
+    dy, _ = to_dev(rng.standard_normal((b, n)), "bf16")
+    L = dbf.Layer.mx(W, max_batch=b)
+    try:
+        clean = L.backward_data(dy)
+        dy[3, 0] = float("nan")
+        dy[40, 70] = float("inf")
+        dx = L.backward_data(dy)
+        keep = torch.ones(b, dtype=torch.bool)
+        keep[[3, 40]] = False
+        assert same_bits(dx[keep.cuda()], clean[keep.cuda()])
+        assert bool(torch.isnan(dx[3]).all()) and not bool(torch.isfinite(dx[40]).any())
     finally:
         L.close()
 
