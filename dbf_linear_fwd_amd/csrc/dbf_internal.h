@@ -275,12 +275,12 @@ struct MxWeight {
     int n = 0, m = 0, n_pad = 0, blocks = 0;
 };
 
-// Few rows (batch <= kMxDecodeBatch): y[i] (batch x n_i, y_type) = x w[i]ᵀ for
-// layers that share x, one launch.  x: batch rows of x_type f16 / bf16
-// (batch <= 16, m a multiple of 8; quantised into `act` blocks), or padded
-// rows of `act` codes (x_type = act) with scales xs.  `first` is filled by
-// the launch.
-constexpr int kMxDecodeBatch = 64;
+// Few rows (batch <= kDecodeMaxBatch, m_pad <= kMxDecodeWidth): y[i] (batch x
+// n_i, y_type) = x w[i]ᵀ for layers that share x, one launch.  x: batch rows of
+// x_type f16 / bf16 (where mx_decode_direct; quantised into `act` blocks), or
+// padded rows of `act` codes (x_type = act) with scales xs.  first and tiles
+// are filled by the launch.
+constexpr int kMxDecodeWidth = 16384;
 struct MxDecodeArgs {
     const void *x = nullptr;
     const uint8_t *xs = nullptr;
@@ -288,8 +288,12 @@ struct MxDecodeArgs {
     int count = 0;
     MxWeight w[kMaxGroup];
     void *y[kMaxGroup] = {};
-    int first[kMaxGroup] = {};  // first workgroup of each layer
+    int first[kMaxGroup] = {};  // first 16-row tile of each layer
+    int tiles = 0;
 };
+// Whether 16-bit rows can go into launch_mx_decode as they are: m a multiple
+// of 8, and their blocks fit LDS.
+bool mx_decode_direct(int batch, int m, int act);
 int launch_mx_decode(MxDecodeArgs &a, void *stream);
 
 // tiled: scales in 32-row tiles (see MxWeight) instead of rows.

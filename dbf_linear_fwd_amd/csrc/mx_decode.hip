@@ -1,38 +1,41 @@
-// Products with a 4-bit block weight for few rows (batch 1..64).
+// Products with a 4-bit block weight for few rows (batch 1..16).
 //
 // The weight's bytes are all there is to move, so the kernel streams them
-// once: a workgroup takes 16 or 32 output rows, its waves cut K between them,
-// and each wave multiplies 16 weight rows x 128 columns with 16 rows of x per
+// once: K is cut between the eight waves of a workgroup, and a workgroup goes
+// through its tiles of 16 output rows, of one or several layers that share x.
+// A wave multiplies 16 weight rows x 128 columns with the rows of x per
 // matrix-core instruction (the weight as the first operand, the batch as the
-// second one's columns; a batch of one costs the same as 16).  The waves'
-// sums meet in LDS and are added in wave order.
+// second one's columns; a batch of one costs the same as 16).  The waves' sums
+// of a tile meet in LDS and are added in wave order, while the next tile's
+// weight is on its way.
 //
 // Of the 16x16x128 instruction a lane (c = lane % 16, g = lane / 16) supplies
 // row c: of an e2m1 operand the 16 bytes of block g; of an e4m3 operand bytes
 // 16 g .. of the first 64 columns and of the second 64.  Its scale byte is
 // block g's either way.
 //
-// f16 and bf16 rows up to batch 16 are quantised in registers, with no pass
-// or launch of their own: an e2m1 lane holds a whole block, an e4m3 lane
-// halves of two blocks, which two lane-group swaps bring together.  Every
-// workgroup quantises the x that it reads; at 16 rows this is about 60
-// instructions per KiB of weight, hidden behind its loads.
+// f16 and bf16 rows are quantised by the kernel itself, with no pass or launch
+// of their own, while the first weight tile is on its way: all threads of a
+// workgroup together, two lanes per block, codes and scales into LDS, where
+// the operands are read for every tile.  (Quantised by each wave in its
+// operand registers, the lanes of absent batch rows repeat the work: batch 1,
+// 4096 x 14336: 13.1 instead of 10.3 us.)  Blocks that do not fit LDS (16 rows
+// from 8912 columns on, e4m3) are quantised in a launch of their own and read
+// from L2 per tile.
+//
+// Graph replays with weights from HBM, f16 to e4m3: 14336 x 4096 at batch 1
+// 8.7 us (3.6 TB/s; a large copy reaches 4.6), batch 16 13.4 us, of which
+// quantising 16 rows in every workgroup is 2 us; 4096 x 14336 at batch 1
+// 10.3 us (one tile per workgroup: nothing to overlap with x's way to LDS);
+// 4096 x 4096 5.4 us; 1024 x 4096 4.0 us.
 
-#include "mx_device.h"
+#include "mx_tile.h"
 
 namespace dbf {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 // Rows of x as the kernel's template argument: 16-bit values, or ready blocks.
 constexpr int kBlocks = -1;
-
-__device__ __forceinline__ i32x8 operand(u32v4 a, u32v4 b) {
-    return i32x8{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
-                 static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
-}
 
 // Largest magnitude of 16-bit values, two per word: sign bits off, as integers.
 __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
@@ -56,9 +59,10 @@ __device__ __forceinline__ uint32_t float_bits(uint32_t m) {
     else return __builtin_bit_cast(uint32_t, F16::get(static_cast<uint16_t>(v)));
 }
 
+// Codes of 16 values (two words of eight each at a and b): e4m3 in four
+// words, e2m1 in two.  Under mx_saturate.
 template <int XT, int ACT>
 __device__ __forceinline__ u32v4 codes16(u32v4 a, u32v4 b, float sc) {
-    // 16 values: e4m3 in four words; e2m1 in two (words 0, 1)
     u32v4 r = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -95,195 +99,210 @@ __device__ __forceinline__ u32v4 codes16(u32v4 a, u32v4 b, float sc) {
     return r;
 }
 
-// The operand words and the scale byte of this lane from its 32 16-bit
-// values v[0..3] (eight each).  FP16_OVFL must be on (e4m3 saturates).
-template <int XT, int ACT>
-__device__ __forceinline__ void quantize_lane(const u32v4 (&v)[4], i32x8 &op, int &scale) {
-    const u32v4 z = {0u, 0u, 0u, 0u};
-    if constexpr (ACT == DBF_TYPE_E2M1) {
-        const uint32_t m = max16x2(absmax(v[0], v[1]), absmax(v[2], v[3]));
-        const uint32_t s = mx_scale_byte<ACT>(float_bits<XT>(m));
-        const float sc = mx_scale_value(s);
-        const u32v4 a = codes16<XT, ACT>(v[0], v[1], sc), b = codes16<XT, ACT>(v[2], v[3], sc);
-        op = operand(u32v4{a[0], a[1], b[0], b[1]}, z);
-        scale = static_cast<int>(s);
-    } else {
-        // lane group g holds half g % 2 of blocks g / 2 and 2 + g / 2.  The
-        // swap exchanges odd lane groups of its first value with even ones of
-        // its second: the two halves of block 0, 2, 1, 3 meet in groups 0..3.
-        const uint32_t m0 = float_bits<XT>(absmax(v[0], v[1])), m1 = float_bits<XT>(absmax(v[2], v[3]));
-        const auto p = __builtin_amdgcn_permlane16_swap(m0, m1, false, false);
-        const uint32_t pa = p[0], pb = p[1];
-        const uint32_t s = mx_scale_byte<ACT>(pa > pb ? pa : pb);  // of block 0, 2, 1, 3 in groups 0..3
-        const auto q = __builtin_amdgcn_permlane16_swap(s, s, false, false);
-        const uint32_t s0 = q[0], s1 = q[1];  // of blocks g / 2 and 2 + g / 2
-        const u32v4 a = codes16<XT, ACT>(v[0], v[1], mx_scale_value(s0));
-        const u32v4 b = codes16<XT, ACT>(v[2], v[3], mx_scale_value(s1));
-        op = operand(a, b);
-        const auto h = __builtin_amdgcn_permlane32_swap(s0, s1, false, false);  // blocks 0 0 2 2 and 1 1 3 3
-        const uint32_t h0 = h[0], h1 = h[1];
-        const auto t = __builtin_amdgcn_permlane16_swap(h0, h1, false, false);  // 0 1 2 3
-        const uint32_t t0 = t[0];
-        scale = static_cast<int>(t0);
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+// x in LDS: rows of codes and of scale bytes, their pitches off a multiple of
+// the banks so that the rows of an operand read fall on different ones.
+template <int ACT>
+struct XLds {
+    __host__ __device__ static int row_bytes(int blocks) { return blocks * (ACT == DBF_TYPE_E4M3 ? 32 : 16); }
+    __host__ __device__ static int code_pitch(int blocks) { return row_bytes(blocks) + 16; }
+    __host__ __device__ static int scale_pitch(int blocks) { return blocks + 4; }
+    static size_t bytes(int batch, int blocks) {
+        return static_cast<size_t>(batch) * (code_pitch(blocks) + scale_pitch(blocks));
     }
-}
+};
+constexpr size_t kSumBytes = 2 * kWaves * 64 * 16;
+constexpr size_t kMaxXBytes = 160 * 1024 - kSumBytes;
 
-// XT: type of x's rows (f16, bf16) or kBlocks; RT: 16-row weight tiles per
-// workgroup; NB: groups of 16 rows of x; U: steps of 128 columns in flight.
-template <int XT, int ACT, typename E, int RT, int NB, int WAVES, int U>
-__global__ __launch_bounds__(64 * WAVES) void mx_decode_kernel(const MxDecodeArgs a) {
-    __shared__ __attribute__((aligned(16))) f32x4 red[WAVES][RT * NB][64];
-    int li = 0;
-    for (int j = 1; j < a.count; ++j)
-        if (static_cast<int>(blockIdx.x) >= a.first[j]) li = j;
-    const MxWeight &w = a.w[li];
-    const int row0 = (static_cast<int>(blockIdx.x) - a.first[li]) * 16 * RT;
+// XT: type of x's rows (f16, bf16) or kBlocks; SPW: steps of 128 columns of a
+// wave at most; LDSX: x goes through LDS (blocks that do not fit it are read
+// from memory for every tile).
+template <int XT, int ACT, typename E, int SPW, bool LDSX>
+__global__ __launch_bounds__(kThreads, 4) void mx_decode_kernel(const MxDecodeArgs a) {
+    constexpr int kAhead = SPW > 8 ? 2 : 4;  // units of a thread in flight while x goes to LDS (registers for two workgroups per CU)
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    f32x4 *red = reinterpret_cast<f32x4 *>(lds);  // [2][kWaves][64]
+    char *xl = lds + kSumBytes;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int blocks = w.blocks, steps = blocks >> 2;
-    const int k0 = wave * steps / WAVES, k1 = (wave + 1) * steps / WAVES;
+    const int blocks = a.w[0].blocks, steps = blocks >> 2;  // (the same for every layer)
+    const int k0 = wave * steps / kWaves, cnt = (wave + 1) * steps / kWaves - k0;
 
-    const uint8_t *wc[RT], *ws[RT];
+    // the layer, output row and weight of tile t
+    int li = 0, row0 = 0;
+    u32v4 wv[SPW];
+    int ws[SPW];
+    auto load_tile = [&](int t) {
+        li = 0;
+        for (int j = 1; j < a.count; ++j)
+            if (t >= a.first[j]) li = j;
+        row0 = (t - a.first[li]) * 16;
+        const int r = row0 + c;  // n_pad is a multiple of 32: every row of the tile is there
+        const uint8_t *wc = a.w[li].codes + ((static_cast<size_t>(r >> 5) * blocks + 4 * k0 + g) * 32 + (r & 31)) * 16;
+        const uint8_t *wsc = a.w[li].scales + ((static_cast<size_t>(r >> 5) * steps + k0) * 32 + (r & 31)) * 4 + g;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int r = row0 + 16 * t + c;  // n_pad is a multiple of 32: every row of the tile is there
-        wc[t] = w.codes + ((static_cast<size_t>(r >> 5) * blocks + g) * 32 + (r & 31)) * 16;
-        ws[t] = w.scales + (static_cast<size_t>(r >> 5) * steps * 32 + (r & 31)) * 4 + g;
-    }
-    const uint8_t *xr[NB], *xsr[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int row = min(16 * b + c, a.batch - 1);  // rows past the batch: multiplied, not written
+        for (int u = 0; u < SPW; ++u)
+            if (u < cnt) {
+                wv[u] = *reinterpret_cast<const u32v4 *>(wc + u * 2048);
+                ws[u] = wsc[u * 128];
+            }
+    };
+    int t = blockIdx.x;
+    load_tile(t);
+
+    using X = XLds<ACT>;
+    const int cp = LDSX ? X::code_pitch(blocks) : X::row_bytes(blocks), sp = LDSX ? X::scale_pitch(blocks) : blocks;
+    if constexpr (LDSX) {
+        char *xsl = xl + a.batch * cp;
         if constexpr (XT == kBlocks) {
-            xr[b] = static_cast<const uint8_t *>(a.x) + static_cast<size_t>(row) * blocks * (ACT == DBF_TYPE_E4M3 ? 32 : 16) + 16 * g;
-            xsr[b] = a.xs + static_cast<size_t>(row) * blocks + g;
-        } else {
-            xr[b] = static_cast<const uint8_t *>(a.x) + (static_cast<size_t>(row) * w.m + (ACT == DBF_TYPE_E4M3 ? 16 : 32) * g) * 2;
-            xsr[b] = nullptr;
-        }
-    }
-    f32x4 acc[RT][NB];
+            const int per = X::row_bytes(blocks) / 16, all = a.batch * per;
+            for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kThreads) {
+                u32v4 v[kAhead];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+                for (int j = 0; j < kAhead; ++j)
+                    if (const int i = i0 + j * kThreads; i < all)
+                        v[j] = *reinterpret_cast<const u32v4 *>(static_cast<const uint8_t *>(a.x) + static_cast<size_t>(i) * 16);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) acc[t][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (XT != kBlocks) mx_saturate(true);
-
-    for (int k = k0; k < k1; k += U) {
-        u32v4 wv[U][RT], xv[U][NB][XT == kBlocks ? 2 : 4];
-        int wsc[U][RT], xsc[U][NB];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int kt = min(k + u, k1 - 1);  // (past the end: loaded, not multiplied)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                wv[u][t] = *reinterpret_cast<const u32v4 *>(wc[t] + static_cast<size_t>(kt) * 2048);
-                wsc[u][t] = ws[t][static_cast<size_t>(kt) * 128];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int kt = min(k + u, k1 - 1);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                if constexpr (XT == kBlocks) {
-                    if constexpr (ACT == DBF_TYPE_E4M3) {
-                        xv[u][b][0] = *reinterpret_cast<const u32v4 *>(xr[b] + static_cast<size_t>(kt) * 128);
-                        xv[u][b][1] = *reinterpret_cast<const u32v4 *>(xr[b] + static_cast<size_t>(kt) * 128 + 64);
-                    } else {
-                        xv[u][b][0] = *reinterpret_cast<const u32v4 *>(xr[b] + static_cast<size_t>(kt) * 64);
-                        xv[u][b][1] = u32v4{0u, 0u, 0u, 0u};
+                for (int j = 0; j < kAhead; ++j)
+                    if (const int i = i0 + j * kThreads; i < all) {
+                        const int row = i / per, q = i - row * per;
+                        *reinterpret_cast<u32v4 *>(xl + row * cp + q * 16) = v[j];
                     }
-                    xsc[u][b] = xsr[b][static_cast<size_t>(kt) * 4];
+            }
+            for (int i = threadIdx.x; i < a.batch * steps; i += kThreads) {
+                const int row = i / steps, q = i - row * steps;
+                *reinterpret_cast<uint32_t *>(xsl + row * sp + q * 4) = reinterpret_cast<const uint32_t *>(a.xs)[i];
+            }
+        } else {
+            const int m = a.w[0].m, per = blocks * 2, all = a.batch * per;  // units of 16 columns
+            mx_saturate(true);
+            for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kThreads) {  // (whole pairs of lanes: per is even)
+                u32v4 lo[kAhead], hi[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int i = i0 + j * kThreads, row = i / per, col = (i - row * per) * 16;
+                    const uint16_t *src = static_cast<const uint16_t *>(a.x) + static_cast<size_t>(row) * m + col;
+                    lo[j] = hi[j] = u32v4{0u, 0u, 0u, 0u};  // columns past m (a multiple of 8) are zeros
+                    if (i < all && col < m) lo[j] = *reinterpret_cast<const u32v4 *>(src);
+                    if (i < all && col + 8 < m) hi[j] = *reinterpret_cast<const u32v4 *>(src + 8);
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int i = i0 + j * kThreads, row = i / per, q = i - row * per, col = q * 16;
+                    if (i >= all) break;
+                    uint32_t mx = float_bits<XT>(absmax(lo[j], hi[j]));
+                    const uint32_t other = __builtin_amdgcn_mov_dpp(mx, 0xB1, 0xf, 0xf, true);  // the pair's other lane
+                    mx = mx > other ? mx : other;
+                    const uint32_t s = mx_scale_byte<ACT>(mx);
+                    const u32v4 r = codes16<XT, ACT>(lo[j], hi[j], mx_scale_value(s));
+                    char *dst = xl + row * cp + col / (ACT == DBF_TYPE_E4M3 ? 1 : 2);
+                    if constexpr (ACT == DBF_TYPE_E4M3) *reinterpret_cast<u32v4 *>(dst) = r;
+                    else *reinterpret_cast<u32v2 *>(dst) = u32v2{r[0], r[1]};
+                    if ((q & 1) == 0) xsl[row * sp + (q >> 1)] = static_cast<char>(s);
+                }
+            }
+            mx_saturate(false);
+        }
+        __syncthreads();
+    }
+
+    // operand and scale byte of this lane's row of x (rows past the batch: any, not written)
+    const int xrow = min(c, a.batch - 1);
+    constexpr int Step = ACT == DBF_TYPE_E4M3 ? 128 : 64;
+    const char *xc = (LDSX ? xl : static_cast<const char *>(a.x)) + static_cast<size_t>(xrow) * cp + k0 * Step + 16 * g;
+    const uint8_t *xs = (LDSX ? reinterpret_cast<const uint8_t *>(xl) + a.batch * cp : a.xs) +
+                        static_cast<size_t>(xrow) * sp + k0 * 4 + g;
+
+    for (int it = 0; t < a.tiles; ++it) {
+        f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        constexpr int FX = ACT == DBF_TYPE_E4M3 ? 0 : 4;
+#pragma unroll
+        for (int u = 0; u < SPW; ++u)
+            if (u < cnt) {
+                u32v4 hi = {0u, 0u, 0u, 0u};
+                if constexpr (ACT == DBF_TYPE_E4M3) hi = *reinterpret_cast<const u32v4 *>(xc + u * Step + 64);
+                const i32x8 op = operand(*reinterpret_cast<const u32v4 *>(xc + u * Step), hi);
+                const int sx = xs[u * 4];
+                acc[u & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(wv[u], u32v4{0u, 0u, 0u, 0u}), op,
+                                                                             acc[u & 1], 4, FX, 0, ws[u], 0, sx);
+            }
+        const int layer = li, row = row0;
+        const int next = t + gridDim.x;
+        if (next < a.tiles) load_tile(next);
+        f32x4 *sums = red + (it & 1) * (kWaves * 64);
+        sums[wave * 64 + lane] = acc[0] + acc[1];
+        __syncthreads();  // (the buffer is written again past the next barrier)
+        if (wave == (it & (kWaves - 1))) {
+            f32x4 s = sums[lane];
+#pragma unroll
+            for (int v = 1; v < kWaves; ++v) s += sums[v * 64 + lane];
+            // result register v of lane (c, g): batch row c, output row 4 g + v
+            const int n = a.w[layer].n, col = row + 4 * g;
+            typename E::T *dst = static_cast<typename E::T *>(a.y[layer]) + static_cast<size_t>(c) * n + col;
+            if (c < a.batch) {
+                if (n % 4 == 0) {
+                    if (col < n)
+                        *reinterpret_cast<u32v2 *>(dst) =
+                            u32v2{static_cast<uint32_t>(E::put(s[0])) | static_cast<uint32_t>(E::put(s[1])) << 16,
+                                  static_cast<uint32_t>(E::put(s[2])) | static_cast<uint32_t>(E::put(s[3])) << 16};
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        // eight values; columns past m (a multiple of 8) are zeros
-                        const int off = ACT == DBF_TYPE_E4M3 ? 64 * (q >> 1) + 8 * (q & 1) : 8 * q;
-                        const int col = kt * 128 + (ACT == DBF_TYPE_E4M3 ? 16 : 32) * g + off;
-                        xv[u][b][q] = u32v4{0u, 0u, 0u, 0u};
-                        if (col < w.m) xv[u][b][q] = *reinterpret_cast<const u32v4 *>(xr[b] + (static_cast<size_t>(kt) * 128 + off) * 2);
-                    }
+                    for (int v = 0; v < 4; ++v)
+                        if (col + v < n) dst[v] = E::put(s[v]);
                 }
             }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (k + u >= k1) break;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                i32x8 op;
-                int sx;
-                if constexpr (XT == kBlocks) {
-                    op = operand(xv[u][b][0], xv[u][b][1]);
-                    sx = xsc[u][b];
-                } else {
-                    quantize_lane<XT, ACT>(xv[u][b], op, sx);
-                }
-                constexpr int FX = ACT == DBF_TYPE_E4M3 ? 0 : 4;
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-                    acc[t][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        operand(wv[u][t], u32v4{0u, 0u, 0u, 0u}), op, acc[t][b], 4, FX, 0, wsc[u][t], 0, sx);
-            }
-        }
-    }
-    if constexpr (XT != kBlocks) mx_saturate(false);
-
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) red[wave][t * NB + b][lane] = acc[t][b];
-    __syncthreads();
-    // result register v of lane (c, g): batch row c, output row 4 g + v
-    typename E::T *y = static_cast<typename E::T *>(a.y[li]);
-    for (int i = threadIdx.x; i < RT * NB * 64; i += 64 * WAVES) {
-        const int f = i >> 6, l = i & 63;
-        f32x4 s = red[0][f][l];
-#pragma unroll
-        for (int v = 1; v < WAVES; ++v) s += red[v][f][l];
-        const int row = (f % NB) * 16 + (l & 15), col = row0 + (f / NB) * 16 + 4 * (l >> 4);
-        if (row >= a.batch) continue;
-        typename E::T *dst = y + static_cast<size_t>(row) * w.n + col;
-        if (w.n % 4 == 0) {
-            if (col < w.n)
-                *reinterpret_cast<u32v2 *>(dst) = u32v2{static_cast<uint32_t>(E::put(s[0])) | static_cast<uint32_t>(E::put(s[1])) << 16,
-                                                        static_cast<uint32_t>(E::put(s[2])) | static_cast<uint32_t>(E::put(s[3])) << 16};
-        } else {
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                if (col + v < w.n) dst[v] = E::put(s[v]);
-        }
+        t = next;
     }
 }
 
-template <int XT, int ACT, typename E, int RT, int NB, int WAVES, int U>
+template <int XT, int ACT, typename E, int SPW, bool LDSX>
 void launch(MxDecodeArgs &a, hipStream_t s) {
-    int n = 0;
+    static std::atomic<uint64_t> asked{0};
+    a.tiles = 0;
     for (int i = 0; i < a.count; ++i) {
-        a.first[i] = n;
-        n += (a.w[i].n + 16 * RT - 1) / (16 * RT);
+        a.first[i] = a.tiles;
+        a.tiles += (a.w[i].n + 15) / 16;
     }
-    launch_kernel(mx_decode_kernel<XT, ACT, E, RT, NB, WAVES, U>, dim3(n), dim3(64 * WAVES), 0, s, a);
+    const size_t bytes = kSumBytes + (LDSX ? XLds<ACT>::bytes(a.batch, a.w[0].blocks) : 0);
+    // One resident wave of workgroups, two per CU where LDS holds both
+    // (14336 x 4096, batch 1: 8.7 us, one per CU 10.1).
+    const int wgs = bytes <= 80 * 1024 ? 512 : 256;
+    const int per = (a.tiles + wgs - 1) / wgs;  // tiles of a workgroup
+    auto kernel = mx_decode_kernel<XT, ACT, E, SPW, LDSX>;
+    if (bytes > 65536) allow_lds(kernel, 160 * 1024, asked);
+    launch_kernel(kernel, dim3((a.tiles + per - 1) / per), dim3(kThreads), bytes, s, a);
 }
 
-template <int XT, int ACT, typename E>
+template <int XT, int ACT, typename E, bool LDSX>
 void choose(MxDecodeArgs &a, hipStream_t s) {
-    if constexpr (XT == kBlocks) {
-        if (a.batch > 32) return launch<XT, ACT, E, 1, 4, 8, 2>(a, s);
-        if (a.batch > 16) return launch<XT, ACT, E, 1, 2, 8, 4>(a, s);
-    }
-    launch<XT, ACT, E, 1, 1, 8, 4>(a, s);
+    const int spw = (a.w[0].blocks / 4 + kWaves - 1) / kWaves;
+    if (spw <= 4) launch<XT, ACT, E, 4, LDSX>(a, s);
+    else if (spw <= 8) launch<XT, ACT, E, 8, LDSX>(a, s);
+    else launch<XT, ACT, E, 16, LDSX>(a, s);
 }
 
 }  // namespace
+
+bool mx_decode_direct(int batch, int m, int act) {
+    const int blocks = round_up_int(m, 128) / 32;
+    return m % 8 == 0 && (act == DBF_TYPE_E4M3 ? XLds<DBF_TYPE_E4M3>::bytes(batch, blocks) : XLds<DBF_TYPE_E2M1>::bytes(batch, blocks)) <= kMaxXBytes;
+}
 
 int launch_mx_decode(MxDecodeArgs &a, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
     auto types = [&](auto xt, auto act) {
         constexpr int XT = decltype(xt)::value, ACT = decltype(act)::value;
-        if (a.y_type == DBF_TYPE_F16) choose<XT, ACT, F16>(a, s);
-        else choose<XT, ACT, BF16>(a, s);
+        const bool fits = XLds<ACT>::bytes(a.batch, a.w[0].blocks) <= kMaxXBytes;
+        auto go = [&](auto e) {
+            using E = decltype(e);
+            if constexpr (XT == kBlocks) {
+                if (!fits) return choose<XT, ACT, E, false>(a, s);
+            }
+            choose<XT, ACT, E, true>(a, s);
+        };
+        if (a.y_type == DBF_TYPE_F16) go(F16{});
+        else go(BF16{});
     };
     using E4 = std::integral_constant<int, DBF_TYPE_E4M3>;
     using E2 = std::integral_constant<int, DBF_TYPE_E2M1>;
@@ -291,6 +310,8 @@ int launch_mx_decode(MxDecodeArgs &a, void *stream) {
         if (a.act == DBF_TYPE_E4M3) types(xt, E4{});
         else types(xt, E2{});
     };
+    const bool real = a.x_type == DBF_TYPE_F16 || a.x_type == DBF_TYPE_BF16;
+    if (real && !mx_decode_direct(a.batch, a.w[0].m, a.act)) return static_cast<int>(hipErrorInvalidValue);
     if (a.x_type == DBF_TYPE_F16) rows(std::integral_constant<int, DBF_TYPE_F16>{});
     else if (a.x_type == DBF_TYPE_BF16) rows(std::integral_constant<int, DBF_TYPE_BF16>{});
     else rows(std::integral_constant<int, kBlocks>{});

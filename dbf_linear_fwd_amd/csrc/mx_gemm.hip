@@ -13,11 +13,6 @@
 namespace dbf {
 namespace {
 
-__device__ __forceinline__ i32x8 operand(u32v4 a, u32v4 b) {
-    return i32x8{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
-                 static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
-}
-
 // ---------------------------------------------------------------------------
 // Tiled product: a BM x BN output tile per workgroup; K goes through a ring of
 // LDS stages that global_load_lds fills several stages ahead.

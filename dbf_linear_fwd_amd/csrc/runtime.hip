@@ -888,6 +888,11 @@ static dbf::MxWeight mx_weight(const dbf_layer *h) {
     return w;
 }
 
+// Whether a forward is one launch of the few-row kernel.
+static bool mx_few(const dbf_layer *h, int32_t batch) {
+    return batch <= dbf::kDecodeMaxBatch && h->m_pad <= dbf::kMxDecodeWidth;
+}
+
 // One or several layers (same m, same activation format) on the input x of
 // x_type (f16 / bf16 rows, or blocks with x_scales); arguments are checked.
 // Few rows: one launch for all the layers, the 16-bit rows quantised by it
@@ -900,8 +905,8 @@ static dbf_status_t forward_mx(dbf_layer *const *hs, int count, const void *x, i
     const bool real = x_type == DBF_TYPE_F16 || x_type == DBF_TYPE_BF16;
     const int act = real ? h->mx_act : x_type;
     const int blocks = h->m_pad / 32;
-    const bool few = batch <= dbf::kMxDecodeBatch;
-    const bool direct = real && batch <= dbf::kDecodeMaxBatch && h->m % 8 == 0;
+    const bool few = mx_few(h, batch);
+    const bool direct = real && few && dbf::mx_decode_direct(batch, h->m, act);
     dbf_status_t st = DBF_OK;
     if (real && !direct) {
         st = timed_launch(h, "mx_quantize", stream, [&] {
@@ -974,8 +979,8 @@ static size_t mx_part_floats(int32_t n, int32_t m, int32_t max_batch) {
     for (int64_t top = 32; top < 65536 + 32; top += 32) {  // (no K parts beyond: the grids are full)
         const int32_t M = static_cast<int32_t>(std::min<int64_t>(top, max_batch));
         most = std::max(most, dbf::mx_backward_parts(M, n, m));
-        if (M > dbf::kMxDecodeBatch)
-            for (int32_t t : {DBF_TYPE_E4M3, DBF_TYPE_E2M1}) most = std::max(most, dbf::mx_product_parts(M, n, blocks, t));
+        for (int32_t t : {DBF_TYPE_E4M3, DBF_TYPE_E2M1})
+            most = std::max(most, dbf::mx_product_parts(M, n, blocks, t));
         if (M == max_batch) break;
     }
     return most;
@@ -1393,7 +1398,7 @@ ScratchPlan plan_scratch(const dbf_layer *h, int32_t batch) {
     if (h->mx) {
         p.xcodes = take(size_t(batch) * dbf_mx_code_bytes(h->m, h->mx_act));
         p.xscales = take(size_t(round_up(batch, 32)) * dbf_mx_scale_bytes(h->m));
-        if (batch > dbf::kMxDecodeBatch) p.split_cap = dbf::mx_product_parts(batch, h->n, h->m_pad / 32, h->mx_act);
+        if (!mx_few(h, batch)) p.split_cap = dbf::mx_product_parts(batch, h->n, h->m_pad / 32, h->mx_act);
         p.split = take(sizeof(float) * p.split_cap);
         p.total = off;
         return p;

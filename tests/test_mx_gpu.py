@@ -261,6 +261,30 @@ def test_forward_large(gpu, b, n, m, name, act):
         L.close()
 
 
+@pytest.mark.parametrize("act", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("b,n,m,name", [(16, 40, 8904, "f16"), (16, 40, 9216, "f16"), (13, 9001, 1100, "bf16"),
+                                        (2, 9200, 4100, "f16"), (5, 33, 16384, "bf16"), (16, 33, 16376, "f16"),
+                                        (3, 70, 16392, "bf16")])
+def test_forward_few_rows(gpu, b, n, m, name, act):
+    """Few rows at the widths where their blocks fill LDS, no longer fit it, or the sums change hands; several tiles
+    of output rows for a workgroup; every run with the same bits."""
+    _say(f"mx forward few rows b={b} n={n} m={m} {name} {act}")
+    rng = np.random.default_rng(b + n + m)
+    W, wv = weight(rng, n, m)
+    xd, xv = to_dev(rows_of(rng, b, m), name)
+    codes, s = O.quantize(xv, act)
+    ref, mag = _device_products(O.values(codes, s, act), wv)
+    L = dbf.Layer.mx(W, max_batch=b, act=act)
+    try:
+        y = L(xd)
+        check(y, ref, mag, m, name, act == "e2m1")
+        for _ in range(3):
+            assert same_bits(L(xd), y)
+        assert same_bits(L.forward(blocks_to_dev(codes, s, m, act), out_dtype=T(name)), y)
+    finally:
+        L.close()
+
+
 def test_forward_batches_of_one_handle(gpu):
     """Every batch up to max_batch on one handle; a row's neighbours do not change it beyond the tolerance, and
     rows behind the batch stay as they were."""
