@@ -173,13 +173,10 @@ __device__ __forceinline__ u32v2 mx_codes8(const float (&v)[8], uint32_t s) {
 // a row, and the block's scale byte at `scale`.
 template <int FMT>
 __device__ __forceinline__ void mx_store8(const float (&v)[8], int col, uint8_t *crow, uint8_t *scale) {
-    uint32_t a = 0;
+    float top = 0.0f;  // (maximum: a NaN stays)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu;
-        a = a > b ? a : b;
-    }
-    a = quad_max(a);
+    for (int i = 0; i < 8; ++i) top = __builtin_elementwise_maximum(top, fabsf(v[i]));
+    const uint32_t a = quad_max(__builtin_bit_cast(uint32_t, top) & 0x7fffffffu);
     const uint32_t s = mx_scale_byte<FMT>(a);
     const u32v2 c = mx_codes8<FMT>(v, s);
     if constexpr (FMT == DBF_TYPE_E4M3) *reinterpret_cast<u32v2 *>(crow + col) = c;

@@ -4,37 +4,64 @@
 //   g = dy w,  dx = rstd (g - h rstd² mean(g h)) + dh,  dw = Σ_rows dy h rstd
 //
 // Every kernel reads a row once and keeps it in registers, eight consecutive
-// columns per lane and chunk, so both directions are bound by memory.  Sums
-// are fp32: a lane's own columns in order, then over the wave, then over the
-// waves in order (no atomics: repeated calls give the same bits).  y leaves
-// in 16 bits, or in e4m3 blocks of 32 columns with one scale each, quantised
-// from the fp32 values: four neighbouring lanes hold a block.
+// columns per lane and chunk, so both directions are bound by memory; the
+// gradient's next row is on its way while one is reduced and written.  Sums
+// are fp32 over eight columns or the rows of a lane.  A row's mean of squares
+// is joined in fp64: its error shifts the whole row at once, and in blocks that
+// shows as codes on the other side of a tie.  All joins are in a fixed order
+// (no atomics: repeated calls give the same bits).
+// y leaves in 16 bits, or in e4m3 blocks of 32 columns with one scale each,
+// quantised from the fp32 values: four neighbouring lanes hold a block.
+//
+// bf16, operands from HBM, graph replays: norm with residual 8192 x 4096
+// 54 us (4.95 TB/s moved; a plain large copy 4.6), with block output 51 us,
+// 2048 x 4096 14.6 and 16.4, one row 2.8 and 3.1; gradient with dh 8192 x 4096
+// 57 us (4.7 TB/s), 2048 x 4096 22 (a second launch and the
+// parts of dw), 65536 x 128 20.
 
 #include "mx_device.h"
 
 namespace dbf {
 namespace {
 
-// Sum over the wave; every lane gets it.
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over the LPR lanes that share a row; every one gets it.  Up to a wave
+// without LDS; wider rows meet in red[waves of the workgroup], one barrier.
+template <int LPR, typename V>
+__device__ __forceinline__ V row_sum(V v, V *red) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    for (int o = (LPR < 64 ? LPR : 64) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    if constexpr (LPR > 64) {
+        const int wave = threadIdx.x >> 6, first = threadIdx.x / LPR * (LPR / 64);
+        if ((threadIdx.x & 63) == 0) red[wave] = v;
+        __syncthreads();
+        v = red[first];
+#pragma unroll
+        for (int i = 1; i < LPR / 64; ++i) v += red[first + i];
+    }
     return v;
 }
 
-// Sum over the WPR waves that share a row (WPR = 1: no LDS, no barrier).
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float *red) {
-    v = wave_sum(v);
-    if constexpr (WPR > 1) {
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) red[wave] = v;
-        __syncthreads();
-        v = red[0];
+// Eight consecutive 16-bit elements as they are (load8's rules).
+template <bool VEC>
+__device__ __forceinline__ u32v4 load_raw(const uint16_t *p, int valid) {
+    u32v4 q = {0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+        if (valid > 0) q = *reinterpret_cast<const u32v4 *>(p);
+    } else {
 #pragma unroll
-        for (int i = 1; i < WPR; ++i) v += red[i];
+        for (int i = 0; i < 8; ++i)
+            if (i < valid) q[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
     }
-    return v;
+    return q;
+}
+
+template <typename E>
+__device__ __forceinline__ void unpack(u32v4 q, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = E::get(static_cast<uint16_t>(q[i] & 0xffffu));
+        v[2 * i + 1] = E::get(static_cast<uint16_t>(q[i] >> 16));
+    }
 }
 
 template <typename E, bool VEC>
@@ -59,47 +86,56 @@ struct NormArgs {
     float *rstd;
 };
 
-// WPR waves per row (4 / WPR rows per workgroup, at least one), NC chunks of
-// 512 * WPR columns.
-template <typename E, bool MX, bool VEC, int WPR, int NC>
-__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rms_norm_kernel(const NormArgs a) {
-    constexpr int RPB = WPR >= 4 ? 1 : 4 / WPR;
-    __shared__ float red[WPR];
+// LPR lanes per row, NC chunks of 8 LPR columns.
+template <typename E, bool MX, bool VEC, int LPR, int NC>
+__global__ __launch_bounds__(LPR > 256 ? LPR : 256) void rms_norm_kernel(const NormArgs a) {
+    constexpr int Threads = LPR > 256 ? LPR : 256, RPB = Threads / LPR;
+    __shared__ double red[Threads / 64];
     using T = typename E::T;
-    const int t = WPR >= 4 ? threadIdx.x : threadIdx.x % (64 * WPR);
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + (WPR >= 4 ? 0 : threadIdx.x / (64 * WPR));
-    if (row >= a.rows) return;  // (WPR = 1 only: no barrier follows)
+    const int t = threadIdx.x % LPR;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / LPR;
+    if (row >= a.rows) return;  // (RPB > 1 only: no barrier follows)
     const size_t base = static_cast<size_t>(row) * a.cols;
-    float h[NC][8];
-    float sum = 0.0f;
+    u32v4 x[NC], r[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int col = (c * 64 * WPR + t) * 8;
-        load8<E, VEC>(static_cast<const T *>(a.x) + base + col, a.cols - col, h[c]);
+        const int col = (c * LPR + t) * 8;
+        x[c] = load_raw<VEC>(static_cast<const T *>(a.x) + base + col, a.cols - col);
+        if (a.r) r[c] = load_raw<VEC>(static_cast<const T *>(a.r) + base + col, a.cols - col);
+    }
+    float h[NC][8], w[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) load_weight<E, VEC>(a.w, a.w_f32, (c * LPR + t) * 8, a.cols, w[c]);
+    double sum = 0.0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int col = (c * LPR + t) * 8;
+        unpack<E>(x[c], h[c]);
         if (a.r) {
-            float r[8];
-            load8<E, VEC>(static_cast<const T *>(a.r) + base + col, a.cols - col, r);
+            float v[8];
+            unpack<E>(r[c], v);
             // the sum of two 16-bit values rounded to fp32 and then to 16
             // bits is their sum rounded once (24 >= 2 * 11 + 2)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[c][i] = E::get(E::put(h[c][i] + r[i]));
+            for (int i = 0; i < 8; ++i) h[c][i] = E::get(E::put(h[c][i] + v[i]));
             if (a.h) store8<E, VEC>(static_cast<T *>(a.h) + base + col, a.cols - col, h[c]);
         }
+        float part = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += h[c][i] * h[c][i];
+        for (int i = 0; i < 8; ++i) part = fmaf(h[c][i], h[c][i], part);
+        sum += part;
     }
-    sum = row_sum<WPR>(sum, red);
-    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
+    sum = row_sum<LPR>(sum, red);
+    const float rstd = static_cast<float>(rsqrt(sum / a.cols + static_cast<double>(a.eps)));
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     const int wide = (a.cols + 127) / 128 * 128;
     if constexpr (MX) mx_saturate(true);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int col = (c * 64 * WPR + t) * 8;
-        float w[8], y[8];
-        load_weight<E, VEC>(a.w, a.w_f32, col, a.cols, w);
+        const int col = (c * LPR + t) * 8;
+        float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = h[c][i] * rstd * w[i];
+        for (int i = 0; i < 8; ++i) y[i] = h[c][i] * rstd * w[c][i];
         if constexpr (MX) {
             if (col < wide) {
                 if (col >= a.cols) {  // padding of the row: zero codes and scales whatever rstd is
@@ -128,124 +164,195 @@ struct NormGradArgs {
     float *part;  // [workgroups][cols] sums of dy h rstd, or null
 };
 
-// Each workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ... and keeps
-// its sums of dw in registers.
-template <typename E, bool VEC, int WPR, int NC>
-__global__ __launch_bounds__(64 * WPR) void rms_norm_grad_kernel(const NormGradArgs a) {
-    __shared__ float red[WPR];
+// LPR lanes per row, Threads / LPR rows of a workgroup at a time, gridDim.x
+// workgroups in turn.  The sums of dw stay in registers over all rows of a
+// lane and are joined in LDS at the end, so a workgroup has one part.
+template <typename E, bool VEC, int LPR, int NC, int Threads>
+__global__ __launch_bounds__(Threads) void rms_norm_grad_kernel(const NormGradArgs a) {
+    constexpr int RPB = Threads / LPR;
+    __shared__ float red[2][Threads / 64];  // (in turn: a row's sums are read while the next row's are written)
+    __shared__ float joined[RPB > 1 ? RPB / 2 : 1][RPB > 1 ? NC * 8 : 1][RPB > 1 ? LPR : 1];
     using T = typename E::T;
-    const int t = threadIdx.x;
+    const int t = threadIdx.x % LPR, sub = threadIdx.x / LPR;
     float dw[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    u32v4 nh[NC], ng[NC], ne[NC];
+    float nr = 0.0f;
+    auto load_row = [&](int64_t row) {
+        if (row >= a.rows) row = a.rows - 1;  // (loaded and not used)
         const size_t base = static_cast<size_t>(row) * a.cols;
-        const float rstd = a.rstd[row];
+        nr = a.rstd[row];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int col = (c * LPR + t) * 8;
+            nh[c] = load_raw<VEC>(static_cast<const T *>(a.h) + base + col, a.cols - col);
+            ng[c] = load_raw<VEC>(static_cast<const T *>(a.dy) + base + col, a.cols - col);
+            if (a.dh) ne[c] = load_raw<VEC>(static_cast<const T *>(a.dh) + base + col, a.cols - col);
+        }
+    };
+    load_row(static_cast<int64_t>(blockIdx.x) * RPB + sub);
+    int turn = 0;
+    // (the same number of steps for every row of the workgroup: a barrier may be inside)
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * RPB;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * RPB; first < a.rows; first += stride, turn ^= 1) {
+        const int64_t row = first + sub;
+        const bool here = row < a.rows;
+        const size_t base = static_cast<size_t>(row) * a.cols;
+        const float rstd = nr;
         float h[NC][8], g[NC][8];
+        u32v4 e[NC];
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int col = (c * 64 * WPR + t) * 8;
+            const int col = (c * LPR + t) * 8;
             float w[8];
-            load8<E, VEC>(static_cast<const T *>(a.h) + base + col, a.cols - col, h[c]);
-            load8<E, VEC>(static_cast<const T *>(a.dy) + base + col, a.cols - col, g[c]);
+            unpack<E>(nh[c], h[c]);
+            unpack<E>(ng[c], g[c]);
+            e[c] = ne[c];
             load_weight<E, VEC>(a.w, a.w_f32, col, a.cols, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 h[c][i] *= rstd;
-                dw[c][i] += g[c][i] * h[c][i];
+                if (here) dw[c][i] += g[c][i] * h[c][i];
                 g[c][i] *= w[i];
                 sum += g[c][i] * h[c][i];
             }
         }
-        sum = row_sum<WPR>(sum, red);
-        if constexpr (WPR > 1) __syncthreads();  // red is free again
+        // the next row is on its way while this one is finished
+        if (first + stride < a.rows) load_row(first + stride + sub);
+        sum = row_sum<LPR>(sum, red[turn]);
         const float mean = sum / static_cast<float>(a.cols);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int col = (c * 64 * WPR + t) * 8;
+            const int col = (c * LPR + t) * 8;
             float d[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] = rstd * (g[c][i] - h[c][i] * mean);
             if (a.dh) {
-                float e[8];
-                load8<E, VEC>(static_cast<const T *>(a.dh) + base + col, a.cols - col, e);
+                float v[8];
+                unpack<E>(e[c], v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] += e[i];
+                for (int i = 0; i < 8; ++i) d[i] += v[i];
             }
-            if (a.dx) store8<E, VEC>(static_cast<T *>(a.dx) + base + col, a.cols - col, d);
+            if (a.dx && here) store8<E, VEC>(static_cast<T *>(a.dx) + base + col, a.cols - col, d);
         }
     }
-    if (a.part) {
+    if (!a.part) return;
+#pragma unroll
+    for (int half = RPB / 2; half > 0; half >>= 1) {
+        if (sub >= half && sub < 2 * half) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) joined[sub - half][c * 8 + i][t] = dw[c][i];
+        }
+        __syncthreads();
+        if (sub < half) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dw[c][i] += joined[sub][c * 8 + i][t];
+        }
+        __syncthreads();
+    }
+    if (sub == 0) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int col = (c * 64 * WPR + t) * 8;
+            const int col = (c * LPR + t) * 8;
             store8<F32, VEC>(a.part + static_cast<size_t>(blockIdx.x) * a.cols + col, a.cols - col, dw[c]);
         }
     }
 }
 
-// dw[c] = Σ_p part[p][c], p in order within each of 16 strips, the strips in order.
+// dw[c] = Σ_p part[p][c]: 64 strips of p, each in order, then eight by eight.
+// 16 columns per workgroup, so that 4096 columns use every CU.
 __global__ __launch_bounds__(1024) void norm_dw_finish_kernel(const float *__restrict__ part, int parts, int cols,
                                                               float *__restrict__ dw) {
-    __shared__ float s[16][65];
-    const int c = threadIdx.x & 63, strip = threadIdx.x >> 6;
-    const int col = blockIdx.x * 64 + c;
-    const int per = (parts + 15) / 16, lo = strip * per, hi = lo + per < parts ? lo + per : parts;
+    __shared__ float s[64][17];
+    const int c = threadIdx.x & 15, strip = threadIdx.x >> 4;
+    const int col = blockIdx.x * 16 + c;
+    const int per = (parts + 63) / 64, lo = strip * per, hi = lo + per < parts ? lo + per : parts;
     float v = 0.0f;
-    if (col < cols)
+    if (col < cols) {
+#pragma unroll 8
         for (int p = lo; p < hi; ++p) v += part[static_cast<size_t>(p) * cols + col];
+    }
     s[strip][c] = v;
     __syncthreads();
+    if (strip < 8) {
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += s[strip * 8 + i][c];
+    }
+    __syncthreads();
+    if (strip < 8) s[strip][c] = v;
+    __syncthreads();
     if (strip == 0 && col < cols) {
-        for (int i = 1; i < 16; ++i) v += s[i][c];
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += s[i][c];
         dw[col] = v;
     }
 }
 
 constexpr int kNormMaxCols = 32768;
 
-// (waves per row, chunks per lane) of a width: one wave up to 1024 columns,
-// four up to 8192, sixteen beyond.
+// f(lanes per row, chunks per lane) for a width: a lane holds one or two
+// chunks of 16 bytes (four from 16384 columns on).  Two of 512 lanes instead
+// of four of 256 at 4096 x 8192: gradient 58 instead of 72 us; a
+// row of 256 columns on 32 lanes instead of 64 at 65536 rows: 32 instead of 54.
+template <int L>
+using Int = std::integral_constant<int, L>;
 template <typename F>
 int by_width(int cols, F f) {
-    if (cols <= 512) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-    if (cols <= 1024) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
-    if (cols <= 2048) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-    if (cols <= 4096) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-    if (cols <= 8192) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
-    if (cols <= 16384) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-    return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+    if (cols <= 128) return f(Int<16>{}, Int<1>{});
+    if (cols <= 256) return f(Int<32>{}, Int<1>{});
+    if (cols <= 512) return f(Int<64>{}, Int<1>{});
+    if (cols <= 1024) return f(Int<64>{}, Int<2>{});
+    if (cols <= 2048) return f(Int<256>{}, Int<1>{});
+    if (cols <= 4096) return f(Int<256>{}, Int<2>{});
+    if (cols <= 8192) return f(Int<512>{}, Int<8192 / 8 / 512>{});
+    if (cols <= 16384) return f(Int<1024>{}, Int<16384 / 8 / 1024>{});
+    return f(Int<1024>{}, Int<4>{});
 }
 
 template <typename E, bool MX>
 int launch_norm(const NormArgs &a, hipStream_t s) {
-    return by_width(a.cols, [&](auto wpr, auto nc) {
-        constexpr int WPR = decltype(wpr)::value, NC = decltype(nc)::value;
-        constexpr int RPB = WPR >= 4 ? 1 : 4 / WPR;
-        const dim3 grid(static_cast<uint32_t>((a.rows + RPB - 1) / RPB)), block(WPR > 4 ? 64 * WPR : 256);
-        if (a.cols % 8 == 0) launch_kernel(rms_norm_kernel<E, MX, true, WPR, NC>, grid, block, 0, s, a);
-        else launch_kernel(rms_norm_kernel<E, MX, false, WPR, NC>, grid, block, 0, s, a);
+    return by_width(a.cols, [&](auto lpr, auto nc) {
+        constexpr int LPR = decltype(lpr)::value, NC = decltype(nc)::value;
+        constexpr int Threads = LPR > 256 ? LPR : 256, RPB = Threads / LPR;
+        const dim3 grid(static_cast<uint32_t>((a.rows + RPB - 1) / RPB)), block(Threads);
+        if (a.cols % 8 == 0) launch_kernel(rms_norm_kernel<E, MX, true, LPR, NC>, grid, block, 0, s, a);
+        else launch_kernel(rms_norm_kernel<E, MX, false, LPR, NC>, grid, block, 0, s, a);
         return static_cast<int>(hipGetLastError());
     });
 }
 
-// Workgroups of the gradient kernel (about as many as stay resident), each
-// with its row of dw partial sums.
+// Threads of a gradient workgroup: as many rows at a time, and so as few parts
+// of dw, as registers allow (two chunks at 1024 threads spill: 8192 x 4096 84
+// instead of 57 us; 256 threads and 512 workgroups: 60 us).
+constexpr int grad_threads(int lpr, int nc) { return nc == 1 ? 1024 : lpr > 512 ? lpr : 512; }
+
+// Workgroups of the gradient kernel, one per CU, each with its part of dw
+// (two per CU at 8192 x 4096: 61 us).
 int norm_grad_parts(int rows, int cols) {
-    const int most = cols <= 1024 ? 2048 : cols <= 8192 ? 512 : 256;
-    return rows < most ? rows : most;
+    return by_width(cols, [&](auto lpr, auto nc) {
+        constexpr int RPB = grad_threads(decltype(lpr)::value, decltype(nc)::value) / decltype(lpr)::value;
+        const int need = (rows + RPB - 1) / RPB;
+        return need < 256 ? need : 256;
+    });
 }
 
 template <typename E>
 int launch_norm_grad(const NormGradArgs &a, hipStream_t s) {
-    return by_width(a.cols, [&](auto wpr, auto nc) {
-        constexpr int WPR = decltype(wpr)::value, NC = decltype(nc)::value;
-        const dim3 grid(static_cast<uint32_t>(norm_grad_parts(a.rows, a.cols))), block(64 * WPR);
-        if (a.cols % 8 == 0) launch_kernel(rms_norm_grad_kernel<E, true, WPR, NC>, grid, block, 0, s, a);
-        else launch_kernel(rms_norm_grad_kernel<E, false, WPR, NC>, grid, block, 0, s, a);
+    return by_width(a.cols, [&](auto lpr, auto nc) {
+        constexpr int LPR = decltype(lpr)::value, NC = decltype(nc)::value, Threads = grad_threads(LPR, NC);
+        const dim3 grid(static_cast<uint32_t>(norm_grad_parts(a.rows, a.cols))), block(Threads);
+        if (a.cols % 8 == 0) launch_kernel(rms_norm_grad_kernel<E, true, LPR, NC, Threads>, grid, block, 0, s, a);
+        else launch_kernel(rms_norm_grad_kernel<E, false, LPR, NC, Threads>, grid, block, 0, s, a);
         return static_cast<int>(hipGetLastError());
     });
 }
@@ -311,7 +418,7 @@ extern "C" dbf_status_t dbf_rms_norm_backward(const void *dy, const void *h, con
         if (e != 0) return DBF_ERR_HIP;
     }
     if (dweight) {  // (no rows: zeros)
-        launch_kernel(norm_dw_finish_kernel, dim3((cols + 63) / 64), dim3(1024), 0, stream,
+        launch_kernel(norm_dw_finish_kernel, dim3((cols + 15) / 16), dim3(1024), 0, stream,
                       static_cast<const float *>(workspace), rows > 0 ? norm_grad_parts(rows, cols) : 0, cols, dweight);
         if (hipGetLastError() != hipSuccess) return DBF_ERR_HIP;
     }

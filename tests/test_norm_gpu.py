@@ -3,8 +3,8 @@
 Tolerances, in units of the compared value: a row's sum of squares is a sum of
 non-negative fp32 terms, at most 32 of a lane in a row, 6 over the wave and 16
 over the waves: relative error at most 56 * 2^-24 < 2^-18, halved by the root;
-with the root, the division and two products: below 2^-18.  Then half a step
-of the output's type.
+with the root, the division and two products: below 2^-18.  (Where the joins
+are in fp64 it is less.)  Then half a step of the output's type.
 
 Every case prints its name before it touches the GPU.
 """
@@ -116,6 +116,33 @@ def test_backward(gpu, rows, cols, name):
             assert np.all(np.abs(dwg.double().cpu().numpy() - dw) <= (n_add + 3) * 2.0 ** -24 * mag + 1e-45)
         again = dbf.rms_norm_backward(dy, h, w, rd, dh=dh)
         assert same_bits(again[0], dx) and same_bits(again[1], dwg)
+
+
+@pytest.mark.parametrize("rows,cols", [(16500, 120), (8300, 256), (4200, 512), (2100, 1000), (1100, 2048), (531, 4096),
+                                       (300, 8192), (257, 16384)])
+def test_backward_many_rows(gpu, rows, cols):
+    """More rows than the workgroups hold at a time, the last step incomplete (fp64 on the GPU; the tolerances of
+    test_backward).  dweight: a lane adds at most rows / 256 rows, then 6 joins and 4 + 16 additions of parts."""
+    import torch
+    _say(f"norm backward many rows {rows}x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    h = torch.randn((rows, cols), generator=g, device="cuda").bfloat16()
+    dy = (0.1 * torch.randn((rows, cols), generator=g, device="cuda")).bfloat16()
+    dh = (0.1 * torch.randn((rows, cols), generator=g, device="cuda")).bfloat16()
+    w = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).bfloat16()
+    rstd = (h.double().square().mean(dim=1) + 1e-5).rsqrt().float()
+    dx, dw = dbf.rms_norm_backward(dy, h, w, rstd, dh=dh)
+    r = rstd.double()[:, None]
+    xh, gw = h.double() * r, dy.double() * w.double()
+    want = r * (gw - xh * (gw * xh).mean(dim=1, keepdim=True)) + dh.double()
+    part = r * (gw.abs() + xh.abs() * (gw * xh).abs().mean(dim=1, keepdim=True))
+    err = REL * part + 2.0 ** -23 * want.abs()
+    assert bool(((dx.double() - want).abs() <= half_step("bf16") * (want.abs() + err) + err + tiny("bf16")).all())
+    mag = (dy.double() * xh).abs().sum(dim=0)
+    bound = (rows / 256 + 26 + 3) * 2.0 ** -24 * mag
+    assert bool(((dw.double() - (dy.double() * xh).sum(dim=0)).abs() <= bound).all())
+    again = dbf.rms_norm_backward(dy, h, w, rstd, dh=dh)
+    assert same_bits(again[0], dx) and same_bits(again[1], dw)
 
 
 def test_gradient_against_differences(gpu):
