@@ -418,10 +418,15 @@ def dbf_timing_read(h: int) -> Dict[str, Dict[str, float]]:
 _TYPE_NAMES = {"e4m3": DBF_TYPE_E4M3, "e2m1": DBF_TYPE_E2M1}
 
 
+_TYPE_CODES: Dict[object, int] = {}
+
+
 def _type_of(dtype) -> int:
     """The library's code of a torch dtype (-1: none)."""
-    import torch
-    return {torch.float16: DBF_TYPE_F16, torch.bfloat16: DBF_TYPE_BF16, torch.float32: DBF_TYPE_F32}.get(dtype, -1)
+    if not _TYPE_CODES:
+        import torch
+        _TYPE_CODES.update({torch.float16: DBF_TYPE_F16, torch.bfloat16: DBF_TYPE_BF16, torch.float32: DBF_TYPE_F32})
+    return _TYPE_CODES.get(dtype, -1)
 
 
 def _block_type(fmt: str) -> int:
@@ -430,15 +435,20 @@ def _block_type(fmt: str) -> int:
     return _TYPE_NAMES[fmt]
 
 
-def _current_stream(t) -> int:
-    import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _call(where: str, t, *args) -> None:
+    """lib().<where>(*args, stream) on t's device and its current stream.
 
-
-def _on_device(t):
-    """Context in which t's device is the current one."""
+    (The raw stream query takes 0.1 us of the host's time, a Stream object 1 to
+    2; switching to the device that is current already another 1.)
+    """
     import torch
-    return torch.cuda.device(t.device)
+    index = t.device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call(where, t, *args)
+    status = getattr(_lib or lib(), where)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != DBF_OK:
+        raise DbfError(status, where)
 
 
 class MxTensor:
@@ -484,19 +494,20 @@ class MxTensor:
         if t < 0:
             raise ValueError("dtype must be float32, float16 or bfloat16")
         out = torch.empty(self.shape, dtype=dtype, device=self.device)
-        with _on_device(out):
-            _check(lib().dbf_mx_dequantize(self.codes.data_ptr(), self.scales.data_ptr(), _TYPE_NAMES[self.fmt],
-                                           out.shape[0], self.cols, out.data_ptr(), t, _current_stream(out)),
-                   "dbf_mx_dequantize")
+        _call("dbf_mx_dequantize", out, self.codes.data_ptr(), self.scales.data_ptr(), _TYPE_NAMES[self.fmt],
+              out.shape[0], self.cols, out.data_ptr(), t)
         return out
 
 
-def _empty_blocks(rows: int, cols: int, fmt: str, device) -> MxTensor:
+def _empty_blocks(rows: int, cols: int, fmt: str, like) -> MxTensor:
+    """Uninitialised blocks on like's device."""
     import torch
     wide = -(-cols // 128) * 128
-    codes = torch.empty((rows, wide if fmt == "e4m3" else wide // 2), dtype=torch.uint8, device=device)
-    scales = torch.empty((rows, wide // 32), dtype=torch.uint8, device=device)
-    return MxTensor(codes, scales, cols, fmt)
+    q = MxTensor.__new__(MxTensor)  # (right by construction: __init__'s checks are for tensors of other origin)
+    q.codes = like.new_empty((rows, wide if fmt == "e4m3" else wide // 2), dtype=torch.uint8)
+    q.scales = like.new_empty((rows, wide // 32), dtype=torch.uint8)
+    q.cols, q.fmt = cols, fmt
+    return q
 
 
 def mx_quantize(x, fmt: str = "e4m3") -> MxTensor:
@@ -505,10 +516,10 @@ def mx_quantize(x, fmt: str = "e4m3") -> MxTensor:
     ft = _block_type(fmt)
     if t < 0 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous() or x.shape[1] < 1:
         raise ValueError("x must be a contiguous 2-D CUDA tensor of float16, bfloat16 or float32")
-    q = _empty_blocks(x.shape[0], x.shape[1], fmt, x.device)
-    with _on_device(x):
-        _check(lib().dbf_mx_quantize(x.data_ptr(), t, x.shape[0], x.shape[1], ft, q.codes.data_ptr(),
-                                     q.scales.data_ptr(), _current_stream(x)), "dbf_mx_quantize")
+    rows, cols = x.shape
+    _check_count(rows, cols)
+    q = _empty_blocks(rows, cols, fmt, x)
+    _call("dbf_mx_quantize", x, x.data_ptr(), t, rows, cols, ft, q.codes.data_ptr(), q.scales.data_ptr())
     return q
 
 
@@ -529,10 +540,16 @@ class RmsNormOutput(NamedTuple):
     rstd: object
 
 
+def _check_count(rows: int, cols: int) -> None:
+    if rows > 0x7fffffff or cols > 0x7fffffff:  # (the C ABI counts in int32)
+        raise ValueError("more than 2^31 - 1 rows or columns")
+
+
 def _check_rows(t, what, like=None):
     import torch
     if t.dtype not in (torch.float16, torch.bfloat16) or not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous 2-D CUDA tensor of float16 or bfloat16")
+    _check_count(*t.shape)
     if like is not None and (t.dtype != like.dtype or t.shape != like.shape or t.device != like.device):
         raise ValueError(f"{what} must match the other rows in shape, type and device")
 
@@ -562,18 +579,16 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, mx: bool = False)
     rows, cols = x.shape
     t = _type_of(x.dtype)
     h = torch.empty_like(x) if residual is not None else x
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    rstd = x.new_empty(rows, dtype=torch.float32)
     if mx:
-        y = _empty_blocks(rows, cols, "e4m3", x.device)
+        y = _empty_blocks(rows, cols, "e4m3", x)
         y_ptr, s_ptr, yt = y.codes.data_ptr(), y.scales.data_ptr(), DBF_TYPE_E4M3
     else:
         y = torch.empty_like(x)
         y_ptr, s_ptr, yt = y.data_ptr(), None, t
-    with _on_device(x):
-        _check(lib().dbf_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(),
-                                  None if weight is None else weight.data_ptr(), t, wt, rows, cols, eps,
-                                  None if residual is None else h.data_ptr(), y_ptr, yt, s_ptr, rstd.data_ptr(),
-                                  _current_stream(x)), "dbf_rms_norm")
+    _call("dbf_rms_norm", x, x.data_ptr(), None if residual is None else residual.data_ptr(),
+          None if weight is None else weight.data_ptr(), t, wt, rows, cols, eps,
+          None if residual is None else h.data_ptr(), y_ptr, yt, s_ptr, rstd.data_ptr())
     return RmsNormOutput(y, h, rstd)
 
 
@@ -590,14 +605,12 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None):
     if rstd.dtype != torch.float32 or tuple(rstd.shape) != (rows,) or not rstd.is_contiguous() or rstd.device != dy.device:
         raise ValueError("rstd must be a contiguous float32 vector with one entry per row, on dy's device")
     dx = torch.empty_like(dy)
-    dw = torch.empty(cols, dtype=torch.float32, device=dy.device)
+    dw = dy.new_empty(cols, dtype=torch.float32)
     nbytes = lib().dbf_rms_norm_backward_workspace(rows, cols)
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dy.device)
-    with _on_device(dy):
-        _check(lib().dbf_rms_norm_backward(dy.data_ptr(), h.data_ptr(), None if weight is None else weight.data_ptr(),
-                                           rstd.data_ptr(), None if dh is None else dh.data_ptr(), _type_of(dy.dtype),
-                                           wt, rows, cols, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes,
-                                           _current_stream(dy)), "dbf_rms_norm_backward")
+    ws = dy.new_empty(max(nbytes, 16), dtype=torch.uint8)
+    _call("dbf_rms_norm_backward", dy, dy.data_ptr(), h.data_ptr(), None if weight is None else weight.data_ptr(),
+          rstd.data_ptr(), None if dh is None else dh.data_ptr(), _type_of(dy.dtype), wt, rows, cols, dx.data_ptr(),
+          dw.data_ptr(), ws.data_ptr(), nbytes)
     return dx, dw
 
 
@@ -671,9 +684,10 @@ class Layer:
         self.k = 0
         self.max_batch = int(max_batch)
         self.act = act
-        with _on_device(W.codes):
+        import torch
+        with torch.cuda.device(W.device):
             self.handle = dbf_mx_pack(self.n, self.m, W.codes.data_ptr(), W.scales.data_ptr(), at, self.max_batch,
-                                      _current_stream(W.codes))
+                                      torch.cuda.current_stream().cuda_stream)
         return self
 
     def _forward_mx(self, x, out, path, out_dtype):
@@ -691,6 +705,7 @@ class Layer:
                 raise ValueError(f"x must be an MxTensor or a contiguous CUDA float16 or bfloat16 tensor of shape "
                                  f"(batch, {self.m})")
             ptr, scales, xt, batch, default = x.data_ptr(), None, _type_of(x.dtype), x.shape[0], x.dtype
+        _check_count(batch, self.m)
         if path == DBF_PATH_DECODE and batch > DECODE_MAX_BATCH:
             raise DbfError(DBF_ERR_INVALID_ARG, "Layer.forward")
         if out is not None:
@@ -700,13 +715,11 @@ class Layer:
         if out_dtype not in (torch.float16, torch.bfloat16):
             raise ValueError("the output is float16 or bfloat16")
         if out is None:
-            out = torch.empty((batch, self.n), dtype=out_dtype, device=x.device)
+            out = (x.codes if isinstance(x, MxTensor) else x).new_empty((batch, self.n), dtype=out_dtype)
         elif (out.shape != (batch, self.n) or out.dtype != out_dtype or not out.is_contiguous()
               or out.device != x.device):
             raise ValueError("out must be a contiguous tensor of shape (batch, n) on x's device")
-        with _on_device(out):
-            _check(lib().dbf_mx_forward(self.handle, ptr, xt, scales, out.data_ptr(), _type_of(out_dtype), batch,
-                                        _current_stream(out)), "dbf_mx_forward")
+        _call("dbf_mx_forward", out, self.handle, ptr, xt, scales, out.data_ptr(), _type_of(out_dtype), batch)
         return out
 
     def info(self) -> Dict[str, int]:
@@ -753,13 +766,12 @@ class Layer:
             if dy.shape[1] != self.n:
                 raise ValueError(f"dy must have {self.n} columns")
             if out is None:
-                out = torch.empty((dy.shape[0], self.m), dtype=dy.dtype, device=dy.device)
+                out = dy.new_empty((dy.shape[0], self.m))
             elif (tuple(out.shape) != (dy.shape[0], self.m) or out.dtype != dy.dtype or not out.is_contiguous()
                   or out.device != dy.device):
                 raise ValueError("out must be a contiguous tensor of shape (batch, m) in dy's type on its device")
-            with _on_device(dy):
-                _check(lib().dbf_mx_backward_data(self.handle, dy.data_ptr(), out.data_ptr(), _type_of(dy.dtype),
-                                                  dy.shape[0], _current_stream(dy)), "dbf_mx_backward_data")
+            _call("dbf_mx_backward_data", dy, self.handle, dy.data_ptr(), out.data_ptr(), _type_of(dy.dtype),
+                  dy.shape[0])
             return out
         self._check_act(dy, self.n, "dy")
         if out is None:

@@ -161,6 +161,15 @@ def test_dequantize_every_code_and_scale(gpu, fmt):
         assert np.array_equal(got, want.to(T(out)).double().numpy(), equal_nan=True), out
 
 
+def test_more_rows_than_the_abi_counts(gpu):
+    torch = _torch()
+    _say("mx 2^31 rows refused")
+    x = torch.empty((2 ** 31, 1), dtype=torch.float16, device="cuda")
+    for call in (lambda: dbf.mx_quantize(x), lambda: dbf.rms_norm(x), lambda: dbf.rms_norm_backward(x, x, None, x)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
 def test_quantize_no_rows(gpu):
     torch = _torch()
     _say("quantize no rows")
