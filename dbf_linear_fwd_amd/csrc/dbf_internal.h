@@ -275,12 +275,10 @@ struct MxWeight {
     int n = 0, m = 0, n_pad = 0, blocks = 0;
 };
 
-// Few rows (batch <= kDecodeMaxBatch, m_pad <= kMxDecodeWidth): y[i] (batch x
-// n_i, y_type) = x w[i]ᵀ for layers that share x, one launch.  x: batch rows of
-// x_type f16 / bf16 (where mx_decode_direct; quantised into `act` blocks), or
-// padded rows of `act` codes (x_type = act) with scales xs.  first and tiles
-// are filled by the launch.
-constexpr int kMxDecodeWidth = 16384;
+// Few rows (mx_decode_takes): y[i] (batch x n_i, y_type) = x w[i]ᵀ for layers
+// that share x, one launch.  x: batch rows of x_type f16 / bf16
+// (mx_decode_quantizes; into `act` blocks), or padded rows of `act` codes
+// (x_type = act) with scales xs.  first and tiles are filled by the launch.
 struct MxDecodeArgs {
     const void *x = nullptr;
     const uint8_t *xs = nullptr;
@@ -291,9 +289,10 @@ struct MxDecodeArgs {
     int first[kMaxGroup] = {};  // first 16-row tile of each layer
     int tiles = 0;
 };
-// Whether 16-bit rows can go into launch_mx_decode as they are: m a multiple
-// of 8, and their blocks fit LDS.
-bool mx_decode_direct(int batch, int m, int act);
+// Whether the kernel for few rows takes a batch (its blocks fit LDS), and
+// whether it quantises 16-bit rows itself.
+bool mx_decode_takes(int batch, int m, int act);
+bool mx_decode_quantizes(int batch, int m);
 int launch_mx_decode(MxDecodeArgs &a, void *stream);
 
 // tiled: scales in 32-row tiles (see MxWeight) instead of rows.

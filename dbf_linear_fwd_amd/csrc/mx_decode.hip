@@ -14,20 +14,21 @@
 // 16 g .. of the first 64 columns and of the second 64.  Its scale byte is
 // block g's either way.
 //
-// f16 and bf16 rows are quantised by the kernel itself, with no pass or launch
-// of their own, while the first weight tile is on its way: all threads of a
-// workgroup together, two lanes per block, codes and scales into LDS, where
-// the operands are read for every tile.  (Quantised by each wave in its
-// operand registers, the lanes of absent batch rows repeat the work: batch 1,
-// 4096 x 14336: 13.1 instead of 10.3 us.)  Blocks that do not fit LDS (16 rows
-// from 8912 columns on, e4m3) are quantised in a launch of their own and read
-// from L2 per tile.
+// x goes through LDS.  Up to 65536 values of 16 bits are quantised on the way,
+// without a launch of their own, while the first weight tile is coming: all
+// threads of a workgroup together, two lanes per block.  (By each wave in its
+// operand registers, where the lanes of absent batch rows repeat the work:
+// batch 1, 4096 x 14336: 13.1 instead of 10.3 us.)  More of them are better
+// quantised once than in every workgroup, at 2.5 us for the launch: 16 x 8192
+// for 8192 rows 16.1 and 16.8 us, 16 x 14336 in e2m1 for 4096 rows 14.9 and
+// 21.8; 16 x 4096 for 4096 rows 8.7 and 7.8.
+// Batches whose blocks do not fit LDS go to the tiled product (read from L2
+// for every tile, 16 x 14336 for 4096 rows took 17 us, the tiles 13).
 //
-// Graph replays with weights from HBM, f16 to e4m3: 14336 x 4096 at batch 1
-// 8.7 us (3.6 TB/s; a large copy reaches 4.6), batch 16 13.4 us, of which
-// quantising 16 rows in every workgroup is 2 us; 4096 x 14336 at batch 1
-// 10.3 us (one tile per workgroup: nothing to overlap with x's way to LDS);
-// 4096 x 4096 5.4 us; 1024 x 4096 4.0 us.
+// Graph replays with weights from HBM: 14336 x 4096 at batch 1 8.7 us (3.6
+// TB/s; a large copy reaches 4.6), batch 16, quantising included, 13; 4096 x
+// 14336 at batch 1 10.3 us (one tile per workgroup: nothing to overlap with
+// x's way to LDS); 4096 x 4096 5.4 us; 1024 x 4096 4.0 us.
 
 #include "mx_tile.h"
 
@@ -100,6 +101,7 @@ __device__ __forceinline__ u32v4 codes16(u32v4 a, u32v4 b, float sc) {
 }
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
+
 // x in LDS: rows of codes and of scale bytes, their pitches off a multiple of
 // the banks so that the rows of an operand read fall on different ones.
 template <int ACT>
@@ -115,11 +117,11 @@ constexpr size_t kSumBytes = 2 * kWaves * 64 * 16;
 constexpr size_t kMaxXBytes = 160 * 1024 - kSumBytes;
 
 // XT: type of x's rows (f16, bf16) or kBlocks; SPW: steps of 128 columns of a
-// wave at most; LDSX: x goes through LDS (blocks that do not fit it are read
-// from memory for every tile).
-template <int XT, int ACT, typename E, int SPW, bool LDSX>
+// wave at most.
+template <int XT, int ACT, typename E, int SPW>
 __global__ __launch_bounds__(kThreads, 4) void mx_decode_kernel(const MxDecodeArgs a) {
-    constexpr int kAhead = SPW > 8 ? 2 : 4;  // units of a thread in flight while x goes to LDS (registers for two workgroups per CU)
+    // units of a thread in flight while x goes to LDS (registers for two workgroups per CU)
+    constexpr int kAhead = SPW > 8 ? 2 : 4;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     f32x4 *red = reinterpret_cast<f32x4 *>(lds);  // [2][kWaves][64]
     char *xl = lds + kSumBytes;
@@ -151,67 +153,64 @@ __global__ __launch_bounds__(kThreads, 4) void mx_decode_kernel(const MxDecodeAr
     load_tile(t);
 
     using X = XLds<ACT>;
-    const int cp = LDSX ? X::code_pitch(blocks) : X::row_bytes(blocks), sp = LDSX ? X::scale_pitch(blocks) : blocks;
-    if constexpr (LDSX) {
-        char *xsl = xl + a.batch * cp;
-        if constexpr (XT == kBlocks) {
-            const int per = X::row_bytes(blocks) / 16, all = a.batch * per;
-            for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kThreads) {
-                u32v4 v[kAhead];
+    const int cp = X::code_pitch(blocks), sp = X::scale_pitch(blocks);
+    char *xsl = xl + a.batch * cp;
+    if constexpr (XT == kBlocks) {
+        const int per = X::row_bytes(blocks) / 16, all = a.batch * per;
+        for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kThreads) {
+            u32v4 v[kAhead];
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (const int i = i0 + j * kThreads; i < all)
-                        v[j] = *reinterpret_cast<const u32v4 *>(static_cast<const uint8_t *>(a.x) + static_cast<size_t>(i) * 16);
+            for (int j = 0; j < kAhead; ++j)
+                if (const int i = i0 + j * kThreads; i < all)
+                    v[j] = *reinterpret_cast<const u32v4 *>(static_cast<const uint8_t *>(a.x) + static_cast<size_t>(i) * 16);
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (const int i = i0 + j * kThreads; i < all) {
-                        const int row = i / per, q = i - row * per;
-                        *reinterpret_cast<u32v4 *>(xl + row * cp + q * 16) = v[j];
-                    }
-            }
-            for (int i = threadIdx.x; i < a.batch * steps; i += kThreads) {
-                const int row = i / steps, q = i - row * steps;
-                *reinterpret_cast<uint32_t *>(xsl + row * sp + q * 4) = reinterpret_cast<const uint32_t *>(a.xs)[i];
-            }
-        } else {
-            const int m = a.w[0].m, per = blocks * 2, all = a.batch * per;  // units of 16 columns
-            mx_saturate(true);
-            for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kThreads) {  // (whole pairs of lanes: per is even)
-                u32v4 lo[kAhead], hi[kAhead];
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const int i = i0 + j * kThreads, row = i / per, col = (i - row * per) * 16;
-                    const uint16_t *src = static_cast<const uint16_t *>(a.x) + static_cast<size_t>(row) * m + col;
-                    lo[j] = hi[j] = u32v4{0u, 0u, 0u, 0u};  // columns past m (a multiple of 8) are zeros
-                    if (i < all && col < m) lo[j] = *reinterpret_cast<const u32v4 *>(src);
-                    if (i < all && col + 8 < m) hi[j] = *reinterpret_cast<const u32v4 *>(src + 8);
+            for (int j = 0; j < kAhead; ++j)
+                if (const int i = i0 + j * kThreads; i < all) {
+                    const int row = i / per, q = i - row * per;
+                    *reinterpret_cast<u32v4 *>(xl + row * cp + q * 16) = v[j];
                 }
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const int i = i0 + j * kThreads, row = i / per, q = i - row * per, col = q * 16;
-                    if (i >= all) break;
-                    uint32_t mx = float_bits<XT>(absmax(lo[j], hi[j]));
-                    const uint32_t other = __builtin_amdgcn_mov_dpp(mx, 0xB1, 0xf, 0xf, true);  // the pair's other lane
-                    mx = mx > other ? mx : other;
-                    const uint32_t s = mx_scale_byte<ACT>(mx);
-                    const u32v4 r = codes16<XT, ACT>(lo[j], hi[j], mx_scale_value(s));
-                    char *dst = xl + row * cp + col / (ACT == DBF_TYPE_E4M3 ? 1 : 2);
-                    if constexpr (ACT == DBF_TYPE_E4M3) *reinterpret_cast<u32v4 *>(dst) = r;
-                    else *reinterpret_cast<u32v2 *>(dst) = u32v2{r[0], r[1]};
-                    if ((q & 1) == 0) xsl[row * sp + (q >> 1)] = static_cast<char>(s);
-                }
-            }
-            mx_saturate(false);
         }
-        __syncthreads();
+        for (int i = threadIdx.x; i < a.batch * steps; i += kThreads) {
+            const int row = i / steps, q = i - row * steps;
+            *reinterpret_cast<uint32_t *>(xsl + row * sp + q * 4) = reinterpret_cast<const uint32_t *>(a.xs)[i];
+        }
+    } else {
+        const int m = a.w[0].m, per = blocks * 2, all = a.batch * per;  // units of 16 columns
+        mx_saturate(true);
+        for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kThreads) {  // (whole pairs of lanes: per is even)
+            u32v4 lo[kAhead], hi[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = i0 + j * kThreads, row = i / per, col = (i - row * per) * 16;
+                const uint16_t *src = static_cast<const uint16_t *>(a.x) + static_cast<size_t>(row) * m + col;
+                lo[j] = hi[j] = u32v4{0u, 0u, 0u, 0u};  // columns past m (a multiple of 8) are zeros
+                if (i < all && col < m) lo[j] = *reinterpret_cast<const u32v4 *>(src);
+                if (i < all && col + 8 < m) hi[j] = *reinterpret_cast<const u32v4 *>(src + 8);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = i0 + j * kThreads, row = i / per, q = i - row * per, col = q * 16;
+                if (i >= all) break;
+                uint32_t mx = float_bits<XT>(absmax(lo[j], hi[j]));
+                const uint32_t other = __builtin_amdgcn_mov_dpp(mx, 0xB1, 0xf, 0xf, true);  // the pair's other lane
+                mx = mx > other ? mx : other;
+                const uint32_t s = mx_scale_byte<ACT>(mx);
+                const u32v4 r = codes16<XT, ACT>(lo[j], hi[j], mx_scale_value(s));
+                char *dst = xl + row * cp + col / (ACT == DBF_TYPE_E4M3 ? 1 : 2);
+                if constexpr (ACT == DBF_TYPE_E4M3) *reinterpret_cast<u32v4 *>(dst) = r;
+                else *reinterpret_cast<u32v2 *>(dst) = u32v2{r[0], r[1]};
+                if ((q & 1) == 0) xsl[row * sp + (q >> 1)] = static_cast<char>(s);
+            }
+        }
+        mx_saturate(false);
     }
+    __syncthreads();
 
     // operand and scale byte of this lane's row of x (rows past the batch: any, not written)
     const int xrow = min(c, a.batch - 1);
     constexpr int Step = ACT == DBF_TYPE_E4M3 ? 128 : 64;
-    const char *xc = (LDSX ? xl : static_cast<const char *>(a.x)) + static_cast<size_t>(xrow) * cp + k0 * Step + 16 * g;
-    const uint8_t *xs = (LDSX ? reinterpret_cast<const uint8_t *>(xl) + a.batch * cp : a.xs) +
-                        static_cast<size_t>(xrow) * sp + k0 * 4 + g;
+    const char *xc = xl + xrow * cp + k0 * Step + 16 * g;
+    const uint8_t *xs = reinterpret_cast<const uint8_t *>(xsl) + xrow * sp + k0 * 4 + g;
 
     for (int it = 0; t < a.tiles; ++it) {
         f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
@@ -256,7 +255,7 @@ __global__ __launch_bounds__(kThreads, 4) void mx_decode_kernel(const MxDecodeAr
     }
 }
 
-template <int XT, int ACT, typename E, int SPW, bool LDSX>
+template <int XT, int ACT, typename E, int SPW>
 void launch(MxDecodeArgs &a, hipStream_t s) {
     static std::atomic<uint64_t> asked{0};
     a.tiles = 0;
@@ -264,45 +263,42 @@ void launch(MxDecodeArgs &a, hipStream_t s) {
         a.first[i] = a.tiles;
         a.tiles += (a.w[i].n + 15) / 16;
     }
-    const size_t bytes = kSumBytes + (LDSX ? XLds<ACT>::bytes(a.batch, a.w[0].blocks) : 0);
+    const size_t bytes = kSumBytes + XLds<ACT>::bytes(a.batch, a.w[0].blocks);
     // One resident wave of workgroups, two per CU where LDS holds both
     // (14336 x 4096, batch 1: 8.7 us, one per CU 10.1).
     const int wgs = bytes <= 80 * 1024 ? 512 : 256;
     const int per = (a.tiles + wgs - 1) / wgs;  // tiles of a workgroup
-    auto kernel = mx_decode_kernel<XT, ACT, E, SPW, LDSX>;
+    auto kernel = mx_decode_kernel<XT, ACT, E, SPW>;
     if (bytes > 65536) allow_lds(kernel, 160 * 1024, asked);
     launch_kernel(kernel, dim3((a.tiles + per - 1) / per), dim3(kThreads), bytes, s, a);
 }
 
-template <int XT, int ACT, typename E, bool LDSX>
+template <int XT, int ACT, typename E>
 void choose(MxDecodeArgs &a, hipStream_t s) {
     const int spw = (a.w[0].blocks / 4 + kWaves - 1) / kWaves;
-    if (spw <= 4) launch<XT, ACT, E, 4, LDSX>(a, s);
-    else if (spw <= 8) launch<XT, ACT, E, 8, LDSX>(a, s);
-    else launch<XT, ACT, E, 16, LDSX>(a, s);
+    if (spw <= 4) launch<XT, ACT, E, 4>(a, s);
+    else if (spw <= 8) launch<XT, ACT, E, 8>(a, s);
+    else launch<XT, ACT, E, 16>(a, s);
 }
 
 }  // namespace
 
-bool mx_decode_direct(int batch, int m, int act) {
+bool mx_decode_takes(int batch, int m, int act) {
     const int blocks = round_up_int(m, 128) / 32;
-    return m % 8 == 0 && (act == DBF_TYPE_E4M3 ? XLds<DBF_TYPE_E4M3>::bytes(batch, blocks) : XLds<DBF_TYPE_E2M1>::bytes(batch, blocks)) <= kMaxXBytes;
+    return batch <= kDecodeMaxBatch && m <= 128 * 16 * kWaves &&
+           (act == DBF_TYPE_E4M3 ? XLds<DBF_TYPE_E4M3>::bytes(batch, blocks)
+                                 : XLds<DBF_TYPE_E2M1>::bytes(batch, blocks)) <= kMaxXBytes;
 }
+
+bool mx_decode_quantizes(int batch, int m) { return m % 8 == 0 && static_cast<int64_t>(batch) * m <= 65536; }
 
 int launch_mx_decode(MxDecodeArgs &a, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!mx_decode_takes(a.batch, a.w[0].m, a.act)) return static_cast<int>(hipErrorInvalidValue);
     auto types = [&](auto xt, auto act) {
         constexpr int XT = decltype(xt)::value, ACT = decltype(act)::value;
-        const bool fits = XLds<ACT>::bytes(a.batch, a.w[0].blocks) <= kMaxXBytes;
-        auto go = [&](auto e) {
-            using E = decltype(e);
-            if constexpr (XT == kBlocks) {
-                if (!fits) return choose<XT, ACT, E, false>(a, s);
-            }
-            choose<XT, ACT, E, true>(a, s);
-        };
-        if (a.y_type == DBF_TYPE_F16) go(F16{});
-        else go(BF16{});
+        if (a.y_type == DBF_TYPE_F16) choose<XT, ACT, F16>(a, s);
+        else choose<XT, ACT, BF16>(a, s);
     };
     using E4 = std::integral_constant<int, DBF_TYPE_E4M3>;
     using E2 = std::integral_constant<int, DBF_TYPE_E2M1>;
@@ -310,8 +306,6 @@ int launch_mx_decode(MxDecodeArgs &a, void *stream) {
         if (a.act == DBF_TYPE_E4M3) types(xt, E4{});
         else types(xt, E2{});
     };
-    const bool real = a.x_type == DBF_TYPE_F16 || a.x_type == DBF_TYPE_BF16;
-    if (real && !mx_decode_direct(a.batch, a.w[0].m, a.act)) return static_cast<int>(hipErrorInvalidValue);
     if (a.x_type == DBF_TYPE_F16) rows(std::integral_constant<int, DBF_TYPE_F16>{});
     else if (a.x_type == DBF_TYPE_BF16) rows(std::integral_constant<int, DBF_TYPE_BF16>{});
     else rows(std::integral_constant<int, kBlocks>{});

@@ -296,19 +296,20 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a)
         store_part<C>(part_at<C>(a.part, split, T, tile, wave, lane), acc);
         return;
     }
-    static_assert(static_cast<size_t>(C::Waves) * 32 * (64 * C::NI + 16) <= C::Lds, "a result fits the ring");
+    static_assert(C::Waves * store_bytes<C>() <= C::Lds, "a result fits the ring");
     __syncthreads();  // every wave's last operands have been read
-    store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, m0, n0, wave, lane);
+    store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.y, a.M, a.w.n, m0, n0, wave, lane);
 }
 
-// The K parts of a tile, added in order and stored.
+// The K parts of a tile, added in order and stored; a workgroup is one wave of
+// the product's (a whole tile in one: 17 x 4096, K 14336: 16.7 instead of 15.2 us).
 template <typename C, typename E>
-__global__ __launch_bounds__(C::Threads) void mx_finish_kernel(const MxGemmArgs a) {
+__global__ __launch_bounds__(64) void mx_finish_kernel(const MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x;
+    const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves;
     int bm, bn;
     tile_at(a.grid, tile, bm, bn);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x;
     f32x16 acc[C::MI][C::NI];
     add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
                  a.grid.nsplit, acc);
@@ -321,19 +322,22 @@ namespace {
 
 // ---- choice of the tile and of the K parts
 
-// A tile's cost: microseconds per 128 columns of K with a workgroup alone on
-// its CU's neighbourhood (few tiles) and with all CUs busy (the matrix cores'
-// clock and the L2s are shared), measured at K 4096 and 14336.
+// A tile's cost: microseconds per 128 columns of K with few workgroups and the
+// weight from HBM (a step is then as long as its loads take), and with one on
+// every CU (the matrix cores' clock and the L2s are shared); fitted to 120
+// sizes of 17 to 1024 rows, K 1024 to 14336, where the chosen tile and parts
+// are within 0.3 % of the best on average and within 11 % everywhere.
 struct TileCost {
     int bm, bn;
     float light[2], full[2];  // e4m3, e2m1
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, {1.05f, 0.66f}, {1.48f, 0.98f}},
-    {128, 256, {0.55f, 0.41f}, {0.78f, 0.53f}},
-    {128, 128, {0.36f, 0.27f}, {0.52f, 0.38f}},
-    {64, 128, {0.24f, 0.21f}, {0.34f, 0.27f}},
-    {64, 64, {0.19f, 0.145f}, {0.28f, 0.19f}},
+    {256, 256, {1.30f, 0.95f}, {1.50f, 0.98f}},
+    {128, 256, {0.81f, 0.60f}, {0.78f, 0.53f}},
+    {128, 128, {0.60f, 0.43f}, {0.64f, 0.38f}},
+    {64, 128, {0.36f, 0.30f}, {0.38f, 0.27f}},
+    {64, 64, {0.28f, 0.19f}, {0.28f, 0.19f}},
+    {32, 64, {0.16f, 0.16f}, {0.17f, 0.16f}},
 };
 constexpr int kTileCount = sizeof(kTiles) / sizeof(kTiles[0]);
 constexpr int kCus = 256;
@@ -346,7 +350,8 @@ struct MxPlan {
 // CUs, each a start of 3 us and its steps; K parts add a launch and the
 // traffic of their fp32 sums.  (2048 x 14336, K 4096, e4m3: 256 x 256 tiles
 // 101 us, 128 x 256 116; 2048 x 4096, K 14336: 130 and 87; 64 x 4096,
-// K 14336: four parts 13, one 25.)
+// K 14336: four parts 13, one 25; 17 x 4096,
+// K 14336, weight from HBM: 32 x 64 in four parts 13, 64 x 64 15.)
 MxPlan mx_plan(int M, int n, int steps, bool x8) {
     MxPlan best;
     float least = 0.0f;
@@ -362,7 +367,7 @@ MxPlan mx_plan(int M, int n, int steps, bool x8) {
             const float rounds = wgs <= kCus ? 1.0f : t < 2 ? static_cast<float>((tiles * sp + kCus - 1) / kCus) : wgs / kCus;
             const float step = c.light[f] + (c.full[f] - c.light[f]) * load;
             float us = rounds * (3.0f + static_cast<float>((steps + sp - 1) / sp) * step);
-            if (sp > 1) us += 3.5f + wgs * c.bm * c.bn * 8.0f * 3e-7f;
+            if (sp > 1) us += 2.1f + wgs * c.bm * c.bn * 8.0f * 3.7e-7f;
             if (least == 0.0f || us < least) {
                 least = us;
                 best.tile = t;
@@ -385,23 +390,21 @@ template <int FMT>
 struct TileOf<FMT, 3> { using C = MxTile<FMT, 2, 1, 1, 4, FMT == DBF_TYPE_E4M3 ? 8 : 6>; };
 template <int FMT>
 struct TileOf<FMT, 4> { using C = MxTile<FMT, 1, 1, 2, 2, FMT == DBF_TYPE_E4M3 ? 8 : 6>; };
+template <int FMT>
+struct TileOf<FMT, 5> { using C = MxTile<FMT, 1, 1, 1, 2, FMT == DBF_TYPE_E4M3 ? 16 : 12>; };
 
 template <typename C, typename E>
 void launch_gemm(MxGemmArgs &a, hipStream_t s) {
-    constexpr size_t kFinishLds = static_cast<size_t>(C::Waves) * 32 * (64 * C::NI + 16);
     auto product = mx_gemm_kernel<C, E>;
     auto finish = mx_finish_kernel<C, E>;
-    static std::atomic<uint64_t> lds_product{0}, lds_finish{0};
+    static std::atomic<uint64_t> lds_product{0};
     TileGrid &t = a.grid;
     t.nbm = (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.n + C::BN - 1) / C::BN;
     t.group = t.nbm < 4 ? t.nbm : 4;
     if constexpr (C::Lds > 65536) allow_lds(product, C::Lds, lds_product);
     launch_kernel(product, dim3(t.nbm * t.nbn * t.nsplit), dim3(C::Threads), C::Lds, s, a);
-    if (a.part) {
-        if constexpr (kFinishLds > 65536) allow_lds(finish, kFinishLds, lds_finish);
-        launch_kernel(finish, dim3(t.nbm * t.nbn), dim3(C::Threads), kFinishLds, s, a);
-    }
+    if (a.part) launch_kernel(finish, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
 }
 
 template <int FMT, typename E, int T = 0>

@@ -352,16 +352,16 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
         return;
     }
     scale_columns<C>(acc, a.w, n0, wn);
-    store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, m0, n0, wave, lane);
+    store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.dx, a.M, a.w.m, m0, n0, wave, lane);
 }
 
 template <typename C, typename E>
-__global__ __launch_bounds__(C::Threads) void mx_grad_finish_kernel(const MxGradArgs a) {
+__global__ __launch_bounds__(64) void mx_grad_finish_kernel(const MxGradArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x;
+    const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves;
     int bm, bn;
     tile_at(a.grid, tile, bm, bn);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x;
     f32x16 acc[C::MI][C::NI];
     add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
                  a.grid.nsplit, acc);
@@ -421,8 +421,7 @@ GradPlan grad_plan(int M, int n, int m) {
 
 template <typename C, typename E>
 void launch_grad(MxGradArgs &a, hipStream_t s) {
-    static std::atomic<uint64_t> lds0{0}, lds1{0}, lds2{0};
-    constexpr size_t kFinishLds = static_cast<size_t>(C::Waves) * 32 * (64 * C::NI + 16);
+    static std::atomic<uint64_t> lds0{0}, lds1{0};
     TileGrid &t = a.grid;
     t.nbm = (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.m + C::BN - 1) / C::BN;
@@ -439,8 +438,7 @@ void launch_grad(MxGradArgs &a, hipStream_t s) {
     }
     if (a.part) {
         auto k = mx_grad_finish_kernel<C, E>;
-        if constexpr (kFinishLds > 65536) allow_lds(k, kFinishLds, lds2);
-        launch_kernel(k, dim3(t.nbm * t.nbn), dim3(C::Threads), kFinishLds, s, a);
+        launch_kernel(k, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
     }
 }
 

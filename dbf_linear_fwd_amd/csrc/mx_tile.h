@@ -80,15 +80,18 @@ __device__ __forceinline__ void tile_at(const TileGrid &a, int tile, int &bm, in
 
 // A wave's results to y.  A 32 x 32 result has one row of y per lane, its
 // columns 8 (v / 4) + 4 g + v % 4 in register v; each wave takes them through
-// its own part of LDS into rows of 16-byte stores.  (Stored from the
+// its own part of LDS (store_bytes at `mine`) into rows of 16-byte stores.  (Stored from the
 // registers, two bytes a lane: 106 instead of 101 us, 256 x 256 tiles of
 // 2048 x 14336, K 4096.)
+template <typename C>
+constexpr size_t store_bytes() { return 32 * (64 * C::NI + 16); }
+
 template <typename C, typename E>
-__device__ __forceinline__ void store_tile(char *lds, const f32x16 (&acc)[C::MI][C::NI], void *out, int M,
+__device__ __forceinline__ void store_tile(char *mine, const f32x16 (&acc)[C::MI][C::NI], void *out, int M,
                                            int n, int m0, int n0, int wave, int lane) {
     const int wm = wave / C::WN, wn = wave % C::WN, l32 = lane & 31, g = lane >> 5;
     constexpr int Cols = 32 * C::NI, Pitch = Cols * 2 + 16;  // 16-bit values of a wave's row, bytes
-    char *mine = lds + wave * (32 * Pitch);
+    static_assert(store_bytes<C>() == 32 * Pitch, "");
     uint16_t *y = static_cast<uint16_t *>(out);
     const int c0 = n0 + wn * Cols;
 #pragma unroll
@@ -154,6 +157,7 @@ __device__ __forceinline__ void add_parts(const float *p, size_t plane, int nspl
         for (int f = 0; f < C::NI; ++f)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.0f;
+#pragma unroll C::MI * C::NI == 1 ? 4 : 1
     for (int s = 0; s < nsplit; ++s, p += plane)
 #pragma unroll
         for (int i = 0; i < C::MI; ++i)

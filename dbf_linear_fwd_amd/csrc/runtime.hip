@@ -888,16 +888,11 @@ static dbf::MxWeight mx_weight(const dbf_layer *h) {
     return w;
 }
 
-// Whether a forward is one launch of the few-row kernel.
-static bool mx_few(const dbf_layer *h, int32_t batch) {
-    return batch <= dbf::kDecodeMaxBatch && h->m_pad <= dbf::kMxDecodeWidth;
-}
-
 // One or several layers (same m, same activation format) on the input x of
 // x_type (f16 / bf16 rows, or blocks with x_scales); arguments are checked.
-// Few rows: one launch for all the layers, the 16-bit rows quantised by it
-// where it can; otherwise x is quantised once into the first handle's
-// workspace and each layer's product is a launch (two with K parts).
+// Few rows: one launch for all the layers.  16-bit rows that it does not
+// quantise itself are quantised once into the first handle's workspace.  More
+// rows: a launch per layer (two with K parts).
 static dbf_status_t forward_mx(dbf_layer *const *hs, int count, const void *x, int32_t x_type,
                                const uint8_t *x_scales, void *const *ys, int32_t y_type, int32_t batch,
                                hipStream_t stream) {
@@ -905,8 +900,8 @@ static dbf_status_t forward_mx(dbf_layer *const *hs, int count, const void *x, i
     const bool real = x_type == DBF_TYPE_F16 || x_type == DBF_TYPE_BF16;
     const int act = real ? h->mx_act : x_type;
     const int blocks = h->m_pad / 32;
-    const bool few = mx_few(h, batch);
-    const bool direct = real && few && dbf::mx_decode_direct(batch, h->m, act);
+    const bool few = dbf::mx_decode_takes(batch, h->m, act);
+    const bool direct = real && few && dbf::mx_decode_quantizes(batch, h->m);
     dbf_status_t st = DBF_OK;
     if (real && !direct) {
         st = timed_launch(h, "mx_quantize", stream, [&] {
@@ -1398,7 +1393,7 @@ ScratchPlan plan_scratch(const dbf_layer *h, int32_t batch) {
     if (h->mx) {
         p.xcodes = take(size_t(batch) * dbf_mx_code_bytes(h->m, h->mx_act));
         p.xscales = take(size_t(round_up(batch, 32)) * dbf_mx_scale_bytes(h->m));
-        if (!mx_few(h, batch)) p.split_cap = dbf::mx_product_parts(batch, h->n, h->m_pad / 32, h->mx_act);
+        if (!dbf::mx_decode_takes(batch, h->m, h->mx_act)) p.split_cap = dbf::mx_product_parts(batch, h->n, h->m_pad / 32, h->mx_act);
         p.split = take(sizeof(float) * p.split_cap);
         p.total = off;
         return p;

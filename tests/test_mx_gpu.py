@@ -248,7 +248,11 @@ def _device_products(a, b):
 LARGE = [(1900, 8100, 1030, "f16", "e4m3"), (1900, 8100, 1030, "bf16", "e2m1"), (1900, 4000, 1540, "bf16", "e4m3"),
          (1901, 4003, 1540, "f16", "e2m1"), (1000, 3990, 700, "f16", "e4m3"), (1000, 3990, 700, "bf16", "e2m1"),
          (300, 1000, 4100, "bf16", "e4m3"), (300, 1001, 4100, "f16", "e2m1"), (130, 500, 9000, "f16", "e4m3"),
-         (1900, 8100, 100, "bf16", "e4m3"), (1900, 8100, 200, "f16", "e2m1"), (70, 60, 4096, "f16", "e2m1")]
+         (1900, 8100, 100, "bf16", "e4m3"), (1900, 8100, 200, "f16", "e2m1"), (70, 60, 4096, "f16", "e2m1"), (400, 5001, 1030, "bf16", "e4m3"),
+         (385, 3001, 1030, "f16", "e4m3"), (700, 2003, 700, "bf16", "e2m1"), (300, 2003, 1540, "f16", "e4m3"),
+         (300, 2008, 1540, "bf16", "e2m1"), (300, 1001, 9000, "f16", "e4m3"), (250, 1001, 6000, "bf16", "e2m1"),
+         (65, 1001, 4100, "f16", "e4m3"), (40, 1000, 4100, "bf16", "e2m1"), (17, 2001, 4096, "bf16", "e4m3"),
+         (300, 1000, 14300, "bf16", "e4m3"), (400, 1000, 14300, "f16", "e2m1")]
 
 
 @pytest.mark.parametrize("b,n,m,name,act", LARGE)
