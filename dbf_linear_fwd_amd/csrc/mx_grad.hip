@@ -14,12 +14,15 @@
 // holds the codes exactly down to scales of 2^-28 of the largest; the sums
 // are multiplied by 2^(smax - 13) at the end.
 //
-// 2048 rows, n 14336, m 4096, bf16: 247 us, 0.98 PFLOP/s.  A step of 64 rows
-// of a 256 x 256 tile takes 1.33 us alone and 1.9 with all CUs at work, where
-// its products take 0.91: reading the operands and converting the weight
-// (190 vector instructions a wave and step beside 32 products) fill the rest
-// as far as they do not overlap.  Placed one by one between the products
-// instead of in front of them: 247 instead of 272 us.
+// 2048 rows, n 14336, m 4096, bf16: 243 us, 0.99 PFLOP/s (217 us, 1.1, with
+// gradients of 0.01 in place of full-range values).  A step of 64 rows of a 256
+// x 256 tile takes 1.2 us alone and 1.85 with all CUs at work, where the clock
+// falls to 1.9 GHz and the matrix cores are busy 55 % of the time; converting
+// the weight and reading the operands fill the rest as far as they do not
+// overlap.  Placed one by one between the products instead of in front of
+// them: 247 instead of 272 us.  Half of the weight's conversion beside each of
+// the first two of a step's four groups of products, instead of beside the
+// first: 1.2 instead of 1.33 us a step alone.
 
 #include "mx_tile.h"
 
@@ -63,16 +66,19 @@ struct MxGradArgs {
     float *part;
 };
 
-// The e5m2 bytes of a block's 32 columns.
-__device__ __forceinline__ void block_values(u32v4 codes, int s, int smax, u32v4 &lo, u32v4 &hi) {
-    // the conversion divides by its scale: 2^-(s - smax + 13)
+// What the conversion to e5m2 divides a block's values by: 2^-(s - smax + 13).
+__device__ __forceinline__ float block_scale(int s, int smax) {
     const int e = 127 - kShift + smax - s;
     const uint32_t bits = s == 255 ? 0x7fc00000u : static_cast<uint32_t>(e < 254 ? e : 254) << 23;
-    const float sc = __builtin_bit_cast(float, bits);
-    uint32_t out[8];
+    return __builtin_bit_cast(float, bits);
+}
+
+// The e5m2 bytes of 16 columns of a block.
+__device__ __forceinline__ u32v4 block_values(uint32_t c0, uint32_t c1, float sc) {
+    u32v4 out;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t w = codes[i >> 1];
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = i < 2 ? c0 : c1;
         s16x2 o = {0, 0};
         if (i & 1) {
             o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2), sc, false);
@@ -83,8 +89,7 @@ __device__ __forceinline__ void block_values(u32v4 codes, int s, int smax, u32v4
         }
         out[i] = __builtin_bit_cast(uint32_t, o);
     }
-    lo = u32v4{out[0], out[1], out[2], out[3]};
-    hi = u32v4{out[4], out[5], out[6], out[7]};
+    return out;
 }
 
 // Transposing read of 8 x 16 bytes by 16 lanes.  (The restrict-qualified
@@ -140,10 +145,16 @@ __device__ __forceinline__ void scale_columns(f32x16 (&acc)[C::MI][C::NI], const
     }
 }
 
-// ROWS16: dy's rows are 16-byte aligned (n a multiple of 8) and go straight
-// into LDS; otherwise by elements through registers.
-template <typename C, typename E, bool ROWS16>
+// How dy and the weight are read.  Whole: n is a multiple of 64, so every step
+// is whole and its addresses are a common base and a lane's constant offset
+// (2048 rows, n 14336, m 4096: 243 us; with a check for the last columns and
+// rows in each step 248).  Rows16: dy's rows are 16-byte aligned (n a multiple
+// of 8).  Elements: any n, dy through registers.
+enum class GradRows { Whole, Rows16, Elements };
+
+template <typename C, typename E, GradRows ROWS>
 __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a) {
+    constexpr bool Whole = ROWS == GradRows::Whole, Dma = ROWS != GradRows::Elements;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int T = a.grid.nbm * a.grid.nbn;
     const int idx = xcd_index(blockIdx.x, T * a.grid.nsplit);
@@ -161,18 +172,26 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
 
     // dy: chunk c of eight columns of row r sits at position c ^ (r & 7)
     const uint16_t *src[C::DA];
+    uint32_t off[C::DA];  // Whole: bytes from the tile's first row and the step's first column
     int col[C::DA];
 #pragma unroll
     for (int q = 0; q < C::DA; ++q) {
-        const int c = (wave * C::DA + q) * 64 + lane, r = c >> 3;
-        col[q] = k0 * C::BK + ((c & 7) ^ (r & 7)) * 8;
-        src[q] = dy + static_cast<size_t>(min(m0 + r, a.M - 1)) * a.w.n + col[q];  // rows past M: not written
+        const int c = (wave * C::DA + q) * 64 + lane, r = c >> 3, at = ((c & 7) ^ (r & 7)) * 8;
+        const int row = min(m0 + r, a.M - 1);  // rows past M: not written
+        col[q] = k0 * C::BK + at;
+        src[q] = dy + static_cast<size_t>(row) * a.w.n + col[q];
+        off[q] = (static_cast<uint32_t>(row - m0) * a.w.n + at) * 2;
     }
+    const char *tile_dy = reinterpret_cast<const char *>(dy + static_cast<size_t>(m0) * a.w.n);
+    int dstep = k0;  // of load_dy's next call
     auto load_dy = [&](int slot) {  // the next step's, each call
         char *st = lds + slot * C::ABytes;
 #pragma unroll
         for (int q = 0; q < C::DA; ++q) {
-            if constexpr (ROWS16) {
+            if constexpr (Whole) {
+                dma16(tile_dy + static_cast<size_t>(min(dstep, steps - 1)) * (2 * C::BK) + off[q],
+                      st + (wave * C::DA + q) * 1024);
+            } else if constexpr (Dma) {
                 // columns past n: zeros, whatever stands in the next row
                 dma16(col[q] < a.w.n ? static_cast<const void *>(src[q]) : a.zeros, st + (wave * C::DA + q) * 1024);
             } else {
@@ -185,9 +204,12 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
                 }
                 *reinterpret_cast<u32v4 *>(st + (wave * C::DA + q) * 1024 + lane * 16) = u32v4{v[0], v[1], v[2], v[3]};
             }
-            src[q] += C::BK;
-            col[q] += C::BK;
+            if constexpr (!Whole) {
+                src[q] += C::BK;
+                col[q] += C::BK;
+            }
         }
+        ++dstep;
     };
     // weight: this thread's blocks are row `lane` of the step, block columns
     // n0 / 32 + NB wave + i
@@ -195,39 +217,57 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
 #pragma unroll
     for (int i = 0; i < C::NB; ++i) {
         kb[i] = min(n0 / 32 + wave * C::NB + i, a.w.blocks - 1);  // block columns past the end: not written
-        smax[i] = a.w.colmax[kb[i]];
+        smax[i] = __builtin_amdgcn_readfirstlane(a.w.colmax[kb[i]]);
     }
-    int wrow = k0 * C::BK + lane;  // of the step that store_w takes next
+    int wrow = k0 * C::BK + lane;  // of the step that take_w takes next
     int lrow = wrow;               // of the step that load_w takes next
+    int lstep = k0;
+    const uint32_t woff = static_cast<uint32_t>(lane >> 5) * a.w.blocks * 512 + (lane & 31) * 16;
+    const uint32_t soff = static_cast<uint32_t>(lane >> 5) * (a.w.blocks >> 2) * 128 + (lane & 31) * 4;
     // Through LDS too, each wave its own (loaded into registers, they would
     // have the compiler wait for every load that is under way).
     auto load_w = [&](int slot) {
-        const int row = min(lrow, a.w.n_pad - 1);
-        const size_t t = static_cast<size_t>(row >> 5);
         char *p = lds + C::RAt + (slot * C::Waves + wave) * C::RBytes;
+        if constexpr (Whole) {
+            const size_t t = 2 * static_cast<size_t>(min(lstep, steps - 1));
 #pragma unroll
-        for (int i = 0; i < C::NB; ++i) {
-            dma16(a.w.codes + ((t * a.w.blocks + kb[i]) * 32 + (row & 31)) * 16, p + i * 1280);
-            dma4(a.w.scales + ((t * (a.w.blocks >> 2) + (kb[i] >> 2)) * 32 + (row & 31)) * 4, p + i * 1280 + 1024);
+            for (int i = 0; i < C::NB; ++i) {
+                dma16(a.w.codes + (t * a.w.blocks + kb[i]) * 512 + woff, p + i * 1280);
+                dma4(a.w.scales + (t * (a.w.blocks >> 2) + (kb[i] >> 2)) * 128 + soff, p + i * 1280 + 1024);
+            }
+            ++lstep;
+        } else {
+            const int row = min(lrow, a.w.n_pad - 1);
+            const size_t t = static_cast<size_t>(row >> 5);
+#pragma unroll
+            for (int i = 0; i < C::NB; ++i) {
+                dma16(a.w.codes + ((t * a.w.blocks + kb[i]) * 32 + (row & 31)) * 16, p + i * 1280);
+                dma4(a.w.scales + ((t * (a.w.blocks >> 2) + (kb[i] >> 2)) * 32 + (row & 31)) * 4, p + i * 1280 + 1024);
+            }
+            lrow += C::BK;
         }
-        lrow += C::BK;
     };
     constexpr int DW = 2 * C::NB;  // loads of a step's weight
-    auto store_w = [&](int slot, int bslot) {
+    u32v4 wcodes[C::NB];
+    float wscale[C::NB];
+    auto take_w = [&](int slot) {
         const char *p = lds + C::RAt + (slot * C::Waves + wave) * C::RBytes;
-        const bool past = wrow >= a.w.n;  // rows past n are zeros
+        const bool past = !Whole && wrow >= a.w.n;  // rows past n are zeros
 #pragma unroll
         for (int i = 0; i < C::NB; ++i) {
-            u32v4 codes, lo, hi;
             uint32_t sw;
-            read_raw(p + i * 1280, lane, codes, sw);
+            read_raw(p + i * 1280, lane, wcodes[i], sw);
             const int sb = static_cast<int>(sw >> (8 * (kb[i] & 3)) & 255u);
-            block_values(past ? u32v4{0u, 0u, 0u, 0u} : codes, past ? 0 : sb, smax[i], lo, hi);
-            char *q = lds + C::BAt + bslot * C::BBytes + lane * C::BPitch + (wave * C::NB + i) * 32;
-            *reinterpret_cast<u32v4 *>(q) = lo;
-            *reinterpret_cast<u32v4 *>(q + 16) = hi;
+            if (past) wcodes[i] = u32v4{0u, 0u, 0u, 0u};
+            wscale[i] = block_scale(past ? 0 : sb, smax[i]);
         }
         wrow += C::BK;
+    };
+    auto put_w = [&](int bslot, int h) {  // half h of the blocks' columns
+#pragma unroll
+        for (int i = 0; i < C::NB; ++i)
+            *reinterpret_cast<u32v4 *>(lds + C::BAt + bslot * C::BBytes + lane * C::BPitch + (wave * C::NB + i) * 32 + h * 16) =
+                block_values(wcodes[i][2 * h], wcodes[i][2 * h + 1], wscale[i]);
     };
 
     f32x16 acc[C::MI][C::NI];
@@ -267,6 +307,8 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
 #pragma unroll
             for (int i = 0; i < C::MI; ++i) acc[i][j] = product<E>(v.w[j], f.d[i], acc[i][j]);
     };
+    // (measured; one product per region leaves less to place)
+    constexpr int V0 = C::MI * C::NI > 1 ? 8 : 6, V1 = V0 - 2;
     // Order of a region: V vector instructions and one LDS read after each product.
     auto interleave = [&](auto v) {
 #pragma unroll
@@ -292,10 +334,12 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
     load_w(1);
     load_dy(1);
     wait_vm<2 * C::DA + DW>();
-    store_w(0, 0);
+    take_w(0);
+    put_w(0, 0);
+    put_w(0, 1);
     load_w(0);
     load_dy(2);
-    if constexpr (ROWS16) wait_vm<2 * C::DA + 2 * DW>();
+    if constexpr (Dma) wait_vm<2 * C::DA + 2 * DW>();
     wait_lds();
     block_barrier();
     load_frags(0, 0, 0, f0);
@@ -304,26 +348,28 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
     int as = 0, bs = 0;
     for (int kt = 0; kt < nk; ++kt) {
         const int a1 = as == 2 ? 0 : as + 1;
-        if constexpr (ROWS16) wait_vm<2 * C::DA + DW>();
+        if constexpr (Dma) wait_vm<2 * C::DA + DW>();
         else wait_vm<DW>();
         keep_order();
         // 0: reads of 2, widening of 1, conversion of the next step's weight
         load_frags(2, as, bs, f2);
         multiply(f0, v0);
         widen_all(f1, v1);
-        store_w(bs ^ 1, bs ^ 1);
-        interleave(Const<12>{});
+        take_w(bs ^ 1);
+        put_w(bs ^ 1, 0);
+        interleave(Const<V0>{});
         load_w(bs ^ 1);
         keep_order();
         // 1: reads of 3, widening of 2
         load_frags(3, as, bs, f0);
         multiply(f1, v1);
         widen_all(f2, v0);
-        interleave(Const<2>{});
+        put_w(bs ^ 1, 1);
+        interleave(Const<V1>{});
         // The next step's dy has landed (younger: its successor's, and two
         // steps' weight).  Past the barrier that holds for every wave, the
         // next step's weight is in LDS, and this step's operands have been read.
-        if constexpr (ROWS16) wait_vm<C::DA + 2 * DW>();
+        if constexpr (Dma) wait_vm<C::DA + 2 * DW>();
         wait_lds();
         block_barrier();
         // 2: reads of the next step's 0, widening of 3
@@ -379,7 +425,7 @@ struct GradCost {
     float light, full;
 };
 constexpr GradCost kGrad[] = {
-    {256, 256, 1.33f, 1.90f},
+    {256, 256, 1.20f, 1.85f},
     {128, 128, 0.64f, 0.66f},
     {32, 128, 0.46f, 0.29f},
 };
@@ -392,8 +438,8 @@ struct GradPlan {
 
 // The tile and K parts of least estimated time; K parts add a launch and the
 // traffic of their fp32 sums.  (2048 rows, n 14336, m 4096, bf16: 256 x 256
-// tiles in two parts 247 us, whole 328, 128 x 128 tiles 296; 512 rows: 128 x
-// 128 in four parts 84, whole 180; 16 rows: 32 x 128 in eight parts 23, whole 105.)
+// tiles in two parts 243 us, whole 316, 128 x 128 tiles 282; 512 rows: 128 x
+// 128 in four parts 80, whole 155; 16 rows: 32 x 128 in eight parts 23, whole 105.)
 GradPlan grad_plan(int M, int n, int m) {
     GradPlan best;
     float least = 0.0f;
@@ -421,21 +467,22 @@ GradPlan grad_plan(int M, int n, int m) {
 
 template <typename C, typename E>
 void launch_grad(MxGradArgs &a, hipStream_t s) {
-    static std::atomic<uint64_t> lds0{0}, lds1{0};
+    static std::atomic<uint64_t> lds0{0}, lds1{0}, lds2{0};
     TileGrid &t = a.grid;
     t.nbm = (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.m + C::BN - 1) / C::BN;
     t.group = t.nbm < 4 ? t.nbm : 4;
     const dim3 grid(t.nbm * t.nbn * t.nsplit);
-    if (a.w.n % 8 == 0) {
-        auto k = mx_grad_kernel<C, E, true>;
-        if constexpr (C::Lds > 65536) allow_lds(k, C::Lds, lds0);
+    auto go = [&](auto rows, std::atomic<uint64_t> &asked) {
+        auto k = mx_grad_kernel<C, E, decltype(rows)::value>;
+        if constexpr (C::Lds > 65536) allow_lds(k, C::Lds, asked);
         launch_kernel(k, grid, dim3(C::Threads), C::Lds, s, a);
-    } else {
-        auto k = mx_grad_kernel<C, E, false>;
-        if constexpr (C::Lds > 65536) allow_lds(k, C::Lds, lds1);
-        launch_kernel(k, grid, dim3(C::Threads), C::Lds, s, a);
-    }
+    };
+    // (offsets inside a tile are 32 bits)
+    if (a.w.n % C::BK == 0 && a.w.n <= 1 << 22 && a.w.blocks <= 1 << 22)
+        go(std::integral_constant<GradRows, GradRows::Whole>{}, lds0);
+    else if (a.w.n % 8 == 0) go(std::integral_constant<GradRows, GradRows::Rows16>{}, lds1);
+    else go(std::integral_constant<GradRows, GradRows::Elements>{}, lds2);
     if (a.part) {
         auto k = mx_grad_finish_kernel<C, E>;
         launch_kernel(k, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);

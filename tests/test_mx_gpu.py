@@ -519,7 +519,9 @@ def test_backward_data(gpu, b, n, m, name):
 
 @pytest.mark.parametrize("b,n,m,name", [(1900, 1032, 8100, "bf16"), (1900, 1030, 8100, "f16"), (700, 2008, 2050, "f16"),
                                         (700, 2001, 2050, "bf16"), (300, 4104, 1000, "bf16"), (33, 4099, 900, "f16"),
-                                        (1900, 40, 8100, "f16"), (1900, 100, 8100, "bf16")])
+                                        (1900, 40, 8100, "f16"), (1900, 100, 8100, "bf16"), (1900, 1024, 8100, "bf16"),
+                                        (1900, 64, 8100, "f16"), (1900, 192, 8100, "bf16"), (700, 2048, 2050, "f16"),
+                                        (300, 4096, 1000, "bf16"), (33, 4096, 900, "f16"), (5, 64, 100, "bf16")])
 def test_backward_large(gpu, b, n, m, name):
     """Every tile, whole and in K parts, fewer steps than the pipeline holds, rows that are not 16-byte aligned."""
     _say(f"mx backward large b={b} n={n} m={m} {name}")
