@@ -493,7 +493,7 @@ class MxTensor:
         t = _type_of(dtype)
         if t < 0:
             raise ValueError("dtype must be float32, float16 or bfloat16")
-        out = torch.empty(self.shape, dtype=dtype, device=self.device)
+        out = self.codes.new_empty(self.shape, dtype=dtype)
         _call("dbf_mx_dequantize", out, self.codes.data_ptr(), self.scales.data_ptr(), _TYPE_NAMES[self.fmt],
               out.shape[0], self.cols, out.data_ptr(), t)
         return out
