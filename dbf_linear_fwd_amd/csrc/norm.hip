@@ -16,8 +16,10 @@
 // bf16, operands from HBM, graph replays: norm with residual 8192 x 4096
 // 54 us (4.95 TB/s moved; a plain large copy 4.6), with block output 51 us,
 // 2048 x 4096 14.6 and 16.4, one row 2.8 and 3.1; gradient with dh 8192 x 4096
-// 57 us (4.7 TB/s), 2048 x 4096 22 (a second launch and the
-// parts of dw), 65536 x 128 20.
+// 57 us (4.7 TB/s), 2048 x 4096 22 (a second launch and the parts of dw),
+// 65536 x 128 20.
+
+#include <algorithm>
 
 #include "mx_device.h"
 
@@ -84,6 +86,25 @@ struct NormArgs {
     void *h, *y;
     uint8_t *ys;   // scales of an e4m3 output
     float *rstd;
+
+    // Rows r0 on, `most` of them at most.
+    template <typename T, bool MX>
+    NormArgs from_row(int64_t r0, int most) const {
+        const size_t at = static_cast<size_t>(r0) * cols, wide = (cols + 127) / 128 * 128;
+        NormArgs b = *this;
+        b.rows = static_cast<int>(std::min<int64_t>(rows - r0, most));
+        b.x = static_cast<const T *>(x) + at;
+        if (r) b.r = static_cast<const T *>(r) + at;
+        if (h) b.h = static_cast<T *>(h) + at;
+        if (rstd) b.rstd = rstd + r0;
+        if (MX) {
+            b.y = static_cast<uint8_t *>(y) + r0 * wide;
+            b.ys = ys + r0 * (wide / 32);
+        } else {
+            b.y = static_cast<T *>(y) + at;
+        }
+        return b;
+    }
 };
 
 // LPR lanes per row, NC chunks of 8 LPR columns.
@@ -324,9 +345,16 @@ int launch_norm(const NormArgs &a, hipStream_t s) {
     return by_width(a.cols, [&](auto lpr, auto nc) {
         constexpr int LPR = decltype(lpr)::value, NC = decltype(nc)::value;
         constexpr int Threads = LPR > 256 ? LPR : 256, RPB = Threads / LPR;
-        const dim3 grid(static_cast<uint32_t>((a.rows + RPB - 1) / RPB)), block(Threads);
-        if (a.cols % 8 == 0) launch_kernel(rms_norm_kernel<E, MX, true, LPR, NC>, grid, block, 0, s, a);
-        else launch_kernel(rms_norm_kernel<E, MX, false, LPR, NC>, grid, block, 0, s, a);
+        const dim3 block(Threads);
+        // A launch holds less than 2^32 threads; more rows are several launches
+        // (a loop over rows in the kernel: 8192 x 4096 60 instead of 55 us).
+        constexpr int kRows = (1 << 21) * RPB;
+        for (int64_t r0 = 0; r0 < a.rows; r0 += kRows) {
+            const NormArgs b = a.template from_row<typename E::T, MX>(r0, kRows);
+            const dim3 grid(static_cast<uint32_t>((b.rows - 1) / RPB + 1));
+            if (a.cols % 8 == 0) launch_kernel(rms_norm_kernel<E, MX, true, LPR, NC>, grid, block, 0, s, b);
+            else launch_kernel(rms_norm_kernel<E, MX, false, LPR, NC>, grid, block, 0, s, b);
+        }
         return static_cast<int>(hipGetLastError());
     });
 }
@@ -341,7 +369,7 @@ constexpr int grad_threads(int lpr, int nc) { return nc == 1 ? 1024 : lpr > 512 
 int norm_grad_parts(int rows, int cols) {
     return by_width(cols, [&](auto lpr, auto nc) {
         constexpr int RPB = grad_threads(decltype(lpr)::value, decltype(nc)::value) / decltype(lpr)::value;
-        const int need = (rows + RPB - 1) / RPB;
+        const int need = (rows - 1) / RPB + 1;
         return need < 256 ? need : 256;
     });
 }

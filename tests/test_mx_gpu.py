@@ -411,6 +411,31 @@ def test_call_forms_agree(gpu, b):
             L.close()
 
 
+@pytest.mark.parametrize("b,m", [(16, 9216), (16, 8192), (13, 4100), (4, 16512)])
+def test_call_forms_agree_at_wide_inputs(gpu, b, m):
+    """Few rows on either side of what fits LDS, of what the product quantises itself, and of the widest input."""
+    torch = _torch()
+    _say(f"mx call forms b={b} m={m}")
+    rng = np.random.default_rng(b + m)
+    layers = [dbf.Layer.mx(weight(rng, n, m)[0], max_batch=b, act=act)
+              for n, act in ((70, "e4m3"), (33, "e2m1"), (70, "e4m3"))]
+    try:
+        xd, _ = to_dev(rows_of(rng, b, m), "f16")
+        own = [L(xd) for L in layers]
+        for L, o in zip(layers, own):
+            assert same_bits(L(dbf.mx_quantize(xd, L.act)), o)
+            y = torch.empty_like(o)
+            dbf.dbf_linear_forward_noalloc(L.handle, xd.data_ptr(), y.data_ptr(), b,
+                                           torch.cuda.current_stream().cuda_stream)
+            assert same_bits(y, o)
+        # the same handle twice in a group too
+        for y, o in zip(dbf.forward_group(layers + layers[:1], xd), own + own[:1]):
+            assert same_bits(y, o)
+    finally:
+        for L in layers:
+            L.close()
+
+
 def test_handle_refusals(gpu):
     torch = _torch()
     _say("mx handle refusals")

@@ -221,6 +221,48 @@ def test_in_place_and_no_rows(gpu):
     assert dx.shape == (0, 64) and bool((dw == 0).all())
 
 
+def test_most_rows(gpu):
+    """As many rows as the interface counts: row offsets past 32 bits, a rounded-up row count past 31."""
+    import torch
+    _say("norm 2^31 - 1 rows")
+    rows = 2 ** 31 - 1
+    x = torch.empty((rows, 1), dtype=torch.float16, device="cuda")
+    x.fill_(2.0)
+    x[-1] = -3.0
+    x[rows // 2] = 0.0
+    out = dbf.rms_norm(x, None, eps=0.25)
+    for i, v in ((0, 2.0), (rows // 2, 0.0), (rows - 2, 2.0), (rows - 1, -3.0)):
+        want = v / np.sqrt(v * v + 0.25)
+        assert abs(float(out.y[i]) - want) <= abs(want) * (half_step("f16") * (1 + REL) + REL)
+    dx, dw = dbf.rms_norm_backward(x, x, None, out.rstd)
+    # dy = h: dx = r (h - h r² h²) and Σ dy h r, all terms equal but two
+    r = 1 / np.sqrt(4.25)
+    want = r * (2 - 2 * r * r * 4)
+    assert abs(float(dx[0]) - want) <= half_step("f16") * abs(want) * (1 + REL) + 8 * REL
+    total = (rows - 2) * 4 * r + 9 / np.sqrt(9.25)
+    # a lane adds 2^31 / 2^14 terms that all round alike: half a step of its sum each time at worst
+    assert abs(float(dw[0]) - total) <= total * 2 ** 17 * 2.0 ** -24
+
+
+def test_more_rows_than_a_launch(gpu):
+    """Rows past one launch's, residual and blocks too: the bits of a small call on the same rows."""
+    import torch
+    _say("norm several launches")
+    rows, cols = 2 ** 25 + 100, 40
+    x = torch.randn((rows, cols), device="cuda").half()
+    r = torch.randn((rows, cols), device="cuda").half()
+    w = torch.randn(cols, device="cuda").half()
+    for mx in (False, True):
+        out = dbf.rms_norm(x, w, residual=r, mx=mx)
+        for part in (slice(0, 64), slice(2 ** 25 - 64, 2 ** 25 + 64), slice(rows - 32, rows)):
+            want = dbf.rms_norm(x[part].clone(), w, residual=r[part].clone(), mx=mx)
+            assert torch.equal(out.h[part], want.h) and torch.equal(out.rstd[part], want.rstd)
+            if mx:
+                assert torch.equal(out.y.codes[part], want.y.codes) and torch.equal(out.y.scales[part], want.y.scales)
+            else:
+                assert torch.equal(out.y[part], want.y)
+
+
 def test_feeds_a_sign_layer(gpu):
     """The 16-bit output in front of a sign-factor layer, as a decoder block runs it."""
     import torch
