@@ -20,9 +20,11 @@ namespace {
 // A stage holds 64 bytes of each of the tile's rows of x (64 columns of e4m3,
 // 128 of e2m1) and the weight's blocks of the same columns; scale words (four
 // bytes: 128 columns) sit in stages of their own kind, one per 128 columns.
-// The 16-byte chunks of a row of x are permuted so that eight rows which one
-// operand read touches fall on different banks; the weight's and the scales'
-// device order is the order in which the lanes read them.
+// The 16-byte chunks of a row of x are permuted so that the 16 rows which an
+// operand read touches in a cycle lie on all 64 banks (as if there were 32: a
+// third of the LDS cycles were conflicts, 6 % now, though the time is the
+// same); the weight's and the scales' device order is the order in which the
+// lanes read them.
 //
 // The unit of work is a half: 64 columns, MI x NI matrix-core instructions
 // per wave.  While a half is multiplied, the operands of the next one are
@@ -174,7 +176,7 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a)
         at[q] = u * 1024;
         constexpr int XU = C::XBytes / 1024;
         if (u < XU) {
-            const int c = u * 64 + lane, r = c >> 2, lc = (c & 3) ^ ((r >> 1) & 3);
+            const int c = u * 64 + lane, r = c >> 2, lc = (c & 3) ^ ((r >> 2) & 3);
             const int row = min(m0 + r, a.M - 1);  // rows past M: multiplied, not written
             src[q] = a.xc + (static_cast<size_t>(row) * steps + k0) * (64 * C::Parts) + lc * 16;
             inc[q] = 64;
@@ -214,7 +216,7 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.0f;
 
-    const int xrow = (wm * C::MI * 32 + l32) * 64, swz = (l32 >> 1) & 3;
+    const int xrow = (wm * C::MI * 32 + l32) * 64, swz = (l32 >> 2) & 3;
     const int wrow = C::XBytes + wn * C::NI * C::WTile + g * 512 + l32 * 16;
     MxFrags<C> f0, f1;
     MxScales<C> sc, sn;

@@ -5,24 +5,18 @@
 // sum has another scale and the scaled matrix-core instructions do not apply:
 // the weight becomes 16-bit values on the way, on the 32x32x16 instructions
 // (2.5 PFLOP/s).  Per 64 rows of the weight a thread takes one block (one row,
-// 32 columns): its codes become e5m2 values relative to the largest scale of
-// their block column, code * 2^(s - smax + 13), one byte each in LDS; the
-// transposing LDS read hands a lane the eight rows of its column, which four
-// conversions turn into the 16-bit operand.  (As 16-bit values in LDS the
-// weight's share of the LDS traffic would double, and the LDS be what bounds
-// a 256 x 256 tile: 2300 of its cycles for 2048 of the matrix cores.)  e5m2
-// holds the codes exactly down to scales of 2^-28 of the largest; the sums
-// are multiplied by 2^(smax - 13) at the end.
+// 32 columns) and widens its codes relative to the largest scale of their
+// block column, code * 2^(s - smax + 13), into LDS; the transposing LDS read
+// hands a lane the rows of its column.  f16 holds the codes exactly down to
+// scales of 2^-28 of the largest and below; the sums are multiplied by
+// 2^(smax - 13) at the end.  (As bytes in LDS, e5m2 of the same values,
+// widened again by every wave that reads them: 243 instead of 237 us.)
 //
-// 2048 rows, n 14336, m 4096, bf16: 243 us, 0.99 PFLOP/s (217 us, 1.1, with
-// gradients of 0.01 in place of full-range values).  A step of 64 rows of a 256
-// x 256 tile takes 1.2 us alone and 1.85 with all CUs at work, where the clock
-// falls to 1.9 GHz and the matrix cores are busy 55 % of the time; converting
-// the weight and reading the operands fill the rest as far as they do not
-// overlap.  Placed one by one between the products instead of in front of
-// them: 247 instead of 272 us.  Half of the weight's conversion beside each of
-// the first two of a step's four groups of products, instead of beside the
-// first: 1.2 instead of 1.33 us a step alone.
+// 2048 rows, n 14336, m 4096, bf16: 237 us, 1.02 PFLOP/s (205 us, 1.17, with
+// gradients of 0.01 in place of full-range values; a library product of 16-bit
+// matrices of that size takes 212).  A step of 64 rows of a 256 x 256 tile
+// takes 1.25 us alone and 1.8 with all CUs at work, where the clock falls to
+// 1.9 GHz; its products are 0.85 us at the highest clock.
 
 #include "mx_tile.h"
 
@@ -33,7 +27,7 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kShift = 13;  // 6 * 2^13 is e5m2's top binade
+constexpr int kShift = 13;  // 6 * 2^13 is within f16
 
 // Waves WM x WN, each MI x NI fragments of 32 x 32.
 template <int MI_, int NI_, int WM_, int WN_>
@@ -42,9 +36,9 @@ struct GradTile {
     static constexpr int Waves = WM * WN, Threads = 64 * Waves;
     static constexpr int BM = 32 * MI * WM, BN = 32 * NI * WN, BK = 64;
     static constexpr int ABytes = BM * BK * 2;
-    static constexpr int BPitch = BN + 32;            // bytes of a weight row: eight rows on different banks
+    static constexpr int BPitch = BN * 2;  // bytes of a weight row
     static constexpr int BBytes = BK * BPitch;
-    static constexpr int AStages = 3, BStages = 2, RStages = 2;
+    static constexpr int AStages = 2, BStages = 2, RStages = 2;
     static constexpr int NB = BN / 32 * BK / Threads;  // weight blocks per thread and step
     static constexpr int RBytes = NB * 1280;           // a wave's codes and scale words of a step
     static constexpr int BAt = AStages * ABytes, RAt = BAt + BStages * BBytes;
@@ -66,61 +60,43 @@ struct MxGradArgs {
     float *part;
 };
 
-// What the conversion to e5m2 divides a block's values by: 2^-(s - smax + 13).
+// The factor of a block's codes: 2^(s - smax + 13).
 __device__ __forceinline__ float block_scale(int s, int smax) {
-    const int e = 127 - kShift + smax - s;
-    const uint32_t bits = s == 255 ? 0x7fc00000u : static_cast<uint32_t>(e < 254 ? e : 254) << 23;
+    const int e = 127 + kShift - smax + s;
+    const uint32_t bits = s == 255 ? 0x7fc00000u : static_cast<uint32_t>(e > 0 ? e : 0) << 23;
     return __builtin_bit_cast(float, bits);
 }
 
-// The e5m2 bytes of 16 columns of a block.
-__device__ __forceinline__ u32v4 block_values(uint32_t c0, uint32_t c1, float sc) {
-    u32v4 out;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w = i < 2 ? c0 : c1;
-        s16x2 o = {0, 0};
-        if (i & 1) {
-            o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2), sc, false);
-            o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3), sc, true);
-        } else {
-            o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0), sc, false);
-            o = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(o, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1), sc, true);
-        }
-        out[i] = __builtin_bit_cast(uint32_t, o);
+// Eight codes as 16-bit values times sc.
+template <typename E>
+__device__ __forceinline__ u32v4 widen(uint32_t w, float sc) {
+    u32v4 r;
+    if constexpr (E::code == DBF_TYPE_BF16) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3));
+    } else {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 0));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 1));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 2));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 3));
     }
-    return out;
+    return r;
 }
 
-// Transposing read of 8 x 16 bytes by 16 lanes.  (The restrict-qualified
+// Transposing read of 4 x 16 16-bit values by 16 lanes.  (The restrict-qualified
 // argument keeps the compiler from waiting for every load into LDS first.)
-__device__ __forceinline__ i32x2 read_columns(const char *__restrict__ p) {
-    typedef __attribute__((address_space(3))) i32x2 lds_i2;
-    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i2 *)p);
+__device__ __forceinline__ u32v2 read_columns(const char *__restrict__ p) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s4;
+    return __builtin_bit_cast(u32v2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p));
 }
 
 // A lane's codes and scale word of a block.
 __device__ __forceinline__ void read_raw(const char *__restrict__ p, int lane, u32v4 &codes, uint32_t &scales) {
     codes = *reinterpret_cast<const u32v4 *>(p + lane * 16);
     scales = *reinterpret_cast<const uint32_t *>(p + 1024 + lane * 4);
-}
-
-// Eight e5m2 bytes as 16-bit values.
-template <typename E>
-__device__ __forceinline__ u32v4 widen(i32x2 b) {
-    u32v4 r;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t w = static_cast<uint32_t>(b[i]);
-        if constexpr (E::code == DBF_TYPE_BF16) {
-            r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, false));
-            r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, true));
-        } else {
-            r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(w, 1.0f, false));
-            r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(w, 1.0f, true));
-        }
-    }
-    return r;
 }
 
 template <typename E>
@@ -148,7 +124,7 @@ __device__ __forceinline__ void scale_columns(f32x16 (&acc)[C::MI][C::NI], const
 // How dy and the weight are read.  Whole: n is a multiple of 64, so every step
 // is whole and its addresses are a common base and a lane's constant offset
 // (2048 rows, n 14336, m 4096: 243 us; with a check for the last columns and
-// rows in each step 248).  Rows16: dy's rows are 16-byte aligned (n a multiple
+// rows in each step 248, on an earlier form of the loop).  Rows16: dy's rows are 16-byte aligned (n a multiple
 // of 8).  Elements: any n, dy through registers.
 enum class GradRows { Whole, Rows16, Elements };
 
@@ -176,7 +152,7 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
     int col[C::DA];
 #pragma unroll
     for (int q = 0; q < C::DA; ++q) {
-        const int c = (wave * C::DA + q) * 64 + lane, r = c >> 3, at = ((c & 7) ^ (r & 7)) * 8;
+        const int c = (wave * C::DA + q) * 64 + lane, r = c >> 3, at = ((c & 7) ^ ((r >> 1) & 7)) * 8;
         const int row = min(m0 + r, a.M - 1);  // rows past M: not written
         col[q] = k0 * C::BK + at;
         src[q] = dy + static_cast<size_t>(row) * a.w.n + col[q];
@@ -250,24 +226,33 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
     constexpr int DW = 2 * C::NB;  // loads of a step's weight
     u32v4 wcodes[C::NB];
     float wscale[C::NB];
-    auto take_w = [&](int slot) {
+    uint32_t wsw[C::NB];
+    auto read_w = [&](int slot) {
         const char *p = lds + C::RAt + (slot * C::Waves + wave) * C::RBytes;
+#pragma unroll
+        for (int i = 0; i < C::NB; ++i) read_raw(p + i * 1280, lane, wcodes[i], wsw[i]);
+    };
+    auto take_w = [&] {
         const bool past = !Whole && wrow >= a.w.n;  // rows past n are zeros
 #pragma unroll
         for (int i = 0; i < C::NB; ++i) {
-            uint32_t sw;
-            read_raw(p + i * 1280, lane, wcodes[i], sw);
-            const int sb = static_cast<int>(sw >> (8 * (kb[i] & 3)) & 255u);
+            const int sb = static_cast<int>(wsw[i] >> (8 * (kb[i] & 3)) & 255u);
             if (past) wcodes[i] = u32v4{0u, 0u, 0u, 0u};
             wscale[i] = block_scale(past ? 0 : sb, smax[i]);
         }
         wrow += C::BK;
     };
-    auto put_w = [&](int bslot, int h) {  // half h of the blocks' columns
+    // The weight's values: 16-byte chunk c (of 16) of each 256 bytes of row r
+    // sits at c ^ (4 (r % 4) + r / 4 % 4): what 16 lanes write, and the four
+    // rows that 32 lanes of a transposing read touch, lie on all 64 banks.
+    const int bswz = ((lane & 3) << 2) | ((lane >> 2) & 3);
+    auto put_w = [&](int bslot, int j) {  // eight columns of each block
 #pragma unroll
-        for (int i = 0; i < C::NB; ++i)
-            *reinterpret_cast<u32v4 *>(lds + C::BAt + bslot * C::BBytes + lane * C::BPitch + (wave * C::NB + i) * 32 + h * 16) =
-                block_values(wcodes[i][2 * h], wcodes[i][2 * h + 1], wscale[i]);
+        for (int i = 0; i < C::NB; ++i) {
+            const int blk = wave * C::NB + i;
+            *reinterpret_cast<u32v4 *>(lds + C::BAt + bslot * C::BBytes + lane * C::BPitch + (blk >> 2) * 256 +
+                                       ((((blk & 3) * 4 + j) ^ bswz) << 4)) = widen<E>(wcodes[i][j], wscale[i]);
+        }
     };
 
     f32x16 acc[C::MI][C::NI];
@@ -278,116 +263,106 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.0f;
 
-    // operands of 16 rows of the weight as they come from LDS
+    // operands of 16 rows of the weight
     struct Frags {
-        u32v4 d[C::MI];
-        i32x2 w[C::NI];
+        u32v4 d[C::MI], w[C::NI];
     };
     const int arow = (wm * C::MI * 32 + l32) * 128;
-    // transposing read: lane i of 16 gives row i / 2, eight columns; gets column i % 16
-    const int brow = C::BAt + (8 * g + (lane & 15) / 2) * C::BPitch + wn * C::NI * 32 + ((lane >> 4) & 1) * 16 + (lane & 1) * 8;
+    // transposing read h of an operand: lane i of 16 gives row 8 g + 4 h + i / 4,
+    // four columns; gets column i, four rows
+    int bat[C::NI][2];
+#pragma unroll
+    for (int j = 0; j < C::NI; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane & 15, blk = wn * C::NI + j, c = (blk & 3) * 4 + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+            bat[j][h] = C::BAt + (8 * g + 4 * h + (i >> 2)) * C::BPitch + (blk >> 2) * 256 +
+                        ((c ^ (((i >> 2) << 2) | ((2 * g + h) & 3))) << 4) + (i & 1) * 8;
+        }
     auto load_frags = [&](int ks, int aslot, int bslot, Frags &f) {
 #pragma unroll
-        for (int i = 0; i < C::MI; ++i)
-            f.d[i] = *reinterpret_cast<const u32v4 *>(lds + aslot * C::ABytes + arow + i * 4096 + (((2 * ks + g) ^ (l32 & 7)) << 4));
+        for (int j = 0; j < C::NI; ++j) {
+            const u32v2 lo = read_columns(lds + bat[j][0] + bslot * C::BBytes + ks * 16 * C::BPitch);
+            const u32v2 hi = read_columns(lds + bat[j][1] + bslot * C::BBytes + ks * 16 * C::BPitch);
+            f.w[j] = u32v4{lo[0], lo[1], hi[0], hi[1]};
+            if (j == 0) {
+#pragma unroll
+                for (int i = 0; i < C::MI; ++i)
+                    f.d[i] = *reinterpret_cast<const u32v4 *>(lds + aslot * C::ABytes + arow + i * 4096 +
+                                                              (((2 * ks + g) ^ ((l32 >> 1) & 7)) << 4));
+            }
+        }
+    };
+    auto multiply = [&](const Frags &f) {
 #pragma unroll
         for (int j = 0; j < C::NI; ++j)
-            f.w[j] = read_columns(lds + brow + bslot * C::BBytes + ks * 16 * C::BPitch + j * 32);
-    };
-    struct Wide {
-        u32v4 w[C::NI];
-    };
-    auto widen_all = [&](const Frags &f, Wide &v) {
 #pragma unroll
-        for (int j = 0; j < C::NI; ++j) v.w[j] = widen<E>(f.w[j]);
+            for (int i = 0; i < C::MI; ++i) acc[i][j] = product<E>(f.w[j], f.d[i], acc[i][j]);
     };
-    auto multiply = [&](const Frags &f, const Wide &v) {
-#pragma unroll
-        for (int j = 0; j < C::NI; ++j)
-#pragma unroll
-            for (int i = 0; i < C::MI; ++i) acc[i][j] = product<E>(v.w[j], f.d[i], acc[i][j]);
-    };
-    // (measured; one product per region leaves less to place)
-    constexpr int V0 = C::MI * C::NI > 1 ? 8 : 6, V1 = V0 - 2;
-    // Order of a region: V vector instructions and one LDS read after each product.
-    auto interleave = [&](auto v) {
+    // Order of a region: its LDS reads behind the first products, two vector
+    // instructions after each.
+    auto interleave = [&] {
 #pragma unroll
         for (int i = 0; i < C::MI * C::NI; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, decltype(v)::value, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
         }
         keep_order();
     };
 
-    // Step kt: dy in slot kt % 3, the weight's values in slot kt % 2.  Under
-    // way: dy of steps kt + 1 and kt + 2, the weight's codes of steps kt + 1 and
-    // kt + 2 (slots kt % 2 again).  Its four times 16 rows are a pipeline: read
-    // from LDS two before, widened one before its products; the next step's
-    // weight is converted beside the first two.  The loads run on past the last
-    // step, to no use: a branch around them would have the compiler move the
-    // products behind it.
-    Frags f0, f1, f2;
-    Wide v0, v1;
+    // Step kt: dy and the weight's values in slots kt % 2.  Under way: dy of step
+    // kt + 1, the weight's codes of steps kt + 1 and kt + 2 (slots kt % 2
+    // again).  The operands of each of its four times 16 rows are read beside the
+    // products before; the next step's weight is converted beside the first
+    // three, its codes read before them.  The loads run on past the last step, to no use: a branch around
+    // them would have the compiler move the products behind it.
+    Frags f0, f1;
     load_w(0);
-    load_dy(0);
     load_w(1);
-    load_dy(1);
-    wait_vm<2 * C::DA + DW>();
-    take_w(0);
-    put_w(0, 0);
-    put_w(0, 1);
+    load_dy(0);
+    wait_vm<(Dma ? C::DA : 0) + DW>();
+    read_w(0);
+    take_w();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) put_w(0, j);
     load_w(0);
-    load_dy(2);
-    if constexpr (Dma) wait_vm<2 * C::DA + 2 * DW>();
+    load_dy(1);
+    if constexpr (Dma) wait_vm<C::DA + DW>();
     wait_lds();
     block_barrier();
     load_frags(0, 0, 0, f0);
-    load_frags(1, 0, 0, f1);
-    widen_all(f0, v0);
-    int as = 0, bs = 0;
+    read_w(1);
+    int s = 0;
     for (int kt = 0; kt < nk; ++kt) {
-        const int a1 = as == 2 ? 0 : as + 1;
-        if constexpr (Dma) wait_vm<2 * C::DA + DW>();
-        else wait_vm<DW>();
+        load_frags(1, s, s, f1);
+        multiply(f0);
+        take_w();
+        put_w(s ^ 1, 0);
+        interleave();
+        load_w(s ^ 1);
         keep_order();
-        // 0: reads of 2, widening of 1, conversion of the next step's weight
-        load_frags(2, as, bs, f2);
-        multiply(f0, v0);
-        widen_all(f1, v1);
-        take_w(bs ^ 1);
-        put_w(bs ^ 1, 0);
-        interleave(Const<V0>{});
-        load_w(bs ^ 1);
-        keep_order();
-        // 1: reads of 3, widening of 2
-        load_frags(3, as, bs, f0);
-        multiply(f1, v1);
-        widen_all(f2, v0);
-        put_w(bs ^ 1, 1);
-        interleave(Const<V1>{});
-        // The next step's dy has landed (younger: its successor's, and two
-        // steps' weight).  Past the barrier that holds for every wave, the
-        // next step's weight is in LDS, and this step's operands have been read.
-        if constexpr (Dma) wait_vm<C::DA + 2 * DW>();
+        load_frags(2, s, s, f0);
+        multiply(f1);
+        put_w(s ^ 1, 1);
+        put_w(s ^ 1, 2);
+        interleave();
+        load_frags(3, s, s, f1);
+        multiply(f0);
+        put_w(s ^ 1, 3);
+        interleave();
+        // The next step's dy and the codes behind it have landed (younger: a
+        // step's codes).  Past the barrier that holds for every wave, the next
+        // step's weight is in LDS, and this step's operands have been read.
+        wait_vm<DW>();
         wait_lds();
         block_barrier();
-        // 2: reads of the next step's 0, widening of 3
-        load_frags(0, a1, bs ^ 1, f1);
-        multiply(f2, v0);
-        widen_all(f0, v1);
-        interleave(Const<2>{});
-        load_dy(as);
-        keep_order();
-        // 3: reads of the next step's 1, widening of its 0
-        load_frags(1, a1, bs ^ 1, f2);
-        multiply(f0, v1);
-        widen_all(f1, v0);
-        interleave(Const<2>{});
-        f0 = f1;
-        f1 = f2;
-        as = a1;
-        bs ^= 1;
+        load_frags(0, s ^ 1, s ^ 1, f0);
+        read_w(s);
+        load_dy(s);
+        multiply(f1);
+        interleave();
+        s ^= 1;
     }
     wait_vm<0>();  // nothing more lands in the LDS that the result goes through
     wait_lds();
@@ -438,8 +413,8 @@ struct GradPlan {
 
 // The tile and K parts of least estimated time; K parts add a launch and the
 // traffic of their fp32 sums.  (2048 rows, n 14336, m 4096, bf16: 256 x 256
-// tiles in two parts 243 us, whole 316, 128 x 128 tiles 282; 512 rows: 128 x
-// 128 in four parts 80, whole 155; 16 rows: 32 x 128 in eight parts 23, whole 105.)
+// tiles in two parts 237 us, whole 314, 128 x 128 tiles 273; 512 rows: 128 x
+// 128 in four parts 78, whole 144; 16 rows: 32 x 128 in eight parts 23, whole 105.)
 GradPlan grad_plan(int M, int n, int m) {
     GradPlan best;
     float least = 0.0f;

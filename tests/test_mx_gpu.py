@@ -621,6 +621,30 @@ def test_backward_scale_range(gpu):
         L.close()
 
 
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+def test_backward_smallest_exact_scales(gpu, name):
+    """Scales of 2^-28 of the block column's largest: every code still exact (2^-16 and up in 16 bits)."""
+    _say(f"mx backward smallest scales {name}")
+    rng = np.random.default_rng(9)
+    n, m, b = 128, 64, 7
+    wc = rng.integers(0, 16, size=(n, m)).astype(np.uint8)
+    ws = np.full((n, m // 32), 127 - 28, dtype=np.uint8)
+    ws[64:] = 127
+    wc[64:] = 0          # (the large rows are zeros: what is left is the small ones alone)
+    wc[64:, ::32] = 1
+    dyd, dyv = to_dev(rng.integers(-64, 65, size=(b, n)) * 2.0 ** 8, name)
+    wv = O.values(wc, ws, "e2m1")
+    ref, _ = O.backward_data(dyv, wv)
+    L = dbf.Layer.mx(blocks_to_dev(wc, ws, m, "e2m1"), max_batch=b)
+    try:
+        dx = L.backward_data(dyd).double().cpu().numpy()
+    finally:
+        L.close()
+    cols = np.arange(m) % 32 != 0
+    # whole numbers of 2^-21 below 2^24 of them: the fp32 sums are exact, one rounding is left
+    assert np.all(np.abs(dx - ref)[:, cols] <= half_step(name) * np.abs(ref)[:, cols] + tiny(name))
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("rows", [1, 7, 130])
