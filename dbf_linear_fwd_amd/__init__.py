@@ -443,7 +443,7 @@ def _call(where: str, t, *args) -> None:
     """
     import torch
     index = t.device.index
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
             return _call(where, t, *args)
     status = getattr(_lib or lib(), where)(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -547,11 +547,15 @@ def _check_count(rows: int, cols: int) -> None:
 
 def _check_rows(t, what, like=None):
     import torch
+    if like is not None:  # (checked itself: its type, device and shape carry over)
+        if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
+            raise ValueError(f"{what} must match the other rows in shape, type and device")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous 2-D CUDA tensor of float16 or bfloat16")
+        return
     if t.dtype not in (torch.float16, torch.bfloat16) or not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous 2-D CUDA tensor of float16 or bfloat16")
     _check_count(*t.shape)
-    if like is not None and (t.dtype != like.dtype or t.shape != like.shape or t.device != like.device):
-        raise ValueError(f"{what} must match the other rows in shape, type and device")
 
 
 def _check_norm_weight(weight, x) -> int:
