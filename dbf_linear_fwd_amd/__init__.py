@@ -33,7 +33,7 @@ __all__ = [
     "dbf_pack_ex", "dbf_linear_backward_data", "dbf_linear_backward", "DBF_PACK_BACKWARD", "dbf_bqq_pack",
     "dbf_factorize", "factorize", "dbf_linear_forward_noalloc", "dbf_bqq_pack_grouped",
     "DBF_TYPE_F16", "DBF_TYPE_BF16", "DBF_TYPE_F32", "DBF_TYPE_E4M3", "DBF_TYPE_E2M1", "MxTensor", "mx_quantize",
-    "dbf_mx_pack", "rms_norm", "RmsNormOutput", "rms_norm_backward",
+    "dbf_mx_pack", "rms_norm", "RmsNormOutput", "rms_norm_backward", "norm_forward_group",
 ]
 
 DBF_OK = 0
@@ -65,7 +65,7 @@ EXPORTED_SYMBOLS = (
     "dbf_pack_signs", "dbf_layout_signs", "dbf_layout_words", "dbf_layout_signs_dec", "dbf_layout_words_dec",
     "dbf_timing_enable", "dbf_timing_read", "dbf_bqq_pack", "dbf_factorize", "dbf_linear_forward_noalloc",
     "dbf_bqq_pack_grouped", "dbf_mx_code_bytes", "dbf_mx_scale_bytes", "dbf_mx_quantize", "dbf_mx_dequantize",
-    "dbf_mx_pack", "dbf_mx_forward", "dbf_mx_backward_data", "dbf_rms_norm", "dbf_rms_norm_backward_workspace",
+    "dbf_mx_pack", "dbf_mx_forward", "dbf_mx_forward_group", "dbf_mx_backward_data", "dbf_rms_norm", "dbf_rms_norm_backward_workspace",
     "dbf_rms_norm_backward",
 )
 
@@ -144,6 +144,8 @@ def lib() -> ctypes.CDLL:
     L.dbf_mx_pack.restype = ctypes.c_int
     L.dbf_mx_forward.argtypes = [vp, vp, i32, vp, vp, i32, i32, vp]
     L.dbf_mx_forward.restype = ctypes.c_int
+    L.dbf_mx_forward_group.argtypes = [ctypes.POINTER(vp), i32, vp, i32, vp, ctypes.POINTER(vp), i32, i32, vp]
+    L.dbf_mx_forward_group.restype = ctypes.c_int
     L.dbf_mx_backward_data.argtypes = [vp, vp, vp, i32, i32, vp]
     L.dbf_mx_backward_data.restype = ctypes.c_int
     L.dbf_rms_norm.argtypes = [vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp, i32, vp, vp, vp]
@@ -322,11 +324,19 @@ def dbf_linear_forward_group(hs, x_ptr: int, y_ptrs, batch: int, stream: int = 0
     _check(lib().dbf_linear_forward_group(harr, len(hs), x_ptr, yarr, batch, stream), "dbf_linear_forward_group")
 
 
-def forward_group(layers, x, outs=None):
+def forward_group(layers, x, outs=None, out_dtype=None):
     """ys[i] = layers[i](x) for Layer objects sharing the input width; one
-    pair of launches for all of them at decode batch sizes."""
+    pair of launches for all of them at decode batch sizes.
+
+    Where every layer is one of ``Layer.mx``, x may also be bfloat16 or an
+    MxTensor, and out_dtype float16 or bfloat16 (default: x's type, float16
+    for an MxTensor).
+    """
     import torch
-    if x.dtype != torch.float16 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
+    other = isinstance(x, MxTensor) or x.dtype == torch.bfloat16 or out_dtype not in (None, torch.float16)
+    if other and layers and all(L.act is not None for L in layers):
+        return _forward_group_mx(layers, x, outs, out_dtype)
+    if other or x.dtype != torch.float16 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D float16 CUDA tensor")
     if outs is None:
         outs = [torch.empty((x.shape[0], L.n), dtype=torch.float16, device=x.device) for L in layers]
@@ -340,6 +350,51 @@ def forward_group(layers, x, outs=None):
     dbf_linear_forward_group([L.handle for L in layers], x.data_ptr(), [y.data_ptr() for y in outs], x.shape[0],
                              stream)
     return outs
+
+
+def _forward_group_mx(layers, x, outs, out_dtype):
+    import torch
+    m = layers[0].m
+    if isinstance(x, MxTensor):
+        like, scales, xt, default = x.codes, x.scales.data_ptr(), _TYPE_NAMES[x.fmt], torch.float16
+        if x.cols != m:
+            raise ValueError(f"x must have {m} columns")
+    else:
+        _check_rows(x, "x")
+        like, scales, xt, default = x, None, _type_of(x.dtype), x.dtype
+        if x.shape[1] != m:
+            raise ValueError(f"x must have {m} columns")
+    batch = like.shape[0]
+    _check_count(batch, m)
+    if out_dtype is None:
+        out_dtype = outs[0].dtype if outs else default
+    if out_dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("the outputs are float16 or bfloat16")
+    if outs is None:
+        outs = [like.new_empty((batch, L.n), dtype=out_dtype) for L in layers]
+    if len(outs) != len(layers):
+        raise ValueError("one output per layer")
+    for L, y in zip(layers, outs):
+        if (y.dtype != out_dtype or tuple(y.shape) != (batch, L.n) or not y.is_contiguous()
+                or y.device != like.device):
+            raise ValueError("outs[i] must be a contiguous tensor of shape (batch, n_i) of one type on x's device")
+    n = len(layers)
+    _call("dbf_mx_forward_group", like, (ctypes.c_void_p * n)(*[L.handle for L in layers]), n, like.data_ptr(), xt,
+          scales, (ctypes.c_void_p * n)(*[y.data_ptr() for y in outs]), _type_of(out_dtype), batch)
+    return outs
+
+
+def norm_forward_group(layers, x, weight=None, residual=None, eps: float = 1e-6, outs=None):
+    """(ys, norm) with norm = rms_norm(x, weight, residual, eps) and ys[i] = layers[i](norm.y): the norm in front of
+    layers that share its result (gate and up, or q, k and v).
+
+    Where every layer is one of ``Layer.mx`` that takes e4m3 blocks, the norm
+    gives its rows in them and nothing is quantised again; otherwise they are
+    in x's type (float16 for the other kinds of layers).
+    """
+    mx = all(L.act == "e4m3" for L in layers)
+    norm = rms_norm(x, weight, residual, eps, mx=mx)
+    return forward_group(layers, norm.y, outs, x.dtype if mx else None), norm
 
 
 def dbf_linear_backward_data(h: int, dy_ptr: int, dx_ptr: int, batch: int, stream: int = 0) -> None:

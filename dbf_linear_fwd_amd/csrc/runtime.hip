@@ -947,9 +947,9 @@ static dbf_status_t forward_mx(dbf_layer *const *hs, int count, const void *x, i
     return st;
 }
 
-// Layers that share the f16 input, those of one activation format together.
-static dbf_status_t forward_mx_group(const dbf_handle_t *hs, int32_t count, const void *x, void *const *ys,
-                                     int32_t batch, hipStream_t stream) {
+// Layers that share 16-bit rows, those of one activation format together.
+static dbf_status_t forward_mx_group(const dbf_handle_t *hs, int32_t count, const void *x, int32_t x_type,
+                                     void *const *ys, int32_t y_type, int32_t batch, hipStream_t stream) {
     for (int32_t act : {DBF_TYPE_E4M3, DBF_TYPE_E2M1}) {
         dbf_layer *sel[dbf::kMaxGroup];
         void *out[dbf::kMaxGroup];
@@ -960,7 +960,7 @@ static dbf_status_t forward_mx_group(const dbf_handle_t *hs, int32_t count, cons
                 out[n++] = ys[i];
             }
         if (n == 0) continue;
-        const dbf_status_t st = forward_mx(sel, n, x, DBF_TYPE_F16, nullptr, out, DBF_TYPE_F16, batch, stream);
+        const dbf_status_t st = forward_mx(sel, n, x, x_type, nullptr, out, y_type, batch, stream);
         if (st != DBF_OK) return st;
     }
     return DBF_OK;
@@ -1031,22 +1031,37 @@ extern "C" dbf_status_t dbf_mx_pack(int32_t n, int32_t m, const void *codes, con
     return DBF_OK;
 }
 
-extern "C" dbf_status_t dbf_mx_forward(dbf_handle_t h, const void *x, int32_t x_type, const uint8_t *x_scales,
-                                       void *y, int32_t y_type, int32_t batch, hipStream_t stream) {
-    if (!h) return DBF_ERR_INVALID_ARG;
-    if (!h->mx) return DBF_ERR_UNSUPPORTED;
-    if (batch < 0 || batch > h->max_batch) return DBF_ERR_INVALID_ARG;
+extern "C" dbf_status_t dbf_mx_forward_group(const dbf_handle_t *hs, int32_t count, const void *x, int32_t x_type,
+                                             const uint8_t *x_scales, void *const *ys, int32_t y_type, int32_t batch,
+                                             hipStream_t stream) {
+    if (!hs || !ys || count < 1 || count > dbf::kMaxGroup || batch < 0) return DBF_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        if (!hs[i]) return DBF_ERR_INVALID_ARG;
+        if (!hs[i]->mx) return DBF_ERR_UNSUPPORTED;
+        if (hs[i]->m != hs[0]->m || hs[i]->device != hs[0]->device || batch > hs[i]->max_batch)
+            return DBF_ERR_INVALID_ARG;
+    }
     const bool real = x_type == DBF_TYPE_F16 || x_type == DBF_TYPE_BF16;
     if (!real && x_type != DBF_TYPE_E4M3 && x_type != DBF_TYPE_E2M1) return DBF_ERR_INVALID_ARG;
     if (y_type != DBF_TYPE_F16 && y_type != DBF_TYPE_BF16) return DBF_ERR_INVALID_ARG;
     if (batch == 0) return DBF_OK;
-    if (!x || !y || !aligned16(x) || !aligned16(y)) return DBF_ERR_INVALID_ARG;
+    if (!x || !aligned16(x)) return DBF_ERR_INVALID_ARG;
     if (real ? x_scales != nullptr : (!x_scales || (reinterpret_cast<uintptr_t>(x_scales) & 3u)))
         return DBF_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i)
+        if (!ys[i] || !aligned16(ys[i])) return DBF_ERR_INVALID_ARG;
     int cur = -1;
     if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
-    if (cur != h->device) return DBF_ERR_INVALID_ARG;
-    return forward_mx(&h, 1, x, x_type, x_scales, &y, y_type, batch, stream);
+    if (cur != hs[0]->device) return DBF_ERR_INVALID_ARG;
+    if (real) return forward_mx_group(hs, count, x, x_type, ys, y_type, batch, stream);
+    dbf_layer *all[dbf::kMaxGroup];
+    for (int i = 0; i < count; ++i) all[i] = hs[i];
+    return forward_mx(all, count, x, x_type, x_scales, ys, y_type, batch, stream);
+}
+
+extern "C" dbf_status_t dbf_mx_forward(dbf_handle_t h, const void *x, int32_t x_type, const uint8_t *x_scales,
+                                       void *y, int32_t y_type, int32_t batch, hipStream_t stream) {
+    return dbf_mx_forward_group(&h, 1, x, x_type, x_scales, &y, y_type, batch, stream);
 }
 
 extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, void *dx, int32_t type, int32_t batch,
@@ -1127,7 +1142,7 @@ extern "C" dbf_status_t dbf_linear_forward_group(const dbf_handle_t *hs, int32_t
     if (cur != hs[0]->device) return DBF_ERR_INVALID_ARG;
     int mx_layers = 0;
     for (int i = 0; i < count; ++i) mx_layers += hs[i]->mx ? 1 : 0;
-    if (mx_layers == count) return forward_mx_group(hs, count, x, ys, batch, stream);
+    if (mx_layers == count) return forward_mx_group(hs, count, x, DBF_TYPE_F16, ys, DBF_TYPE_F16, batch, stream);
     if (mx_layers > 0) {
         // layers of both kinds: each layer's own forward
         for (int i = 0; i < count; ++i) {

@@ -409,7 +409,7 @@ dbf_status_t dbf_mx_dequantize(const void *codes, const uint8_t *scales, int32_t
  * dbf_linear_forward_ex (paths AUTO, DECODE, PREFILL: the batch chooses the
  * kernel; TABLE and EXACT are DBF_ERR_UNSUPPORTED), dbf_linear_forward_group,
  * dbf_linear_forward_noalloc, dbf_linear_backward_data (no flag needed),
- * dbf_mx_forward, dbf_mx_backward_data, dbf_get_info, timing and dbf_free;
+ * dbf_mx_forward(_group), dbf_mx_backward_data, dbf_get_info, timing and dbf_free;
  * dbf_linear_backward is DBF_ERR_UNSUPPORTED (the weight is not trained).
  *   codes, scales  device, in the padded row layout above, 16-byte aligned;
  *                  read during the call and not retained.
@@ -437,9 +437,20 @@ dbf_status_t dbf_mx_pack(int32_t n, int32_t m, const void *codes, const uint8_t 
  * 2^-12 of the largest ones; e2m1 products are exact.)  A NaN block of x makes
  * its row NaN, a NaN block of the weight its output column.  Pointer, batch
  * and ordering rules as dbf_linear_forward.
+ *
+ * dbf_mx_forward_group -- the same for count handles of dbf_mx_pack that read
+ * the same x (1 <= count <= 8, one input width and device): ys[i] = x W_i^T,
+ * with the bits of each layer's own dbf_mx_forward.  Few rows (those whose
+ * blocks fit a compute unit's local memory, 16 at most) are one launch for all
+ * of them; 16-bit rows are quantised once for the layers of one act_type.
+ * Other rules as dbf_linear_forward_group; a handle of another kind is
+ * DBF_ERR_UNSUPPORTED.
  */
 dbf_status_t dbf_mx_forward(dbf_handle_t h, const void *x, int32_t x_type, const uint8_t *x_scales, void *y,
                             int32_t y_type, int32_t batch, hipStream_t stream);
+dbf_status_t dbf_mx_forward_group(const dbf_handle_t *hs, int32_t count, const void *x, int32_t x_type,
+                                  const uint8_t *x_scales, void *const *ys, int32_t y_type, int32_t batch,
+                                  hipStream_t stream);
 
 /*
  * dbf_mx_backward_data -- dx[r][l] = rne( Σ_o dy[r][o] W[o][l] ): the gradient

@@ -69,6 +69,32 @@ def test_forward_and_backward_refuse_a_null_handle():
     assert L.dbf_mx_backward_data(None, P, P, F16, 1, None) == E
 
 
+def test_forward_group_refusals():
+    L = dbf.lib()
+    one = (ctypes.c_void_p * 9)()
+    ys = (ctypes.c_void_p * 9)(*[4096] * 9)
+    f = lambda hs, n, y, b=1: L.dbf_mx_forward_group(hs, n, P, F16, None, y, F16, b, None)  # noqa: E731
+    assert f(None, 1, ys) == E and f(one, 1, None) == E
+    assert f(one, 0, ys) == E and f(one, 9, ys) == E and f(one, 1, ys, -1) == E
+    assert f(one, 2, ys) == E  # null handles
+
+
+def test_binding_group_refusals():
+    import torch
+
+    class Other:
+        act, n, m = None, 8, 64
+
+    for layers in ([Other()], []):
+        for t in (torch.float16, torch.bfloat16):
+            with pytest.raises(ValueError):
+                dbf.forward_group(layers, torch.zeros(1, 64, dtype=t))
+    with pytest.raises(ValueError):
+        dbf.forward_group([Other()], torch.zeros(1, 64, dtype=torch.float16), out_dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        dbf.norm_forward_group([Other()], torch.zeros(1, 64, dtype=torch.float16))
+
+
 def _norm(x=P, r=None, w=P, t=F16, wt=F16, rows=4, cols=8, eps=1e-6, h=None, y=P, yt=F16, ys=None, rstd=None):
     return dbf.lib().dbf_rms_norm(x, r, w, t, wt, rows, cols, eps, h, y, yt, ys, rstd, None)
 

@@ -411,6 +411,77 @@ def test_call_forms_agree(gpu, b):
             L.close()
 
 
+@pytest.mark.parametrize("b", [1, 5, 40, 300])
+def test_group_of_blocks_and_bf16(gpu, b):
+    """Layers that share blocks of either format, or bf16 rows: the bits of each layer's own forward."""
+    torch = _torch()
+    _say(f"mx group b={b}")
+    rng = np.random.default_rng(b)
+    m = 1000
+    layers = [dbf.Layer.mx(weight(rng, n, m)[0], max_batch=b, act=act)
+              for n, act in ((256, "e4m3"), (33, "e2m1"), (300, "e4m3"))]
+    try:
+        xd, _ = to_dev(rows_of(rng, b, m), "bf16")
+        for x in (xd, dbf.mx_quantize(xd, "e4m3"), dbf.mx_quantize(xd, "e2m1")):
+            for t in (torch.float16, torch.bfloat16):
+                own = [L.forward(x, out_dtype=t) for L in layers]
+                for y, o in zip(dbf.forward_group(layers, x, out_dtype=t), own):
+                    assert y.dtype == t and same_bits(y, o)
+                outs = [torch.empty_like(o) for o in own]
+                assert dbf.forward_group(layers, x, outs=outs)[0] is outs[0]
+                for y, o in zip(outs, own):
+                    assert same_bits(y, o)
+        with pytest.raises(ValueError):
+            dbf.forward_group(layers, xd, outs=[torch.empty_like(o) for o in own[:2]])
+        with pytest.raises(ValueError):
+            dbf.forward_group(layers, xd[:, :512].contiguous())
+        with pytest.raises(ValueError):
+            dbf.forward_group(layers, xd, out_dtype=torch.float32)
+        with pytest.raises(dbf.DbfError):
+            dbf.forward_group(layers, torch.cat([xd, xd]))  # above max_batch
+    finally:
+        for L in layers:
+            L.close()
+
+
+@pytest.mark.parametrize("b", [1, 3, 16, 70])
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+def test_norm_in_front_of_a_group(gpu, b, name):
+    """Norm and the layers behind it: blocks where all take e4m3, 16 bits otherwise, sign layers among them."""
+    torch = _torch()
+    _say(f"norm and group b={b} {name}")
+    rng = np.random.default_rng(b)
+    m = 256
+    up, gate = (dbf.Layer.mx(weight(rng, 400, m)[0], max_batch=b) for _ in range(2))
+    low = dbf.Layer.mx(weight(rng, 96, m)[0], max_batch=b, act="e2m1")
+    R = inputs.random_layer("norm group", 64, m, 128, 0, 0.05, 0.05, 0.05, (b,))
+    signs = dbf.Layer(R.A, R.B, R.a, R.mid, R.b, max_batch=b)
+    try:
+        x, _ = to_dev(rows_of(rng, b, m), name)
+        r, _ = to_dev(rows_of(rng, b, m), name)
+        w, _ = to_dev(1 + 0.1 * rng.standard_normal(m), name)
+        q = dbf.rms_norm(x, w, residual=r, eps=1e-5, mx=True)
+        ys, norm = dbf.norm_forward_group([up, gate], x, w, residual=r, eps=1e-5)
+        assert isinstance(norm.y, dbf.MxTensor) and torch.equal(norm.y.codes, q.y.codes) and same_bits(norm.h, q.h)
+        for y, L in zip(ys, (up, gate)):
+            assert y.dtype == x.dtype and same_bits(y, L.forward(q.y, out_dtype=x.dtype))
+        plain = dbf.rms_norm(x, w, residual=r, eps=1e-5)
+        ys, norm = dbf.norm_forward_group([up, low], x, w, residual=r, eps=1e-5)
+        assert same_bits(norm.y, plain.y)
+        for y, L in zip(ys, (up, low)):
+            assert same_bits(y, L(plain.y))
+        if name == "f16":
+            ys, norm = dbf.norm_forward_group([signs, up], x, w, residual=r, eps=1e-5)
+            for y, L in zip(ys, (signs, up)):
+                assert same_bits(y, L(plain.y))
+        else:
+            with pytest.raises(ValueError):
+                dbf.norm_forward_group([signs, up], x, w, residual=r)
+    finally:
+        for L in (up, gate, low, signs):
+            L.close()
+
+
 @pytest.mark.parametrize("b,m", [(16, 9216), (16, 8192), (13, 4100), (4, 16512)])
 def test_call_forms_agree_at_wide_inputs(gpu, b, m):
     """Few rows on either side of what fits LDS, of what the product quantises itself, and of the widest input."""
