@@ -315,8 +315,9 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
     // kt + 1, the weight's codes of steps kt + 1 and kt + 2 (slots kt % 2
     // again).  The operands of each of its four times 16 rows are read beside the
     // products before; the next step's weight is converted beside the first
-    // three, its codes read before them.  The loads run on past the last step, to no use: a branch around
-    // them would have the compiler move the products behind it.
+    // three, its codes read before them.  The loads run on past the last step, to
+    // no use: a branch around them would have the compiler move the products
+    // behind it.
     Frags f0, f1;
     load_w(0);
     load_w(1);
@@ -326,9 +327,10 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
     take_w();
 #pragma unroll
     for (int j = 0; j < 4; ++j) put_w(0, j);
+    keep_order();  // (step 0's codes have been read)
     load_w(0);
     load_dy(1);
-    if constexpr (Dma) wait_vm<C::DA + DW>();
+    wait_vm<(Dma ? C::DA : 0) + DW>();
     wait_lds();
     block_barrier();
     load_frags(0, 0, 0, f0);
