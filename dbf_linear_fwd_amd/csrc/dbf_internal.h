@@ -303,10 +303,17 @@ int launch_mx_dequantize(const void *codes, const uint8_t *scales, int fmt, int 
 int launch_mx_layout(const void *codes, const uint8_t *scales, int n, int m, uint8_t *out_codes, uint8_t *out_scales,
                      uint8_t *colmax, void *stream);
 
+// How a tiled product runs: which of its tiles, and in how many K parts (more
+// than one: the product's launch leaves fp32 sums, and a join follows it).
+struct MxPlan {
+    int tile = 0, nsplit = 1;
+};
+
 // y (M x n, y_type f16 / bf16) = x wᵀ with x in blocks: codes in padded rows
 // of w.blocks blocks (x_type e4m3 / e2m1), scales in 32-row tiles like the
 // weight's (launch_mx_tile_scales, or launch_mx_quantize with tiled).  part:
-// at least mx_product_parts() floats for the sums of K parts.
+// at least mx_product_parts() floats for the sums of K parts.  Where the plan
+// has K parts, launch_mx_product_join is the second launch.
 struct MxProduct {
     const void *xcodes = nullptr;
     const uint8_t *xscales = nullptr;
@@ -316,14 +323,17 @@ struct MxProduct {
     int y_type = 0;
     float *part = nullptr;
     size_t part_cap = 0;
+    MxPlan plan;
 };
+MxPlan mx_product_plan(int M, int n, int blocks, int x_type);
 // Floats of K-part sums that the product of this shape uses (0: K whole).
 size_t mx_product_parts(int M, int n, int blocks, int x_type);
 // Padded scale rows into 32-row tiles: round_up(M, 32) * blocks bytes.
 int launch_mx_tile_scales(const uint8_t *xs, int M, int blocks, uint8_t *out, void *stream);
 int launch_mx_product(const MxProduct &p, void *stream);
+int launch_mx_product_join(const MxProduct &p, void *stream);
 // dx (M x m) = dy (M x n) w, both f16 or bf16 (type).  zeros: 16 zero bytes
-// on the device; part: at least mx_backward_parts() floats.
+// on the device; part: at least mx_backward_parts() floats.  The join as above.
 struct MxBackward {
     const void *dy = nullptr, *zeros = nullptr;
     int type = 0, M = 0;
@@ -331,9 +341,12 @@ struct MxBackward {
     void *dx = nullptr;
     float *part = nullptr;
     size_t part_cap = 0;
+    MxPlan plan;
 };
+MxPlan mx_backward_plan(int M, int n, int m);
 size_t mx_backward_parts(int M, int n, int m);
 int launch_mx_backward(const MxBackward &b, void *stream);
+int launch_mx_backward_join(const MxBackward &b, void *stream);
 
 }  // namespace dbf
 

@@ -344,10 +344,6 @@ constexpr TileCost kTiles[] = {
 constexpr int kTileCount = sizeof(kTiles) / sizeof(kTiles[0]);
 constexpr int kCus = 256;
 
-struct MxPlan {
-    int tile = 0, nsplit = 1;
-};
-
 // The tile and K parts of least estimated time: rounds of workgroups over the
 // CUs, each a start of 3 us and its steps; K parts add a launch and the
 // traffic of their fp32 sums.  (2048 x 14336, K 4096, e4m3: 256 x 256 tiles
@@ -395,8 +391,9 @@ struct TileOf<FMT, 4> { using C = MxTile<FMT, 1, 1, 2, 2, FMT == DBF_TYPE_E4M3 ?
 template <int FMT>
 struct TileOf<FMT, 5> { using C = MxTile<FMT, 1, 1, 1, 2, FMT == DBF_TYPE_E4M3 ? 16 : 12>; };
 
+// The product's launch, or the join of its K parts.
 template <typename C, typename E>
-void launch_gemm(MxGemmArgs &a, hipStream_t s) {
+void launch_gemm(MxGemmArgs &a, bool join, hipStream_t s) {
     auto product = mx_gemm_kernel<C, E>;
     auto finish = mx_finish_kernel<C, E>;
     static std::atomic<uint64_t> lds_product{0};
@@ -404,28 +401,61 @@ void launch_gemm(MxGemmArgs &a, hipStream_t s) {
     t.nbm = (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.n + C::BN - 1) / C::BN;
     t.group = t.nbm < 4 ? t.nbm : 4;
+    if (join) {
+        launch_kernel(finish, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
+        return;
+    }
     if constexpr (C::Lds > 65536) allow_lds(product, C::Lds, lds_product);
     launch_kernel(product, dim3(t.nbm * t.nbn * t.nsplit), dim3(C::Threads), C::Lds, s, a);
-    if (a.part) launch_kernel(finish, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
 }
 
 template <int FMT, typename E, int T = 0>
-void launch_tile(int tile, MxGemmArgs &a, hipStream_t s) {
+void launch_tile(int tile, MxGemmArgs &a, bool join, hipStream_t s) {
     if constexpr (T < kTileCount) {
         using C = typename TileOf<FMT, T>::C;
         static_assert(C::BM == kTiles[T].bm && C::BN == kTiles[T].bn, "the table's tile");
-        if (tile == T) launch_gemm<C, E>(a, s);
-        else launch_tile<FMT, E, T + 1>(tile, a, s);
+        if (tile == T) launch_gemm<C, E>(a, join, s);
+        else launch_tile<FMT, E, T + 1>(tile, a, join, s);
     }
+}
+
+// Floats of the sums of a plan's K parts.
+size_t part_floats(const MxPlan &p, int M, int n) {
+    if (p.nsplit == 1) return 0;
+    const TileCost &c = kTiles[p.tile];
+    return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((n + c.bn - 1) / c.bn * c.bn);
+}
+
+int launch_either(const MxProduct &p, bool join, void *stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p.plan.nsplit > 1 && (!p.part || p.part_cap < part_floats(p.plan, p.M, p.w.n)))
+        return static_cast<int>(hipErrorInvalidValue);
+    MxGemmArgs a{};
+    a.xc = static_cast<const uint8_t *>(p.xcodes);
+    a.xs = p.xscales;
+    a.M = p.M;
+    a.w = p.w;
+    a.y = p.y;
+    a.grid.nsplit = p.plan.nsplit;
+    a.part = p.plan.nsplit > 1 ? p.part : nullptr;
+    auto pick = [&](auto f) {
+        constexpr int FMT = decltype(f)::value;
+        if (p.y_type == DBF_TYPE_F16) launch_tile<FMT, F16>(p.plan.tile, a, join, s);
+        else launch_tile<FMT, BF16>(p.plan.tile, a, join, s);
+    };
+    if (p.x_type == DBF_TYPE_E4M3) pick(Const<DBF_TYPE_E4M3>{});
+    else pick(Const<DBF_TYPE_E2M1>{});
+    return static_cast<int>(hipGetLastError());
 }
 
 }  // namespace
 
+MxPlan mx_product_plan(int M, int n, int blocks, int x_type) {
+    return mx_plan(M, n, blocks / 4, x_type == DBF_TYPE_E4M3);
+}
+
 size_t mx_product_parts(int M, int n, int blocks, int x_type) {
-    const MxPlan p = mx_plan(M, n, blocks / 4, x_type == DBF_TYPE_E4M3);
-    if (p.nsplit == 1) return 0;
-    const TileCost &c = kTiles[p.tile];
-    return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((n + c.bn - 1) / c.bn * c.bn);
+    return part_floats(mx_product_plan(M, n, blocks, x_type), M, n);
 }
 
 int launch_mx_tile_scales(const uint8_t *xs, int M, int blocks, uint8_t *out, void *stream) {
@@ -437,27 +467,8 @@ int launch_mx_tile_scales(const uint8_t *xs, int M, int blocks, uint8_t *out, vo
     return static_cast<int>(hipGetLastError());
 }
 
-int launch_mx_product(const MxProduct &p, void *stream) {
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    MxGemmArgs a{};
-    a.xc = static_cast<const uint8_t *>(p.xcodes);
-    a.xs = p.xscales;
-    a.M = p.M;
-    a.w = p.w;
-    a.y = p.y;
-    const MxPlan plan = mx_plan(p.M, p.w.n, p.w.blocks / 4, p.x_type == DBF_TYPE_E4M3);
-    a.grid.nsplit = plan.nsplit;
-    a.part = plan.nsplit > 1 ? p.part : nullptr;
-    if (plan.nsplit > 1 && (!p.part || p.part_cap < mx_product_parts(p.M, p.w.n, p.w.blocks, p.x_type)))
-        return static_cast<int>(hipErrorInvalidValue);
-    auto pick = [&](auto f) {
-        constexpr int FMT = decltype(f)::value;
-        if (p.y_type == DBF_TYPE_F16) launch_tile<FMT, F16>(plan.tile, a, s);
-        else launch_tile<FMT, BF16>(plan.tile, a, s);
-    };
-    if (p.x_type == DBF_TYPE_E4M3) pick(Const<DBF_TYPE_E4M3>{});
-    else pick(Const<DBF_TYPE_E2M1>{});
-    return static_cast<int>(hipGetLastError());
-}
+int launch_mx_product(const MxProduct &p, void *stream) { return launch_either(p, false, stream); }
+
+int launch_mx_product_join(const MxProduct &p, void *stream) { return launch_either(p, true, stream); }
 
 }  // namespace dbf

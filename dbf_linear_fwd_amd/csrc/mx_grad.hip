@@ -409,16 +409,12 @@ constexpr GradCost kGrad[] = {
 constexpr int kGradCount = sizeof(kGrad) / sizeof(kGrad[0]);
 constexpr int kCus = 256;
 
-struct GradPlan {
-    int tile = 0, nsplit = 1;
-};
-
 // The tile and K parts of least estimated time; K parts add a launch and the
 // traffic of their fp32 sums.  (2048 rows, n 14336, m 4096, bf16: 256 x 256
 // tiles in two parts 237 us, whole 314, 128 x 128 tiles 273; 512 rows: 128 x
 // 128 in four parts 78, whole 144; 16 rows: 32 x 128 in eight parts 23, whole 105.)
-GradPlan grad_plan(int M, int n, int m) {
-    GradPlan best;
+MxPlan grad_plan(int M, int n, int m) {
+    MxPlan best;
     float least = 0.0f;
     const int steps = (n + 63) / 64;
     for (int t = 0; t < kGradCount; ++t) {
@@ -442,13 +438,19 @@ GradPlan grad_plan(int M, int n, int m) {
     return best;
 }
 
+// The product's launch, or the join of its K parts.
 template <typename C, typename E>
-void launch_grad(MxGradArgs &a, hipStream_t s) {
+void launch_grad(MxGradArgs &a, bool join, hipStream_t s) {
     static std::atomic<uint64_t> lds0{0}, lds1{0}, lds2{0};
     TileGrid &t = a.grid;
     t.nbm = (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.m + C::BN - 1) / C::BN;
     t.group = t.nbm < 4 ? t.nbm : 4;
+    if (join) {
+        auto k = mx_grad_finish_kernel<C, E>;
+        launch_kernel(k, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
+        return;
+    }
     const dim3 grid(t.nbm * t.nbn * t.nsplit);
     auto go = [&](auto rows, std::atomic<uint64_t> &asked) {
         auto k = mx_grad_kernel<C, E, decltype(rows)::value>;
@@ -460,43 +462,46 @@ void launch_grad(MxGradArgs &a, hipStream_t s) {
         go(std::integral_constant<GradRows, GradRows::Whole>{}, lds0);
     else if (a.w.n % 8 == 0) go(std::integral_constant<GradRows, GradRows::Rows16>{}, lds1);
     else go(std::integral_constant<GradRows, GradRows::Elements>{}, lds2);
-    if (a.part) {
-        auto k = mx_grad_finish_kernel<C, E>;
-        launch_kernel(k, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
-    }
 }
 
-}  // namespace
-
-size_t mx_backward_parts(int M, int n, int m) {
-    const GradPlan p = grad_plan(M, n, m);
+// Floats of the sums of a plan's K parts.
+size_t part_floats(const MxPlan &p, int M, int m) {
     if (p.nsplit == 1) return 0;
     const GradCost &c = kGrad[p.tile];
     return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((m + c.bn - 1) / c.bn * c.bn);
 }
 
-int launch_mx_backward(const MxBackward &b, void *stream) {
+int launch_either(const MxBackward &b, bool join, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const GradPlan plan = grad_plan(b.M, b.w.n, b.w.m);
+    if (b.plan.nsplit > 1 && (!b.part || b.part_cap < part_floats(b.plan, b.M, b.w.m)))
+        return static_cast<int>(hipErrorInvalidValue);
     MxGradArgs a{};
     a.dy = b.dy;
     a.zeros = b.zeros;
     a.M = b.M;
     a.w = b.w;
     a.dx = b.dx;
-    a.grid.nsplit = plan.nsplit;
-    a.part = plan.nsplit > 1 ? b.part : nullptr;
-    if (plan.nsplit > 1 && (!b.part || b.part_cap < mx_backward_parts(b.M, b.w.n, b.w.m)))
-        return static_cast<int>(hipErrorInvalidValue);
+    a.grid.nsplit = b.plan.nsplit;
+    a.part = b.plan.nsplit > 1 ? b.part : nullptr;
     auto go = [&](auto e) {
         using E = decltype(e);
-        if (plan.tile == 0) launch_grad<GradTile<4, 2, 2, 4>, E>(a, s);
-        else if (plan.tile == 1) launch_grad<GradTile<2, 2, 2, 2>, E>(a, s);
-        else launch_grad<GradTile<1, 1, 1, 4>, E>(a, s);
+        if (b.plan.tile == 0) launch_grad<GradTile<4, 2, 2, 4>, E>(a, join, s);
+        else if (b.plan.tile == 1) launch_grad<GradTile<2, 2, 2, 2>, E>(a, join, s);
+        else launch_grad<GradTile<1, 1, 1, 4>, E>(a, join, s);
     };
     if (b.type == DBF_TYPE_BF16) go(BF16{});
     else go(F16{});
     return static_cast<int>(hipGetLastError());
 }
+
+}  // namespace
+
+MxPlan mx_backward_plan(int M, int n, int m) { return grad_plan(M, n, m); }
+
+size_t mx_backward_parts(int M, int n, int m) { return part_floats(grad_plan(M, n, m), M, m); }
+
+int launch_mx_backward(const MxBackward &b, void *stream) { return launch_either(b, false, stream); }
+
+int launch_mx_backward_join(const MxBackward &b, void *stream) { return launch_either(b, true, stream); }
 
 }  // namespace dbf

@@ -942,7 +942,10 @@ static dbf_status_t forward_mx(dbf_layer *const *hs, int count, const void *x, i
         p.y = ys[i];
         p.part = hs[i]->split;
         p.part_cap = hs[i]->split_cap;
+        p.plan = dbf::mx_product_plan(batch, p.w.n, p.w.blocks, act);
         st = timed_launch(h, "mx_product", stream, [&] { return dbf::launch_mx_product(p, stream); });
+        if (st == DBF_OK && p.plan.nsplit > 1)
+            st = timed_launch(h, "mx_product_join", stream, [&] { return dbf::launch_mx_product_join(p, stream); });
     }
     return st;
 }
@@ -1084,7 +1087,11 @@ extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, voi
     b.dx = dx;
     b.part = h->split;
     b.part_cap = h->split_cap;
-    return timed_launch(h, "mx_backward", stream, [&] { return dbf::launch_mx_backward(b, stream); });
+    b.plan = dbf::mx_backward_plan(batch, h->n, h->m);
+    dbf_status_t st = timed_launch(h, "mx_backward", stream, [&] { return dbf::launch_mx_backward(b, stream); });
+    if (st == DBF_OK && b.plan.nsplit > 1)
+        st = timed_launch(h, "mx_backward_join", stream, [&] { return dbf::launch_mx_backward_join(b, stream); });
+    return st;
 }
 
 extern "C" dbf_status_t dbf_linear_forward_ex(dbf_handle_t h, const void *x, void *y, int32_t batch, int32_t path,
