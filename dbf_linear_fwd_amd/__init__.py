@@ -329,14 +329,13 @@ def forward_group(layers, x, outs=None, out_dtype=None):
     pair of launches for all of them at decode batch sizes.
 
     Where every layer is one of ``Layer.mx``, x may also be bfloat16 or an
-    MxTensor, and out_dtype float16 or bfloat16 (default: x's type, float16
-    for an MxTensor).
+    MxTensor, and the results float16 or bfloat16: out_dtype, by default the
+    type of outs, without them x's (float16 for an MxTensor).
     """
     import torch
-    other = isinstance(x, MxTensor) or x.dtype == torch.bfloat16 or out_dtype not in (None, torch.float16)
-    if other and layers and all(L.act is not None for L in layers):
+    if layers and all(L.act is not None for L in layers):
         return _forward_group_mx(layers, x, outs, out_dtype)
-    if other or x.dtype != torch.float16 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
+    if isinstance(x, MxTensor) or out_dtype not in (None, torch.float16) or x.dtype != torch.float16 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D float16 CUDA tensor")
     if outs is None:
         outs = [torch.empty((x.shape[0], L.n), dtype=torch.float16, device=x.device) for L in layers]
@@ -390,11 +389,15 @@ def norm_forward_group(layers, x, weight=None, residual=None, eps: float = 1e-6,
 
     Where every layer is one of ``Layer.mx`` that takes e4m3 blocks, the norm
     gives its rows in them and nothing is quantised again; otherwise they are
-    in x's type (float16 for the other kinds of layers).
+    in x's type (float16 for the other kinds of layers).  The results are in
+    the type of outs, without them in x's.
     """
+    import torch
+    if x.dtype != torch.float16 and not all(L.act is not None for L in layers):
+        raise ValueError("x must be float16 for layers that are not of Layer.mx")
     mx = all(L.act == "e4m3" for L in layers)
     norm = rms_norm(x, weight, residual, eps, mx=mx)
-    return forward_group(layers, norm.y, outs, x.dtype if mx else None), norm
+    return forward_group(layers, norm.y, outs, x.dtype if mx and not outs else None), norm
 
 
 def dbf_linear_backward_data(h: int, dy_ptr: int, dx_ptr: int, batch: int, stream: int = 0) -> None:
