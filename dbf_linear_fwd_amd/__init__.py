@@ -337,6 +337,8 @@ def forward_group(layers, x, outs=None, out_dtype=None):
         return _forward_group_mx(layers, x, outs, out_dtype)
     if isinstance(x, MxTensor) or out_dtype not in (None, torch.float16) or x.dtype != torch.float16 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D float16 CUDA tensor")
+    if any(L.m != x.shape[1] for L in layers):
+        raise ValueError("x must have the layers' input width")
     if outs is None:
         outs = [torch.empty((x.shape[0], L.n), dtype=torch.float16, device=x.device) for L in layers]
     if len(outs) != len(layers):
