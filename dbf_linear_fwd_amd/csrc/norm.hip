@@ -5,11 +5,12 @@
 //
 // Every kernel reads a row once and keeps it in registers, eight consecutive
 // columns per lane and chunk, so both directions are bound by memory; the
-// gradient's next row is on its way while one is reduced and written.  Sums
-// are fp32 over eight columns or the rows of a lane.  A row's mean of squares
-// is joined in fp64: its error shifts the whole row at once, and in blocks that
-// shows as codes on the other side of a tie.  All joins are in a fixed order
-// (no atomics: repeated calls give the same bits).
+// gradient's next row is on its way while one is reduced and written.  A row's
+// squares are formed and added in fp64: a bf16 row's may be far outside of
+// fp32, and an error of their mean shifts the whole row at once, which in
+// blocks shows as codes on the other side of a tie.  The gradient's sums are
+// fp32, over the columns or the rows of a lane.  All joins are in a fixed
+// order (no atomics: repeated calls give the same bits).
 // y leaves in 16 bits, or in e4m3 blocks of 32 columns with one scale each,
 // quantised from the fp32 values: four neighbouring lanes hold a block.
 //
@@ -141,13 +142,14 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void rms_norm_kernel(const N
             for (int i = 0; i < 8; ++i) h[c][i] = E::get(E::put(h[c][i] + v[i]));
             if (a.h) store8<E, VEC>(static_cast<T *>(a.h) + base + col, a.cols - col, h[c]);
         }
-        float part = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part = fmaf(h[c][i], h[c][i], part);
-        sum += part;
+        for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(h[c][i]), static_cast<double>(h[c][i]), sum);
     }
     sum = row_sum<LPR>(sum, red);
-    const float rstd = static_cast<float>(rsqrt(sum / a.cols + static_cast<double>(a.eps)));
+    const double square = sum / a.cols + static_cast<double>(a.eps);
+    // 0 where 1 / rms is below fp32's normal numbers: fewer bits than the gradient needs
+    const double inv = square >= 0x1p252 ? 0.0 : rsqrt(square);
+    const float rstd = static_cast<float>(inv);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     const int wide = (a.cols + 127) / 128 * 128;
     if constexpr (MX) mx_saturate(true);
