@@ -15,8 +15,8 @@
 // quantised from the fp32 values: four neighbouring lanes hold a block.
 //
 // bf16, operands from HBM, graph replays: norm with residual 8192 x 4096
-// 54 us (4.95 TB/s moved; a plain large copy 4.6), with block output 51 us,
-// 2048 x 4096 14.6 and 16.4, one row 2.8 and 3.1; gradient with dh 8192 x 4096
+// 56 us (4.8 TB/s moved; squares in fp32 54), with block output 52 us,
+// 2048 x 4096 15.2 and 17.9, one row 3.2 and 3.6; gradient with dh 8192 x 4096
 // 57 us (4.7 TB/s), 2048 x 4096 22 (a second launch and the parts of dw),
 // 65536 x 128 20.
 
@@ -148,9 +148,19 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void rms_norm_kernel(const N
     sum = row_sum<LPR>(sum, red);
     const double square = sum / a.cols + static_cast<double>(a.eps);
     // 0 where 1 / rms is below fp32's normal numbers: fewer bits than the gradient needs
-    const double inv = square >= 0x1p252 ? 0.0 : rsqrt(square);
-    const float rstd = static_cast<float>(inv);
-    if (a.rstd && t == 0) a.rstd[row] = rstd;
+    double inv = square >= 0x1p252 ? 0.0 : rsqrt(square);
+    if (a.rstd && t == 0) a.rstd[row] = static_cast<float>(inv);
+    // Rows far from 1 go by a power of two first: no product below leaves
+    // fp32's range where the result does not (for weights below 2^104).
+    if (!(inv >= 0x1p-16 && inv <= 0x1p16) && inv != 0.0) {
+        int ex = 0;
+        inv = frexp(inv, &ex);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[c][i] = ldexpf(h[c][i], ex);
+    }
+    const float rstd = static_cast<float>(inv), low = static_cast<float>(inv - static_cast<double>(rstd));
     const int wide = (a.cols + 127) / 128 * 128;
     if constexpr (MX) mx_saturate(true);
 #pragma unroll
@@ -159,6 +169,25 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void rms_norm_kernel(const N
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = h[c][i] * rstd * w[c][i];
+        if constexpr (MX) {
+            // Codes show an error of the last fp32 bit where a value is next
+            // to the middle of two: one rounding of the product with rstd +
+            // low (48 bits), as from 64 bits.  2048 x 4096 17.9 us; three
+            // fp32 roundings 17.5, products in fp64 18.7.
+            if (!a.w_f32) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p = h[c][i] * w[c][i];  // exact: 11 or 8 bits each
+                    y[i] = fmaf(p, rstd, p * low);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float q = h[c][i] * rstd;
+                    y[i] = fmaf(q, w[c][i], fmaf(h[c][i], low, fmaf(h[c][i], rstd, -q)) * w[c][i]);
+                }
+            }
+        }
         if constexpr (MX) {
             if (col < wide) {
                 if (col >= a.cols) {  // padding of the row: zero codes and scales whatever rstd is

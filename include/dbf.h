@@ -480,7 +480,8 @@ dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, void *dx, int3
  *             16-bit y may be x or residual itself (not h).
  *   rstd      out, fp32, rows; or NULL.
  * The mean of squares is fp64, products are fp32, one rounding to each output;
- * a row's result does not depend on the other rows.  A NaN in h makes its row
+ * e4m3 codes are those of the exact values rounded once to fp32.  A row's
+ * result does not depend on the other rows.  A NaN in h makes its row
  * NaN.  Where mean(h^2) + eps is 2^252 or more (an infinity in h, or a row
  * whose 1 / rms is below fp32's normal numbers), rstd is 0 (y is 0 for finite
  * h, NaN for infinite).  Pointers 16-byte aligned (scales, rstd: 4); 1 <= cols <= 32768
