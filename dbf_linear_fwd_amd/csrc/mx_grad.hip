@@ -6,10 +6,10 @@
 // the weight becomes 16-bit values on the way, on the 32x32x16 instructions
 // (2.5 PFLOP/s).  Per 64 rows of the weight a thread takes one block (one row,
 // 32 columns) and widens its codes relative to the largest scale of their
-// block column, code * 2^(s - smax + 13), into LDS; the transposing LDS read
+// block column, code * 2^(s - smax + kShift), into LDS; the transposing LDS read
 // hands a lane the rows of its column.  f16 holds the codes exactly down to
 // scales of 2^-28 of the largest and below; the sums are multiplied by
-// 2^(smax - 13) at the end.  (As bytes in LDS, e5m2 of the same values,
+// 2^(smax - kShift) at the end.  (As bytes in LDS, e5m2 of the same values,
 // widened again by every wave that reads them: 243 instead of 237 us.)
 //
 // 2048 rows, n 14336, m 4096, bf16: 237 us, 1.02 PFLOP/s (205 us, 1.17, with
@@ -27,7 +27,11 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kShift = 13;  // 6 * 2^13 is within f16
+// Exponent that the largest scale of a block column stands at: in f16 the
+// largest code, 6 * 2^13, is within the type and the small ones reach furthest
+// down; bf16 has fp32's range, and a sum overflows where dy's own does.
+template <typename E>
+constexpr int kShift = E::code == DBF_TYPE_F16 ? 13 : 0;
 
 // Waves WM x WN, each MI x NI fragments of 32 x 32.
 template <int MI_, int NI_, int WM_, int WN_>
@@ -60,9 +64,10 @@ struct MxGradArgs {
     float *part;
 };
 
-// The factor of a block's codes: 2^(s - smax + 13).
+// The factor of a block's codes: 2^(s - smax + kShift).
+template <typename E>
 __device__ __forceinline__ float block_scale(int s, int smax) {
-    const int e = 127 + kShift - smax + s;
+    const int e = 127 + kShift<E> - smax + s;
     const uint32_t bits = s == 255 ? 0x7fc00000u : static_cast<uint32_t>(e > 0 ? e : 0) << 23;
     return __builtin_bit_cast(float, bits);
 }
@@ -107,13 +112,13 @@ __device__ __forceinline__ f32x16 product(u32v4 w, u32v4 d, f32x16 acc) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, d), acc, 0, 0, 0);
 }
 
-// The sums times 2^(smax - 13) of their block column.
-template <typename C>
+// The sums times 2^(smax - kShift) of their block column.
+template <typename C, typename E>
 __device__ __forceinline__ void scale_columns(f32x16 (&acc)[C::MI][C::NI], const MxWeight &w, int n0, int wn) {
 #pragma unroll
     for (int f = 0; f < C::NI; ++f) {
         const int kb = min(n0 / 32 + wn * C::NI + f, w.blocks - 1);
-        const int e = static_cast<int>(w.colmax[kb]) - 127 - kShift;
+        const int e = static_cast<int>(w.colmax[kb]) - 127 - kShift<E>;
 #pragma unroll
         for (int i = 0; i < C::MI; ++i)
 #pragma unroll
@@ -238,7 +243,7 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
         for (int i = 0; i < C::NB; ++i) {
             const int sb = static_cast<int>(wsw[i] >> (8 * (kb[i] & 3)) & 255u);
             if (past) wcodes[i] = u32v4{0u, 0u, 0u, 0u};
-            wscale[i] = block_scale(past ? 0 : sb, smax[i]);
+            wscale[i] = block_scale<E>(past ? 0 : sb, smax[i]);
         }
         wrow += C::BK;
     };
@@ -374,7 +379,7 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
         store_part<C>(part_at<C>(a.part, split, T, tile, wave, lane), acc);
         return;
     }
-    scale_columns<C>(acc, a.w, n0, wn);
+    scale_columns<C, E>(acc, a.w, n0, wn);
     store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.dx, a.M, a.w.m, m0, n0, wave, lane);
 }
 
@@ -388,7 +393,7 @@ __global__ __launch_bounds__(64) void mx_grad_finish_kernel(const MxGradArgs a) 
     f32x16 acc[C::MI][C::NI];
     add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
                  a.grid.nsplit, acc);
-    scale_columns<C>(acc, a.w, bn * C::BN, wave % C::WN);
+    scale_columns<C, E>(acc, a.w, bn * C::BN, wave % C::WN);
     store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, bm * C::BM, bn * C::BN, wave, lane);
 }
 
