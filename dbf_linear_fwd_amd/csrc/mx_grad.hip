@@ -8,8 +8,9 @@
 // 32 columns) and widens its codes relative to the largest scale of their
 // block column, code * 2^(s - smax + kShift), into LDS; the transposing LDS read
 // hands a lane the rows of its column.  f16 holds the codes exactly down to
-// scales of 2^-28 of the largest and below; the sums are multiplied by
-// 2^(smax - kShift) at the end.  (As bytes in LDS, e5m2 of the same values,
+// scales of 2^-36 of the largest (0.5 is 2^-24 then), bf16 to 2^-125; smaller
+// ones lose bits or vanish.  The sums are multiplied by 2^(smax - kShift) at
+// the end.  (As bytes in LDS, e5m2 of the same values,
 // widened again by every wave that reads them: 243 instead of 237 us.)
 //
 // 2048 rows, n 14336, m 4096, bf16: 237 us, 1.02 PFLOP/s (205 us, 1.17, with

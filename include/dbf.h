@@ -458,7 +458,9 @@ dbf_status_t dbf_mx_forward_group(const dbf_handle_t *hs, int32_t count, const v
  * quantisation).  dy batch x n and dx batch x m, both of `type` (f16 or
  * bf16).  The weight's values enter the 16-bit matrix cores relative to the
  * largest scale of their block of 32 columns (over all rows): exact where
- * their scale is at least 2^-28 of it; smaller ones lose bits or vanish.
+ * their scale is at least 2^-36 (f16) or 2^-125 (bf16) of it; smaller ones
+ * lose bits or vanish.  The fp32 sums hold dy times codes of at most 6
+ * (bf16), or 6 * 2^13 (f16).
  * Products accumulate in fp32.  Pointer, batch and ordering rules as
  * dbf_linear_forward.
  */

@@ -10,7 +10,7 @@ import pytest
 
 import dbf_linear_fwd_amd as dbf
 from oracle import mx_oracle as O
-from tests.test_mx_gpu import half_step, rows_of, tiny, to_dev, weight
+from tests.test_mx_gpu import blocks_to_dev, half_step, rows_of, tiny, to_dev, weight
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,26 @@ def test_rows_of_any_magnitude(gpu, b, n, m, power):
     tol = half_step("bf16") * (np.abs(ref) + acc * mag) + acc * mag + tiny("bf16")
     d = np.abs(dx - ref)
     assert np.all(d <= tol), float((d / tol).max())
+
+
+@pytest.mark.parametrize("b,n,m", [(7, 192, 96), (130, 1030, 300)])
+@pytest.mark.parametrize("name,low", [("f16", 36), ("bf16", 125)])
+def test_smallest_exact_scales(gpu, name, low, b, n, m):
+    """Scales of 2^-36 (f16) and 2^-125 (bf16) of the block column's largest: every code enters exactly (0.5 is then
+    f16's smallest number and bf16's smallest normal one), the sums of whole numbers are exact in fp32, and one
+    rounding is left."""
+    _say(f"mx backward smallest scales {name} 2^-{low} b={b} n={n} m={m}")
+    rng = np.random.default_rng(low)
+    wc = rng.integers(0, 16, size=(n, m)).astype(np.uint8)
+    ws = np.full((n, -(-m // 32)), 127, dtype=np.uint8)
+    ws[-64:] = 127 + low
+    wc[-64:] = 0  # the large rows only set the common exponent
+    dyd, dyv = to_dev(rng.integers(-4, 5, size=(b, n)).astype(np.float64), name)
+    ref, mag = O.backward_data(dyv, O.values(wc, ws, "e2m1"))
+    assert (2 * mag).max() < 2 ** 24 and np.abs(ref).max() < 65504
+    L = dbf.Layer.mx(blocks_to_dev(wc, ws, m, "e2m1"), max_batch=b)
+    try:
+        dx = L.backward_data(dyd).double().cpu().numpy()
+    finally:
+        L.close()
+    assert np.all(np.abs(dx - ref) <= half_step(name) * np.abs(ref))
