@@ -33,7 +33,7 @@ __all__ = [
     "dbf_pack_ex", "dbf_linear_backward_data", "dbf_linear_backward", "DBF_PACK_BACKWARD", "dbf_bqq_pack",
     "dbf_factorize", "factorize", "dbf_linear_forward_noalloc", "dbf_bqq_pack_grouped",
     "DBF_TYPE_F16", "DBF_TYPE_BF16", "DBF_TYPE_F32", "DBF_TYPE_E4M3", "DBF_TYPE_E2M1", "MxTensor", "mx_quantize",
-    "dbf_mx_pack", "rms_norm", "RmsNormOutput", "rms_norm_backward", "norm_forward_group",
+    "dbf_mx_pack", "dbf_mx_forward_plan", "dbf_mx_backward_plan", "rms_norm", "RmsNormOutput", "rms_norm_backward", "norm_forward_group",
 ]
 
 DBF_OK = 0
@@ -65,8 +65,8 @@ EXPORTED_SYMBOLS = (
     "dbf_pack_signs", "dbf_layout_signs", "dbf_layout_words", "dbf_layout_signs_dec", "dbf_layout_words_dec",
     "dbf_timing_enable", "dbf_timing_read", "dbf_bqq_pack", "dbf_factorize", "dbf_linear_forward_noalloc",
     "dbf_bqq_pack_grouped", "dbf_mx_code_bytes", "dbf_mx_scale_bytes", "dbf_mx_quantize", "dbf_mx_dequantize",
-    "dbf_mx_pack", "dbf_mx_forward", "dbf_mx_forward_group", "dbf_mx_backward_data", "dbf_rms_norm", "dbf_rms_norm_backward_workspace",
-    "dbf_rms_norm_backward",
+    "dbf_mx_pack", "dbf_mx_forward", "dbf_mx_forward_group", "dbf_mx_backward_data", "dbf_mx_forward_plan",
+    "dbf_mx_backward_plan", "dbf_rms_norm", "dbf_rms_norm_backward_workspace", "dbf_rms_norm_backward",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -148,6 +148,10 @@ def lib() -> ctypes.CDLL:
     L.dbf_mx_forward_group.restype = ctypes.c_int
     L.dbf_mx_backward_data.argtypes = [vp, vp, vp, i32, i32, vp]
     L.dbf_mx_backward_data.restype = ctypes.c_int
+    L.dbf_mx_forward_plan.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i32)]
+    L.dbf_mx_forward_plan.restype = ctypes.c_int
+    L.dbf_mx_backward_plan.argtypes = [i32, i32, i32, ctypes.POINTER(i32)]
+    L.dbf_mx_backward_plan.restype = ctypes.c_int
     L.dbf_rms_norm.argtypes = [vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp, i32, vp, vp, vp]
     L.dbf_rms_norm.restype = ctypes.c_int
     L.dbf_rms_norm_backward_workspace.argtypes = [i32, i32]
@@ -590,6 +594,20 @@ def dbf_mx_pack(n: int, m: int, codes_ptr: int, scales_ptr: int, act_type: int, 
     _check(lib().dbf_mx_pack(n, m, codes_ptr, scales_ptr, act_type, max_batch, stream, ctypes.byref(h)),
            "dbf_mx_pack")
     return h.value
+
+
+def dbf_mx_forward_plan(batch: int, n: int, m: int, x_type: int):
+    """(tile rows, tile columns, K parts) of a forward's product (see dbf_mx_forward_plan in include/dbf.h)."""
+    plan = (ctypes.c_int32 * 3)()
+    _check(lib().dbf_mx_forward_plan(batch, n, m, x_type, plan), "dbf_mx_forward_plan")
+    return tuple(plan)
+
+
+def dbf_mx_backward_plan(batch: int, n: int, m: int):
+    """The same of an input gradient."""
+    plan = (ctypes.c_int32 * 3)()
+    _check(lib().dbf_mx_backward_plan(batch, n, m, plan), "dbf_mx_backward_plan")
+    return tuple(plan)
 
 
 class RmsNormOutput(NamedTuple):

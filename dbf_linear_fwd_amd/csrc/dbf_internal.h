@@ -326,6 +326,7 @@ struct MxProduct {
     MxPlan plan;
 };
 MxPlan mx_product_plan(int M, int n, int blocks, int x_type);
+void mx_product_tile(const MxPlan &p, int32_t *rows, int32_t *cols);
 // Floats of K-part sums that the product of this shape uses (0: K whole).
 size_t mx_product_parts(int M, int n, int blocks, int x_type);
 // Padded scale rows into 32-row tiles: round_up(M, 32) * blocks bytes.
@@ -344,6 +345,7 @@ struct MxBackward {
     MxPlan plan;
 };
 MxPlan mx_backward_plan(int M, int n, int m);
+void mx_backward_tile(const MxPlan &p, int32_t *rows, int32_t *cols);
 size_t mx_backward_parts(int M, int n, int m);
 int launch_mx_backward(const MxBackward &b, void *stream);
 int launch_mx_backward_join(const MxBackward &b, void *stream);

@@ -454,6 +454,11 @@ MxPlan mx_product_plan(int M, int n, int blocks, int x_type) {
     return mx_plan(M, n, blocks / 4, x_type == DBF_TYPE_E4M3);
 }
 
+void mx_product_tile(const MxPlan &p, int32_t *rows, int32_t *cols) {
+    *rows = kTiles[p.tile].bm;
+    *cols = kTiles[p.tile].bn;
+}
+
 size_t mx_product_parts(int M, int n, int blocks, int x_type) {
     return part_floats(mx_product_plan(M, n, blocks, x_type), M, n);
 }

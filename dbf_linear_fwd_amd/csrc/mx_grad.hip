@@ -504,6 +504,11 @@ int launch_either(const MxBackward &b, bool join, void *stream) {
 
 MxPlan mx_backward_plan(int M, int n, int m) { return grad_plan(M, n, m); }
 
+void mx_backward_tile(const MxPlan &p, int32_t *rows, int32_t *cols) {
+    *rows = kGrad[p.tile].bm;
+    *cols = kGrad[p.tile].bn;
+}
+
 size_t mx_backward_parts(int M, int n, int m) { return part_floats(grad_plan(M, n, m), M, m); }
 
 int launch_mx_backward(const MxBackward &b, void *stream) { return launch_either(b, false, stream); }

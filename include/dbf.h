@@ -468,6 +468,17 @@ dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, void *dx, int3
                                   hipStream_t stream);
 
 /*
+ * dbf_mx_forward_plan, dbf_mx_backward_plan -- how a call of this size runs:
+ * plan[0] x plan[1] results (rows of the batch x output columns) to a
+ * workgroup, the sum cut into plan[2] parts (above 1: a second launch adds
+ * them).  0 x 0 and 1 part: the forward's kernel for few rows.  x_type: the
+ * blocks that the product takes, DBF_TYPE_E4M3 or DBF_TYPE_E2M1.  Host-only.
+ * Errors: DBF_ERR_INVALID_ARG (batch, n or m below 1, another type, NULL).
+ */
+dbf_status_t dbf_mx_forward_plan(int32_t batch, int32_t n, int32_t m, int32_t x_type, int32_t plan[3]);
+dbf_status_t dbf_mx_backward_plan(int32_t batch, int32_t n, int32_t m, int32_t plan[3]);
+
+/*
  * dbf_rms_norm -- h = rne(x + residual), rstd = 1 / sqrt(mean(h^2) + eps) per
  * row, y = h * rstd * weight: the norm in front of a linear layer, with the
  * residual's addition and, for a block-quantised product, its output in
