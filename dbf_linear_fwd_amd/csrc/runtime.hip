@@ -1095,7 +1095,8 @@ extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, voi
 }
 
 extern "C" dbf_status_t dbf_mx_forward_plan(int32_t batch, int32_t n, int32_t m, int32_t x_type, int32_t plan[3]) {
-    if (batch < 1 || n < 1 || m < 1 || m > (1 << 30) || !plan) return DBF_ERR_INVALID_ARG;
+    const int32_t lim = 1 << 30;
+    if (batch < 1 || n < 1 || m < 1 || batch > lim || n > lim || m > lim || !plan) return DBF_ERR_INVALID_ARG;
     if (x_type != DBF_TYPE_E4M3 && x_type != DBF_TYPE_E2M1) return DBF_ERR_INVALID_ARG;
     plan[0] = plan[1] = 0;
     plan[2] = 1;
@@ -1107,7 +1108,8 @@ extern "C" dbf_status_t dbf_mx_forward_plan(int32_t batch, int32_t n, int32_t m,
 }
 
 extern "C" dbf_status_t dbf_mx_backward_plan(int32_t batch, int32_t n, int32_t m, int32_t plan[3]) {
-    if (batch < 1 || n < 1 || m < 1 || !plan) return DBF_ERR_INVALID_ARG;
+    const int32_t lim = 1 << 30;
+    if (batch < 1 || n < 1 || m < 1 || batch > lim || n > lim || m > lim || !plan) return DBF_ERR_INVALID_ARG;
     const dbf::MxPlan p = dbf::mx_backward_plan(batch, n, m);
     dbf::mx_backward_tile(p, &plan[0], &plan[1]);
     plan[2] = p.nsplit;

@@ -474,7 +474,8 @@ dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, void *dx, int3
  * workgroup, the sum cut into plan[2] parts (above 1: a second launch adds
  * them).  0 x 0 and 1 part: the forward's kernel for few rows.  x_type: the
  * blocks that the product takes, DBF_TYPE_E4M3 or DBF_TYPE_E2M1.  Host-only.
- * Errors: DBF_ERR_INVALID_ARG (batch, n or m below 1, another type, NULL).
+ * Errors: DBF_ERR_INVALID_ARG (batch, n or m below 1 or above 2^30, another
+ * type, NULL).
  */
 dbf_status_t dbf_mx_forward_plan(int32_t batch, int32_t n, int32_t m, int32_t x_type, int32_t plan[3]);
 dbf_status_t dbf_mx_backward_plan(int32_t batch, int32_t n, int32_t m, int32_t plan[3]);
@@ -498,7 +499,8 @@ dbf_status_t dbf_mx_backward_plan(int32_t batch, int32_t n, int32_t m, int32_t p
  * result does not depend on the other rows.  A NaN in h makes its row
  * NaN.  Where mean(h^2) + eps is 2^252 or more (an infinity in h, or a row
  * whose 1 / rms is below fp32's normal numbers), rstd is 0 (y is 0 for finite
- * h, NaN for infinite).  Pointers 16-byte aligned (scales, rstd: 4); 1 <= cols <= 32768
+ * h, NaN for infinite); where it is below 2^-256, rstd is infinite and y that of
+ * the exact value (NaN for a row of zeros).  Pointers 16-byte aligned (scales, rstd: 4); 1 <= cols <= 32768
  * (DBF_ERR_SHAPE above); rows = 0 returns DBF_OK without launching.  The
  * current HIP device must be the one that holds the buffers.
  */

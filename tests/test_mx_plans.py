@@ -73,7 +73,8 @@ def test_plan_of_few_rows_and_refusals():
     assert dbf.dbf_mx_forward_plan(16, 4096, 14336, E4M3)[0] > 0  # its blocks do not fit one compute unit
     L, plan = dbf.lib(), (ctypes.c_int32 * 3)()
     assert L.dbf_mx_forward_plan(1, 1, 1, E4M3, None) == E and L.dbf_mx_backward_plan(1, 1, 1, None) == E
-    for b, n, m in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (-1, 1, 1)):
+    for b, n, m in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (-1, 1, 1), (2 ** 31 - 1, 64, 64), (4, 2 ** 31 - 1, 64),
+                    (4, 64, 2 ** 31 - 1)):
         assert L.dbf_mx_forward_plan(b, n, m, E4M3, plan) == E and L.dbf_mx_backward_plan(b, n, m, plan) == E
     for t in (dbf.DBF_TYPE_F16, dbf.DBF_TYPE_BF16, dbf.DBF_TYPE_F32, 9):
         assert L.dbf_mx_forward_plan(4, 64, 64, t, plan) == E
