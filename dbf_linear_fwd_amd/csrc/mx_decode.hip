@@ -23,12 +23,14 @@
 // for 8192 rows 16.1 and 16.8 us, 16 x 14336 in e2m1 for 4096 rows 14.9 and
 // 21.8; 16 x 4096 for 4096 rows 8.7 and 7.8.
 // Batches whose blocks do not fit LDS go to the tiled product (read from L2
-// for every tile, 16 x 14336 for 4096 rows took 17 us, the tiles 13).
+// for every tile, 16 x 14336 for 4096 rows took 17 us where the tiles took 13).
 //
-// Graph replays with weights from HBM: 14336 x 4096 at batch 1 8.7 us (3.6
-// TB/s; a large copy reaches 4.6), batch 16, quantising included, 13; 4096 x
-// 14336 at batch 1 10.3 us (one tile per workgroup: nothing to overlap with
-// x's way to LDS); 4096 x 4096 5.4 us; 1024 x 4096 4.0 us.
+// Graph replays with weights from HBM: 14336 x 4096 at batch 1 9.3 us (3.4
+// TB/s; a large copy reaches 4.6; 7.5 from the last-level cache), batch 16,
+// quantising included, 12.9; 4096 x 14336 at batch 1 10.6 us (one tile per
+// workgroup: nothing to overlap with x's way to LDS); 4096 x 4096 5.2 us;
+// 1024 x 4096 4.5 us; three layers of 4096, 1024 and 1024 rows that share 4096
+// columns 6.5 us in one launch, 14.3 in three.
 
 #include "mx_tile.h"
 

@@ -10,12 +10,13 @@
 // hands a lane the rows of its column.  f16 holds the codes exactly down to
 // scales of 2^-36 of the largest (0.5 is 2^-24 then), bf16 to 2^-125; smaller
 // ones lose bits or vanish.  The sums are multiplied by 2^(smax - kShift) at
-// the end.  (As bytes in LDS, e5m2 of the same values,
-// widened again by every wave that reads them: 243 instead of 237 us.)
+// the end.  (As bytes in LDS, e5m2 of the same values, widened again by every
+// wave that reads them: 243 us where this took 237.)
 //
-// 2048 rows, n 14336, m 4096, bf16: 237 us, 1.02 PFLOP/s (205 us, 1.17, with
-// gradients of 0.01 in place of full-range values; a library product of 16-bit
-// matrices of that size takes 212).  A step of 64 rows of a 256 x 256 tile
+// 2048 rows, n 14336, m 4096, bf16: 205 to 225 us as the clock goes, 1.07 to
+// 1.17 PFLOP/s (a library product of 16-bit matrices of that size takes 211);
+// n 14344, no whole steps, 217 to 234; n 14337, rows that are not 16-byte
+// aligned and go through registers, 612.  A step of 64 rows of a 256 x 256 tile
 // takes 1.25 us alone and 1.8 with all CUs at work, where the clock falls to
 // 1.9 GHz; its products are 0.85 us at the highest clock.
 
@@ -23,10 +24,6 @@
 
 namespace dbf {
 namespace {
-
-typedef int i32x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Exponent that the largest scale of a block column stands at: in f16 the
 // largest code, 6 * 2^13, is within the type and the small ones reach furthest
@@ -129,9 +126,9 @@ __device__ __forceinline__ void scale_columns(f32x16 (&acc)[C::MI][C::NI], const
 
 // How dy and the weight are read.  Whole: n is a multiple of 64, so every step
 // is whole and its addresses are a common base and a lane's constant offset
-// (2048 rows, n 14336, m 4096: 243 us; with a check for the last columns and
-// rows in each step 248, on an earlier form of the loop).  Rows16: dy's rows are 16-byte aligned (n a multiple
-// of 8).  Elements: any n, dy through registers.
+// (2048 rows, n 14336, m 4096: 209 us; with a check for the last columns and
+// rows in each step, at n 14344, 217).  Rows16: dy's rows are 16-byte aligned
+// (n a multiple of 8).  Elements: any n, dy through registers.
 enum class GradRows { Whole, Rows16, Elements };
 
 template <typename C, typename E, GradRows ROWS>
@@ -416,9 +413,13 @@ constexpr int kGradCount = sizeof(kGrad) / sizeof(kGrad[0]);
 constexpr int kCus = 256;
 
 // The tile and K parts of least estimated time; K parts add a launch and the
-// traffic of their fp32 sums.  (2048 rows, n 14336, m 4096, bf16: 256 x 256
-// tiles in two parts 237 us, whole 314, 128 x 128 tiles 273; 512 rows: 128 x
-// 128 in four parts 78, whole 144; 16 rows: 32 x 128 in eight parts 23, whole 105.)
+// traffic of their fp32 sums.  (n 14336, m 4096, bf16, weight from HBM: 2048
+// rows in 256 x 256 tiles and two parts 206 us, whole 288, 128 x 128 tiles 242;
+// 1024 rows in four parts 116, 128 x 128 tiles in two 136; 16 rows in 32 x 128
+// tiles and twelve parts 21.7, whole 100.  Parts are priced too high: at 35
+// sizes the choice is 4.4 % from the best on average; 512 rows take 88 us in
+// 128 x 128 tiles and two parts, 77.5 in 256 x 256 and eight; at worst 45.5
+// where 35 is the best, 128 rows of n 4096, m 14336.)
 MxPlan grad_plan(int M, int n, int m) {
     MxPlan best;
     float least = 0.0f;
