@@ -34,6 +34,7 @@ __all__ = [
     "dbf_factorize", "factorize", "dbf_linear_forward_noalloc", "dbf_bqq_pack_grouped",
     "DBF_TYPE_F16", "DBF_TYPE_BF16", "DBF_TYPE_F32", "DBF_TYPE_E4M3", "DBF_TYPE_E2M1", "MxTensor", "mx_quantize",
     "dbf_mx_pack", "dbf_mx_forward_plan", "dbf_mx_backward_plan", "rms_norm", "RmsNormOutput", "rms_norm_backward", "norm_forward_group",
+    "RowGroups", "group_rows", "dbf_experts_pack", "Experts", "Adapters", "AdapterOutput",
 ]
 
 DBF_OK = 0
@@ -67,6 +68,9 @@ EXPORTED_SYMBOLS = (
     "dbf_bqq_pack_grouped", "dbf_mx_code_bytes", "dbf_mx_scale_bytes", "dbf_mx_quantize", "dbf_mx_dequantize",
     "dbf_mx_pack", "dbf_mx_forward", "dbf_mx_forward_group", "dbf_mx_backward_data", "dbf_mx_forward_plan",
     "dbf_mx_backward_plan", "dbf_rms_norm", "dbf_rms_norm_backward_workspace", "dbf_rms_norm_backward",
+    "dbf_group_rows_workspace", "dbf_group_rows", "dbf_experts_pack", "dbf_experts_forward",
+    "dbf_experts_backward_data", "dbf_adapter_workspace", "dbf_adapter_forward", "dbf_adapter_backward_workspace",
+    "dbf_adapter_backward",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -158,6 +162,24 @@ def lib() -> ctypes.CDLL:
     L.dbf_rms_norm_backward_workspace.restype = sz
     L.dbf_rms_norm_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
     L.dbf_rms_norm_backward.restype = ctypes.c_int
+    L.dbf_group_rows_workspace.argtypes = [i32, i32]
+    L.dbf_group_rows_workspace.restype = sz
+    L.dbf_group_rows.argtypes = [vp, i32, i32, i32, vp, vp, vp, sz, vp]
+    L.dbf_group_rows.restype = ctypes.c_int
+    L.dbf_experts_pack.argtypes = [i32, i32, i32, vp, vp, i32, i32, vp, ctypes.POINTER(vp)]
+    L.dbf_experts_pack.restype = ctypes.c_int
+    L.dbf_experts_forward.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, i32, vp]
+    L.dbf_experts_forward.restype = ctypes.c_int
+    L.dbf_experts_backward_data.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp]
+    L.dbf_experts_backward_data.restype = ctypes.c_int
+    for name in ("dbf_adapter_workspace", "dbf_adapter_backward_workspace"):
+        getattr(L, name).argtypes = [i32, i32, i32, i32, i32]
+        getattr(L, name).restype = sz
+    L.dbf_adapter_forward.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+    L.dbf_adapter_forward.restype = ctypes.c_int
+    L.dbf_adapter_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp,
+                                       vp, sz, vp]
+    L.dbf_adapter_backward.restype = ctypes.c_int
     L.dbf_free.argtypes = [vp]
     L.dbf_free.restype = None
     L.dbf_get_info.argtypes = [vp, ctypes.POINTER(_Info)]
@@ -694,6 +716,271 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None):
           rstd.data_ptr(), None if dh is None else dh.data_ptr(), _type_of(dy.dtype), wt, rows, cols, dx.data_ptr(),
           dw.data_ptr(), ws.data_ptr(), nbytes)
     return dx, dw
+
+
+class RowGroups:
+    """Rows in groups (see "Rows in groups" in include/dbf.h): ``order`` (int32, rows) holds the row at each place of
+    the grouped order, ``offsets`` (int32, count + 1) the first place of each group and of the rows of no group.
+    Contiguous CUDA vectors, as `group_rows` makes them."""
+
+    __slots__ = ("order", "offsets")
+
+    def __init__(self, order, offsets):
+        import torch
+        for a, what in ((order, "order"), (offsets, "offsets")):
+            if a.dtype != torch.int32 or not a.is_cuda or a.dim() != 1 or not a.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous CUDA int32 vector")
+        if offsets.numel() < 2 or order.device != offsets.device:
+            raise ValueError("offsets must hold count + 1 entries, on order's device")
+        self.order, self.offsets = order, offsets
+
+    @property
+    def rows(self) -> int:
+        return self.order.numel()
+
+    @property
+    def count(self) -> int:
+        return self.offsets.numel() - 1
+
+
+def group_rows(index, count: int) -> RowGroups:
+    """The grouped order of the rows that `index` (contiguous CUDA vector, int32 or int64) assigns to `count` groups;
+    entries outside [0, count) are of no group.  Once for all the layers that the rows pass."""
+    import torch
+    if (index.dtype not in (torch.int32, torch.int64) or not index.is_cuda or index.dim() != 1
+            or not index.is_contiguous()):
+        raise ValueError("index must be a contiguous CUDA vector of int32 or int64")
+    count, rows = int(count), index.numel()
+    if not 1 <= count <= 1024 or rows > 1 << 24:
+        raise ValueError("1 to 1024 groups and up to 2^24 rows")
+    order = index.new_empty(rows, dtype=torch.int32)
+    offsets = index.new_empty(count + 1, dtype=torch.int32)
+    nbytes = lib().dbf_group_rows_workspace(rows, count)
+    ws = index.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    _call("dbf_group_rows", index, index.data_ptr(), index.element_size() * 8, rows, count, order.data_ptr(),
+          offsets.data_ptr(), None if ws is None else ws.data_ptr(), nbytes)
+    g = RowGroups.__new__(RowGroups)  # (right by construction)
+    g.order, g.offsets = order, offsets
+    return g
+
+
+def _check_groups(groups, count: int, rows: Optional[int], device) -> None:
+    if not isinstance(groups, RowGroups):
+        raise ValueError("groups must be the RowGroups of group_rows")
+    if groups.count != count:
+        raise ValueError(f"groups must have {count} groups")
+    if rows is not None and groups.rows != rows:
+        raise ValueError(f"groups must have {rows} rows")
+    if groups.order.device != device:
+        raise ValueError("groups must be on the rows' device")
+
+
+def dbf_experts_pack(count: int, n: int, m: int, codes_ptr: int, scales_ptr: int, act_type: int, max_rows: int,
+                     stream: int = 0) -> int:
+    """Handle of experts with e2m1 block weights (see dbf_experts_pack in include/dbf.h)."""
+    h = ctypes.c_void_p()
+    _check(lib().dbf_experts_pack(count, n, m, codes_ptr, scales_ptr, act_type, max_rows, stream, ctypes.byref(h)),
+           "dbf_experts_pack")
+    return h.value
+
+
+class Experts:
+    """`count` 4-bit weights of n x m, each for the rows of one group (the experts of a sparse MLP).
+
+    W is an e2m1 MxTensor of count * n rows, one weight after the other;
+    max_rows is the most places (tokens times experts of a token) of a call.
+    `groups` (of `group_rows`) assigns each place to an expert.
+    """
+
+    def __init__(self, W: MxTensor, count: int, max_rows: int, act: str = "e4m3"):
+        import torch
+        if not isinstance(W, MxTensor) or W.fmt != "e2m1":
+            raise ValueError("W must be an e2m1 MxTensor")
+        self.count = int(count)
+        if self.count < 1 or W.shape[0] < 1 or W.shape[0] % self.count:
+            raise ValueError("W must have the same number of rows for each of count weights")
+        at = _block_type(act)
+        self.n, self.m = W.shape[0] // self.count, W.cols
+        self.max_rows, self.act = int(max_rows), act
+        _check_count(self.n, self.max_rows)
+        with torch.cuda.device(W.device):
+            self.handle = dbf_experts_pack(self.count, self.n, self.m, W.codes.data_ptr(), W.scales.data_ptr(), at,
+                                           self.max_rows, torch.cuda.current_stream().cuda_stream)
+
+    def _rows(self, groups, gather: int, rows: int, device) -> int:
+        """Checked number of places."""
+        _check_groups(groups, self.count, None, device)
+        slots = groups.rows
+        if slots > self.max_rows:
+            raise ValueError(f"more than {self.max_rows} rows")
+        if gather < 0 or rows * max(gather, 1) != slots:
+            raise ValueError("the rows must be one for each place, or with gather = k one for each k of them")
+        return slots
+
+    @staticmethod
+    def _out(out, like, slots, width, dtype):
+        if out is None:
+            return like.new_empty((slots, width), dtype=dtype)
+        if (tuple(out.shape) != (slots, width) or out.dtype != dtype or not out.is_contiguous()
+                or out.device != like.device):
+            raise ValueError(f"out must be a contiguous tensor of shape ({slots}, {width}) on the rows' device")
+        return out
+
+    def forward(self, x, groups: RowGroups, gather: int = 0, scatter: bool = False, out=None, out_dtype=None):
+        """y[place] = x[row of the place] W_eᵀ, e the place's expert; zeros for places of none (see
+        dbf_experts_forward in include/dbf.h).
+
+        x: float16 or bfloat16 rows, quantised into `act` blocks by the call,
+        or an MxTensor.  gather 0: x has a row for each place, in the grouped
+        order; k: x is in the index's order, k consecutive entries share a
+        row (tokens with k experts each).  scatter: results in the index's
+        order instead of the grouped order.
+        """
+        import torch
+        gather = int(gather)
+        if isinstance(x, MxTensor):
+            if x.cols != self.m:
+                raise ValueError(f"x must have {self.m} columns")
+            like, scales, xt, default = x.codes, x.scales.data_ptr(), _TYPE_NAMES[x.fmt], torch.float16
+        else:
+            _check_rows(x, "x")
+            if x.shape[1] != self.m:
+                raise ValueError(f"x must have {self.m} columns")
+            like, scales, xt, default = x, None, _type_of(x.dtype), x.dtype
+        slots = self._rows(groups, gather, like.shape[0], like.device)
+        if out_dtype is None:
+            out_dtype = default if out is None else out.dtype
+        if out_dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("the output is float16 or bfloat16")
+        out = self._out(out, like, slots, self.n, out_dtype)
+        _call("dbf_experts_forward", like, self.handle, like.data_ptr(), xt, scales, groups.order.data_ptr(),
+              groups.offsets.data_ptr(), slots, gather, 1 if scatter else 0, out.data_ptr(), _type_of(out_dtype))
+        return out
+
+    __call__ = forward
+
+    def backward_data(self, dy, groups: RowGroups, gather: int = 0, scatter: bool = False, out=None):
+        """dx[place] = dy[row of the place] W_e for dy (float16 or bfloat16); gather and scatter as in forward."""
+        gather = int(gather)
+        _check_rows(dy, "dy")
+        if dy.shape[1] != self.n:
+            raise ValueError(f"dy must have {self.n} columns")
+        slots = self._rows(groups, gather, dy.shape[0], dy.device)
+        out = self._out(out, dy, slots, self.m, dy.dtype)
+        _call("dbf_experts_backward_data", dy, self.handle, dy.data_ptr(), _type_of(dy.dtype),
+              groups.order.data_ptr(), groups.offsets.data_ptr(), slots, gather, 1 if scatter else 0, out.data_ptr())
+        return out
+
+    def info(self) -> Dict[str, int]:
+        return dbf_get_info(self.handle)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            dbf_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class AdapterOutput(NamedTuple):
+    """y: base + scale B A x; t: A x, float32 (rows x rank), which the backward pass takes."""
+    y: object
+    t: object
+
+
+class Adapters:
+    """`count` low-rank adapters beside a layer of any kind: y = base + scale_a B_a (A_a x) for rows of adapter a.
+
+    A (count, rank, m) and B (count, n, rank) are contiguous CUDA tensors of
+    float16 or bfloat16, scale a float32 vector or None (1).  They are read by
+    each call and not copied, so a training step may change them in place.
+    `groups` (of `group_rows`) assigns each row to an adapter, or to none.
+    """
+
+    def __init__(self, A, B, scale=None):
+        import torch
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2] or 0 in A.shape + B.shape:
+            raise ValueError("A must be (count, rank, m) and B (count, n, rank)")
+        for a, what in ((A, "A"), (B, "B")):
+            if (a.dtype not in (torch.float16, torch.bfloat16) or a.dtype != A.dtype or not a.is_cuda
+                    or not a.is_contiguous() or a.device != A.device):
+                raise ValueError(f"{what} must be a contiguous CUDA tensor of float16 or bfloat16, like A")
+        if scale is not None and (scale.dtype != torch.float32 or tuple(scale.shape) != (A.shape[0],)
+                                  or not scale.is_contiguous() or scale.device != A.device):
+            raise ValueError("scale must be a contiguous float32 vector with one entry per adapter, on A's device")
+        self.A, self.B, self.scale = A, B, scale
+        self.count, self.rank, self.m = A.shape
+        self.n = B.shape[1]
+
+    def _check(self, t, width, what):
+        if (t.dtype != self.A.dtype or t.dim() != 2 or t.shape[1] != width or not t.is_contiguous()
+                or t.device != self.A.device):
+            raise ValueError(f"{what} must be a contiguous tensor of shape (rows, {width}) in A's type on its device")
+
+    def _low(self, t, rows):
+        import torch
+        if t.dtype != torch.float32 or tuple(t.shape) != (rows, self.rank) or not t.is_contiguous() or t.device != self.A.device:
+            raise ValueError(f"t must be a contiguous float32 tensor of shape ({rows}, {self.rank}) on A's device")
+
+    def forward(self, x, base, groups: RowGroups, out=None) -> AdapterOutput:
+        """(y, t) for rows x and the layer's results base; out may be base itself (see dbf_adapter_forward in
+        include/dbf.h)."""
+        import torch
+        self._check(x, self.m, "x")
+        self._check(base, self.n, "base")
+        rows = x.shape[0]
+        if base.shape[0] != rows:
+            raise ValueError("x and base must have the same rows")
+        _check_groups(groups, self.count, rows, x.device)
+        if out is None:
+            out = torch.empty_like(base)
+        else:
+            self._check(out, self.n, "out")
+            if out.shape[0] != rows:
+                raise ValueError("out must have x's rows")
+        t = x.new_empty((rows, self.rank), dtype=torch.float32)
+        nbytes = lib().dbf_adapter_workspace(rows, self.n, self.m, self.rank, self.count)
+        ws = x.new_empty(max(nbytes, 16), dtype=torch.uint8)
+        _call("dbf_adapter_forward", x, x.data_ptr(), base.data_ptr(), self.A.data_ptr(), self.B.data_ptr(),
+              None if self.scale is None else self.scale.data_ptr(), _type_of(x.dtype), groups.order.data_ptr(),
+              groups.offsets.data_ptr(), rows, self.n, self.m, self.rank, self.count, out.data_ptr(), t.data_ptr(),
+              ws.data_ptr(), nbytes)
+        return AdapterOutput(out, t)
+
+    __call__ = forward
+
+    def backward(self, dy, x, t, groups: RowGroups, dx=None, out=None):
+        """(dx', dA, dB) at rows x with the forward's t for the upstream gradient dy: dx' = dx + scale (dy B) A with
+        the layer's own input gradient dx (None: zeros); dA and dB are float32.  out (for dx') may be dx itself."""
+        import torch
+        self._check(dy, self.n, "dy")
+        self._check(x, self.m, "x")
+        rows = x.shape[0]
+        if dy.shape[0] != rows:
+            raise ValueError("x and dy must have the same rows")
+        self._low(t, rows)
+        _check_groups(groups, self.count, rows, x.device)
+        for a, what in ((dx, "dx"), (out, "out")):
+            if a is not None:
+                self._check(a, self.m, what)
+                if a.shape[0] != rows:
+                    raise ValueError(f"{what} must have x's rows")
+        if out is None:
+            out = torch.empty_like(x)
+        dA = x.new_empty(self.A.shape, dtype=torch.float32)
+        dB = x.new_empty(self.B.shape, dtype=torch.float32)
+        nbytes = lib().dbf_adapter_backward_workspace(rows, self.n, self.m, self.rank, self.count)
+        ws = x.new_empty(max(nbytes, 16), dtype=torch.uint8)
+        _call("dbf_adapter_backward", x, dy.data_ptr(), x.data_ptr(), t.data_ptr(),
+              None if dx is None else dx.data_ptr(), self.A.data_ptr(), self.B.data_ptr(),
+              None if self.scale is None else self.scale.data_ptr(), _type_of(x.dtype), groups.order.data_ptr(),
+              groups.offsets.data_ptr(), rows, self.n, self.m, self.rank, self.count, out.data_ptr(), dA.data_ptr(),
+              dB.data_ptr(), ws.data_ptr(), nbytes)
+        return out, dA, dB
 
 
 class Layer:

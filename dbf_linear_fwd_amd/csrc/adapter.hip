@@ -1,0 +1,821 @@
+// Low-rank adapters of rows in groups, and their gradients (include/dbf.h).
+//
+//   t = x A_aᵀ          y  = base + s_a t B_aᵀ
+//   u = s_a dy B_a      dx' = dx + u A_a     dA_a = Σ u xᵀ    dB_a = s_a Σ dy tᵀ
+//
+// Three kernels on the 16x16x32 16-bit matrix-core instructions, operands from
+// memory straight into registers:
+//   shrink  rows x K -> rows x rank (t, u): K cut between the waves of a
+//           workgroup and into parts, whose fp32 sums go to memory;
+//   expand  rows x rank -> rows x columns (y, dx'): adds the parts of t, one
+//           wave for all of its row tile, and goes through the columns;
+//   outer   the sums over a group's rows (dA, dB): the rows of a group in
+//           chunks, joined in order by a fourth kernel where a group has several.
+// The rank is small (16 to 64), so all of them are bound by the rows' memory
+// traffic: a product needs rank / 2 to rank operations per byte of x, dy or y.
+//
+// Of an instruction a lane (c = lane % 16, g = lane / 16) supplies row c of each
+// operand, eight values of K from 8 g on, and gets results 4 g .. 4 g + 3 of
+// the first operand for row c of the second.  An operand that has K contiguous
+// in memory is one 16-byte load; one with K along the rows (B in u, A in dx',
+// x and dy in the gradients) is loaded as eight rows of neighbouring columns
+// and its halves are picked by byte permutes, four per operand.
+//
+// t and u stay fp32 in memory and become 16-bit operands in parts: f16 two
+// parts of t 2^k, k from the largest of the row (of a wave's rows in the
+// gradients), 22 bits and more; bf16 two parts (16 bits) where a 16-bit result
+// follows, three (24 bits) for the fp32 gradients.
+
+#include <algorithm>
+
+#include "mx_tile.h"
+#include "rows_device.h"
+
+namespace dbf {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kMaxRank = 128, kMaxGroups = 1024;
+constexpr int kMaxParts = 16;
+
+template <typename E>
+__device__ __forceinline__ f32x4 mma(u32v4 a, u32v4 b, f32x4 acc) {
+    if constexpr (E::code == DBF_TYPE_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+}
+
+// N consecutive 16-bit elements from p into words, the first `valid` of them
+// (VEC: all or none, p aligned to them), zeros for the rest.
+template <int N, bool VEC>
+__device__ __forceinline__ void load_n(const uint16_t *p, int valid, uint32_t (&w)[(N + 1) / 2]) {
+#pragma unroll
+    for (int i = 0; i < (N + 1) / 2; ++i) w[i] = 0;
+    if constexpr (VEC) {
+        if (valid <= 0) return;
+        if constexpr (N == 1) w[0] = *p;
+        else if constexpr (N == 2) w[0] = *reinterpret_cast<const uint32_t *>(p);
+        else if constexpr (N == 4) {
+            const u32v2 v = *reinterpret_cast<const u32v2 *>(p);
+            w[0] = v[0];
+            w[1] = v[1];
+        } else {
+            const u32v4 v = *reinterpret_cast<const u32v4 *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = v[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < valid) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ u32v4 load_row8(const uint16_t *p, int valid) {
+    uint32_t w[4];
+    load_n<8, VEC>(p, valid, w);
+    return u32v4{w[0], w[1], w[2], w[3]};
+}
+
+// Element i of eight rows of N: the operand whose K runs along the rows.
+template <int N>
+__device__ __forceinline__ u32v4 pick_column(const uint32_t (&q)[8][(N + 1) / 2], int i) {
+    const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;  // the high or the low halves of (second, first)
+    u32v4 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = __builtin_amdgcn_perm(q[2 * k + 1][i >> 1], q[2 * k][i >> 1], sel);
+    return r;
+}
+
+// Two neighbouring values of part P (0, 1, 2) of v: rounded to 16 bits, the
+// rest of that rounded, the rest of that.
+template <typename E>
+__device__ __forceinline__ uint16_t part_of(float v, int part) {
+    uint16_t h = E::put(v);
+    for (int p = 0; p < part; ++p) {
+        const float top = E::get(h);
+        v = __builtin_isfinite(top) ? v - top : 0.0f;
+        h = E::put(v);
+    }
+    return h;
+}
+template <typename E>
+__device__ __forceinline__ u32v4 pack_part(const float (&v)[8], int part) {
+    u32v4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = static_cast<uint32_t>(part_of<E>(v[2 * i], part)) | static_cast<uint32_t>(part_of<E>(v[2 * i + 1], part)) << 16;
+    return r;
+}
+
+// The power of two that brings `top` (a largest magnitude) to [2^14, 2^15).
+__device__ __forceinline__ int f16_shift(float top) {
+    int ex = 0;
+    (void)frexpf(top, &ex);
+    return top > 0.0f ? 15 - ex : 0;
+}
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a < __builtin_inff() ? a : 0.0f;  // (a NaN: 0)
+}
+
+// ---------------------------------------------------------------------------
+
+struct ShrinkArgs {
+    const uint16_t *x, *w;      // rows x K; count x rank x K, or (LEAD) count x K x rank
+    const int32_t *order, *offsets;
+    int rows, K, rank, count, parts;
+    float *out;                 // [parts][rows][16 RT], by place
+};
+
+// MT tiles of 16 rows, ranks c RT + i (i < RT) in lane c's operand i.
+template <typename E, bool LEAD, int MT, int RT, bool VEC>
+__global__ __launch_bounds__(kThreads) void shrink_kernel(const ShrinkArgs a) {
+    constexpr int RP = 16 * RT, Rows = 16 * MT, Pitch = RP + 4;
+    __shared__ __attribute__((aligned(16))) float red[kWaves][Rows][Pitch];
+    const int tile = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+    RowTile rt;
+    if (!find_row_tile(a.offsets, a.count, a.rows, Rows, tile, rt) || rt.group >= a.count) return;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int steps = (a.K + 31) / 32, pw = part * kWaves + wave, all = a.parts * kWaves;
+    const int k0 = static_cast<int>(static_cast<int64_t>(pw) * steps / all);
+    const int k1 = static_cast<int>(static_cast<int64_t>(pw + 1) * steps / all);
+    const uint16_t *xr[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int row = min(max(a.order[rt.first + min(16 * i + c, rt.rows - 1)], 0), a.rows - 1);
+        xr[i] = a.x + static_cast<size_t>(row) * a.K + 8 * g;
+    }
+    const uint16_t *w = a.w + static_cast<size_t>(rt.group) * a.rank * a.K;
+    f32x4 acc[MT][RT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = k0; s < k1; ++s) {
+        const int k = 32 * s, left = a.K - k - 8 * g;
+        u32v4 xf[MT], wf[RT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) xf[i] = load_row8<VEC>(xr[i] + k, left);
+        if constexpr (LEAD) {
+            uint32_t q[8][(RT + 1) / 2];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                load_n<RT, VEC>(w + static_cast<size_t>(k + 8 * g + j) * a.rank + c * RT, j < left ? a.rank - c * RT : 0, q[j]);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) wf[i] = pick_column<RT>(q, i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int j = c * RT + i;
+                wf[i] = load_row8<VEC>(w + static_cast<size_t>(j) * a.K + k + 8 * g, j < a.rank ? left : 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) acc[i][j] = mma<E>(wf[j], xf[i], acc[i][j]);
+    }
+    // lane (c, g): ranks (4 g + v) RT + i of row c
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) red[wave][16 * i + c][(4 * g + v) * RT + j] = acc[i][j][v];
+    __syncthreads();
+    float *out = a.out + (static_cast<size_t>(part) * a.rows + rt.first) * RP;
+    for (int i = threadIdx.x; i < rt.rows * (RP / 4); i += kThreads) {
+        const int r = i / (RP / 4), j = i % (RP / 4) * 4;
+        f32x4 s = *reinterpret_cast<const f32x4 *>(&red[0][r][j]);
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v) s += *reinterpret_cast<const f32x4 *>(&red[v][r][j]);
+        *reinterpret_cast<f32x4 *>(out + static_cast<size_t>(r) * RP + j) = s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+struct ExpandArgs {
+    const float *in;            // [parts][rows][16 RT], by place
+    const uint16_t *w;          // count x cols x rank, or (LEAD) count x rank x cols
+    const float *scale;
+    const int32_t *order, *offsets;
+    int rows, cols, rank, count, parts;
+    const uint16_t *base;       // rows x cols, or null
+    uint16_t *out;              // rows x cols, or null: low alone
+    float *low;                 // out, rows x rank, or null
+    int low_scaled;             // low with the group's scale
+    int per;                    // 64-column chunks of a wave
+};
+
+template <typename E, bool LEAD, int MT, int RT, bool VEC, bool VOUT>
+__global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
+    constexpr int RP = 16 * RT, Rows = 16 * MT;
+    constexpr int WF = RP < 32 ? 1 : RP / 32;  // 32-rank pieces
+    constexpr int KS = RT;                     // instructions of two parts: 2 RP / 32
+    RowTile rt;
+    const int blocks = (a.cols + 64 * kWaves * a.per - 1) / (64 * kWaves * a.per);
+    const int tile = blockIdx.x / blocks, block = blockIdx.x % blocks;
+    if (!find_row_tile(a.offsets, a.count, a.rows, Rows, tile, rt)) return;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool none = rt.group >= a.count;
+    const float scale = none || !a.scale ? 1.0f : a.scale[rt.group];
+    const int j0 = RP < 32 ? 8 * (g & 1) : 8 * g;  // this lane's ranks of a piece
+
+    int64_t row[MT];
+    u32v4 tf[MT][KS];
+    int shift[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int at = rt.first + min(16 * i + c, rt.rows - 1);
+        const int r = a.order[at];
+        row[i] = 16 * i + c < rt.rows && r >= 0 && r < a.rows ? r : -1;
+        float v[WF][8];
+#pragma unroll
+        for (int f = 0; f < WF; ++f)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[f][j] = 0.0f;
+        if (!none) {
+            for (int p = 0; p < a.parts; ++p) {
+                const float *src = a.in + (static_cast<size_t>(p) * a.rows + at) * RP + j0;
+#pragma unroll
+                for (int f = 0; f < WF; ++f)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const f32x4 q = *reinterpret_cast<const f32x4 *>(src + 32 * f + 4 * h);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[f][4 * h + j] += q[j];
+                    }
+            }
+        }
+        if (a.low && block == 0 && wave == 0 && row[i] >= 0 && (RP >= 32 || g < 2)) {
+            const float by = a.low_scaled ? scale : 1.0f;
+#pragma unroll
+            for (int f = 0; f < WF; ++f)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (32 * f + j0 + j < a.rank) a.low[row[i] * a.rank + 32 * f + j0 + j] = v[f][j] * by;
+        }
+        shift[i] = 0;
+        float top = 0.0f;
+#pragma unroll
+        for (int f = 0; f < WF; ++f)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[f][j] *= scale;
+                top = fmaxf(top, finite_abs(v[f][j]));
+            }
+        if constexpr (E::code == DBF_TYPE_F16) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            shift[i] = f16_shift(top);
+#pragma unroll
+            for (int f = 0; f < WF; ++f)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[f][j] = ldexpf(v[f][j], shift[i]);
+        }
+        if constexpr (RP < 32) {
+            const u32v4 hi = pack_part<E>(v[0], 0), lo = pack_part<E>(v[0], 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tf[i][0][k] = g < 2 ? hi[k] : lo[k];
+        } else {
+#pragma unroll
+            for (int f = 0; f < WF; ++f) {
+                tf[i][f] = pack_part<E>(v[f], 0);
+                tf[i][WF + f] = pack_part<E>(v[f], 1);
+            }
+        }
+    }
+    if (!a.out || (none && a.base == a.out)) return;
+    const uint16_t *w = a.w + static_cast<size_t>(none ? 0 : rt.group) * a.rank * a.cols;
+    for (int it = 0; it < a.per; ++it) {
+        const int col0 = ((block * a.per + it) * kWaves + wave) * 64;
+        if (col0 >= a.cols) break;
+        // operand i of lane c: column col0 + 4 c + i
+        u32v4 wf[WF][4];
+        if (!none) {
+#pragma unroll
+            for (int f = 0; f < WF; ++f) {
+                if constexpr (LEAD) {
+                    uint32_t q[8][2];
+                    const int col = col0 + 4 * c;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int rk = 32 * f + j0 + j;
+                        load_n<4, VEC>(w + static_cast<size_t>(rk) * a.cols + col, rk < a.rank ? a.cols - col : 0, q[j]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) wf[f][i] = pick_column<4>(q, i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int col = col0 + 4 * c + i, rk = 32 * f + j0;
+                        wf[f][i] = load_row8<VEC>(w + static_cast<size_t>(col) * a.rank + rk, col < a.cols ? a.rank - rk : 0);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (16 * m >= rt.rows) break;
+            // lane (c, g): columns col + 4 v + i of row c
+            const int col = col0 + 16 * g, valid = a.cols - col;
+            const size_t at = static_cast<size_t>(row[m] < 0 ? 0 : row[m]) * a.cols + col;
+            u32v4 b[2] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+            if (a.base && row[m] >= 0) {
+                b[0] = load_row8<VOUT>(a.base + at, valid);
+                b[1] = load_row8<VOUT>(a.base + at + 8, valid - 8);
+            }
+            if (!none) {
+                f32x4 acc[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) acc[i] = mma<E>(wf[s % WF][i], tf[m][s], acc[i]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o = 0;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = 8 * h + 2 * k + e;
+                            const float d = ldexpf(acc[i & 3][i >> 2], -shift[m]);
+                            const uint32_t old = b[h][k];
+                            o |= static_cast<uint32_t>(E::put(E::get(static_cast<uint16_t>(old >> (16 * e))) + d)) << (16 * e);
+                        }
+                        b[h][k] = o;
+                    }
+            }
+            if (row[m] < 0) continue;
+            if constexpr (VOUT) {
+                if (valid > 0) *reinterpret_cast<u32v4 *>(a.out + at) = b[0];
+                if (valid > 8) *reinterpret_cast<u32v4 *>(a.out + at + 8) = b[1];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < valid) a.out[at + i] = static_cast<uint16_t>(b[i >> 3][i >> 1 & 3] >> (16 * (i & 1)));
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+// One of the two gradients: Σ over a group's rows of p (rows x rank, fp32)
+// times q (rows x cols); out: count x rank x cols, or (along) count x cols x rank.
+struct OuterSide {
+    const float *p = nullptr;
+    const uint16_t *q = nullptr;
+    int cols = 0, along = 0, strips = 0;  // strips of 128 columns (0: not computed)
+    const float *scale = nullptr;
+    float *out = nullptr, *part = nullptr;  // part: [places of chunks][rank][cols] or [cols][rank]
+};
+struct OuterArgs {
+    OuterSide side[2];
+    const int32_t *order, *offsets;
+    int rows, rank, count, chunk;  // rows of a chunk
+    int most;                      // chunks in the partial sums
+};
+
+// Chunk `index` of the groups' chunks; slot: its place among the chunks of
+// groups that have several, -1 for the only one of a group.
+__device__ __forceinline__ bool find_chunk(const OuterArgs &a, int index, RowTile &out, int &slot) {
+    const int lane = threadIdx.x & 63;
+    int before = 0, several = 0;
+    for (int e0 = 0; e0 < a.count; e0 += 64) {
+        int lo = 0, hi = 0;
+        if (e0 + lane < a.count) group_places(a.offsets, a.count, a.rows, e0 + lane, lo, hi);
+        const int n = (hi - lo + a.chunk - 1) / a.chunk, many = n > 1 ? n : 0;
+        const int upto = before + wave_scan(n, lane), sev = several + wave_scan(many, lane);
+        const uint64_t past = __ballot(upto > index);
+        if (past) {
+            const int at = __builtin_ctzll(past), i = index - __builtin_amdgcn_readlane(upto - n, at);
+            out.group = e0 + at;
+            out.first = __builtin_amdgcn_readlane(lo, at) + i * a.chunk;
+            out.rows = min(a.chunk, __builtin_amdgcn_readlane(hi, at) - out.first);
+            slot = __builtin_amdgcn_readlane(many, at) ? __builtin_amdgcn_readlane(sev - many, at) + i : -1;
+            return true;
+        }
+        before = __builtin_amdgcn_readlane(upto, 63);
+        several = __builtin_amdgcn_readlane(sev, 63);
+    }
+    return false;
+}
+
+constexpr int kMaxChunk = 2048;
+
+// A chunk's rows x 128 columns x 16 RT ranks per workgroup; the waves take 32
+// rows in turn.
+template <typename E, int RT, bool VEC>
+__global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
+    constexpr int RP = 16 * RT, Cols = 128, Pitch = Cols + 4;
+    constexpr int NP = E::code == DBF_TYPE_F16 ? 2 : 3;
+    __shared__ __attribute__((aligned(16))) float sums[RP][Pitch];
+    __shared__ __attribute__((aligned(16))) int rowid[kMaxChunk];
+    const int strips = a.side[0].strips + a.side[1].strips;
+    const int chunk = blockIdx.x / strips, st = blockIdx.x % strips;
+    const bool second = st >= a.side[0].strips;
+    const OuterSide &sd = a.side[second ? 1 : 0];
+    const int strip = second ? st - a.side[0].strips : st, jb = blockIdx.y * RP;
+    RowTile rt;
+    int slot;
+    if (!find_chunk(a, chunk, rt, slot)) return;
+    if (slot >= a.most) return;  // (offsets that are not of an order)
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int i = threadIdx.x; i < (rt.rows + 31) / 32 * 32; i += kThreads)
+        rowid[i] = i < rt.rows ? min(max(a.order[rt.first + i], 0), a.rows - 1) : -1;
+    __syncthreads();
+    const int steps = (rt.rows + 31) / 32, col0 = strip * Cols, col = col0 + 8 * c;
+    const int rk = jb + c * RT;  // this lane's first rank
+
+    // p of eight rows: ranks rk .. rk + RT - 1
+    auto load_p = [&](int s, float (&p)[8][RT]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = rowid[32 * s + 8 * g + j];
+            const float *src = sd.p + static_cast<size_t>(r < 0 ? 0 : r) * a.rank + rk;
+            bool vec = false;
+            if constexpr (RT > 1) vec = VEC && a.rank % RT == 0;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) p[j][i] = 0.0f;
+            if (r < 0) continue;
+            if (vec) {
+                if (rk < a.rank) {
+                    if constexpr (RT == 2) {
+                        const float2 v = *reinterpret_cast<const float2 *>(src);
+                        p[j][0] = v.x;
+                        p[j][1] = v.y;
+                    } else if constexpr (RT == 4) {
+                        const f32x4 v = *reinterpret_cast<const f32x4 *>(src);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p[j][i] = v[i];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    if (rk + i < a.rank) p[j][i] = src[i];
+            }
+        }
+    };
+    int shift = 0;
+    if constexpr (E::code == DBF_TYPE_F16) {
+        float top = 0.0f;
+        for (int s = wave; s < steps; s += kWaves) {
+            float p[8][RT];
+            load_p(s, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) top = fmaxf(top, finite_abs(p[j][i]));
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+        shift = f16_shift(top);
+    }
+    f32x4 acc[8][RT];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = wave; s < steps; s += kWaves) {
+        uint32_t q[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = rowid[32 * s + 8 * g + j];
+            load_n<8, VEC>(sd.q + static_cast<size_t>(r < 0 ? 0 : r) * sd.cols + col, r < 0 ? 0 : sd.cols - col, q[j]);
+        }
+        float p[8][RT];
+        load_p(s, p);
+        u32v4 pf[RT][NP];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = E::code == DBF_TYPE_F16 ? ldexpf(p[j][i], shift) : p[j][i];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) pf[i][n] = pack_part<E>(v, n);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const u32v4 qf = pick_column<8>(q, i);
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int n = 0; n < NP; ++n) acc[i][j] = mma<E>(qf, pf[j][n], acc[i][j]);
+        }
+    }
+    // lane (c, g): rank c RT + j, column 8 (4 g + v) + i; the waves' sums in order
+    for (int w = 0; w < kWaves; ++w) {
+        if (wave == w) {
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float &d = sums[c * RT + j][32 * g + 8 * v + i];
+                        const float x = ldexpf(acc[i][j][v], -shift);
+                        d = w == 0 ? x : d + x;
+                    }
+        }
+        __syncthreads();
+    }
+    const float scale = sd.scale ? sd.scale[rt.group] : 1.0f;
+    const size_t each = static_cast<size_t>(a.rank) * sd.cols;
+    float *out = slot < 0 ? sd.out + static_cast<size_t>(rt.group) * each : sd.part + static_cast<size_t>(slot) * each;
+    const int nr = min(RP, a.rank - jb), nc = min(Cols, sd.cols - col0);
+    if (sd.along) {
+        for (int i = threadIdx.x; i < nr * nc; i += kThreads) {
+            const int x = i / nr, j = i - x * nr;
+            out[static_cast<size_t>(col0 + x) * a.rank + jb + j] = sums[j][x] * scale;
+        }
+    } else {
+        for (int i = threadIdx.x; i < nr * nc; i += kThreads) {
+            const int j = i / nc, x = i - j * nc;
+            out[static_cast<size_t>(jb + j) * sd.cols + col0 + x] = sums[j][x] * scale;
+        }
+    }
+}
+
+// The chunks of each group that has several, added in order; zeros for groups
+// without rows.
+__global__ __launch_bounds__(kThreads) void outer_join_kernel(const OuterArgs a, int blocks0) {
+    const int group = blockIdx.y;
+    const bool second = static_cast<int>(blockIdx.x) >= blocks0;
+    const OuterSide &sd = a.side[second ? 1 : 0];
+    const int block = second ? blockIdx.x - blocks0 : blockIdx.x;
+    int lo, hi;
+    group_places(a.offsets, a.count, a.rows, group, lo, hi);
+    const int n = (hi - lo + a.chunk - 1) / a.chunk;
+    if (n == 1) return;
+    int first = 0;  // chunks of the groups with several before this one
+    const int lane = threadIdx.x & 63;
+    for (int e0 = 0; e0 < group; e0 += 64) {
+        int l = 0, h = 0;
+        if (e0 + lane < group) group_places(a.offsets, a.count, a.rows, e0 + lane, l, h);
+        const int k = (h - l + a.chunk - 1) / a.chunk;
+        first += __builtin_amdgcn_readlane(wave_scan(k > 1 ? k : 0, lane), 63);
+    }
+    const size_t each = static_cast<size_t>(a.rank) * sd.cols;
+    const size_t at = (static_cast<size_t>(block) * kThreads + threadIdx.x) * 4;
+    float *out = sd.out + static_cast<size_t>(group) * each;
+    for (int i = 0; i < 4; ++i) {
+        if (at + i >= each) break;
+        float v = 0.0f;
+        for (int k = 0; k < n && first + k < a.most; ++k) v += sd.part[static_cast<size_t>(first + k) * each + at + i];
+        out[at + i] = v;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+
+// 16-row tiles of a row tile: several where the groups fill them (their rows share the weight's operands).
+int row_frags(int rows, int count, int rt) {
+    const int used = rows < count ? rows : count;
+    return rows / used < 32 ? 1 : rt == 8 ? 2 : 4;
+}
+
+// K parts of a shrink: about two workgroups per CU, two steps of 32 for a wave at least.
+int shrink_parts(int rows, int count, int K, int rank) {
+    const int64_t tiles = grouped_row_tiles(rows, count, 16 * row_frags(rows, count, rank_tiles(rank)));
+    const int64_t steps = (K + 31) / 32, want = (512 + tiles - 1) / tiles, most = std::max<int64_t>(1, steps / (2 * kWaves));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, kMaxParts})));
+}
+
+size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+
+size_t part_bytes(int rows, int count, int K, int rank) {
+    return align16(sizeof(float) * static_cast<size_t>(shrink_parts(rows, count, K, rank)) * rows * 16 * rank_tiles(rank));
+}
+
+// Rows of a chunk: enough chunks to fill the GPU.
+int outer_chunk(int rows, int n, int m) {
+    const int64_t strips = (n + 127) / 128 + (m + 127) / 128;
+    int chunk = kMaxChunk;
+    while (chunk > 128 && (rows / chunk) * strips < 1024) chunk /= 2;
+    return chunk;
+}
+// Chunks of groups that have several: ceil(c / chunk) of more than chunk rows
+// each are less than twice rows / chunk.
+int64_t outer_slots(int rows, int chunk) { return rows > chunk ? 2 * static_cast<int64_t>(rows) / chunk : 0; }
+
+template <int V>
+using Tag = std::integral_constant<int, V>;
+template <typename F>
+void by_rank(int rank, F f) {
+    switch (rank_tiles(rank)) {
+        case 1: f(Tag<1>{}); break;
+        case 2: f(Tag<2>{}); break;
+        case 4: f(Tag<4>{}); break;
+        default: f(Tag<8>{}); break;
+    }
+}
+
+template <typename E, bool LEAD>
+void launch_shrink(const ShrinkArgs &a, hipStream_t s) {
+    by_rank(a.rank, [&](auto rt) {
+        constexpr int RT = decltype(rt)::value, Big = RT == 8 ? 2 : 4;
+        const bool vec = a.K % 8 == 0 && (!LEAD || a.rank % RT == 0);
+        auto go = [&](auto mt) {
+            constexpr int MT = decltype(mt)::value;
+            const dim3 grid(static_cast<uint32_t>(row_tiles_bound(a.rows, a.count, 16 * MT) * a.parts));
+            if (vec) launch_kernel(shrink_kernel<E, LEAD, MT, RT, true>, grid, dim3(kThreads), 0, s, a);
+            else launch_kernel(shrink_kernel<E, LEAD, MT, RT, false>, grid, dim3(kThreads), 0, s, a);
+        };
+        if (row_frags(a.rows, a.count, RT) == 1) go(Tag<1>{});
+        else go(Tag<Big>{});
+    });
+}
+
+template <typename E, bool LEAD>
+void launch_expand(ExpandArgs &a, hipStream_t s) {
+    by_rank(a.rank, [&](auto rt) {
+        constexpr int RT = decltype(rt)::value, Big = RT == 8 ? 2 : 4;
+        const bool vec = LEAD ? a.cols % 4 == 0 : a.rank % 8 == 0, vout = a.cols % 8 == 0;
+        auto go = [&](auto mt) {
+            constexpr int MT = decltype(mt)::value;
+            const int64_t tiles = row_tiles_bound(a.rows, a.count, 16 * MT);
+            const int64_t chunks = a.out ? (a.cols + 64 * kWaves - 1) / (64 * kWaves) : 1;
+            a.per = static_cast<int>(std::min<int64_t>(chunks, std::max<int64_t>(1, tiles * chunks / 1024)));
+            if (!a.out) a.per = static_cast<int>((static_cast<int64_t>(a.cols) + 64 * kWaves - 1) / (64 * kWaves));
+            const int64_t blocks = (a.cols + 64 * kWaves * a.per - 1) / (64 * kWaves * a.per);
+            const dim3 grid(static_cast<uint32_t>(tiles * blocks));
+            auto k = [&](auto v, auto o) {
+                launch_kernel(expand_kernel<E, LEAD, MT, RT, decltype(v)::value, decltype(o)::value>, grid, dim3(kThreads),
+                              0, s, a);
+            };
+            if (vec && vout) k(std::true_type{}, std::true_type{});
+            else if (vout) k(std::false_type{}, std::true_type{});
+            else k(std::false_type{}, std::false_type{});
+        };
+        if (row_frags(a.rows, a.count, RT) == 1) go(Tag<1>{});
+        else go(Tag<Big>{});
+    });
+}
+
+template <typename E>
+void launch_outer(const OuterArgs &a, hipStream_t s) {
+    const int rt = std::min(rank_tiles(a.rank), 4);
+    const int strips = a.side[0].strips + a.side[1].strips;
+    const dim3 grid(static_cast<uint32_t>(row_tiles_bound(a.rows, a.count, a.chunk) * strips), (a.rank + 16 * rt - 1) / (16 * rt));
+    bool vec = true;
+    for (const OuterSide &sd : a.side)
+        if (sd.strips > 0 && sd.cols % 8 != 0) vec = false;
+    auto go = [&](auto r) {
+        constexpr int RT = decltype(r)::value;
+        if (vec) launch_kernel(outer_kernel<E, RT, true>, grid, dim3(kThreads), 0, s, a);
+        else launch_kernel(outer_kernel<E, RT, false>, grid, dim3(kThreads), 0, s, a);
+    };
+    if (rt == 1) go(Tag<1>{});
+    else if (rt == 2) go(Tag<2>{});
+    else go(Tag<4>{});
+}
+
+void launch_outer_join(const OuterArgs &a, hipStream_t s) {
+    auto blocks = [&](const OuterSide &sd) {
+        return sd.strips > 0 ? static_cast<int>((static_cast<int64_t>(a.rank) * sd.cols + 4 * kThreads - 1) / (4 * kThreads)) : 0;
+    };
+    const int b0 = blocks(a.side[0]), b1 = blocks(a.side[1]);
+    launch_kernel(outer_join_kernel, dim3(b0 + b1, a.count), dim3(kThreads), 0, s, a, b0);
+}
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+dbf_status_t check_sizes(int32_t type, int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count) {
+    if (rows < 0 || n < 1 || m < 1 || rank < 1 || count < 1) return DBF_ERR_INVALID_ARG;
+    if (type != DBF_TYPE_F16 && type != DBF_TYPE_BF16) return DBF_ERR_INVALID_ARG;
+    // (the last: threads of the gradients' join)
+    const int64_t wide = std::max(n, m);
+    if (rank > kMaxRank || count > kMaxGroups || wide > (1 << 20) || rows > (1 << 24) || rows * wide > int64_t(1) << 40 ||
+        int64_t(count) * rank * wide > int64_t(1) << 32)
+        return DBF_ERR_SHAPE;
+    return DBF_OK;
+}
+bool sizes_ok(int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count) {
+    return check_sizes(DBF_TYPE_F16, rows, n, m, rank, count) == DBF_OK && rows > 0;
+}
+
+}  // namespace
+}  // namespace dbf
+
+extern "C" size_t dbf_adapter_workspace(int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count) {
+    using namespace dbf;
+    return sizes_ok(rows, n, m, rank, count) ? part_bytes(rows, count, m, rank) : 0;
+}
+
+extern "C" dbf_status_t dbf_adapter_forward(const void *x, const void *base, const void *A, const void *B,
+                                            const float *scale, int32_t type, const int32_t *order,
+                                            const int32_t *offsets, int32_t rows, int32_t n, int32_t m, int32_t rank,
+                                            int32_t count, void *y, float *t, void *workspace, size_t workspace_bytes,
+                                            hipStream_t stream) {
+    using namespace dbf;
+    const dbf_status_t st = check_sizes(type, rows, n, m, rank, count);
+    if (st != DBF_OK || rows == 0) return st;
+    for (const void *p : {x, base, A, B, static_cast<const void *>(y), static_cast<const void *>(workspace)})
+        if (!p || !aligned(p, 16)) return DBF_ERR_INVALID_ARG;
+    if (!order || !offsets || !aligned(order, 4) || !aligned(offsets, 4) || !aligned(scale, 4) || !aligned(t, 16) ||
+        workspace_bytes < part_bytes(rows, count, m, rank))
+        return DBF_ERR_INVALID_ARG;
+    const ShrinkArgs s{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(A), order, offsets, rows, m, rank,
+                       count, shrink_parts(rows, count, m, rank), static_cast<float *>(workspace)};
+    ExpandArgs e{s.out, static_cast<const uint16_t *>(B), scale, order, offsets, rows, n, rank, count, s.parts,
+                 static_cast<const uint16_t *>(base), static_cast<uint16_t *>(y), t, 0, 1};
+    if (type == DBF_TYPE_F16) {
+        launch_shrink<F16, false>(s, stream);
+        launch_expand<F16, false>(e, stream);
+    } else {
+        launch_shrink<BF16, false>(s, stream);
+        launch_expand<BF16, false>(e, stream);
+    }
+    return hipGetLastError() == hipSuccess ? DBF_OK : DBF_ERR_HIP;
+}
+
+// Workspace of the backward pass: the parts of u, u, and the chunks of both gradients.
+namespace {
+struct BackwardPlan {
+    size_t u = 0, dA = 0, dB = 0, total = 0;
+};
+BackwardPlan backward_plan(int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count) {
+    using namespace dbf;
+    BackwardPlan p;
+    p.u = part_bytes(rows, count, n, rank);
+    p.dA = p.u + align16(sizeof(float) * static_cast<size_t>(rows) * rank);
+    const size_t slots = static_cast<size_t>(outer_slots(rows, outer_chunk(rows, n, m)));
+    p.dB = p.dA + align16(sizeof(float) * slots * rank * m);
+    p.total = p.dB + align16(sizeof(float) * slots * rank * n);
+    return p;
+}
+}  // namespace
+
+extern "C" size_t dbf_adapter_backward_workspace(int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count) {
+    return dbf::sizes_ok(rows, n, m, rank, count) ? backward_plan(rows, n, m, rank, count).total : 0;
+}
+
+extern "C" dbf_status_t dbf_adapter_backward(const void *dy, const void *x, const float *t, const void *dx,
+                                             const void *A, const void *B, const float *scale, int32_t type,
+                                             const int32_t *order, const int32_t *offsets, int32_t rows, int32_t n,
+                                             int32_t m, int32_t rank, int32_t count, void *dx_out, float *dA, float *dB,
+                                             void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    using namespace dbf;
+    const dbf_status_t st = check_sizes(type, rows, n, m, rank, count);
+    if (st != DBF_OK) return st;
+    if (!dA && !dB && (!dx_out || rows == 0)) return DBF_OK;
+    if (!aligned(dA, 16) || !aligned(dB, 16) || !aligned(offsets, 4) || !offsets) return DBF_ERR_INVALID_ARG;
+    if (rows > 0) {
+        if (!dy || !B || !order || !workspace || (dB && !t) || (dA && !x) || (dx_out && !A)) return DBF_ERR_INVALID_ARG;
+        for (const void *p : {dy, x, dx, A, B, static_cast<const void *>(dx_out), static_cast<const void *>(workspace)})
+            if (!aligned(p, 16)) return DBF_ERR_INVALID_ARG;
+        if (!aligned(order, 4) || !aligned(scale, 4) || !aligned(t, 16) ||
+            workspace_bytes < backward_plan(rows, n, m, rank, count).total)
+            return DBF_ERR_INVALID_ARG;
+    }
+    const BackwardPlan plan = rows > 0 ? backward_plan(rows, n, m, rank, count) : BackwardPlan{};
+    char *ws = static_cast<char *>(workspace);
+    float *u = reinterpret_cast<float *>(ws + plan.u);
+    if (rows > 0 && (dx_out || dA)) {
+        const ShrinkArgs s{static_cast<const uint16_t *>(dy), static_cast<const uint16_t *>(B), order, offsets, rows, n,
+                           rank, count, shrink_parts(rows, count, n, rank), static_cast<float *>(workspace)};
+        ExpandArgs e{s.out, static_cast<const uint16_t *>(A), scale, order, offsets, rows, m, rank, count, s.parts,
+                     static_cast<const uint16_t *>(dx), static_cast<uint16_t *>(dx_out), dA ? u : nullptr, 1, 1};
+        if (type == DBF_TYPE_F16) {
+            launch_shrink<F16, true>(s, stream);
+            launch_expand<F16, true>(e, stream);
+        } else {
+            launch_shrink<BF16, true>(s, stream);
+            launch_expand<BF16, true>(e, stream);
+        }
+    }
+    if (dA || dB) {
+        OuterArgs o{};
+        o.order = order;
+        o.offsets = offsets;
+        o.rows = rows;
+        o.rank = rank;
+        o.count = count;
+        o.chunk = rows > 0 ? outer_chunk(rows, n, m) : 128;
+        o.most = rows > 0 ? static_cast<int>(outer_slots(rows, o.chunk)) : 0;
+        if (dA) o.side[0] = {u, static_cast<const uint16_t *>(x), m, 0, (m + 127) / 128, nullptr, dA,
+                             reinterpret_cast<float *>(ws + plan.dA)};
+        if (dB) o.side[1] = {t, static_cast<const uint16_t *>(dy), n, 1, (n + 127) / 128, scale, dB,
+                             reinterpret_cast<float *>(ws + plan.dB)};
+        if (rows > 0) {
+            if (type == DBF_TYPE_F16) launch_outer<F16>(o, stream);
+            else launch_outer<BF16>(o, stream);
+        }
+        launch_outer_join(o, stream);
+    }
+    return hipGetLastError() == hipSuccess ? DBF_OK : DBF_ERR_HIP;
+}

@@ -309,11 +309,36 @@ struct MxPlan {
     int tile = 0, nsplit = 1;
 };
 
+// Rows of a product that belong to groups, each with its own weight (include/dbf.h,
+// "Rows in groups"): `slots` places in the grouped order, those from
+// offsets[count] on of no group.  table[0].x is the number of row tiles,
+// table[1 + i] tile i: {group, first place, places, 0}; launch_row_tiles makes
+// it.  The input's row of a place is the place itself (per = 0) or its
+// order / per of in_rows; the result's row the place or (scatter) its order.
+// Values out of range are clamped, or not written.
+struct RowTile {
+    int32_t group, first, rows, zero;
+};
+struct MxRows {
+    const int32_t *order = nullptr;
+    const RowTile *table = nullptr;
+    int count = 0, slots = 0, per = 0, in_rows = 0, scatter = 0;
+    size_t code_stride = 0, scale_stride = 0, colmax_stride = 0;  // from a group's weight to the next
+};
+// Row tiles of `tile` places that groups of `slots` places can make at most.
+DBF_HD inline int64_t row_tiles_bound(int64_t slots, int count, int tile) {
+    return slots / tile + (slots < count + 1 ? slots : count + 1);
+}
+// bound: entries of the table past the first.
+int launch_row_tiles(const int32_t *offsets, int count, int slots, int tile, RowTile *table, int64_t bound, void *stream);
+
 // y (M x n, y_type f16 / bf16) = x wᵀ with x in blocks: codes in padded rows
 // of w.blocks blocks (x_type e4m3 / e2m1), scales in 32-row tiles like the
 // weight's (launch_mx_tile_scales, or launch_mx_quantize with tiled).  part:
 // at least mx_product_parts() floats for the sums of K parts.  Where the plan
-// has K parts, launch_mx_product_join is the second launch.
+// has K parts, launch_mx_product_join is the second launch.  rows (null: one
+// group of M rows): M = slots, w the first group's weight, and xscales in
+// padded rows like xcodes.
 struct MxProduct {
     const void *xcodes = nullptr;
     const uint8_t *xscales = nullptr;
@@ -324,8 +349,12 @@ struct MxProduct {
     float *part = nullptr;
     size_t part_cap = 0;
     MxPlan plan;
+    const MxRows *rows = nullptr;
 };
 MxPlan mx_product_plan(int M, int n, int blocks, int x_type);
+// The same for `slots` rows that up to `count` groups share.
+MxPlan mx_grouped_plan(int slots, int count, int n, int blocks, int x_type);
+size_t mx_grouped_parts(int slots, int count, int n, int blocks, int x_type);
 void mx_product_tile(const MxPlan &p, int32_t *rows, int32_t *cols);
 // Floats of K-part sums that the product of this shape uses (0: K whole).
 size_t mx_product_parts(int M, int n, int blocks, int x_type);
@@ -343,8 +372,11 @@ struct MxBackward {
     float *part = nullptr;
     size_t part_cap = 0;
     MxPlan plan;
+    const MxRows *rows = nullptr;  // as in MxProduct
 };
 MxPlan mx_backward_plan(int M, int n, int m);
+MxPlan mx_grouped_backward_plan(int slots, int count, int n, int m);
+size_t mx_grouped_backward_parts(int slots, int count, int n, int m);
 void mx_backward_tile(const MxPlan &p, int32_t *rows, int32_t *cols);
 size_t mx_backward_parts(int M, int n, int m);
 int launch_mx_backward(const MxBackward &b, void *stream);

@@ -156,27 +156,38 @@ struct MxGemmArgs {
     void *y;
     TileGrid grid;
     float *part;             // null: whole sums to y
+    MxRows rows;             // grouped products
 };
 
-template <typename C, typename E>
-__global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a) {
+// G: rows in groups.  A tile's rows are those of one group, m0 = 0 its first
+// and M their number.
+template <typename C, typename E, bool G>
+__global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    if constexpr (G) {
+        a.grid.nbm = a.rows.table[0].group;
+        a.grid.group = min(a.grid.nbm, 4);
+    }
     const int T = a.grid.nbm * a.grid.nbn;
+    if (G && static_cast<int>(blockIdx.x) >= T * a.grid.nsplit) return;
     const int idx = xcd_index(blockIdx.x, T * a.grid.nsplit);
     const int split = idx / T, tile = idx - split * T;
     int bm, bn;
     tile_at(a.grid, tile, bm, bn);
-    const int m0 = bm * C::BM, n0 = bn * C::BN;
+    const int m0 = G ? 0 : bm * C::BM, n0 = bn * C::BN;
+    [[maybe_unused]] const RowPlaces place = take_group<G>(a.rows, bm, a.w, a.M);
     const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
     const int steps = a.w.blocks >> 2;  // of 128 columns
     const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / a.grid.nsplit);
-    const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * steps / a.grid.nsplit) - k0;
+    // (rows of no group: no steps, their results are zeros)
+    const int nk = G && place.none ? 0 : static_cast<int>(static_cast<int64_t>(split + 1) * steps / a.grid.nsplit) - k0;
 
     // sources of this wave's loads; a stage moves them by inc bytes
     const uint8_t *src[C::D16 + C::D4];
     int inc[C::D16], at[C::D16 + C::D4];
+    int inc4[C::D4];
 #pragma unroll
     for (int q = 0; q < C::D16; ++q) {
         const int u = min(wave * C::D16 + q, C::Units16 - 1);  // (a unit too many: loaded twice, the same bytes)
@@ -184,7 +195,8 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a)
         constexpr int XU = C::XBytes / 1024;
         if (u < XU) {
             const int c = u * 64 + lane, r = c >> 2, lc = (c & 3) ^ ((r >> 2) & 3);
-            const int row = min(m0 + r, a.M - 1);  // rows past M: multiplied, not written
+            int64_t row = min(m0 + r, a.M - 1);  // rows past M: multiplied, not written
+            if constexpr (G) row = place.in(a.rows, static_cast<int>(row));
             src[q] = a.xc + (static_cast<size_t>(row) * steps + k0) * (64 * C::Parts) + lc * 16;
             inc[q] = 64;
         } else {
@@ -203,6 +215,12 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a)
         // 32-row tiles; those past the end (and the padding of the last load): any valid one
         const int t = x ? min((m0 + r) / 32, (a.M + 31) / 32 - 1) : min((n0 + r - C::BM) / 32, a.w.n_pad / 32 - 1);
         src[q] = (x ? a.xs : a.w.scales) + (static_cast<size_t>(t) * steps + k0) * 128 + (r & 31) * 4;
+        inc4[q - C::D16] = 128;
+        if constexpr (G)
+            if (x) {
+                src[q] = a.xs + (static_cast<size_t>(place.in(a.rows, min(r, a.M - 1))) * steps + k0) * 4;
+                inc4[q - C::D16] = 4;
+            }
     }
     // load q of the stage in slot `slot`
     auto issue_one = [&](int slot, int q) {
@@ -211,7 +229,7 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a)
             src[q] += inc[q];
         } else {
             dma4(src[q], lds + (slot / C::Parts) * C::SBytes + at[q]);
-            src[q] += 128;
+            src[q] += G ? inc4[q - C::D16] : 128;
         }
     };
 
@@ -307,22 +325,35 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(const MxGemmArgs a)
     }
     static_assert(C::Waves * store_bytes<C>() <= C::Lds, "a result fits the ring");
     __syncthreads();  // every wave's last operands have been read
-    store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.y, a.M, a.w.n, m0, n0, wave, lane);
+    if constexpr (G)
+        store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.y, a.M, a.w.n, m0, n0, wave, lane,
+                         [&](int r) { return place.out(a.rows, r); });
+    else store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.y, a.M, a.w.n, m0, n0, wave, lane);
 }
 
 // The K parts of a tile, added in order and stored; a workgroup is one wave of
 // the product's (a whole tile in one: 17 x 4096, K 14336: 16.7 instead of 15.2 us).
-template <typename C, typename E>
-__global__ __launch_bounds__(64) void mx_finish_kernel(const MxGemmArgs a) {
+template <typename C, typename E, bool G>
+__global__ __launch_bounds__(64) void mx_finish_kernel(MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    if constexpr (G) {
+        a.grid.nbm = a.rows.table[0].group;
+        a.grid.group = min(a.grid.nbm, 4);
+    }
     const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves;
+    if (G && tile >= T) return;
     int bm, bn;
     tile_at(a.grid, tile, bm, bn);
     const int lane = threadIdx.x;
     f32x16 acc[C::MI][C::NI];
     add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
                  a.grid.nsplit, acc);
-    store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, bm * C::BM, bn * C::BN, wave, lane);
+    if constexpr (G) {
+        const RowPlaces place = take_group<G>(a.rows, bm, a.w, a.M);
+        store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, 0, bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
+    } else {
+        store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, bm * C::BM, bn * C::BN, wave, lane);
+    }
 }
 
 }  // namespace
@@ -358,13 +389,15 @@ constexpr int kCus = 256;
 // 14336, K 4096: 256 x 256 tiles 99 to 114 us, 128 x 256 117; 2048 x 4096,
 // K 14336: 134 and 91; 64 x 4096, K 14336, 64 x 64 tiles: four parts 18.7, one
 // 34.7; 17 x 4096, K 14336, four parts: 32 x 64 14.9, 64 x 64 17.1.)
-MxPlan mx_plan(int M, int n, int steps, bool x8) {
+// row_tiles(rows of a tile): the product's row tiles.
+template <typename F>
+MxPlan mx_plan(F row_tiles, int n, int steps, bool x8) {
     MxPlan best;
     float least = 0.0f;
     const int f = x8 ? 0 : 1;
     for (int t = 0; t < kTileCount; ++t) {
         const TileCost &c = kTiles[t];
-        const int64_t tiles = static_cast<int64_t>((M + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
+        const int64_t tiles = row_tiles(c.bm) * ((n + c.bn - 1) / c.bn);
         for (int sp : {1, 2, 3, 4, 6, 8}) {
             if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
             const float wgs = static_cast<float>(tiles) * sp;
@@ -400,13 +433,14 @@ template <int FMT>
 struct TileOf<FMT, 5> { using C = MxTile<FMT, 1, 1, 1, 2, FMT == DBF_TYPE_E4M3 ? 16 : 12>; };
 
 // The product's launch, or the join of its K parts.
-template <typename C, typename E>
+template <typename C, typename E, bool G>
 void launch_gemm(MxGemmArgs &a, bool join, hipStream_t s) {
-    auto product = mx_gemm_kernel<C, E>;
-    auto finish = mx_finish_kernel<C, E>;
+    auto product = mx_gemm_kernel<C, E, G>;
+    auto finish = mx_finish_kernel<C, E, G>;
     static std::atomic<uint64_t> lds_product{0};
     TileGrid &t = a.grid;
-    t.nbm = (a.M + C::BM - 1) / C::BM;
+    // (of rows in groups the number of row tiles is on the device: the grid holds the most there can be)
+    t.nbm = G ? static_cast<int>(row_tiles_bound(a.M, a.rows.count, C::BM)) : (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.n + C::BN - 1) / C::BN;
     t.group = t.nbm < 4 ? t.nbm : 4;
     if (join) {
@@ -417,13 +451,13 @@ void launch_gemm(MxGemmArgs &a, bool join, hipStream_t s) {
     launch_kernel(product, dim3(t.nbm * t.nbn * t.nsplit), dim3(C::Threads), C::Lds, s, a);
 }
 
-template <int FMT, typename E, int T = 0>
+template <int FMT, typename E, bool G, int T = 0>
 void launch_tile(int tile, MxGemmArgs &a, bool join, hipStream_t s) {
     if constexpr (T < kTileCount) {
         using C = typename TileOf<FMT, T>::C;
         static_assert(C::BM == kTiles[T].bm && C::BN == kTiles[T].bn, "the table's tile");
-        if (tile == T) launch_gemm<C, E>(a, join, s);
-        else launch_tile<FMT, E, T + 1>(tile, a, join, s);
+        if (tile == T) launch_gemm<C, E, G>(a, join, s);
+        else launch_tile<FMT, E, G, T + 1>(tile, a, join, s);
     }
 }
 
@@ -433,10 +467,16 @@ size_t part_floats(const MxPlan &p, int M, int n) {
     const TileCost &c = kTiles[p.tile];
     return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((n + c.bn - 1) / c.bn * c.bn);
 }
+size_t grouped_part_floats(const MxPlan &p, int slots, int count, int n) {
+    if (p.nsplit == 1) return 0;
+    const TileCost &c = kTiles[p.tile];
+    return static_cast<size_t>(p.nsplit) * (row_tiles_bound(slots, count, c.bm) * c.bm) * ((n + c.bn - 1) / c.bn * c.bn);
+}
 
 int launch_either(const MxProduct &p, bool join, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (p.plan.nsplit > 1 && (!p.part || p.part_cap < part_floats(p.plan, p.M, p.w.n)))
+    if (p.plan.nsplit > 1 && (!p.part || p.part_cap < (p.rows ? grouped_part_floats(p.plan, p.M, p.rows->count, p.w.n)
+                                                              : part_floats(p.plan, p.M, p.w.n))))
         return static_cast<int>(hipErrorInvalidValue);
     MxGemmArgs a{};
     a.xc = static_cast<const uint8_t *>(p.xcodes);
@@ -446,10 +486,16 @@ int launch_either(const MxProduct &p, bool join, void *stream) {
     a.y = p.y;
     a.grid.nsplit = p.plan.nsplit;
     a.part = p.plan.nsplit > 1 ? p.part : nullptr;
+    if (p.rows) a.rows = *p.rows;
     auto pick = [&](auto f) {
         constexpr int FMT = decltype(f)::value;
-        if (p.y_type == DBF_TYPE_F16) launch_tile<FMT, F16>(p.plan.tile, a, join, s);
-        else launch_tile<FMT, BF16>(p.plan.tile, a, join, s);
+        if (p.rows) {
+            if (p.y_type == DBF_TYPE_F16) launch_tile<FMT, F16, true>(p.plan.tile, a, join, s);
+            else launch_tile<FMT, BF16, true>(p.plan.tile, a, join, s);
+        } else {
+            if (p.y_type == DBF_TYPE_F16) launch_tile<FMT, F16, false>(p.plan.tile, a, join, s);
+            else launch_tile<FMT, BF16, false>(p.plan.tile, a, join, s);
+        }
     };
     if (p.x_type == DBF_TYPE_E4M3) pick(Const<DBF_TYPE_E4M3>{});
     else pick(Const<DBF_TYPE_E2M1>{});
@@ -459,7 +505,18 @@ int launch_either(const MxProduct &p, bool join, void *stream) {
 }  // namespace
 
 MxPlan mx_product_plan(int M, int n, int blocks, int x_type) {
-    return mx_plan(M, n, blocks / 4, x_type == DBF_TYPE_E4M3);
+    return mx_plan([&](int bm) { return static_cast<int64_t>((M + bm - 1) / bm); }, n, blocks / 4,
+                   x_type == DBF_TYPE_E4M3);
+}
+
+// The groups' sizes are on the device: every group is taken to have its share
+// of the rows, and half a tile's loss at its end.
+MxPlan mx_grouped_plan(int slots, int count, int n, int blocks, int x_type) {
+    return mx_plan([&](int bm) { return grouped_row_tiles(slots, count, bm); }, n, blocks / 4, x_type == DBF_TYPE_E4M3);
+}
+
+size_t mx_grouped_parts(int slots, int count, int n, int blocks, int x_type) {
+    return grouped_part_floats(mx_grouped_plan(slots, count, n, blocks, x_type), slots, count, n);
 }
 
 void mx_product_tile(const MxPlan &p, int32_t *rows, int32_t *cols) {

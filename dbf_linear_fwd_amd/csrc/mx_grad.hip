@@ -60,6 +60,7 @@ struct MxGradArgs {
     void *dx;
     TileGrid grid;
     float *part;
+    MxRows rows;  // grouped products
 };
 
 // The factor of a block's codes: 2^(s - smax + kShift).
@@ -131,16 +132,23 @@ __device__ __forceinline__ void scale_columns(f32x16 (&acc)[C::MI][C::NI], const
 // (n a multiple of 8).  Elements: any n, dy through registers.
 enum class GradRows { Whole, Rows16, Elements };
 
-template <typename C, typename E, GradRows ROWS>
-__global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a) {
+// G: rows in groups (as in the forward's product).
+template <typename C, typename E, GradRows ROWS, bool G>
+__global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
     constexpr bool Whole = ROWS == GradRows::Whole, Dma = ROWS != GradRows::Elements;
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    if constexpr (G) {
+        a.grid.nbm = a.rows.table[0].group;
+        a.grid.group = min(a.grid.nbm, 4);
+        if (static_cast<int>(blockIdx.x) >= a.grid.nbm * a.grid.nbn * a.grid.nsplit) return;
+    }
     const int T = a.grid.nbm * a.grid.nbn;
     const int idx = xcd_index(blockIdx.x, T * a.grid.nsplit);
     const int split = idx / T, tile = idx - split * T;
     int bm, bn;
     tile_at(a.grid, tile, bm, bn);
-    const int m0 = bm * C::BM, n0 = bn * C::BN;
+    const int m0 = G ? 0 : bm * C::BM, n0 = bn * C::BN;
+    [[maybe_unused]] const RowPlaces place = take_group<G>(a.rows, bm, a.w, a.M);
     const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
@@ -158,8 +166,13 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
         const int c = (wave * C::DA + q) * 64 + lane, r = c >> 3, at = ((c & 7) ^ ((r >> 1) & 7)) * 8;
         const int row = min(m0 + r, a.M - 1);  // rows past M: not written
         col[q] = k0 * C::BK + at;
-        src[q] = dy + static_cast<size_t>(row) * a.w.n + col[q];
-        off[q] = (static_cast<uint32_t>(row - m0) * a.w.n + at) * 2;
+        if constexpr (G) {
+            // Whole: the row's first step, the others by their number
+            src[q] = dy + static_cast<size_t>(place.in(a.rows, row)) * a.w.n + (Whole ? at : col[q]);
+        } else {
+            src[q] = dy + static_cast<size_t>(row) * a.w.n + col[q];
+            off[q] = (static_cast<uint32_t>(row - m0) * a.w.n + at) * 2;
+        }
     }
     const char *tile_dy = reinterpret_cast<const char *>(dy + static_cast<size_t>(m0) * a.w.n);
     int dstep = k0;  // of load_dy's next call
@@ -167,7 +180,9 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
         char *st = lds + slot * C::ABytes;
 #pragma unroll
         for (int q = 0; q < C::DA; ++q) {
-            if constexpr (Whole) {
+            if constexpr (Whole && G) {
+                dma16(src[q] + static_cast<size_t>(min(dstep, steps - 1)) * C::BK, st + (wave * C::DA + q) * 1024);
+            } else if constexpr (Whole) {
                 dma16(tile_dy + static_cast<size_t>(min(dstep, steps - 1)) * (2 * C::BK) + off[q],
                       st + (wave * C::DA + q) * 1024);
             } else if constexpr (Dma) {
@@ -339,7 +354,8 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
     load_frags(0, 0, 0, f0);
     read_w(1);
     int s = 0;
-    for (int kt = 0; kt < nk; ++kt) {
+    // (rows of no group: no step, their results are zeros)
+    for (int kt = G && place.none ? nk : 0; kt < nk; ++kt) {
         load_frags(1, s, s, f1);
         multiply(f0);
         take_w();
@@ -378,12 +394,20 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(const MxGradArgs a)
         return;
     }
     scale_columns<C, E>(acc, a.w, n0, wn);
-    store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.dx, a.M, a.w.m, m0, n0, wave, lane);
+    if constexpr (G)
+        store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.dx, a.M, a.w.m, m0, n0, wave, lane,
+                         [&](int r) { return place.out(a.rows, r); });
+    else store_tile<C, E>(lds + wave * store_bytes<C>(), acc, a.dx, a.M, a.w.m, m0, n0, wave, lane);
 }
 
-template <typename C, typename E>
-__global__ __launch_bounds__(64) void mx_grad_finish_kernel(const MxGradArgs a) {
+template <typename C, typename E, bool G>
+__global__ __launch_bounds__(64) void mx_grad_finish_kernel(MxGradArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    if constexpr (G) {
+        a.grid.nbm = a.rows.table[0].group;
+        a.grid.group = min(a.grid.nbm, 4);
+        if (static_cast<int>(blockIdx.x) >= a.grid.nbm * a.grid.nbn * C::Waves) return;
+    }
     const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves;
     int bm, bn;
     tile_at(a.grid, tile, bm, bn);
@@ -391,8 +415,11 @@ __global__ __launch_bounds__(64) void mx_grad_finish_kernel(const MxGradArgs a) 
     f32x16 acc[C::MI][C::NI];
     add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
                  a.grid.nsplit, acc);
+    [[maybe_unused]] const RowPlaces place = take_group<G>(a.rows, bm, a.w, a.M);
     scale_columns<C, E>(acc, a.w, bn * C::BN, wave % C::WN);
-    store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, bm * C::BM, bn * C::BN, wave, lane);
+    if constexpr (G)
+        store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, 0, bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
+    else store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, bm * C::BM, bn * C::BN, wave, lane);
 }
 
 // ---- choice of the tile and of the K parts
@@ -420,13 +447,15 @@ constexpr int kCus = 256;
 // sizes the choice is 4.4 % from the best on average; 512 rows take 88 us in
 // 128 x 128 tiles and two parts, 77.5 in 256 x 256 and eight; at worst 45.5
 // where 35 is the best, 128 rows of n 4096, m 14336.)
-MxPlan grad_plan(int M, int n, int m) {
+// row_tiles(rows of a tile): the product's row tiles.
+template <typename F>
+MxPlan grad_plan(F row_tiles, int n, int m) {
     MxPlan best;
     float least = 0.0f;
     const int steps = (n + 63) / 64;
     for (int t = 0; t < kGradCount; ++t) {
         const GradCost &c = kGrad[t];
-        const int64_t tiles = static_cast<int64_t>((M + c.bm - 1) / c.bm) * ((m + c.bn - 1) / c.bn);
+        const int64_t tiles = row_tiles(c.bm) * ((m + c.bn - 1) / c.bn);
         for (int sp : {1, 2, 3, 4, 6, 8, 12}) {
             if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
             const float wgs = static_cast<float>(tiles) * sp;
@@ -446,21 +475,21 @@ MxPlan grad_plan(int M, int n, int m) {
 }
 
 // The product's launch, or the join of its K parts.
-template <typename C, typename E>
+template <typename C, typename E, bool G>
 void launch_grad(MxGradArgs &a, bool join, hipStream_t s) {
     static std::atomic<uint64_t> lds0{0}, lds1{0}, lds2{0};
     TileGrid &t = a.grid;
-    t.nbm = (a.M + C::BM - 1) / C::BM;
+    t.nbm = G ? static_cast<int>(row_tiles_bound(a.M, a.rows.count, C::BM)) : (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.m + C::BN - 1) / C::BN;
     t.group = t.nbm < 4 ? t.nbm : 4;
     if (join) {
-        auto k = mx_grad_finish_kernel<C, E>;
+        auto k = mx_grad_finish_kernel<C, E, G>;
         launch_kernel(k, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
         return;
     }
     const dim3 grid(t.nbm * t.nbn * t.nsplit);
     auto go = [&](auto rows, std::atomic<uint64_t> &asked) {
-        auto k = mx_grad_kernel<C, E, decltype(rows)::value>;
+        auto k = mx_grad_kernel<C, E, decltype(rows)::value, G>;
         if constexpr (C::Lds > 65536) allow_lds(k, C::Lds, asked);
         launch_kernel(k, grid, dim3(C::Threads), C::Lds, s, a);
     };
@@ -477,10 +506,16 @@ size_t part_floats(const MxPlan &p, int M, int m) {
     const GradCost &c = kGrad[p.tile];
     return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((m + c.bn - 1) / c.bn * c.bn);
 }
+size_t grouped_part_floats(const MxPlan &p, int slots, int count, int m) {
+    if (p.nsplit == 1) return 0;
+    const GradCost &c = kGrad[p.tile];
+    return static_cast<size_t>(p.nsplit) * (row_tiles_bound(slots, count, c.bm) * c.bm) * ((m + c.bn - 1) / c.bn * c.bn);
+}
 
 int launch_either(const MxBackward &b, bool join, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (b.plan.nsplit > 1 && (!b.part || b.part_cap < part_floats(b.plan, b.M, b.w.m)))
+    if (b.plan.nsplit > 1 && (!b.part || b.part_cap < (b.rows ? grouped_part_floats(b.plan, b.M, b.rows->count, b.w.m)
+                                                              : part_floats(b.plan, b.M, b.w.m))))
         return static_cast<int>(hipErrorInvalidValue);
     MxGradArgs a{};
     a.dy = b.dy;
@@ -490,27 +525,43 @@ int launch_either(const MxBackward &b, bool join, void *stream) {
     a.dx = b.dx;
     a.grid.nsplit = b.plan.nsplit;
     a.part = b.plan.nsplit > 1 ? b.part : nullptr;
-    auto go = [&](auto e) {
+    if (b.rows) a.rows = *b.rows;
+    auto go = [&](auto e, auto grouped) {
         using E = decltype(e);
-        if (b.plan.tile == 0) launch_grad<GradTile<4, 2, 2, 4>, E>(a, join, s);
-        else if (b.plan.tile == 1) launch_grad<GradTile<2, 2, 2, 2>, E>(a, join, s);
-        else launch_grad<GradTile<1, 1, 1, 4>, E>(a, join, s);
+        constexpr bool G = decltype(grouped)::value;
+        if (b.plan.tile == 0) launch_grad<GradTile<4, 2, 2, 4>, E, G>(a, join, s);
+        else if (b.plan.tile == 1) launch_grad<GradTile<2, 2, 2, 2>, E, G>(a, join, s);
+        else launch_grad<GradTile<1, 1, 1, 4>, E, G>(a, join, s);
     };
-    if (b.type == DBF_TYPE_BF16) go(BF16{});
-    else go(F16{});
+    auto type = [&](auto grouped) {
+        if (b.type == DBF_TYPE_BF16) go(BF16{}, grouped);
+        else go(F16{}, grouped);
+    };
+    if (b.rows) type(std::true_type{});
+    else type(std::false_type{});
     return static_cast<int>(hipGetLastError());
 }
 
 }  // namespace
 
-MxPlan mx_backward_plan(int M, int n, int m) { return grad_plan(M, n, m); }
+MxPlan mx_backward_plan(int M, int n, int m) {
+    return grad_plan([&](int bm) { return static_cast<int64_t>((M + bm - 1) / bm); }, n, m);
+}
+
+MxPlan mx_grouped_backward_plan(int slots, int count, int n, int m) {
+    return grad_plan([&](int bm) { return grouped_row_tiles(slots, count, bm); }, n, m);
+}
+
+size_t mx_grouped_backward_parts(int slots, int count, int n, int m) {
+    return grouped_part_floats(mx_grouped_backward_plan(slots, count, n, m), slots, count, m);
+}
 
 void mx_backward_tile(const MxPlan &p, int32_t *rows, int32_t *cols) {
     *rows = kGrad[p.tile].bm;
     *cols = kGrad[p.tile].bn;
 }
 
-size_t mx_backward_parts(int M, int n, int m) { return part_floats(grad_plan(M, n, m), M, m); }
+size_t mx_backward_parts(int M, int n, int m) { return part_floats(mx_backward_plan(M, n, m), M, m); }
 
 int launch_mx_backward(const MxBackward &b, void *stream) { return launch_either(b, false, stream); }
 

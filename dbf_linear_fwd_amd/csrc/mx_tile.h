@@ -3,6 +3,7 @@
 #ifndef DBF_MX_TILE_H_
 #define DBF_MX_TILE_H_
 
+#include <algorithm>
 #include <atomic>
 
 #include "mx_device.h"
@@ -78,6 +79,45 @@ __device__ __forceinline__ void tile_at(const TileGrid &a, int tile, int &bm, in
     bm = band * a.group + at - bn * rows;
 }
 
+// The rows of one tile of a product on rows in groups (MxRows).
+struct RowPlaces {
+    int first = 0;      // the tile's first place in the grouped order
+    bool none = false;  // rows of no group
+    // row of the input / of the result for row r of the tile (-1: not written)
+    __device__ __forceinline__ int64_t in(const MxRows &a, int r) const {
+        int64_t at = first + r;
+        if (a.per > 0) at = a.order[at] / a.per;
+        return at < 0 ? 0 : at < a.in_rows ? at : a.in_rows - 1;
+    }
+    __device__ __forceinline__ int64_t out(const MxRows &a, int r) const {
+        const int64_t at = a.scatter ? a.order[first + r] : first + r;
+        return at < a.slots ? at : -1;
+    }
+};
+
+// The rows of row tile bm, and their group's weight in place of the first.
+template <bool G>
+__device__ __forceinline__ RowPlaces take_group(const MxRows &a, int bm, MxWeight &w, int &M) {
+    RowPlaces p;
+    if constexpr (G) {
+        const RowTile t = a.table[1 + bm];
+        p.first = t.first;
+        p.none = t.group >= a.count;
+        M = t.rows;
+        const size_t e = p.none ? 0 : t.group;
+        w.codes += e * a.code_stride;
+        w.scales += e * a.scale_stride;
+        w.colmax += e * a.colmax_stride;
+    }
+    return p;
+}
+
+// Row tiles of `bm` places to reckon with where `count` groups share `slots` rows.
+inline int64_t grouped_row_tiles(int slots, int count, int bm) {
+    const int64_t used = slots < count ? slots : count;
+    return std::max<int64_t>(used, slots / bm + used / 2);
+}
+
 // A wave's results to y.  A 32 x 32 result has one row of y per lane, its
 // columns 8 (v / 4) + 4 g + v % 4 in register v; each wave takes them through
 // its own part of LDS (store_bytes at `mine`) into rows of 16-byte stores.  (Stored from the
@@ -86,9 +126,10 @@ __device__ __forceinline__ void tile_at(const TileGrid &a, int tile, int &bm, in
 template <typename C>
 constexpr size_t store_bytes() { return 32 * (64 * C::NI + 16); }
 
-template <typename C, typename E>
+// row_of(r): where row r < M of the results lies in y, -1: nowhere.
+template <typename C, typename E, typename R>
 __device__ __forceinline__ void store_tile(char *mine, const f32x16 (&acc)[C::MI][C::NI], void *out, int M,
-                                           int n, int m0, int n0, int wave, int lane) {
+                                           int n, int m0, int n0, int wave, int lane, R row_of) {
     const int wm = wave / C::WN, wn = wave % C::WN, l32 = lane & 31, g = lane >> 5;
     constexpr int Cols = 32 * C::NI, Pitch = Cols * 2 + 16;  // 16-bit values of a wave's row, bytes
     static_assert(store_bytes<C>() == 32 * Pitch, "");
@@ -116,18 +157,29 @@ __device__ __forceinline__ void store_tile(char *mine, const f32x16 (&acc)[C::MI
             for (int j = 0; j < 32; j += Rows) {
                 const int r = j + lane / Per;
                 const u32v4 v = *reinterpret_cast<const u32v4 *>(mine + r * Pitch + c * 2);
-                if (r0 + r < M && c0 + c < n)
-                    *reinterpret_cast<u32v4 *>(y + static_cast<size_t>(r0 + r) * n + c0 + c) = v;
+                if (r0 + r < M && c0 + c < n) {
+                    const int64_t at = row_of(r0 + r);
+                    if (at >= 0) *reinterpret_cast<u32v4 *>(y + static_cast<size_t>(at) * n + c0 + c) = v;
+                }
             }
         } else {
             for (int j = lane; j < 32 * Cols; j += 64) {
                 const int r = j / Cols, c = j % Cols;
-                if (r0 + r < M && c0 + c < n)
-                    y[static_cast<size_t>(r0 + r) * n + c0 + c] =
-                        *reinterpret_cast<const uint16_t *>(mine + r * Pitch + c * 2);
+                if (r0 + r < M && c0 + c < n) {
+                    const int64_t at = row_of(r0 + r);
+                    if (at >= 0)
+                        y[static_cast<size_t>(at) * n + c0 + c] =
+                            *reinterpret_cast<const uint16_t *>(mine + r * Pitch + c * 2);
+                }
             }
         }
     }
+}
+
+template <typename C, typename E>
+__device__ __forceinline__ void store_tile(char *mine, const f32x16 (&acc)[C::MI][C::NI], void *out, int M,
+                                           int n, int m0, int n0, int wave, int lane) {
+    store_tile<C, E>(mine, acc, out, M, n, m0, n0, wave, lane, [](int r) { return static_cast<int64_t>(r); });
 }
 
 // The sums of a K part of a tile as they are (a wave's 1024 floats per 32 x 32

@@ -1,0 +1,58 @@
+// Rows in groups on the device (include/dbf.h, "Rows in groups").
+#ifndef DBF_ROWS_DEVICE_H_
+#define DBF_ROWS_DEVICE_H_
+
+#include <hip/hip_runtime.h>
+
+#include "dbf_internal.h"
+
+namespace dbf {
+
+// Places [lo, hi) of group e (e = count: of no group), whatever stands in offsets.
+__device__ __forceinline__ void group_places(const int32_t *offsets, int count, int slots, int e, int &lo, int &hi) {
+    lo = min(max(offsets[e], 0), slots);
+    hi = e < count ? min(max(offsets[e + 1], lo), slots) : slots;
+}
+
+// Sum of v over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(v, o);
+        if (lane >= o) v += up;
+    }
+    return v;
+}
+
+// Row tile `index` of the groups' tiles of `tile` places, group after group,
+// those of no group (group = count) last: false past the last.  A wave finds
+// it by itself, 64 groups at a time: two loads and a scan instead of a launch
+// that writes a table.
+__device__ __forceinline__ bool find_row_tile(const int32_t *offsets, int count, int slots, int tile, int index,
+                                              RowTile &out) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int e0 = 0; e0 <= count; e0 += 64) {
+        int lo = 0, hi = 0;
+        if (e0 + lane <= count) group_places(offsets, count, slots, e0 + lane, lo, hi);
+        const int tiles = (hi - lo + tile - 1) / tile;
+        const int upto = before + wave_scan(tiles, lane);
+        const uint64_t past = __ballot(upto > index);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            const int first = __builtin_amdgcn_readlane(lo, at) +
+                              (index - __builtin_amdgcn_readlane(upto - tiles, at)) * tile;
+            out.group = e0 + at;
+            out.first = first;
+            out.rows = min(tile, __builtin_amdgcn_readlane(hi, at) - first);
+            out.zero = 0;
+            return true;
+        }
+        before = __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+
+}  // namespace dbf
+
+#endif  // DBF_ROWS_DEVICE_H_

@@ -66,6 +66,10 @@ struct dbf_layer {
     int32_t mx_act = DBF_TYPE_E4M3;
     uint8_t *mx_codes = nullptr, *mx_scales = nullptr, *mx_colmax = nullptr;
     uint8_t *mx_xcodes = nullptr, *mx_xscales = nullptr;
+    // experts (dbf_experts_pack; mx is set too): that many such weights of n x m
+    // one after the other, and the row tiles of a call's product
+    int32_t experts = 0;
+    dbf::RowTile *row_tiles = nullptr;
     size_t packed_bytes = 0, scale_bytes = 0, workspace_bytes = 0;
     // backward (dbf_pack_ex with DBF_PACK_BACKWARD): the transposed layer
     // Wᵀ = diag(b) Bᵀ diag(mid) Aᵀ diag(a), and fp32 intermediates of the
@@ -136,6 +140,7 @@ void release(dbf_layer *h) {
     (void)hipFree(h->mx_colmax);
     (void)hipFree(h->mx_xcodes);
     (void)hipFree(h->mx_xscales);
+    (void)hipFree(h->row_tiles);
     release(h->bwd);
     for (auto &p : h->pending) {
         (void)hipEventDestroy(p.start);
@@ -1040,7 +1045,7 @@ extern "C" dbf_status_t dbf_mx_forward_group(const dbf_handle_t *hs, int32_t cou
     if (!hs || !ys || count < 1 || count > dbf::kMaxGroup || batch < 0) return DBF_ERR_INVALID_ARG;
     for (int i = 0; i < count; ++i) {
         if (!hs[i]) return DBF_ERR_INVALID_ARG;
-        if (!hs[i]->mx) return DBF_ERR_UNSUPPORTED;
+        if (!hs[i]->mx || hs[i]->experts > 0) return DBF_ERR_UNSUPPORTED;
         if (hs[i]->m != hs[0]->m || hs[i]->device != hs[0]->device || batch > hs[i]->max_batch)
             return DBF_ERR_INVALID_ARG;
     }
@@ -1070,7 +1075,7 @@ extern "C" dbf_status_t dbf_mx_forward(dbf_handle_t h, const void *x, int32_t x_
 extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, void *dx, int32_t type, int32_t batch,
                                              hipStream_t stream) {
     if (!h) return DBF_ERR_INVALID_ARG;
-    if (!h->mx) return DBF_ERR_UNSUPPORTED;
+    if (!h->mx || h->experts > 0) return DBF_ERR_UNSUPPORTED;
     if (batch < 0 || batch > h->max_batch) return DBF_ERR_INVALID_ARG;
     if (type != DBF_TYPE_F16 && type != DBF_TYPE_BF16) return DBF_ERR_INVALID_ARG;
     if (batch == 0) return DBF_OK;
@@ -1089,6 +1094,190 @@ extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, voi
     b.part_cap = h->split_cap;
     b.plan = dbf::mx_backward_plan(batch, h->n, h->m);
     dbf_status_t st = timed_launch(h, "mx_backward", stream, [&] { return dbf::launch_mx_backward(b, stream); });
+    if (st == DBF_OK && b.plan.nsplit > 1)
+        st = timed_launch(h, "mx_backward_join", stream, [&] { return dbf::launch_mx_backward_join(b, stream); });
+    return st;
+}
+
+// ---------------------------------------------------------------------------
+// Experts: 4-bit block weights of one size, each for the rows of one group.
+
+// Floats of K-part sums of any call of up to max_rows places.
+static size_t experts_part_floats(int32_t count, int32_t n, int32_t m, int32_t max_rows) {
+    const int32_t blocks = round_up(m, 128) / 32;
+    size_t most = 0;
+    for (int64_t slots = 1; slots <= max_rows && slots <= 65536; slots += slots < 256 ? 1 : 32) {
+        const int32_t s = static_cast<int32_t>(slots);
+        most = std::max(most, dbf::mx_grouped_backward_parts(s, count, n, m));
+        for (int32_t t : {DBF_TYPE_E4M3, DBF_TYPE_E2M1})
+            most = std::max(most, dbf::mx_grouped_parts(s, count, n, blocks, t));
+    }
+    return most;
+}
+
+extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, const void *codes, const uint8_t *scales,
+                                         int32_t act_type, int32_t max_rows, hipStream_t stream, dbf_handle_t *out) {
+    if (out) *out = nullptr;
+    if (!out || !codes || !scales || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u))
+        return DBF_ERR_INVALID_ARG;
+    if (count < 1 || n < 1 || m < 1 || max_rows < 1) return DBF_ERR_INVALID_ARG;
+    if (act_type != DBF_TYPE_E4M3 && act_type != DBF_TYPE_E2M1) return DBF_ERR_INVALID_ARG;
+    const int64_t lim = int64_t(1) << 30;
+    if (count > 1024 || n > lim || m > lim || max_rows > (1 << 24)) return DBF_ERR_SHAPE;
+    const int32_t n_pad = round_up(n, 32), m_pad = round_up(m, 128);
+    if (int64_t(n_pad) * m_pad > (int64_t(1) << 36) || int64_t(max_rows) * m_pad > (int64_t(1) << 31) ||
+        int64_t(max_rows) * n > (int64_t(1) << 31))
+        return DBF_ERR_SHAPE;
+    g_alloc_calls = 0;
+    dbf_layer *h = new (std::nothrow) dbf_layer();
+    if (!h) return DBF_ERR_OOM;
+    h->mx = true;
+    h->experts = count;
+    h->mx_act = act_type;
+    h->n = n;
+    h->m = m;
+    h->n_pad = n_pad;
+    h->m_pad = m_pad;
+    h->max_batch = max_rows;
+    const size_t blocks = static_cast<size_t>(m_pad) / 32, each = static_cast<size_t>(n_pad) * blocks;
+    const size_t max_bytes = blocks + 16;  // (blocks: a multiple of 4)
+    const size_t xc_bytes = static_cast<size_t>(max_rows) * dbf_mx_code_bytes(m, act_type);
+    const size_t xs_bytes = static_cast<size_t>(max_rows) * blocks;
+    const size_t tile_bytes = (dbf::row_tiles_bound(max_rows, count, 32) + 1) * sizeof(dbf::RowTile);
+    const size_t parts = experts_part_floats(count, n, m, max_rows);
+    dbf_status_t st = hipGetDevice(&h->device) == hipSuccess ? DBF_OK : DBF_ERR_HIP;
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_codes), count * each * 16);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_scales), count * each);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_colmax), count * max_bytes);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xcodes), xc_bytes);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xscales), xs_bytes);
+    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->row_tiles), tile_bytes);
+    if (st == DBF_OK && parts > 0) st = dev_alloc(reinterpret_cast<void **>(&h->split), sizeof(float) * parts);
+    if (st == DBF_OK) h->split_cap = parts;
+    const size_t row_bytes = dbf_mx_code_bytes(m, DBF_TYPE_E2M1);
+    for (int32_t e = 0; e < count && st == DBF_OK; ++e) {
+        const size_t row = static_cast<size_t>(e) * n;
+        if (dbf::launch_mx_layout(static_cast<const uint8_t *>(codes) + row * row_bytes, scales + row * blocks, n, m,
+                                  h->mx_codes + e * each * 16, h->mx_scales + e * each, h->mx_colmax + e * max_bytes,
+                                  stream) != 0)
+            st = DBF_ERR_HIP;
+    }
+    // the weights are in place when the call returns, for any stream
+    if (st == DBF_OK && hipStreamSynchronize(stream) != hipSuccess) st = DBF_ERR_HIP;
+    if (st != DBF_OK) {
+        release(h);
+        return st;
+    }
+    h->packed_bytes = count * each * 16;
+    h->scale_bytes = count * (each + max_bytes);
+    h->workspace_bytes = xc_bytes + xs_bytes + tile_bytes + sizeof(float) * parts;
+    *out = h;
+    return DBF_OK;
+}
+
+// Checks of a call's places, and the rows of its product.
+static dbf_status_t experts_rows(const dbf_layer *h, const int32_t *order, const int32_t *offsets, int32_t slots,
+                                 int32_t gather, int32_t scatter, dbf::MxRows *rows) {
+    if (slots < 0 || slots > h->max_batch || gather < 0 || (scatter != 0 && scatter != 1)) return DBF_ERR_INVALID_ARG;
+    if (gather > 0 && slots % gather != 0) return DBF_ERR_INVALID_ARG;
+    if (slots == 0) return DBF_OK;
+    if (!offsets || (reinterpret_cast<uintptr_t>(offsets) & 3u)) return DBF_ERR_INVALID_ARG;
+    if ((gather > 0 || scatter) && (!order || (reinterpret_cast<uintptr_t>(order) & 3u))) return DBF_ERR_INVALID_ARG;
+    const size_t blocks = static_cast<size_t>(h->m_pad) / 32, each = static_cast<size_t>(h->n_pad) * blocks;
+    rows->order = order;
+    rows->table = h->row_tiles;
+    rows->count = h->experts;
+    rows->slots = slots;
+    rows->per = gather;
+    rows->in_rows = gather > 0 ? slots / gather : slots;
+    rows->scatter = scatter;
+    rows->code_stride = each * 16;
+    rows->scale_stride = each;
+    rows->colmax_stride = blocks + 16;
+    return DBF_OK;
+}
+
+extern "C" dbf_status_t dbf_experts_forward(dbf_handle_t h, const void *x, int32_t x_type, const uint8_t *x_scales,
+                                            const int32_t *order, const int32_t *offsets, int32_t slots, int32_t gather,
+                                            int32_t scatter, void *y, int32_t y_type, hipStream_t stream) {
+    if (!h) return DBF_ERR_INVALID_ARG;
+    if (h->experts < 1) return DBF_ERR_UNSUPPORTED;
+    const bool real = x_type == DBF_TYPE_F16 || x_type == DBF_TYPE_BF16;
+    if (!real && x_type != DBF_TYPE_E4M3 && x_type != DBF_TYPE_E2M1) return DBF_ERR_INVALID_ARG;
+    if (y_type != DBF_TYPE_F16 && y_type != DBF_TYPE_BF16) return DBF_ERR_INVALID_ARG;
+    dbf::MxRows rows;
+    dbf_status_t st = experts_rows(h, order, offsets, slots, gather, scatter, &rows);
+    if (st != DBF_OK || slots == 0) return st;
+    if (!x || !aligned16(x) || !y || !aligned16(y)) return DBF_ERR_INVALID_ARG;
+    if (real ? x_scales != nullptr : (!x_scales || (reinterpret_cast<uintptr_t>(x_scales) & 3u)))
+        return DBF_ERR_INVALID_ARG;
+    int cur = -1;
+    if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
+    if (cur != h->device) return DBF_ERR_INVALID_ARG;
+    const int act = real ? h->mx_act : x_type;
+    if (real) {
+        st = timed_launch(h, "mx_quantize", stream, [&] {
+            return dbf::launch_mx_quantize(x, x_type, rows.in_rows, h->m, act, h->mx_xcodes, h->mx_xscales, false, stream);
+        });
+        x = h->mx_xcodes;
+        x_scales = h->mx_xscales;
+    }
+    dbf::MxProduct p;
+    p.xcodes = x;
+    p.xscales = x_scales;
+    p.x_type = act;
+    p.M = slots;
+    p.w = mx_weight(h);
+    p.y = y;
+    p.y_type = y_type;
+    p.part = h->split;
+    p.part_cap = h->split_cap;
+    p.plan = dbf::mx_grouped_plan(slots, h->experts, h->n, p.w.blocks, act);
+    p.rows = &rows;
+    int32_t bm = 0, bn = 0;
+    dbf::mx_product_tile(p.plan, &bm, &bn);
+    if (st == DBF_OK)
+        st = timed_launch(h, "row_tiles", stream, [&] {
+            return dbf::launch_row_tiles(offsets, h->experts, slots, bm, h->row_tiles,
+                                         dbf::row_tiles_bound(slots, h->experts, bm), stream);
+        });
+    if (st == DBF_OK) st = timed_launch(h, "mx_product", stream, [&] { return dbf::launch_mx_product(p, stream); });
+    if (st == DBF_OK && p.plan.nsplit > 1)
+        st = timed_launch(h, "mx_product_join", stream, [&] { return dbf::launch_mx_product_join(p, stream); });
+    return st;
+}
+
+extern "C" dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy, int32_t type, const int32_t *order,
+                                                  const int32_t *offsets, int32_t slots, int32_t gather,
+                                                  int32_t scatter, void *dx, hipStream_t stream) {
+    if (!h) return DBF_ERR_INVALID_ARG;
+    if (h->experts < 1) return DBF_ERR_UNSUPPORTED;
+    if (type != DBF_TYPE_F16 && type != DBF_TYPE_BF16) return DBF_ERR_INVALID_ARG;
+    dbf::MxRows rows;
+    dbf_status_t st = experts_rows(h, order, offsets, slots, gather, scatter, &rows);
+    if (st != DBF_OK || slots == 0) return st;
+    if (!dy || !aligned16(dy) || !dx || !aligned16(dx)) return DBF_ERR_INVALID_ARG;
+    int cur = -1;
+    if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
+    if (cur != h->device) return DBF_ERR_INVALID_ARG;
+    dbf::MxBackward b;
+    b.dy = dy;
+    b.zeros = h->mx_colmax + h->m_pad / 32;
+    b.type = type;
+    b.M = slots;
+    b.w = mx_weight(h);
+    b.dx = dx;
+    b.part = h->split;
+    b.part_cap = h->split_cap;
+    b.plan = dbf::mx_grouped_backward_plan(slots, h->experts, h->n, h->m);
+    b.rows = &rows;
+    int32_t bm = 0, bn = 0;
+    dbf::mx_backward_tile(b.plan, &bm, &bn);
+    st = timed_launch(h, "row_tiles", stream, [&] {
+        return dbf::launch_row_tiles(offsets, h->experts, slots, bm, h->row_tiles,
+                                     dbf::row_tiles_bound(slots, h->experts, bm), stream);
+    });
+    if (st == DBF_OK) st = timed_launch(h, "mx_backward", stream, [&] { return dbf::launch_mx_backward(b, stream); });
     if (st == DBF_OK && b.plan.nsplit > 1)
         st = timed_launch(h, "mx_backward_join", stream, [&] { return dbf::launch_mx_backward_join(b, stream); });
     return st;
@@ -1119,6 +1308,7 @@ extern "C" dbf_status_t dbf_mx_backward_plan(int32_t batch, int32_t n, int32_t m
 extern "C" dbf_status_t dbf_linear_forward_ex(dbf_handle_t h, const void *x, void *y, int32_t batch, int32_t path,
                                               hipStream_t stream) {
     if (!h) return DBF_ERR_INVALID_ARG;
+    if (h->experts > 0) return DBF_ERR_UNSUPPORTED;
     if (batch < 0 || batch > h->max_batch) return DBF_ERR_INVALID_ARG;
     if (path != DBF_PATH_AUTO && path != DBF_PATH_DECODE && path != DBF_PATH_PREFILL &&
         path != DBF_PATH_DECODE_TABLE && path != DBF_PATH_DECODE_EXACT)
@@ -1160,7 +1350,7 @@ extern "C" dbf_status_t dbf_linear_forward_group(const dbf_handle_t *hs, int32_t
         if (!hs[i]) return DBF_ERR_INVALID_ARG;
         if (hs[i]->m != hs[0]->m || hs[i]->device != hs[0]->device || batch > hs[i]->max_batch)
             return DBF_ERR_INVALID_ARG;
-        if (hs[i]->binary) return DBF_ERR_UNSUPPORTED;
+        if (hs[i]->binary || hs[i]->experts > 0) return DBF_ERR_UNSUPPORTED;
     }
     if (batch == 0) return DBF_OK;
     if (!x || !aligned16(x)) return DBF_ERR_INVALID_ARG;
@@ -1471,6 +1661,7 @@ ScratchPlan plan_scratch(const dbf_layer *h, int32_t batch) {
 extern "C" dbf_status_t dbf_linear_forward_noalloc(dbf_handle_t h, const void *x, void *y, int32_t batch,
                                                    hipStream_t stream) {
     if (!h) return DBF_ERR_INVALID_ARG;
+    if (h->experts > 0) return DBF_ERR_UNSUPPORTED;
     if (batch < 0 || batch > h->max_batch) return DBF_ERR_INVALID_ARG;
     if (batch == 0) return DBF_OK;
     if (!x || !y || !aligned16(x) || !aligned16(y)) return DBF_ERR_INVALID_ARG;

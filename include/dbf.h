@@ -526,6 +526,113 @@ dbf_status_t dbf_rms_norm_backward(const void *dy, const void *h, const void *we
                                    void *dx, float *dweight, void *workspace, size_t workspace_bytes,
                                    hipStream_t stream);
 
+/*
+ * Rows in groups
+ * --------------
+ * Rows that an index assigns to groups (the slots of tokens routed to
+ * experts, the rows of requests with adapters of their own) stand in the
+ * grouped order: those of group 0 first, in rising order, then those of group
+ * 1 and so on, those of no group last.  `order` (int32) holds the row at each
+ * place of it, `offsets` (int32, count + 1) the first place of each group and,
+ * last, of the rows of no group.  The calls below take them from
+ * dbf_group_rows, once for all the layers that the rows pass.  (Orders and
+ * offsets of other origin: values out of range are clamped or their rows left
+ * out, so that nothing outside the buffers is touched.)
+ *
+ * dbf_group_rows -- the grouped order of an index.
+ *   index       device, `rows` whole numbers of index_bits (32 or 64) bits, signed;
+ *               those outside [0, count) are of no group.
+ *   order       out, rows.   offsets  out, count + 1.
+ *   workspace   dbf_group_rows_workspace(rows, count) bytes (0 up to 16384 rows;
+ *               NULL then), 4-byte aligned.
+ * Stable, without atomics.  rows = 0 writes offsets only.  1 <= count <= 1024,
+ * rows <= 2^24 (DBF_ERR_SHAPE above; the workspace of such sizes is 0).
+ */
+size_t dbf_group_rows_workspace(int32_t rows, int32_t count);
+dbf_status_t dbf_group_rows(const void *index, int32_t index_bits, int32_t rows, int32_t count, int32_t *order,
+                            int32_t *offsets, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * dbf_experts_pack -- `count` weights of n x m in e2m1 blocks (codes and scales
+ * of count * n rows, one weight after the other), each for the rows of one
+ * group.  Arguments as dbf_mx_pack; scales 4-byte aligned; max_rows: the most
+ * places (slots) of a call.  The handle takes dbf_experts_forward,
+ * dbf_experts_backward_data, dbf_get_info (n, m of one weight), timing and
+ * dbf_free; the other entry points return DBF_ERR_UNSUPPORTED.
+ * count <= 1024, max_rows <= 2^24 (DBF_ERR_SHAPE above).
+ *
+ * dbf_experts_forward -- for each place s < slots, of group e,
+ *   y[out(s)][o] = rne( Σ_l xq[in(s)][l] W_e[o][l] ).
+ *   gather   0: in(s) = s, x has a row for every place.  k >= 1:
+ *            in(s) = order[s] / k, x has slots / k rows in the index's order,
+ *            each shared by k consecutive entries (a token and its k experts);
+ *            k divides slots.
+ *   scatter  0: out(s) = s.  1: out(s) = order[s], results in the index's order.
+ *   x, x_type, x_scales, y, y_type  as dbf_mx_forward; y has `slots` rows, all
+ *            written: those of rows of no group with zeros.
+ *   order    may be NULL where gather and scatter are 0.
+ * Rows are quantised once, however many experts they go to.  A row's result
+ * has the numerics of dbf_mx_forward; how its sum is cut into parts depends on
+ * slots, count, n and m, not on how the rows are spread over the groups.  y
+ * overlaps nothing.  Calls on one handle must be ordered.
+ *
+ * dbf_experts_backward_data -- dx[out(s)][l] = rne( Σ_o dy[in(s)][o] W_e[o][l] ),
+ * the gradient of each place's input, as dbf_mx_backward_data computes it;
+ * gather, scatter and the rest as above.
+ */
+dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, const void *codes, const uint8_t *scales,
+                              int32_t act_type, int32_t max_rows, hipStream_t stream, dbf_handle_t *out);
+dbf_status_t dbf_experts_forward(dbf_handle_t h, const void *x, int32_t x_type, const uint8_t *x_scales,
+                                 const int32_t *order, const int32_t *offsets, int32_t slots, int32_t gather,
+                                 int32_t scatter, void *y, int32_t y_type, hipStream_t stream);
+dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy, int32_t type, const int32_t *order,
+                                       const int32_t *offsets, int32_t slots, int32_t gather, int32_t scatter,
+                                       void *dx, hipStream_t stream);
+
+/*
+ * dbf_adapter_forward -- low-rank adapters beside a layer: for row r of group a,
+ *   t[r] = A_a x[r]  (fp32),   y[r] = rne( base[r] + scale_a B_a t[r] ),
+ * for rows of no group t[r] = 0 and y[r] = base[r].
+ *   x       rows x m, base and y rows x n (base: the layer's result), of `type`
+ *           (f16 or bf16).  y may be base itself.
+ *   A, B    count x rank x m and count x n x rank, of `type`.
+ *   scale   count values, fp32, or NULL (1).
+ *   order, offsets  the grouped order of the rows (dbf_group_rows).
+ *   t       out, rows x rank fp32 (the backward pass takes it), or NULL.
+ *   workspace  dbf_adapter_workspace(rows, n, m, rank, count) bytes, 16-byte
+ *           aligned.
+ * Sums are fp32; t enters the second product in two 16-bit parts (f16: 22 bits
+ * of the row's largest, bf16: 16 bits of each), a rounding of 2^-17 of t at most where
+ * y's own is 2^-9 (2^-22 and 2^-12).  Sums are in a fixed order (no atomics).
+ * 1 <= rank <= 128, count <= 1024, n, m <= 2^20, rows <= 2^24, rows * max(n, m) <= 2^40,
+ * count * rank * max(n, m) <= 2^32 (DBF_ERR_SHAPE above).
+ * Pointers 16-byte aligned (order, offsets, scale: 4).  rows = 0 returns
+ * DBF_OK without launching.  The current HIP device must hold the buffers.
+ *
+ * dbf_adapter_backward -- for an upstream gradient dy (rows x n), with
+ * u[r] = scale_a B_aᵀ dy[r] (fp32) for row r of group a,
+ *   dx_out[r] = rne( dx[r] + A_aᵀ u[r] )   (dx: the layer's own input gradient, or
+ *               NULL: 0; rows of no group: dx[r]),
+ *   dA_a = Σ_r u[r] x[r]ᵀ,  dB_a = scale_a Σ_r dy[r] t[r]ᵀ   over the rows of group a
+ *               (fp32, of A's and B's shapes; zeros for a group without rows).
+ * dx_out, dA or dB may be NULL (not computed); dx_out may be dx itself.  t as the
+ * forward gave it (needed for dB), x needed for dA.  u and t enter the
+ * gradients' products in three bf16 parts (24 bits), or in two f16 parts
+ * (22 bits of the group's largest).  Sums are in a fixed order.  rows = 0 writes
+ * zeros to dA and dB.  Other rules as above.
+ */
+size_t dbf_adapter_workspace(int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count);
+dbf_status_t dbf_adapter_forward(const void *x, const void *base, const void *A, const void *B, const float *scale,
+                                 int32_t type, const int32_t *order, const int32_t *offsets, int32_t rows, int32_t n,
+                                 int32_t m, int32_t rank, int32_t count, void *y, float *t, void *workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+size_t dbf_adapter_backward_workspace(int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count);
+dbf_status_t dbf_adapter_backward(const void *dy, const void *x, const float *t, const void *dx, const void *A,
+                                  const void *B, const float *scale, int32_t type, const int32_t *order,
+                                  const int32_t *offsets, int32_t rows, int32_t n, int32_t m, int32_t rank,
+                                  int32_t count, void *dx_out, float *dA, float *dB, void *workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
 /* dbf_free -- release the handle and its device memory.  NULL is a no-op.
  * Synchronises the handle's device first, so pending work on it finishes. */
 void dbf_free(dbf_handle_t h);
