@@ -46,22 +46,27 @@ __device__ __forceinline__ f32x4 mma(u32v4 a, u32v4 b, f32x4 acc) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
 }
 
+// 16-byte and shorter accesses at any element (the memory takes them unaligned).
+typedef u32v4 u32v4_any __attribute__((aligned(2)));
+typedef u32v2 u32v2_any __attribute__((aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(2)));
+
 // N consecutive 16-bit elements from p into words, the first `valid` of them
-// (VEC: all or none, p aligned to them), zeros for the rest.
+// (VEC: all or none), zeros for the rest.
 template <int N, bool VEC>
 __device__ __forceinline__ void load_n(const uint16_t *p, int valid, uint32_t (&w)[(N + 1) / 2]) {
 #pragma unroll
     for (int i = 0; i < (N + 1) / 2; ++i) w[i] = 0;
-    if constexpr (VEC) {
-        if (valid <= 0) return;
+    if (valid <= 0) return;
+    if (VEC || valid >= N) {
         if constexpr (N == 1) w[0] = *p;
-        else if constexpr (N == 2) w[0] = *reinterpret_cast<const uint32_t *>(p);
+        else if constexpr (N == 2) w[0] = *reinterpret_cast<const u32_any *>(p);
         else if constexpr (N == 4) {
-            const u32v2 v = *reinterpret_cast<const u32v2 *>(p);
+            const u32v2 v = *reinterpret_cast<const u32v2_any *>(p);
             w[0] = v[0];
             w[1] = v[1];
         } else {
-            const u32v4 v = *reinterpret_cast<const u32v4 *>(p);
+            const u32v4 v = *reinterpret_cast<const u32v4_any *>(p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = v[i];
         }
@@ -155,29 +160,39 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(const ShrinkArgs a) {
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = k0; s < k1; ++s) {
-        const int k = 32 * s, left = a.K - k - 8 * g;
-        u32v4 xf[MT], wf[RT];
+    // U steps' operands are on their way at a time
+    constexpr int U = MT + RT <= 3 ? 4 : MT + RT <= 6 ? 2 : 1;
+    for (int s0 = k0; s0 < k1; s0 += U) {
+        u32v4 xf[U][MT], wf[U][RT];
+        uint32_t q[U][8][(RT + 1) / 2];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) xf[i] = load_row8<VEC>(xr[i] + k, left);
-        if constexpr (LEAD) {
-            uint32_t q[8][(RT + 1) / 2];
+        for (int u = 0; u < U; ++u) {
+            const int k = 32 * (s0 + u), left = s0 + u < k1 ? a.K - k - 8 * g : 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                load_n<RT, VEC>(w + static_cast<size_t>(k + 8 * g + j) * a.rank + c * RT, j < left ? a.rank - c * RT : 0, q[j]);
+            for (int i = 0; i < MT; ++i) xf[u][i] = load_row8<VEC>(xr[i] + k, left);
+            if constexpr (LEAD) {
 #pragma unroll
-            for (int i = 0; i < RT; ++i) wf[i] = pick_column<RT>(q, i);
-        } else {
+                for (int j = 0; j < 8; ++j)
+                    load_n<RT, VEC>(w + static_cast<size_t>(k + 8 * g + j) * a.rank + c * RT, j < left ? a.rank - c * RT : 0, q[u][j]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const int j = c * RT + i;
-                wf[i] = load_row8<VEC>(w + static_cast<size_t>(j) * a.K + k + 8 * g, j < a.rank ? left : 0);
+                for (int i = 0; i < RT; ++i) {
+                    const int j = c * RT + i;
+                    wf[u][i] = load_row8<VEC>(w + static_cast<size_t>(j) * a.K + k + 8 * g, j < a.rank ? left : 0);
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int u = 0; u < U; ++u) {
+            if constexpr (LEAD) {
 #pragma unroll
-            for (int j = 0; j < RT; ++j) acc[i][j] = mma<E>(wf[j], xf[i], acc[i][j]);
+                for (int i = 0; i < RT; ++i) wf[u][i] = pick_column<RT>(q[u], i);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < RT; ++j) acc[i][j] = mma<E>(wf[u][j], xf[u][i], acc[i][j]);
+        }
     }
     // lane (c, g): ranks (4 g + v) RT + i of row c
 #pragma unroll
@@ -212,11 +227,14 @@ struct ExpandArgs {
     int per;                    // 64-column chunks of a wave
 };
 
-template <typename E, bool LEAD, int MT, int RT, bool VEC, bool VOUT>
+template <typename E, bool LEAD, int MT, int RT, bool VEC>
 __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
-    constexpr int RP = 16 * RT, Rows = 16 * MT;
+    constexpr int RP = 16 * RT, Rows = 16 * MT, Units = RP / 8;
     constexpr int WF = RP < 32 ? 1 : RP / 32;  // 32-rank pieces
     constexpr int KS = RT;                     // instructions of two parts: 2 RP / 32
+    constexpr int Pitch = RP + 8;
+    __shared__ __attribute__((aligned(16))) uint16_t parts[2][Rows][Pitch];
+    __shared__ int shifts[Rows];
     RowTile rt;
     const int blocks = (a.cols + 64 * kWaves * a.per - 1) / (64 * kWaves * a.per);
     const int tile = blockIdx.x / blocks, block = blockIdx.x % blocks;
@@ -224,144 +242,156 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool none = rt.group >= a.count;
-    const float scale = none || !a.scale ? 1.0f : a.scale[rt.group];
     const int j0 = RP < 32 ? 8 * (g & 1) : 8 * g;  // this lane's ranks of a piece
 
     int64_t row[MT];
-    u32v4 tf[MT][KS];
-    int shift[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int at = rt.first + min(16 * i + c, rt.rows - 1);
-        const int r = a.order[at];
+        const int r = a.order[rt.first + min(16 * i + c, rt.rows - 1)];
         row[i] = 16 * i + c < rt.rows && r >= 0 && r < a.rows ? r : -1;
-        float v[WF][8];
-#pragma unroll
-        for (int f = 0; f < WF; ++f)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[f][j] = 0.0f;
-        if (!none) {
-            for (int p = 0; p < a.parts; ++p) {
-                const float *src = a.in + (static_cast<size_t>(p) * a.rows + at) * RP + j0;
-#pragma unroll
-                for (int f = 0; f < WF; ++f)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const f32x4 q = *reinterpret_cast<const f32x4 *>(src + 32 * f + 4 * h);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[f][4 * h + j] += q[j];
-                    }
-            }
-        }
-        if (a.low && block == 0 && wave == 0 && row[i] >= 0 && (RP >= 32 || g < 2)) {
-            const float by = a.low_scaled ? scale : 1.0f;
-#pragma unroll
-            for (int f = 0; f < WF; ++f)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (32 * f + j0 + j < a.rank) a.low[row[i] * a.rank + 32 * f + j0 + j] = v[f][j] * by;
-        }
-        shift[i] = 0;
-        float top = 0.0f;
-#pragma unroll
-        for (int f = 0; f < WF; ++f)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[f][j] *= scale;
-                top = fmaxf(top, finite_abs(v[f][j]));
-            }
-        if constexpr (E::code == DBF_TYPE_F16) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            shift[i] = f16_shift(top);
-#pragma unroll
-            for (int f = 0; f < WF; ++f)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[f][j] = ldexpf(v[f][j], shift[i]);
-        }
-        if constexpr (RP < 32) {
-            const u32v4 hi = pack_part<E>(v[0], 0), lo = pack_part<E>(v[0], 1);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tf[i][0][k] = g < 2 ? hi[k] : lo[k];
-        } else {
-#pragma unroll
-            for (int f = 0; f < WF; ++f) {
-                tf[i][f] = pack_part<E>(v[f], 0);
-                tf[i][WF + f] = pack_part<E>(v[f], 1);
-            }
-        }
     }
-    if (!a.out || (none && a.base == a.out)) return;
+    // Columns of a wave's chunk: operand 2 h + e of lane c has column 32 h + 2 c + e,
+    // so that lane (c, g) gets columns 32 h + 8 g .. + 7 of row c: 16 bytes, and
+    // 64 of a row in the lanes of one store.
     const uint16_t *w = a.w + static_cast<size_t>(none ? 0 : rt.group) * a.rank * a.cols;
-    for (int it = 0; it < a.per; ++it) {
-        const int col0 = ((block * a.per + it) * kWaves + wave) * 64;
-        if (col0 >= a.cols) break;
-        // operand i of lane c: column col0 + 4 c + i
-        u32v4 wf[WF][4];
-        if (!none) {
+    u32v4 wf[WF][4], base[MT][2];
+    auto load_chunk = [&](int col0) {
 #pragma unroll
-            for (int f = 0; f < WF; ++f) {
-                if constexpr (LEAD) {
-                    uint32_t q[8][2];
-                    const int col = col0 + 4 * c;
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = col0 + 32 * h + 8 * g;
+                base[m][h] = u32v4{0u, 0u, 0u, 0u};
+                if (a.base && row[m] >= 0)
+                    base[m][h] = load_row8<VEC>(a.base + static_cast<size_t>(row[m]) * a.cols + col, a.cols - col);
+            }
+        if (none) return;
+#pragma unroll
+        for (int f = 0; f < WF; ++f) {
+            if constexpr (LEAD) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t q[8][1];
+                    const int col = col0 + 32 * h + 2 * c;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int rk = 32 * f + j0 + j;
-                        load_n<4, VEC>(w + static_cast<size_t>(rk) * a.cols + col, rk < a.rank ? a.cols - col : 0, q[j]);
+                        load_n<2, VEC>(w + static_cast<size_t>(rk) * a.cols + col, rk < a.rank ? a.cols - col : 0, q[j]);
                     }
+                    wf[f][2 * h] = pick_column<2>(q, 0);
+                    wf[f][2 * h + 1] = pick_column<2>(q, 1);
+                }
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) wf[f][i] = pick_column<4>(q, i);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int col = col0 + 4 * c + i, rk = 32 * f + j0;
-                        wf[f][i] = load_row8<VEC>(w + static_cast<size_t>(col) * a.rank + rk, col < a.cols ? a.rank - rk : 0);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int col = col0 + 32 * (i >> 1) + 2 * c + (i & 1), rk = 32 * f + j0;
+                    wf[f][i] = load_row8<VEC>(w + static_cast<size_t>(col) * a.rank + rk, col < a.cols ? a.rank - rk : 0);
                 }
             }
         }
+    };
+    auto column = [&](int it) { return ((block * a.per + it) * kWaves + wave) * 64; };
+    const bool skip = !a.out || (none && a.base == a.out);
+    if (!skip && column(0) < a.cols) load_chunk(column(0));  // (on its way while t is added up)
+
+    // The tile's rows of t, once per workgroup: the parts added in order, and
+    // the two 16-bit parts of scale * t into LDS.
+    if (!none || (a.low && block == 0)) {
+        const float scale = none || !a.scale ? 1.0f : a.scale[rt.group];
+        for (int i = threadIdx.x; i < rt.rows * Units; i += kThreads) {
+            const int r = i / Units, j = i % Units * 8, at = rt.first + r;
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+            if (!none) {
+                const float *src = a.in + static_cast<size_t>(at) * RP + j;
+                const size_t plane = static_cast<size_t>(a.rows) * RP;
+#pragma unroll 4
+                for (int p = 0; p < a.parts; ++p, src += plane) {
+                    const f32x4 lo = reinterpret_cast<const f32x4 *>(src)[0], hi = reinterpret_cast<const f32x4 *>(src)[1];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[k] += lo[k];
+                        v[4 + k] += hi[k];
+                    }
+                }
+            }
+            if (a.low && block == 0) {
+                const int to = a.order[at];
+                const float by = a.low_scaled ? scale : 1.0f;
+                if (to >= 0 && to < a.rows) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (j + k < a.rank) a.low[static_cast<size_t>(to) * a.rank + j + k] = v[k] * by;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= scale;
+            if constexpr (E::code == DBF_TYPE_F16) {
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, finite_abs(v[k]));
+#pragma unroll
+                for (int o = 1; o < Units; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+                const int shift = f16_shift(top);
+                if (j == 0) shifts[r] = shift;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = ldexpf(v[k], shift);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) *reinterpret_cast<u32v4 *>(&parts[p][r][j]) = pack_part<E>(v, p);
+        }
+    }
+    __syncthreads();
+    if (skip) return;
+    for (int it = 0; it < a.per; ++it) {
+        const int col0 = column(it);
+        if (col0 >= a.cols) break;
+        if (it > 0) load_chunk(col0);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             if (16 * m >= rt.rows) break;
-            // lane (c, g): columns col + 4 v + i of row c
-            const int col = col0 + 16 * g, valid = a.cols - col;
-            const size_t at = static_cast<size_t>(row[m] < 0 ? 0 : row[m]) * a.cols + col;
-            u32v4 b[2] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
-            if (a.base && row[m] >= 0) {
-                b[0] = load_row8<VOUT>(a.base + at, valid);
-                b[1] = load_row8<VOUT>(a.base + at + 8, valid - 8);
-            }
             if (!none) {
+                u32v4 tf[KS];
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    tf[s] = RP < 32 ? *reinterpret_cast<const u32v4 *>(&parts[g >> 1][16 * m + c][j0])
+                                    : *reinterpret_cast<const u32v4 *>(&parts[s / WF][16 * m + c][32 * (s % WF) + j0]);
+                const int shift = E::code == DBF_TYPE_F16 ? -shifts[16 * m + c] : 0;
                 f32x4 acc[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) acc[i] = mma<E>(wf[s % WF][i], tf[m][s], acc[i]);
+                    for (int s = 0; s < KS; ++s) acc[i] = mma<E>(wf[s % WF][i], tf[s], acc[i]);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
+                        const uint32_t old = base[m][h][k];
                         uint32_t o = 0;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int i = 8 * h + 2 * k + e;
-                            const float d = ldexpf(acc[i & 3][i >> 2], -shift[m]);
-                            const uint32_t old = b[h][k];
+                            float d = acc[2 * h + e][k];
+                            if constexpr (E::code == DBF_TYPE_F16) d = ldexpf(d, shift);
                             o |= static_cast<uint32_t>(E::put(E::get(static_cast<uint16_t>(old >> (16 * e))) + d)) << (16 * e);
                         }
-                        b[h][k] = o;
+                        base[m][h][k] = o;
                     }
             }
             if (row[m] < 0) continue;
-            if constexpr (VOUT) {
-                if (valid > 0) *reinterpret_cast<u32v4 *>(a.out + at) = b[0];
-                if (valid > 8) *reinterpret_cast<u32v4 *>(a.out + at + 8) = b[1];
-            } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < valid) a.out[at + i] = static_cast<uint16_t>(b[i >> 3][i >> 1 & 3] >> (16 * (i & 1)));
+            for (int h = 0; h < 2; ++h) {
+                const int col = col0 + 32 * h + 8 * g, valid = a.cols - col;
+                uint16_t *dst = a.out + static_cast<size_t>(row[m]) * a.cols + col;
+                if (VEC ? valid > 0 : valid >= 8) {
+                    *reinterpret_cast<u32v4_any *>(dst) = base[m][h];
+                } else if (!VEC) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < valid) dst[i] = static_cast<uint16_t>(base[m][h][i >> 1] >> (16 * (i & 1)));
+                }
             }
         }
     }
@@ -549,7 +579,9 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
 
 // The chunks of each group that has several, added in order; zeros for groups
 // without rows.
-__global__ __launch_bounds__(kThreads) void outer_join_kernel(const OuterArgs a, int blocks0) {
+constexpr int kJoinThreads = 64;
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+__global__ __launch_bounds__(kJoinThreads) void outer_join_kernel(const OuterArgs a, int blocks0) {
     const int group = blockIdx.y;
     const bool second = static_cast<int>(blockIdx.x) >= blocks0;
     const OuterSide &sd = a.side[second ? 1 : 0];
@@ -567,13 +599,22 @@ __global__ __launch_bounds__(kThreads) void outer_join_kernel(const OuterArgs a,
         first += __builtin_amdgcn_readlane(wave_scan(k > 1 ? k : 0, lane), 63);
     }
     const size_t each = static_cast<size_t>(a.rank) * sd.cols;
-    const size_t at = (static_cast<size_t>(block) * kThreads + threadIdx.x) * 4;
-    float *out = sd.out + static_cast<size_t>(group) * each;
-    for (int i = 0; i < 4; ++i) {
-        if (at + i >= each) break;
-        float v = 0.0f;
-        for (int k = 0; k < n && first + k < a.most; ++k) v += sd.part[static_cast<size_t>(first + k) * each + at + i];
-        out[at + i] = v;
+    const size_t at = (static_cast<size_t>(block) * kJoinThreads + threadIdx.x) * 4;
+    if (at >= each) return;
+    float *out = sd.out + static_cast<size_t>(group) * each + at;
+    const float *src = sd.part + static_cast<size_t>(first) * each + at;
+    const int most = min(n, a.most - first);
+    if (at + 4 <= each) {
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int k = 0; k < most; ++k, src += each) v += *reinterpret_cast<const f32x4_any *>(src);
+        *reinterpret_cast<f32x4_any *>(out) = v;
+    } else {
+        for (int i = 0; at + i < each; ++i) {
+            float v = 0.0f;
+            for (int k = 0; k < most; ++k) v += src[k * each + i];
+            out[i] = v;
+        }
     }
 }
 
@@ -582,15 +623,15 @@ __global__ __launch_bounds__(kThreads) void outer_join_kernel(const OuterArgs a,
 
 int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
-// 16-row tiles of a row tile: several where the groups fill them (their rows share the weight's operands).
-int row_frags(int rows, int count, int rt) {
-    const int used = rows < count ? rows : count;
-    return rows / used < 32 ? 1 : rt == 8 ? 2 : 4;
-}
+// 16-row tiles of a row tile: several where the groups fill them (their rows
+// share the weight's operands), as many as registers and LDS allow.
+constexpr int shrink_most(int rt) { return rt == 1 ? 4 : rt <= 4 ? 2 : 1; }
+constexpr int expand_most(int rt) { return rt == 8 ? 2 : 4; }
+bool full_groups(int rows, int count) { return rows / (rows < count ? rows : count) >= 32; }
 
 // K parts of a shrink: about two workgroups per CU, two steps of 32 for a wave at least.
 int shrink_parts(int rows, int count, int K, int rank) {
-    const int64_t tiles = grouped_row_tiles(rows, count, 16 * row_frags(rows, count, rank_tiles(rank)));
+    const int64_t tiles = grouped_row_tiles(rows, count, full_groups(rows, count) ? 16 * shrink_most(rank_tiles(rank)) : 16);
     const int64_t steps = (K + 31) / 32, want = (512 + tiles - 1) / tiles, most = std::max<int64_t>(1, steps / (2 * kWaves));
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, kMaxParts})));
 }
@@ -627,7 +668,7 @@ void by_rank(int rank, F f) {
 template <typename E, bool LEAD>
 void launch_shrink(const ShrinkArgs &a, hipStream_t s) {
     by_rank(a.rank, [&](auto rt) {
-        constexpr int RT = decltype(rt)::value, Big = RT == 8 ? 2 : 4;
+        constexpr int RT = decltype(rt)::value, Big = shrink_most(RT);
         const bool vec = a.K % 8 == 0 && (!LEAD || a.rank % RT == 0);
         auto go = [&](auto mt) {
             constexpr int MT = decltype(mt)::value;
@@ -635,7 +676,7 @@ void launch_shrink(const ShrinkArgs &a, hipStream_t s) {
             if (vec) launch_kernel(shrink_kernel<E, LEAD, MT, RT, true>, grid, dim3(kThreads), 0, s, a);
             else launch_kernel(shrink_kernel<E, LEAD, MT, RT, false>, grid, dim3(kThreads), 0, s, a);
         };
-        if (row_frags(a.rows, a.count, RT) == 1) go(Tag<1>{});
+        if (!full_groups(a.rows, a.count)) go(Tag<1>{});
         else go(Tag<Big>{});
     });
 }
@@ -643,25 +684,19 @@ void launch_shrink(const ShrinkArgs &a, hipStream_t s) {
 template <typename E, bool LEAD>
 void launch_expand(ExpandArgs &a, hipStream_t s) {
     by_rank(a.rank, [&](auto rt) {
-        constexpr int RT = decltype(rt)::value, Big = RT == 8 ? 2 : 4;
-        const bool vec = LEAD ? a.cols % 4 == 0 : a.rank % 8 == 0, vout = a.cols % 8 == 0;
+        constexpr int RT = decltype(rt)::value, Big = expand_most(RT);
+        const bool vec = a.cols % 8 == 0 && (LEAD || a.rank % 8 == 0);
         auto go = [&](auto mt) {
             constexpr int MT = decltype(mt)::value;
             const int64_t tiles = row_tiles_bound(a.rows, a.count, 16 * MT);
-            const int64_t chunks = a.out ? (a.cols + 64 * kWaves - 1) / (64 * kWaves) : 1;
-            a.per = static_cast<int>(std::min<int64_t>(chunks, std::max<int64_t>(1, tiles * chunks / 1024)));
-            if (!a.out) a.per = static_cast<int>((static_cast<int64_t>(a.cols) + 64 * kWaves - 1) / (64 * kWaves));
-            const int64_t blocks = (a.cols + 64 * kWaves * a.per - 1) / (64 * kWaves * a.per);
-            const dim3 grid(static_cast<uint32_t>(tiles * blocks));
-            auto k = [&](auto v, auto o) {
-                launch_kernel(expand_kernel<E, LEAD, MT, RT, decltype(v)::value, decltype(o)::value>, grid, dim3(kThreads),
-                              0, s, a);
-            };
-            if (vec && vout) k(std::true_type{}, std::true_type{});
-            else if (vout) k(std::false_type{}, std::true_type{});
-            else k(std::false_type{}, std::false_type{});
+            const int64_t chunks = (static_cast<int64_t>(a.cols) + 64 * kWaves - 1) / (64 * kWaves);
+            // (results of t alone: one workgroup per row tile)
+            a.per = static_cast<int>(a.out ? std::min<int64_t>(chunks, std::max<int64_t>(1, tiles * chunks / 512)) : chunks);
+            const dim3 grid(static_cast<uint32_t>(tiles * ((chunks + a.per - 1) / a.per)));
+            if (vec) launch_kernel(expand_kernel<E, LEAD, MT, RT, true>, grid, dim3(kThreads), 0, s, a);
+            else launch_kernel(expand_kernel<E, LEAD, MT, RT, false>, grid, dim3(kThreads), 0, s, a);
         };
-        if (row_frags(a.rows, a.count, RT) == 1) go(Tag<1>{});
+        if (!full_groups(a.rows, a.count)) go(Tag<1>{});
         else go(Tag<Big>{});
     });
 }
@@ -686,10 +721,10 @@ void launch_outer(const OuterArgs &a, hipStream_t s) {
 
 void launch_outer_join(const OuterArgs &a, hipStream_t s) {
     auto blocks = [&](const OuterSide &sd) {
-        return sd.strips > 0 ? static_cast<int>((static_cast<int64_t>(a.rank) * sd.cols + 4 * kThreads - 1) / (4 * kThreads)) : 0;
+        return sd.strips > 0 ? static_cast<int>((static_cast<int64_t>(a.rank) * sd.cols + 4 * kJoinThreads - 1) / (4 * kJoinThreads)) : 0;
     };
     const int b0 = blocks(a.side[0]), b1 = blocks(a.side[1]);
-    launch_kernel(outer_join_kernel, dim3(b0 + b1, a.count), dim3(kThreads), 0, s, a, b0);
+    launch_kernel(outer_join_kernel, dim3(b0 + b1, a.count), dim3(kJoinThreads), 0, s, a, b0);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

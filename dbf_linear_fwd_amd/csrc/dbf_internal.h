@@ -311,17 +311,19 @@ struct MxPlan {
 
 // Rows of a product that belong to groups, each with its own weight (include/dbf.h,
 // "Rows in groups"): `slots` places in the grouped order, those from
-// offsets[count] on of no group.  table[0].x is the number of row tiles,
-// table[1 + i] tile i: {group, first place, places, 0}; launch_row_tiles makes
-// it.  The input's row of a place is the place itself (per = 0) or its
-// order / per of in_rows; the result's row the place or (scatter) its order.
-// Values out of range are clamped, or not written.
+// offsets[count] on of no group.  The row tiles of up to kScanGroups groups are
+// found by each workgroup; those of more come in a table that launch_row_tiles
+// makes: table[0].group is their number, table[1 + i] tile i (group, first
+// place, places).  The input's row of a place is the place itself (per = 0) or
+// its order / per of in_rows; the result's row the place or (scatter) its
+// order.  Values out of range are clamped, or not written.
+constexpr int kScanGroups = 64;
 struct RowTile {
     int32_t group, first, rows, zero;
 };
 struct MxRows {
-    const int32_t *order = nullptr;
-    const RowTile *table = nullptr;
+    const int32_t *order = nullptr, *offsets = nullptr;
+    const RowTile *table = nullptr;  // null: up to kScanGroups groups
     int count = 0, slots = 0, per = 0, in_rows = 0, scatter = 0;
     size_t code_stride = 0, scale_stride = 0, colmax_stride = 0;  // from a group's weight to the next
 };

@@ -164,8 +164,10 @@ struct MxGemmArgs {
 template <typename C, typename E, bool G>
 __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    [[maybe_unused]] RowTiles tiles;
     if constexpr (G) {
-        a.grid.nbm = a.rows.table[0].group;
+        tiles = scan_rows<C::BM>(a.rows);
+        a.grid.nbm = tiles.total;
         a.grid.group = min(a.grid.nbm, 4);
     }
     const int T = a.grid.nbm * a.grid.nbn;
@@ -175,7 +177,8 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(MxGemmArgs a) {
     int bm, bn;
     tile_at(a.grid, tile, bm, bn);
     const int m0 = G ? 0 : bm * C::BM, n0 = bn * C::BN;
-    [[maybe_unused]] const RowPlaces place = take_group<G>(a.rows, bm, a.w, a.M);
+    [[maybe_unused]] RowPlaces place;
+    if constexpr (G) place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
     const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
@@ -336,8 +339,10 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(MxGemmArgs a) {
 template <typename C, typename E, bool G>
 __global__ __launch_bounds__(64) void mx_finish_kernel(MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    [[maybe_unused]] RowTiles tiles;
     if constexpr (G) {
-        a.grid.nbm = a.rows.table[0].group;
+        tiles = scan_rows<C::BM>(a.rows);
+        a.grid.nbm = tiles.total;
         a.grid.group = min(a.grid.nbm, 4);
     }
     const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves;
@@ -349,7 +354,7 @@ __global__ __launch_bounds__(64) void mx_finish_kernel(MxGemmArgs a) {
     add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
                  a.grid.nsplit, acc);
     if constexpr (G) {
-        const RowPlaces place = take_group<G>(a.rows, bm, a.w, a.M);
+        const RowPlaces place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
         store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, 0, bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
     } else {
         store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, bm * C::BM, bn * C::BN, wave, lane);
@@ -389,15 +394,13 @@ constexpr int kCus = 256;
 // 14336, K 4096: 256 x 256 tiles 99 to 114 us, 128 x 256 117; 2048 x 4096,
 // K 14336: 134 and 91; 64 x 4096, K 14336, 64 x 64 tiles: four parts 18.7, one
 // 34.7; 17 x 4096, K 14336, four parts: 32 x 64 14.9, 64 x 64 17.1.)
-// row_tiles(rows of a tile): the product's row tiles.
-template <typename F>
-MxPlan mx_plan(F row_tiles, int n, int steps, bool x8) {
+MxPlan mx_plan(int M, int n, int steps, bool x8) {
     MxPlan best;
     float least = 0.0f;
     const int f = x8 ? 0 : 1;
     for (int t = 0; t < kTileCount; ++t) {
         const TileCost &c = kTiles[t];
-        const int64_t tiles = row_tiles(c.bm) * ((n + c.bn - 1) / c.bn);
+        const int64_t tiles = static_cast<int64_t>((M + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn);
         for (int sp : {1, 2, 3, 4, 6, 8}) {
             if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
             const float wgs = static_cast<float>(tiles) * sp;
@@ -407,6 +410,39 @@ MxPlan mx_plan(F row_tiles, int n, int steps, bool x8) {
             const float step = c.light[f] + (c.full[f] - c.light[f]) * load;
             float us = rounds * (3.0f + static_cast<float>((steps + sp - 1) / sp) * step);
             if (sp > 1) us += 2.1f + wgs * c.bm * c.bn * 8.0f * 3.7e-7f;
+            if (least == 0.0f || us < least) {
+                least = us;
+                best.tile = t;
+                best.nsplit = sp;
+            }
+        }
+    }
+    return best;
+}
+
+// The same for rows in groups, e4m3 and e2m1.  Against every tile and 1, 2 and 4
+// parts at 164 sizes (2 to 128 groups of 640 to 14336 by 512 to 14336, 1 to 16384
+// rows, unevenly spread) the choice is 3 % from the best on average; the plan
+// for one weight was 12 %: 4096 rows of 64 groups, 4096 x 1024, 62 instead of 47 us.
+constexpr GroupedCost kGrouped[kTileCount][2] = {
+    {{4.1f, 0.98f, 4.4f, 1.68f}, {3.4f, 0.64f, 4.4f, 1.20f}},
+    {{3.3f, 0.53f, 4.9f, 0.94f}, {3.2f, 0.37f, 5.3f, 0.71f}},
+    {{2.1f, 0.32f, 0.4f, 0.55f}, {1.9f, 0.26f, 0.7f, 0.42f}},
+    {{1.8f, 0.24f, 1.0f, 0.33f}, {1.6f, 0.21f, 1.2f, 0.26f}},
+    {{1.7f, 0.20f, 0.4f, 0.23f}, {1.5f, 0.16f, 0.5f, 0.17f}},
+    {{1.7f, 0.16f, 1.1f, 0.13f}, {1.4f, 0.15f, 1.1f, 0.12f}},
+};
+MxPlan mx_plan_grouped(int slots, int count, int n, int steps, bool x8) {
+    MxPlan best;
+    float least = 0.0f;
+    for (int t = 0; t < kTileCount; ++t) {
+        const TileCost &c = kTiles[t];
+        const int64_t tiles = grouped_row_tiles(slots, count, c.bm) * ((n + c.bn - 1) / c.bn);
+        for (int sp : {1, 2, 3, 4, 6, 8}) {
+            if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
+            const float wgs = static_cast<float>(tiles) * sp;
+            float us = grouped_time(kGrouped[t][x8 ? 0 : 1], (steps + sp - 1) / sp, wgs / kCus, t == 0);
+            if (sp > 1) us += 2.5f + wgs * c.bm * c.bn * 8.0f * 3.7e-7f;
             if (least == 0.0f || us < least) {
                 least = us;
                 best.tile = t;
@@ -505,14 +541,11 @@ int launch_either(const MxProduct &p, bool join, void *stream) {
 }  // namespace
 
 MxPlan mx_product_plan(int M, int n, int blocks, int x_type) {
-    return mx_plan([&](int bm) { return static_cast<int64_t>((M + bm - 1) / bm); }, n, blocks / 4,
-                   x_type == DBF_TYPE_E4M3);
+    return mx_plan(M, n, blocks / 4, x_type == DBF_TYPE_E4M3);
 }
 
-// The groups' sizes are on the device: every group is taken to have its share
-// of the rows, and half a tile's loss at its end.
 MxPlan mx_grouped_plan(int slots, int count, int n, int blocks, int x_type) {
-    return mx_plan([&](int bm) { return grouped_row_tiles(slots, count, bm); }, n, blocks / 4, x_type == DBF_TYPE_E4M3);
+    return mx_plan_grouped(slots, count, n, blocks / 4, x_type == DBF_TYPE_E4M3);
 }
 
 size_t mx_grouped_parts(int slots, int count, int n, int blocks, int x_type) {

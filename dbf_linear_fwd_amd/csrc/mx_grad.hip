@@ -137,8 +137,10 @@ template <typename C, typename E, GradRows ROWS, bool G>
 __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
     constexpr bool Whole = ROWS == GradRows::Whole, Dma = ROWS != GradRows::Elements;
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    [[maybe_unused]] RowTiles tiles;
     if constexpr (G) {
-        a.grid.nbm = a.rows.table[0].group;
+        tiles = scan_rows<C::BM>(a.rows);
+        a.grid.nbm = tiles.total;
         a.grid.group = min(a.grid.nbm, 4);
         if (static_cast<int>(blockIdx.x) >= a.grid.nbm * a.grid.nbn * a.grid.nsplit) return;
     }
@@ -148,7 +150,8 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
     int bm, bn;
     tile_at(a.grid, tile, bm, bn);
     const int m0 = G ? 0 : bm * C::BM, n0 = bn * C::BN;
-    [[maybe_unused]] const RowPlaces place = take_group<G>(a.rows, bm, a.w, a.M);
+    [[maybe_unused]] RowPlaces place;
+    if constexpr (G) place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
     const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
@@ -403,8 +406,10 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
 template <typename C, typename E, bool G>
 __global__ __launch_bounds__(64) void mx_grad_finish_kernel(MxGradArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    [[maybe_unused]] RowTiles tiles;
     if constexpr (G) {
-        a.grid.nbm = a.rows.table[0].group;
+        tiles = scan_rows<C::BM>(a.rows);
+        a.grid.nbm = tiles.total;
         a.grid.group = min(a.grid.nbm, 4);
         if (static_cast<int>(blockIdx.x) >= a.grid.nbm * a.grid.nbn * C::Waves) return;
     }
@@ -415,7 +420,8 @@ __global__ __launch_bounds__(64) void mx_grad_finish_kernel(MxGradArgs a) {
     f32x16 acc[C::MI][C::NI];
     add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
                  a.grid.nsplit, acc);
-    [[maybe_unused]] const RowPlaces place = take_group<G>(a.rows, bm, a.w, a.M);
+    [[maybe_unused]] RowPlaces place;
+    if constexpr (G) place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
     scale_columns<C, E>(acc, a.w, bn * C::BN, wave % C::WN);
     if constexpr (G)
         store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, 0, bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
@@ -447,15 +453,13 @@ constexpr int kCus = 256;
 // sizes the choice is 4.4 % from the best on average; 512 rows take 88 us in
 // 128 x 128 tiles and two parts, 77.5 in 256 x 256 and eight; at worst 45.5
 // where 35 is the best, 128 rows of n 4096, m 14336.)
-// row_tiles(rows of a tile): the product's row tiles.
-template <typename F>
-MxPlan grad_plan(F row_tiles, int n, int m) {
+MxPlan grad_plan(int M, int n, int m) {
     MxPlan best;
     float least = 0.0f;
     const int steps = (n + 63) / 64;
     for (int t = 0; t < kGradCount; ++t) {
         const GradCost &c = kGrad[t];
-        const int64_t tiles = row_tiles(c.bm) * ((m + c.bn - 1) / c.bn);
+        const int64_t tiles = static_cast<int64_t>((M + c.bm - 1) / c.bm) * ((m + c.bn - 1) / c.bn);
         for (int sp : {1, 2, 3, 4, 6, 8, 12}) {
             if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
             const float wgs = static_cast<float>(tiles) * sp;
@@ -464,6 +468,35 @@ MxPlan grad_plan(F row_tiles, int n, int m) {
             const float step = c.full * per_cu > c.light ? c.full * per_cu : c.light;
             float us = 3.0f + static_cast<float>((steps + sp - 1) / sp) * step;
             if (sp > 1) us += 3.5f + wgs * c.bm * c.bn * 8.0f * 3e-7f;
+            if (least == 0.0f || us < least) {
+                least = us;
+                best.tile = t;
+                best.nsplit = sp;
+            }
+        }
+    }
+    return best;
+}
+
+// The same for rows in groups.  Against every tile and 1, 2 and 4 parts at 164
+// sizes the choice is 2 % from the best on average.
+constexpr GroupedCost kGrouped[kGradCount] = {
+    {6.2f, 1.20f, 6.0f, 1.69f},
+    {3.5f, 0.56f, 2.1f, 0.56f},
+    {2.8f, 0.43f, 1.1f, 0.29f},
+};
+MxPlan grad_plan_grouped(int slots, int count, int n, int m) {
+    MxPlan best;
+    float least = 0.0f;
+    const int steps = (n + 63) / 64;
+    for (int t = 0; t < kGradCount; ++t) {
+        const GradCost &c = kGrad[t];
+        const int64_t tiles = grouped_row_tiles(slots, count, c.bm) * ((m + c.bn - 1) / c.bn);
+        for (int sp : {1, 2, 3, 4, 6, 8, 12}) {
+            if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
+            const float wgs = static_cast<float>(tiles) * sp;
+            float us = grouped_time(kGrouped[t], (steps + sp - 1) / sp, wgs / kCus, t == 0);
+            if (sp > 1) us += 2.5f + wgs * c.bm * c.bn * 8.0f * 3.7e-7f;
             if (least == 0.0f || us < least) {
                 least = us;
                 best.tile = t;
@@ -544,13 +577,9 @@ int launch_either(const MxBackward &b, bool join, void *stream) {
 
 }  // namespace
 
-MxPlan mx_backward_plan(int M, int n, int m) {
-    return grad_plan([&](int bm) { return static_cast<int64_t>((M + bm - 1) / bm); }, n, m);
-}
+MxPlan mx_backward_plan(int M, int n, int m) { return grad_plan(M, n, m); }
 
-MxPlan mx_grouped_backward_plan(int slots, int count, int n, int m) {
-    return grad_plan([&](int bm) { return grouped_row_tiles(slots, count, bm); }, n, m);
-}
+MxPlan mx_grouped_backward_plan(int slots, int count, int n, int m) { return grad_plan_grouped(slots, count, n, m); }
 
 size_t mx_grouped_backward_parts(int slots, int count, int n, int m) {
     return grouped_part_floats(mx_grouped_backward_plan(slots, count, n, m), slots, count, m);

@@ -5,8 +5,10 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "mx_device.h"
+#include "rows_device.h"
 
 namespace dbf {
 namespace {
@@ -95,27 +97,84 @@ struct RowPlaces {
     }
 };
 
-// The rows of row tile bm, and their group's weight in place of the first.
-template <bool G>
-__device__ __forceinline__ RowPlaces take_group(const MxRows &a, int bm, MxWeight &w, int &M) {
-    RowPlaces p;
-    if constexpr (G) {
-        const RowTile t = a.table[1 + bm];
-        p.first = t.first;
-        p.none = t.group >= a.count;
-        M = t.rows;
-        const size_t e = p.none ? 0 : t.group;
-        w.codes += e * a.code_stride;
-        w.scales += e * a.scale_stride;
-        w.colmax += e * a.colmax_stride;
+// The row tiles of a product, as a wave sees them.
+struct RowTiles {
+    int total = 0;                          // those of no group included
+    int grouped = 0, upto, tiles, lo, hi;   // without a table: lane e has group e
+};
+template <int BM>
+__device__ __forceinline__ RowTiles scan_rows(const MxRows &a) {
+    RowTiles t;
+    if (a.table) {
+        t.total = a.table[0].group;
+        return t;
     }
+    const int lane = threadIdx.x & 63;
+    t.lo = t.hi = 0;
+    if (lane < a.count) group_places(a.offsets, a.count, a.slots, lane, t.lo, t.hi);
+    int lo, hi;
+    group_places(a.offsets, a.count, a.slots, a.count, lo, hi);
+    t.tiles = (t.hi - t.lo + BM - 1) / BM;
+    t.upto = wave_scan(t.tiles, lane);
+    t.grouped = __builtin_amdgcn_readlane(t.upto, 63);
+    // (never more than an order's groups make: the grid and the parts' memory are for so many)
+    t.total = __builtin_amdgcn_readfirstlane(min(t.grouped + (hi - lo + BM - 1) / BM,
+                                                 static_cast<int>(row_tiles_bound(a.slots, a.count, BM))));
+    return t;
+}
+
+// The rows of row tile bm, and their group's weight in place of the first.
+template <int BM>
+__device__ __forceinline__ RowPlaces take_group(const MxRows &a, const RowTiles &t, int bm, MxWeight &w, int &M) {
+    RowPlaces p;
+    int e;
+    if (a.table) {
+        const RowTile r = a.table[1 + bm];
+        e = r.group;
+        p.first = r.first;
+        M = r.rows;
+    } else {
+        int lo, hi, at;
+        if (bm < t.grouped) {
+            e = __builtin_ctzll(__ballot(t.upto > bm));
+            lo = __builtin_amdgcn_readlane(t.lo, e);
+            hi = __builtin_amdgcn_readlane(t.hi, e);
+            at = bm - __builtin_amdgcn_readlane(t.upto - t.tiles, e);
+        } else {
+            e = a.count;
+            group_places(a.offsets, a.count, a.slots, e, lo, hi);
+            at = bm - t.grouped;
+        }
+        p.first = __builtin_amdgcn_readfirstlane(lo + at * BM);
+        M = __builtin_amdgcn_readfirstlane(min(BM, hi - (lo + at * BM)));
+    }
+    p.none = e >= a.count;
+    const size_t at = p.none ? 0 : e;
+    w.codes += at * a.code_stride;
+    w.scales += at * a.scale_stride;
+    w.colmax += at * a.colmax_stride;
     return p;
 }
 
-// Row tiles of `bm` places to reckon with where `count` groups share `slots` rows.
+// Row tiles of `bm` places to reckon with where `count` groups share `slots`
+// rows: the sizes are on the device, so they are taken to be spread as routers
+// spread them, exponentially around their mean, whose tiles are geometric.
 inline int64_t grouped_row_tiles(int slots, int count, int bm) {
-    const int64_t used = slots < count ? slots : count;
-    return std::max<int64_t>(used, slots / bm + used / 2);
+    const int used = slots < count ? slots : count;
+    return static_cast<int64_t>(used / (1.0 - std::exp(-static_cast<double>(bm) * used / slots)) + 0.5);
+}
+
+// Cost of a tile of a grouped product in microseconds: a workgroup with few
+// others, start and step, and its share of a full CU.  K steps are cheaper and
+// starts dearer than where one weight serves all workgroups: a tile has few
+// rows of its own, and many starts overlap on a CU.
+struct GroupedCost {
+    float light0, light, full0, full;
+};
+inline float grouped_time(const GroupedCost &c, int steps, float per_cu, bool alone) {
+    // (the largest tile has a CU to itself: whole rounds, until there are many)
+    if (alone && per_cu > 1.0f && per_cu < 4.0f) per_cu = std::ceil(per_cu - 0.05f);
+    return std::max(c.light0 + steps * c.light, per_cu * (c.full0 + steps * c.full));
 }
 
 // A wave's results to y.  A 32 x 32 result has one row of y per lane, its

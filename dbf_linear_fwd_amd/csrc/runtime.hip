@@ -67,7 +67,7 @@ struct dbf_layer {
     uint8_t *mx_codes = nullptr, *mx_scales = nullptr, *mx_colmax = nullptr;
     uint8_t *mx_xcodes = nullptr, *mx_xscales = nullptr;
     // experts (dbf_experts_pack; mx is set too): that many such weights of n x m
-    // one after the other, and the row tiles of a call's product
+    // one after the other, and the row tiles of a call's product (more than kScanGroups)
     int32_t experts = 0;
     dbf::RowTile *row_tiles = nullptr;
     size_t packed_bytes = 0, scale_bytes = 0, workspace_bytes = 0;
@@ -1143,7 +1143,8 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     const size_t max_bytes = blocks + 16;  // (blocks: a multiple of 4)
     const size_t xc_bytes = static_cast<size_t>(max_rows) * dbf_mx_code_bytes(m, act_type);
     const size_t xs_bytes = static_cast<size_t>(max_rows) * blocks;
-    const size_t tile_bytes = (dbf::row_tiles_bound(max_rows, count, 32) + 1) * sizeof(dbf::RowTile);
+    const size_t tile_bytes =
+        count <= dbf::kScanGroups ? 0 : (dbf::row_tiles_bound(max_rows, count, 32) + 1) * sizeof(dbf::RowTile);
     const size_t parts = experts_part_floats(count, n, m, max_rows);
     dbf_status_t st = hipGetDevice(&h->device) == hipSuccess ? DBF_OK : DBF_ERR_HIP;
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_codes), count * each * 16);
@@ -1151,7 +1152,7 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_colmax), count * max_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xcodes), xc_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xscales), xs_bytes);
-    if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->row_tiles), tile_bytes);
+    if (st == DBF_OK && tile_bytes > 0) st = dev_alloc(reinterpret_cast<void **>(&h->row_tiles), tile_bytes);
     if (st == DBF_OK && parts > 0) st = dev_alloc(reinterpret_cast<void **>(&h->split), sizeof(float) * parts);
     if (st == DBF_OK) h->split_cap = parts;
     const size_t row_bytes = dbf_mx_code_bytes(m, DBF_TYPE_E2M1);
@@ -1185,7 +1186,8 @@ static dbf_status_t experts_rows(const dbf_layer *h, const int32_t *order, const
     if ((gather > 0 || scatter) && (!order || (reinterpret_cast<uintptr_t>(order) & 3u))) return DBF_ERR_INVALID_ARG;
     const size_t blocks = static_cast<size_t>(h->m_pad) / 32, each = static_cast<size_t>(h->n_pad) * blocks;
     rows->order = order;
-    rows->table = h->row_tiles;
+    rows->offsets = offsets;
+    rows->table = h->row_tiles;  // (null for few experts)
     rows->count = h->experts;
     rows->slots = slots;
     rows->per = gather;
@@ -1236,7 +1238,7 @@ extern "C" dbf_status_t dbf_experts_forward(dbf_handle_t h, const void *x, int32
     p.rows = &rows;
     int32_t bm = 0, bn = 0;
     dbf::mx_product_tile(p.plan, &bm, &bn);
-    if (st == DBF_OK)
+    if (st == DBF_OK && rows.table)
         st = timed_launch(h, "row_tiles", stream, [&] {
             return dbf::launch_row_tiles(offsets, h->experts, slots, bm, h->row_tiles,
                                          dbf::row_tiles_bound(slots, h->experts, bm), stream);
@@ -1273,7 +1275,7 @@ extern "C" dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy
     b.rows = &rows;
     int32_t bm = 0, bn = 0;
     dbf::mx_backward_tile(b.plan, &bm, &bn);
-    st = timed_launch(h, "row_tiles", stream, [&] {
+    if (rows.table) st = timed_launch(h, "row_tiles", stream, [&] {
         return dbf::launch_row_tiles(offsets, h->experts, slots, bm, h->row_tiles,
                                      dbf::row_tiles_bound(slots, h->experts, bm), stream);
     });

@@ -319,7 +319,7 @@ def test_other_stream_timing_info_and_refusals(gpu):
     assert info["n"] == 40 and info["m"] == 64 and info["max_batch"] == 12
     dbf.dbf_timing_enable(ex.handle)
     ex(x, g)
-    assert {"row_tiles", "mx_quantize", "mx_product"} <= set(dbf.dbf_timing_read(ex.handle))
+    assert {"mx_quantize", "mx_product"} <= set(dbf.dbf_timing_read(ex.handle))
     dbf.dbf_timing_enable(ex.handle, False)
 
     wide = torch.randn(12, 65, device="cuda", dtype=torch.float16)
