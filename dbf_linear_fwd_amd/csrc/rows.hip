@@ -6,9 +6,15 @@
 // each other by a ballot per bit of the key, so a row's place is its key's
 // next place plus the lanes of its key below it, and no atomic is needed:
 // the order is that of the rows.  Counts of each wave stand in LDS and are
-// summed over the keys before and the waves before.  Up to kBlockRows rows
-// are one workgroup and one launch; more are one workgroup each, with a
-// launch that adds up their counts between the counting and the placing.
+// summed over the keys before and the waves before.
+//
+// Latency is all it costs.  Up to 4096 rows are one workgroup and one launch;
+// more are cut into workgroups of 1024, 4096 or 16384 rows, one launch that
+// counts and one that places, where every workgroup adds up the counts of the
+// others (of more than kDirectParts, a launch between does).  Graph replays, 64
+// groups: 128 rows 4.4 us (16 steps of 64 rows unrolled, most of them skipped:
+// 6.2), 2048 rows 5.9, 4096 8.0, 16384 8.9 (in one workgroup 22), 65536 10.9
+// (in workgroups of 4096 rows 14.3), 262144 16.4 (of 16384 36), 2^20 39.
 
 #include <algorithm>
 #include <atomic>
@@ -20,8 +26,9 @@ namespace dbf {
 namespace {
 
 constexpr int kWaves = 16, kThreads = 64 * kWaves;
-constexpr int kSteps = 16;                            // of 64 rows, per wave
-constexpr int kBlockRows = kWaves * kSteps * 64;      // 16384
+constexpr int block_rows(int steps) { return kThreads * steps; }  // steps of 64 rows per wave
+constexpr int kMaxSteps = 16;
+constexpr int kDirectParts = 64;
 constexpr int kMaxGroups = 1024;
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 
@@ -40,6 +47,13 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits, uint64_t on) {
         m &= bit ? s : ~s;
     }
     return m;
+}
+
+// The lanes of a wave see what each other wrote to LDS (whose accesses are in
+// order for a wave: nothing is waited for).
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // Exclusive sum over the workgroup's threads; total is everyone's.
@@ -63,40 +77,42 @@ struct SortArgs {
     int64_t rows;
     int count, bits;
     int32_t *order, *offsets;
-    int32_t *counts;  // [workgroups][count + 1]: of each workgroup's keys, then their first places
+    int32_t *counts;  // [workgroups][count + 1]: of each workgroup's keys; scanned: their first places
+    int parts, scanned;
 };
 
 enum class Sort { Whole, Count, Place };
 
 // Whole: all rows in one workgroup.  Count: the counts of a workgroup's rows
-// to memory.  Place: its rows to their places, from the first places there.
-template <typename I, Sort S>
+// to memory.  Place: its rows to their places.
+template <typename I, Sort S, int Steps>
 __global__ __launch_bounds__(kThreads) void sort_kernel(const SortArgs a) {
     extern __shared__ int hist[];  // [kWaves][keys]
     __shared__ int tmp[kWaves];
     const int keys = a.count + 1;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const I *index = static_cast<const I *>(a.index);
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kBlockRows;
-    const int here = static_cast<int>(a.rows - first < kBlockRows ? a.rows - first : kBlockRows);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * block_rows(Steps);
+    const int here = static_cast<int>(a.rows - first < block_rows(Steps) ? a.rows - first : block_rows(Steps));
     const int steps = ((here + 63) / 64 + kWaves - 1) / kWaves;  // per wave
     const int row0 = wave * steps * 64 + lane;
 
     for (int i = threadIdx.x; i < kWaves * keys; i += kThreads) hist[i] = 0;
-    int key[kSteps];
+    int key[Steps];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
+    for (int s = 0; s < Steps; ++s) {
         const int r = row0 + s * 64;
         if (s < steps && r < here) key[s] = key_of(index, first + r, a.count);
     }
     __syncthreads();
     int *mine = hist + wave * keys;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int s = 0; s < Steps; ++s)
         if (s < steps) {
             const bool on = row0 + s * 64 < here;
             const uint64_t same = same_key(on ? key[s] : 0, a.bits, __ballot(on));
             if (on && (same & ((1ull << lane) - 1)) == 0) mine[key[s]] += __popcll(same);
+            wave_fence();
         }
     __syncthreads();
     // the waves' counts of a key become their places behind the waves before
@@ -112,14 +128,29 @@ __global__ __launch_bounds__(kThreads) void sort_kernel(const SortArgs a) {
         if constexpr (S == Sort::Count) {
             if (k < keys) a.counts[static_cast<size_t>(blockIdx.x) * keys + k] = sum;
         } else {
-            int start;
-            if constexpr (S == Sort::Whole) {
+            int start = 0, all = sum;  // of the workgroups before, and of all
+            if constexpr (S == Sort::Place) {
+                const int32_t *c = a.counts + k;
+                if (a.scanned) {
+                    if (k < keys) start = c[static_cast<size_t>(blockIdx.x) * keys];
+                } else {
+                    all = 0;
+                    if (k < keys) {
+#pragma unroll 8
+                        for (int p = 0; p < a.parts; ++p) {
+                            const int n = c[p * keys];
+                            if (p < static_cast<int>(blockIdx.x)) start += n;
+                            all += n;
+                        }
+                    }
+                }
+            }
+            if (S == Sort::Whole || !a.scanned) {
                 int total;
-                start = before + block_scan(sum, tmp, total);
+                const int at = before + block_scan(all, tmp, total);
                 before += total;
-                if (k < keys) a.offsets[k] = start;
-            } else {
-                start = k < keys ? a.counts[static_cast<size_t>(blockIdx.x) * keys + k] : 0;
+                if (k < keys && blockIdx.x == 0) a.offsets[k] = at;
+                start += at;
             }
             if (k < keys)
                 for (int w = 0; w < kWaves; ++w) hist[w * keys + k] += start;
@@ -128,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void sort_kernel(const SortArgs a) {
     if constexpr (S == Sort::Count) return;
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int s = 0; s < Steps; ++s)
         if (s < steps) {
             const bool on = row0 + s * 64 < here;
             const uint64_t same = same_key(on ? key[s] : 0, a.bits, __ballot(on));
@@ -139,6 +170,7 @@ __global__ __launch_bounds__(kThreads) void sort_kernel(const SortArgs a) {
                 // (a wave's LDS accesses are in order: every lane has read its place)
                 if (below == 0) mine[key[s]] = at + __popcll(same);
             }
+            wave_fence();
         }
 }
 
@@ -197,26 +229,55 @@ __global__ __launch_bounds__(kThreads) void row_tiles_kernel(const int32_t *offs
     }
 }
 
+// Steps of a wave: one workgroup up to 4096 rows, then as many workgroups as add up each other's counts.
+int sort_steps(int64_t rows) {
+    for (int steps : {1, 2, 4})
+        if (rows <= block_rows(steps)) return steps;
+    for (int steps : {1, 4})
+        if (rows <= static_cast<int64_t>(kDirectParts) * block_rows(steps)) return steps;
+    return kMaxSteps;
+}
+int sort_parts(int64_t rows) {
+    const int64_t per = block_rows(sort_steps(rows));
+    return static_cast<int>(rows <= per ? 1 : (rows + per - 1) / per);
+}
 size_t sort_bytes(int64_t rows, int count) {
-    return rows <= kBlockRows ? 0 : static_cast<size_t>((rows + kBlockRows - 1) / kBlockRows) * (count + 1) * sizeof(int32_t);
+    const int parts = sort_parts(rows);
+    return parts == 1 ? 0 : static_cast<size_t>(parts) * (count + 1) * sizeof(int32_t);
+}
+
+template <typename I, int Steps>
+void launch_sort(SortArgs &a, hipStream_t s) {
+    const size_t lds = sizeof(int) * kWaves * (a.count + 1);
+    auto go = [&](auto kernel, std::atomic<uint64_t> &asked) {
+        if (lds > 60 * 1024) allow_lds(kernel, sizeof(int) * kWaves * (kMaxGroups + 1), asked);
+        launch_kernel(kernel, dim3(a.parts), dim3(kThreads), lds, s, a);
+    };
+    if (a.parts == 1) {
+        if constexpr (Steps <= 4) {
+            static std::atomic<uint64_t> whole{0};
+            go(sort_kernel<I, Sort::Whole, Steps>, whole);
+        }
+        return;
+    }
+    if constexpr (Steps != 2) {
+        static std::atomic<uint64_t> counting{0}, placing{0};
+        go(sort_kernel<I, Sort::Count, Steps>, counting);
+        if (a.scanned)
+            launch_kernel(sort_scan_kernel, dim3(1), dim3(kThreads), 0, s, a.counts, a.parts, a.count + 1, a.offsets);
+        go(sort_kernel<I, Sort::Place, Steps>, placing);
+    }
 }
 
 template <typename I>
 int launch_sort(SortArgs &a, hipStream_t s) {
-    static std::atomic<uint64_t> whole{0}, counting{0}, placing{0};
-    const size_t lds = sizeof(int) * kWaves * (a.count + 1);
-    auto go = [&](auto kernel, std::atomic<uint64_t> &asked, uint32_t grid) {
-        allow_lds(kernel, sizeof(int) * kWaves * (kMaxGroups + 1), asked);
-        launch_kernel(kernel, dim3(grid), dim3(kThreads), lds, s, a);
-    };
-    if (a.rows <= kBlockRows) {
-        go(sort_kernel<I, Sort::Whole>, whole, 1);
-    } else {
-        const uint32_t parts = static_cast<uint32_t>((a.rows + kBlockRows - 1) / kBlockRows);
-        go(sort_kernel<I, Sort::Count>, counting, parts);
-        launch_kernel(sort_scan_kernel, dim3(1), dim3(kThreads), 0, s, a.counts, static_cast<int>(parts), a.count + 1,
-                      a.offsets);
-        go(sort_kernel<I, Sort::Place>, placing, parts);
+    a.parts = sort_parts(a.rows);
+    a.scanned = a.parts > kDirectParts;
+    switch (sort_steps(a.rows)) {
+        case 1: launch_sort<I, 1>(a, s); break;
+        case 2: launch_sort<I, 2>(a, s); break;
+        case 4: launch_sort<I, 4>(a, s); break;
+        default: launch_sort<I, kMaxSteps>(a, s); break;
     }
     return static_cast<int>(hipGetLastError());
 }
@@ -248,7 +309,7 @@ extern "C" dbf_status_t dbf_group_rows(const void *index, int32_t index_bits, in
     if (rows > 0 && (!aligned(index, index_bits / 8) || !aligned(order, 4))) return DBF_ERR_INVALID_ARG;
     const size_t need = sort_bytes(rows, count);
     if (need > 0 && (!aligned(workspace, 4) || workspace_bytes < need)) return DBF_ERR_INVALID_ARG;
-    SortArgs a{index, rows, count, 0, order, offsets, static_cast<int32_t *>(workspace)};
+    SortArgs a{index, rows, count, 0, order, offsets, static_cast<int32_t *>(workspace), 1, 0};
     while ((1 << a.bits) < count + 1) ++a.bits;
     const int e = index_bits == 32 ? launch_sort<int32_t>(a, stream) : launch_sort<int64_t>(a, stream);
     return e == 0 ? DBF_OK : DBF_ERR_HIP;

@@ -543,7 +543,7 @@ dbf_status_t dbf_rms_norm_backward(const void *dy, const void *h, const void *we
  *   index       device, `rows` whole numbers of index_bits (32 or 64) bits, signed;
  *               those outside [0, count) are of no group.
  *   order       out, rows.   offsets  out, count + 1.
- *   workspace   dbf_group_rows_workspace(rows, count) bytes (0 up to 16384 rows;
+ *   workspace   dbf_group_rows_workspace(rows, count) bytes (0 up to 4096 rows;
  *               NULL then), 4-byte aligned.
  * Stable, without atomics.  rows = 0 writes offsets only.  1 <= count <= 1024,
  * rows <= 2^24 (DBF_ERR_SHAPE above; the workspace of such sizes is 0).

@@ -33,12 +33,26 @@ def same(index, count, dtype):
 
 @pytest.mark.parametrize("bits", [32, 64])
 @pytest.mark.parametrize("count", [1, 2, 7, 64, 1000, 1024])
-@pytest.mark.parametrize("rows", [0, 1, 2, 63, 64, 65, 128, 1000, 1025, 16383, 16384, 16385, 50001])
+@pytest.mark.parametrize("rows", [0, 1, 2, 63, 64, 65, 128, 1000, 1025, 2048, 2049, 4096, 4097, 16385, 32768, 32769, 131072, 131073])
 def test_order(gpu, rows, count, bits):
     _say(f"group_rows {rows} rows {count} groups int{bits}")
     rng = np.random.default_rng(rows + count)
     index = rng.integers(-1, count + 1, size=rows)  # count: of no group, as -1 is
     same(index, count, _torch().int64 if bits == 64 else _torch().int32)
+
+
+def test_a_million_rows(gpu):
+    """More workgroups than add up each other's counts."""
+    torch = _torch()
+    for rows, count in ((1 << 20, 64), ((1 << 20) + 1, 1000), (3_000_001, 7)):
+        _say(f"group_rows {rows} rows {count} groups")
+        index = torch.randint(-1, count, (rows,), dtype=torch.int32, device="cuda")
+        g = dbf.group_rows(index, count)
+        key = torch.where(index < 0, count, index)
+        order = torch.sort(key, stable=True).indices
+        assert torch.equal(g.order, order.int())
+        assert torch.equal(g.offsets, torch.bincount(key, minlength=count + 1).cumsum(0)[:count + 1].int()
+                           - torch.bincount(key, minlength=count + 1)[:count + 1].int())
 
 
 @pytest.mark.parametrize("rows", [70, 20000])
