@@ -304,7 +304,9 @@ int launch_mx_layout(const void *codes, const uint8_t *scales, int n, int m, uin
                      uint8_t *colmax, void *stream);
 
 // How a tiled product runs: which of its tiles, and in how many K parts (more
-// than one: the product's launch leaves fp32 sums, and a join follows it).
+// than one: the product's launch leaves fp32 sums, and a join follows it).  Of
+// rows in groups, whose number of tiles is on the device, nsplit is the most
+// parts into which the tiles that fill no round of workgroups are cut.
 struct MxPlan {
     int tile = 0, nsplit = 1;
 };
@@ -313,11 +315,13 @@ struct MxPlan {
 // "Rows in groups"): `slots` places in the grouped order, those from
 // offsets[count] on of no group.  The row tiles of up to kScanGroups groups are
 // found by each workgroup; those of more come in a table that launch_row_tiles
-// makes: table[0].group is their number, table[1 + i] tile i (group, first
-// place, places).  The input's row of a place is the place itself (per = 0) or
-// its order / per of in_rows; the result's row the place or (scatter) its
-// order.  Values out of range are clamped, or not written.
+// makes.  The input's row of a place is the place itself (per = 0) or its
+// order / per of in_rows; the result's row the place or (scatter) its order.
+// Values out of range are clamped, or not written.
 constexpr int kScanGroups = 64;
+// The order of row tiles: those of more than half a tile first, group after
+// group, then the others, then those of no group.  A table's first entry holds
+// the number of the former two kinds (group) and of all (first).
 struct RowTile {
     int32_t group, first, rows, zero;
 };
@@ -356,7 +360,8 @@ struct MxProduct {
 MxPlan mx_product_plan(int M, int n, int blocks, int x_type);
 // The same for `slots` rows that up to `count` groups share.
 MxPlan mx_grouped_plan(int slots, int count, int n, int blocks, int x_type);
-size_t mx_grouped_parts(int slots, int count, int n, int blocks, int x_type);
+// Floats of K-part sums of any call of up to `slots` rows.
+size_t mx_grouped_parts(int slots, int count, int n, int blocks);
 void mx_product_tile(const MxPlan &p, int32_t *rows, int32_t *cols);
 // Floats of K-part sums that the product of this shape uses (0: K whole).
 size_t mx_product_parts(int M, int n, int blocks, int x_type);

@@ -164,28 +164,34 @@ struct MxGemmArgs {
 template <typename C, typename E, bool G>
 __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    [[maybe_unused]] RowTiles tiles;
-    if constexpr (G) {
-        tiles = scan_rows<C::BM>(a.rows);
-        a.grid.nbm = tiles.total;
-        a.grid.group = min(a.grid.nbm, 4);
-    }
-    const int T = a.grid.nbm * a.grid.nbn;
-    if (G && static_cast<int>(blockIdx.x) >= T * a.grid.nsplit) return;
-    const int idx = xcd_index(blockIdx.x, T * a.grid.nsplit);
-    const int split = idx / T, tile = idx - split * T;
-    int bm, bn;
-    tile_at(a.grid, tile, bm, bn);
-    const int m0 = G ? 0 : bm * C::BM, n0 = bn * C::BN;
+    int bm, bn, split, nsplit = a.grid.nsplit, T, tile;
     [[maybe_unused]] RowPlaces place;
-    if constexpr (G) place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
+    if constexpr (G) {
+        const RowTiles tiles = scan_rows<C::BM>(a.rows);
+        const GroupedWork w = grouped_work(tiles, a.grid.nbn, a.w.blocks >> 2, a.grid.group, nsplit, blockIdx.x);
+        if (w.bm < 0) return;
+        bm = w.bm;
+        bn = w.bn;
+        split = w.split;
+        nsplit = w.nsplit;
+        T = w.cut;
+        tile = w.at;
+        place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
+    } else {
+        T = a.grid.nbm * a.grid.nbn;
+        const int idx = xcd_index(blockIdx.x, T * nsplit);
+        split = idx / T;
+        tile = idx - split * T;
+        tile_at(a.grid, tile, bm, bn);
+    }
+    const int m0 = G ? 0 : bm * C::BM, n0 = bn * C::BN;
     const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
     const int steps = a.w.blocks >> 2;  // of 128 columns
-    const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / a.grid.nsplit);
+    const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / nsplit);
     // (rows of no group: no steps, their results are zeros)
-    const int nk = G && place.none ? 0 : static_cast<int>(static_cast<int64_t>(split + 1) * steps / a.grid.nsplit) - k0;
+    const int nk = G && place.none ? 0 : static_cast<int>(static_cast<int64_t>(split + 1) * steps / nsplit) - k0;
 
     // sources of this wave's loads; a stage moves them by inc bytes
     const uint8_t *src[C::D16 + C::D4];
@@ -294,35 +300,54 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(MxGemmArgs a) {
     // before it have returned, so that one's slot is free for the next loads.
     // The last half reads past the last stage, in LDS and to no use.
     int slot = 0;
-    auto chunk = [&](auto go) {
-        constexpr bool GO = decltype(go)::value != 0;
+    auto chunk = [&](auto go, auto work) {
+        constexpr bool GO = decltype(go)::value != 0, Work = decltype(work)::value != 0;
         constexpr int W0 = GO ? C::younger(0, C::S - 2) : 0, W1 = GO ? C::younger(1, C::S - 2) : 0;
+        auto run = [&](auto t, auto part, const MxFrags<C> &cur, MxFrags<C> &nxt, int nslot, int fslot) {
+            if constexpr (Work) {
+                half(t, part, cur, nxt, nslot, fslot);
+            } else {
+                constexpr int P = decltype(part)::value, NL = P >= 0 ? C::loads(P) : 0;
+#pragma unroll
+                for (int q = 0; q < NL; ++q) issue_one(fslot, q);
+            }
+        };
         if constexpr (C::Parts == 2) {
             const int s1 = slot + 1, s2 = next(s1);
             wait_vm<W1>();
             wait_lds();
             block_barrier();
-            half(Const<0>{}, Const<GO ? 0 : -1>{}, f0, f1, s1, slot);
+            run(Const<0>{}, Const<GO ? 0 : -1>{}, f0, f1, s1, slot);
             wait_vm<W0>();
             wait_lds();
             block_barrier();
-            half(Const<1>{}, Const<GO ? 1 : -1>{}, f1, f0, s2, s1);
+            run(Const<1>{}, Const<GO ? 1 : -1>{}, f1, f0, s2, s1);
             slot = s2;
         } else {
             const int s1 = next(slot);
-            half(Const<0>{}, Const<-1>{}, f0, f1, slot, 0);
+            run(Const<0>{}, Const<-1>{}, f0, f1, slot, 0);
             wait_vm<W0>();
             wait_lds();
             block_barrier();
-            half(Const<1>{}, Const<GO ? 0 : -1>{}, f1, f0, s1, slot);
+            run(Const<1>{}, Const<GO ? 0 : -1>{}, f1, f0, s1, slot);
             slot = s1;
         }
     };
-    int left = nk;
-    for (; left > Chunks; --left) chunk(Const<1>{});
-    for (; left > 0; --left) chunk(Const<0>{});
+    auto chunks = [&](auto work) {
+        int left = nk;
+        for (; left > Chunks; --left) chunk(Const<1>{}, work);
+        for (; left > 0; --left) chunk(Const<0>{}, work);
+    };
+    // Waves whose rows are all past the group's last only load: where two share
+    // a SIMD, as in the largest tile, the other one has it to itself.
+    if constexpr (G && C::Waves == 8) {
+        if (wm * C::MI * 32 >= a.M) chunks(Const<0>{});
+        else chunks(Const<1>{});
+    } else {
+        chunks(Const<1>{});
+    }
 
-    if (a.part) {
+    if (G ? nsplit > 1 : a.part != nullptr) {
         store_part<C>(part_at<C>(a.part, split, T, tile, wave, lane), acc);
         return;
     }
@@ -339,24 +364,25 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(MxGemmArgs a) {
 template <typename C, typename E, bool G>
 __global__ __launch_bounds__(64) void mx_finish_kernel(MxGemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    [[maybe_unused]] RowTiles tiles;
-    if constexpr (G) {
-        tiles = scan_rows<C::BM>(a.rows);
-        a.grid.nbm = tiles.total;
-        a.grid.group = min(a.grid.nbm, 4);
-    }
-    const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves;
-    if (G && tile >= T) return;
-    int bm, bn;
-    tile_at(a.grid, tile, bm, bn);
-    const int lane = threadIdx.x;
+    const int tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves, lane = threadIdx.x;
+    constexpr size_t Each = static_cast<size_t>(C::Waves) * (C::MI * C::NI * 1024);
     f32x16 acc[C::MI][C::NI];
-    add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
-                 a.grid.nsplit, acc);
     if constexpr (G) {
-        const RowPlaces place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
-        store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, 0, bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
+        const RowTiles tiles = scan_rows<C::BM>(a.rows);
+        const int all = tiles.work * a.grid.nbn;
+        int head, parts;
+        cut_tiles(all, a.w.blocks >> 2, a.grid.group, a.grid.nsplit, head, parts);
+        if (tile >= all - head) return;
+        GroupedWork w;
+        place_tile(head + tile, a.grid.nbn, w);
+        const RowPlaces place = take_group<C::BM>(a.rows, tiles, w.bm, a.w, a.M);
+        add_parts<C>(part_at<C>(a.part, 0, all - head, tile, wave, lane), Each * (all - head), parts, acc);
+        store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, 0, w.bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
     } else {
+        const int T = a.grid.nbm * a.grid.nbn;
+        int bm, bn;
+        tile_at(a.grid, tile, bm, bn);
+        add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), Each * T, a.grid.nsplit, acc);
         store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, bm * C::BM, bn * C::BN, wave, lane);
     }
 }
@@ -424,6 +450,7 @@ MxPlan mx_plan(int M, int n, int steps, bool x8) {
 // parts at 164 sizes (2 to 128 groups of 640 to 14336 by 512 to 14336, 1 to 16384
 // rows, unevenly spread) the choice is 3 % from the best on average; the plan
 // for one weight was 12 %: 4096 rows of 64 groups, 4096 x 1024, 62 instead of 47 us.
+constexpr float kWorthCutting = 12.0f;
 constexpr GroupedCost kGrouped[kTileCount][2] = {
     {{4.1f, 0.98f, 4.4f, 1.68f}, {3.4f, 0.64f, 4.4f, 1.20f}},
     {{3.3f, 0.53f, 4.9f, 0.94f}, {3.2f, 0.37f, 5.3f, 0.71f}},
@@ -432,22 +459,29 @@ constexpr GroupedCost kGrouped[kTileCount][2] = {
     {{1.7f, 0.20f, 0.4f, 0.23f}, {1.5f, 0.16f, 0.5f, 0.17f}},
     {{1.7f, 0.16f, 1.1f, 0.13f}, {1.4f, 0.15f, 1.1f, 0.12f}},
 };
+// Workgroups of a tile that the GPU holds at a time: a round.
+constexpr int grouped_room(int tile) { return tile == 0 ? kCus : 2 * kCus; }
+constexpr int kMostParts = 8, kCutSteps = 8;
 MxPlan mx_plan_grouped(int slots, int count, int n, int steps, bool x8) {
     MxPlan best;
     float least = 0.0f;
     for (int t = 0; t < kTileCount; ++t) {
         const TileCost &c = kTiles[t];
+        const GroupedCost &cost = kGrouped[t][x8 ? 0 : 1];
         const int64_t tiles = grouped_row_tiles(slots, count, c.bm) * ((n + c.bn - 1) / c.bn);
-        for (int sp : {1, 2, 3, 4, 6, 8}) {
-            if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
-            const float wgs = static_cast<float>(tiles) * sp;
-            float us = grouped_time(kGrouped[t][x8 ? 0 : 1], (steps + sp - 1) / sp, wgs / kCus, t == 0);
-            if (sp > 1) us += 2.5f + wgs * c.bm * c.bn * 8.0f * 3.7e-7f;
-            if (least == 0.0f || us < least) {
-                least = us;
-                best.tile = t;
-                best.nsplit = sp;
-            }
+        const float per_cu = static_cast<float>(tiles) / kCus;
+        // cut where a round is long against the join
+        const bool cut = steps >= kCutSteps && grouped_time(cost, steps, 0.0f) > kWorthCutting;
+        float us = grouped_time(cost, steps, t == 0 && !cut ? std::ceil(per_cu) : per_cu);
+        if (cut) {
+            const int parts = static_cast<int>(std::min<int64_t>({kMostParts, steps / 4, std::max<int64_t>(1, grouped_room(t) / tiles)}));
+            if (parts > 1) us = grouped_time(cost, (steps + parts - 1) / parts, per_cu * parts);
+            us += 3.0f;
+        }
+        if (least == 0.0f || us < least) {
+            least = us;
+            best.tile = t;
+            best.nsplit = cut ? kMostParts : 1;
         }
     }
     return best;
@@ -475,16 +509,25 @@ void launch_gemm(MxGemmArgs &a, bool join, hipStream_t s) {
     auto finish = mx_finish_kernel<C, E, G>;
     static std::atomic<uint64_t> lds_product{0};
     TileGrid &t = a.grid;
-    // (of rows in groups the number of row tiles is on the device: the grid holds the most there can be)
-    t.nbm = G ? static_cast<int>(row_tiles_bound(a.M, a.rows.count, C::BM)) : (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.n + C::BN - 1) / C::BN;
-    t.group = t.nbm < 4 ? t.nbm : 4;
+    dim3 grid, joined;
+    if constexpr (G) {
+        // (the number of row tiles is on the device: the grids hold the most there can be)
+        const int64_t rows = row_tiles_bound(a.M, a.rows.count, C::BM);
+        grid = dim3(static_cast<uint32_t>(grouped_grid(rows, t.nbn, t.group)));
+        joined = dim3(static_cast<uint32_t>(std::min<int64_t>(t.group / 2, rows * t.nbn) * C::Waves));
+    } else {
+        t.nbm = (a.M + C::BM - 1) / C::BM;
+        t.group = t.nbm < 4 ? t.nbm : 4;
+        grid = dim3(t.nbm * t.nbn * t.nsplit);
+        joined = dim3(t.nbm * t.nbn * C::Waves);
+    }
     if (join) {
-        launch_kernel(finish, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
+        launch_kernel(finish, joined, dim3(64), store_bytes<C>(), s, a);
         return;
     }
     if constexpr (C::Lds > 65536) allow_lds(product, C::Lds, lds_product);
-    launch_kernel(product, dim3(t.nbm * t.nbn * t.nsplit), dim3(C::Threads), C::Lds, s, a);
+    launch_kernel(product, grid, dim3(C::Threads), C::Lds, s, a);
 }
 
 template <int FMT, typename E, bool G, int T = 0>
@@ -503,10 +546,12 @@ size_t part_floats(const MxPlan &p, int M, int n) {
     const TileCost &c = kTiles[p.tile];
     return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((n + c.bn - 1) / c.bn * c.bn);
 }
+// (a round of parts at most)
 size_t grouped_part_floats(const MxPlan &p, int slots, int count, int n) {
     if (p.nsplit == 1) return 0;
     const TileCost &c = kTiles[p.tile];
-    return static_cast<size_t>(p.nsplit) * (row_tiles_bound(slots, count, c.bm) * c.bm) * ((n + c.bn - 1) / c.bn * c.bn);
+    const int64_t tiles = row_tiles_bound(slots, count, c.bm) * ((n + c.bn - 1) / c.bn);
+    return static_cast<size_t>(std::min<int64_t>(grouped_room(p.tile), tiles * p.nsplit)) * c.bm * c.bn;
 }
 
 int launch_either(const MxProduct &p, bool join, void *stream) {
@@ -522,7 +567,10 @@ int launch_either(const MxProduct &p, bool join, void *stream) {
     a.y = p.y;
     a.grid.nsplit = p.plan.nsplit;
     a.part = p.plan.nsplit > 1 ? p.part : nullptr;
-    if (p.rows) a.rows = *p.rows;
+    if (p.rows) {
+        a.rows = *p.rows;
+        a.grid.group = grouped_room(p.plan.tile);
+    }
     auto pick = [&](auto f) {
         constexpr int FMT = decltype(f)::value;
         if (p.rows) {
@@ -548,8 +596,11 @@ MxPlan mx_grouped_plan(int slots, int count, int n, int blocks, int x_type) {
     return mx_plan_grouped(slots, count, n, blocks / 4, x_type == DBF_TYPE_E4M3);
 }
 
-size_t mx_grouped_parts(int slots, int count, int n, int blocks, int x_type) {
-    return grouped_part_floats(mx_grouped_plan(slots, count, n, blocks, x_type), slots, count, n);
+size_t mx_grouped_parts(int slots, int count, int n, int blocks) {
+    size_t most = 0;
+    for (int t = 0; t < kTileCount && blocks / 4 >= kCutSteps; ++t)
+        most = std::max(most, grouped_part_floats({t, kMostParts}, slots, count, n));
+    return most;
 }
 
 void mx_product_tile(const MxPlan &p, int32_t *rows, int32_t *cols) {

@@ -137,27 +137,33 @@ template <typename C, typename E, GradRows ROWS, bool G>
 __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
     constexpr bool Whole = ROWS == GradRows::Whole, Dma = ROWS != GradRows::Elements;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    [[maybe_unused]] RowTiles tiles;
-    if constexpr (G) {
-        tiles = scan_rows<C::BM>(a.rows);
-        a.grid.nbm = tiles.total;
-        a.grid.group = min(a.grid.nbm, 4);
-        if (static_cast<int>(blockIdx.x) >= a.grid.nbm * a.grid.nbn * a.grid.nsplit) return;
-    }
-    const int T = a.grid.nbm * a.grid.nbn;
-    const int idx = xcd_index(blockIdx.x, T * a.grid.nsplit);
-    const int split = idx / T, tile = idx - split * T;
-    int bm, bn;
-    tile_at(a.grid, tile, bm, bn);
-    const int m0 = G ? 0 : bm * C::BM, n0 = bn * C::BN;
+    int bm, bn, split, nsplit = a.grid.nsplit, T, tile;
     [[maybe_unused]] RowPlaces place;
-    if constexpr (G) place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
+    if constexpr (G) {
+        const RowTiles tiles = scan_rows<C::BM>(a.rows);
+        const GroupedWork w = grouped_work(tiles, a.grid.nbn, (a.w.n + C::BK - 1) / C::BK, a.grid.group, nsplit, blockIdx.x);
+        if (w.bm < 0) return;
+        bm = w.bm;
+        bn = w.bn;
+        split = w.split;
+        nsplit = w.nsplit;
+        T = w.cut;
+        tile = w.at;
+        place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
+    } else {
+        T = a.grid.nbm * a.grid.nbn;
+        const int idx = xcd_index(blockIdx.x, T * nsplit);
+        split = idx / T;
+        tile = idx - split * T;
+        tile_at(a.grid, tile, bm, bn);
+    }
+    const int m0 = G ? 0 : bm * C::BM, n0 = bn * C::BN;
     const int lane = threadIdx.x & 63, l32 = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
     const int steps = (a.w.n + C::BK - 1) / C::BK;
-    const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / a.grid.nsplit);
-    const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * steps / a.grid.nsplit) - k0;
+    const int k0 = static_cast<int>(static_cast<int64_t>(split) * steps / nsplit);
+    const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * steps / nsplit) - k0;
     const uint16_t *dy = static_cast<const uint16_t *>(a.dy);
 
     // dy: chunk c of eight columns of row r sits at position c ^ (r & 7)
@@ -358,41 +364,61 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
     read_w(1);
     int s = 0;
     // (rows of no group: no step, their results are zeros)
-    for (int kt = G && place.none ? nk : 0; kt < nk; ++kt) {
-        load_frags(1, s, s, f1);
-        multiply(f0);
-        take_w();
-        put_w(s ^ 1, 0);
-        interleave();
-        load_w(s ^ 1);
-        keep_order();
-        load_frags(2, s, s, f0);
-        multiply(f1);
-        put_w(s ^ 1, 1);
-        put_w(s ^ 1, 2);
-        interleave();
-        load_frags(3, s, s, f1);
-        multiply(f0);
-        put_w(s ^ 1, 3);
-        interleave();
-        // The next step's dy and the codes behind it have landed (younger: a
-        // step's codes).  Past the barrier that holds for every wave, the next
-        // step's weight is in LDS, and this step's operands have been read.
-        wait_vm<DW>();
-        wait_lds();
-        block_barrier();
-        load_frags(0, s ^ 1, s ^ 1, f0);
-        read_w(s);
-        load_dy(s);
-        multiply(f1);
-        interleave();
-        s ^= 1;
+    const int turns = G && place.none ? 0 : nk;
+    // Waves whose rows are all past the group's last leave the products to
+    // the other wave of their SIMD and only bring their part of the operands.
+    const bool idle = G && C::Waves == 8 && wm * C::MI * 32 >= a.M;
+    if (idle) {
+        for (int kt = 0; kt < turns; ++kt) {
+            take_w();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) put_w(s ^ 1, j);
+            keep_order();
+            load_w(s ^ 1);
+            wait_vm<DW>();
+            wait_lds();
+            block_barrier();
+            read_w(s);
+            load_dy(s);
+            s ^= 1;
+        }
+    } else {
+        for (int kt = 0; kt < turns; ++kt) {
+            load_frags(1, s, s, f1);
+            multiply(f0);
+            take_w();
+            put_w(s ^ 1, 0);
+            interleave();
+            load_w(s ^ 1);
+            keep_order();
+            load_frags(2, s, s, f0);
+            multiply(f1);
+            put_w(s ^ 1, 1);
+            put_w(s ^ 1, 2);
+            interleave();
+            load_frags(3, s, s, f1);
+            multiply(f0);
+            put_w(s ^ 1, 3);
+            interleave();
+            // The next step's dy and the codes behind it have landed (younger: a
+            // step's codes).  Past the barrier that holds for every wave, the next
+            // step's weight is in LDS, and this step's operands have been read.
+            wait_vm<DW>();
+            wait_lds();
+            block_barrier();
+            load_frags(0, s ^ 1, s ^ 1, f0);
+            read_w(s);
+            load_dy(s);
+            multiply(f1);
+            interleave();
+            s ^= 1;
+        }
     }
     wait_vm<0>();  // nothing more lands in the LDS that the result goes through
     wait_lds();
     block_barrier();
 
-    if (a.part) {
+    if (G ? nsplit > 1 : a.part != nullptr) {
         store_part<C>(part_at<C>(a.part, split, T, tile, wave, lane), acc);
         return;
     }
@@ -406,26 +432,29 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
 template <typename C, typename E, bool G>
 __global__ __launch_bounds__(64) void mx_grad_finish_kernel(MxGradArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    [[maybe_unused]] RowTiles tiles;
-    if constexpr (G) {
-        tiles = scan_rows<C::BM>(a.rows);
-        a.grid.nbm = tiles.total;
-        a.grid.group = min(a.grid.nbm, 4);
-        if (static_cast<int>(blockIdx.x) >= a.grid.nbm * a.grid.nbn * C::Waves) return;
-    }
-    const int T = a.grid.nbm * a.grid.nbn, tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves;
-    int bm, bn;
-    tile_at(a.grid, tile, bm, bn);
-    const int lane = threadIdx.x;
+    const int tile = blockIdx.x / C::Waves, wave = blockIdx.x % C::Waves, lane = threadIdx.x;
+    constexpr size_t Each = static_cast<size_t>(C::Waves) * (C::MI * C::NI * 1024);
     f32x16 acc[C::MI][C::NI];
-    add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), static_cast<size_t>(T) * C::Waves * (C::MI * C::NI * 1024),
-                 a.grid.nsplit, acc);
-    [[maybe_unused]] RowPlaces place;
-    if constexpr (G) place = take_group<C::BM>(a.rows, tiles, bm, a.w, a.M);
-    scale_columns<C, E>(acc, a.w, bn * C::BN, wave % C::WN);
-    if constexpr (G)
-        store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, 0, bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
-    else store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, bm * C::BM, bn * C::BN, wave, lane);
+    if constexpr (G) {
+        const RowTiles tiles = scan_rows<C::BM>(a.rows);
+        const int all = tiles.work * a.grid.nbn;
+        int head, parts;
+        cut_tiles(all, (a.w.n + C::BK - 1) / C::BK, a.grid.group, a.grid.nsplit, head, parts);
+        if (tile >= all - head) return;
+        GroupedWork w;
+        place_tile(head + tile, a.grid.nbn, w);
+        const RowPlaces place = take_group<C::BM>(a.rows, tiles, w.bm, a.w, a.M);
+        add_parts<C>(part_at<C>(a.part, 0, all - head, tile, wave, lane), Each * (all - head), parts, acc);
+        scale_columns<C, E>(acc, a.w, w.bn * C::BN, wave % C::WN);
+        store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, 0, w.bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
+    } else {
+        const int T = a.grid.nbm * a.grid.nbn;
+        int bm, bn;
+        tile_at(a.grid, tile, bm, bn);
+        add_parts<C>(part_at<C>(a.part, 0, T, tile, wave, lane), Each * T, a.grid.nsplit, acc);
+        scale_columns<C, E>(acc, a.w, bn * C::BN, wave % C::WN);
+        store_tile<C, E>(lds, acc, a.dx, a.M, a.w.m, bm * C::BM, bn * C::BN, wave, lane);
+    }
 }
 
 // ---- choice of the tile and of the K parts
@@ -485,23 +514,30 @@ constexpr GroupedCost kGrouped[kGradCount] = {
     {3.5f, 0.56f, 2.1f, 0.56f},
     {2.8f, 0.43f, 1.1f, 0.29f},
 };
+constexpr int grouped_room(int tile) { return tile == 0 ? kCus : 2 * kCus; }
+constexpr int kMostParts = 12, kCutSteps = 8;
+constexpr float kWorthCutting = 12.0f;
 MxPlan grad_plan_grouped(int slots, int count, int n, int m) {
     MxPlan best;
     float least = 0.0f;
     const int steps = (n + 63) / 64;
     for (int t = 0; t < kGradCount; ++t) {
         const GradCost &c = kGrad[t];
+        const GroupedCost &cost = kGrouped[t];
         const int64_t tiles = grouped_row_tiles(slots, count, c.bm) * ((m + c.bn - 1) / c.bn);
-        for (int sp : {1, 2, 3, 4, 6, 8, 12}) {
-            if (sp > 1 && (steps < 4 * sp || tiles * sp > 2 * kCus)) break;
-            const float wgs = static_cast<float>(tiles) * sp;
-            float us = grouped_time(kGrouped[t], (steps + sp - 1) / sp, wgs / kCus, t == 0);
-            if (sp > 1) us += 2.5f + wgs * c.bm * c.bn * 8.0f * 3.7e-7f;
-            if (least == 0.0f || us < least) {
-                least = us;
-                best.tile = t;
-                best.nsplit = sp;
-            }
+        const float per_cu = static_cast<float>(tiles) / kCus;
+        // cut where a round is long against the join
+        const bool cut = steps >= kCutSteps && grouped_time(cost, steps, 0.0f) > kWorthCutting;
+        float us = grouped_time(cost, steps, t == 0 && !cut ? std::ceil(per_cu) : per_cu);
+        if (cut) {
+            const int parts = static_cast<int>(std::min<int64_t>({kMostParts, steps / 4, std::max<int64_t>(1, grouped_room(t) / tiles)}));
+            if (parts > 1) us = grouped_time(cost, (steps + parts - 1) / parts, per_cu * parts);
+            us += 3.0f;
+        }
+        if (least == 0.0f || us < least) {
+            least = us;
+            best.tile = t;
+            best.nsplit = cut ? kMostParts : 1;
         }
     }
     return best;
@@ -512,15 +548,23 @@ template <typename C, typename E, bool G>
 void launch_grad(MxGradArgs &a, bool join, hipStream_t s) {
     static std::atomic<uint64_t> lds0{0}, lds1{0}, lds2{0};
     TileGrid &t = a.grid;
-    t.nbm = G ? static_cast<int>(row_tiles_bound(a.M, a.rows.count, C::BM)) : (a.M + C::BM - 1) / C::BM;
     t.nbn = (a.w.m + C::BN - 1) / C::BN;
-    t.group = t.nbm < 4 ? t.nbm : 4;
+    dim3 grid, joined;
+    if constexpr (G) {
+        const int64_t rows = row_tiles_bound(a.M, a.rows.count, C::BM);
+        grid = dim3(static_cast<uint32_t>(grouped_grid(rows, t.nbn, t.group)));
+        joined = dim3(static_cast<uint32_t>(std::min<int64_t>(t.group / 2, rows * t.nbn) * C::Waves));
+    } else {
+        t.nbm = (a.M + C::BM - 1) / C::BM;
+        t.group = t.nbm < 4 ? t.nbm : 4;
+        grid = dim3(t.nbm * t.nbn * t.nsplit);
+        joined = dim3(t.nbm * t.nbn * C::Waves);
+    }
     if (join) {
         auto k = mx_grad_finish_kernel<C, E, G>;
-        launch_kernel(k, dim3(t.nbm * t.nbn * C::Waves), dim3(64), store_bytes<C>(), s, a);
+        launch_kernel(k, joined, dim3(64), store_bytes<C>(), s, a);
         return;
     }
-    const dim3 grid(t.nbm * t.nbn * t.nsplit);
     auto go = [&](auto rows, std::atomic<uint64_t> &asked) {
         auto k = mx_grad_kernel<C, E, decltype(rows)::value, G>;
         if constexpr (C::Lds > 65536) allow_lds(k, C::Lds, asked);
@@ -539,10 +583,12 @@ size_t part_floats(const MxPlan &p, int M, int m) {
     const GradCost &c = kGrad[p.tile];
     return static_cast<size_t>(p.nsplit) * ((M + c.bm - 1) / c.bm * c.bm) * ((m + c.bn - 1) / c.bn * c.bn);
 }
+// (a round of parts at most)
 size_t grouped_part_floats(const MxPlan &p, int slots, int count, int m) {
     if (p.nsplit == 1) return 0;
     const GradCost &c = kGrad[p.tile];
-    return static_cast<size_t>(p.nsplit) * (row_tiles_bound(slots, count, c.bm) * c.bm) * ((m + c.bn - 1) / c.bn * c.bn);
+    const int64_t tiles = row_tiles_bound(slots, count, c.bm) * ((m + c.bn - 1) / c.bn);
+    return static_cast<size_t>(std::min<int64_t>(grouped_room(p.tile), tiles * p.nsplit)) * c.bm * c.bn;
 }
 
 int launch_either(const MxBackward &b, bool join, void *stream) {
@@ -558,7 +604,10 @@ int launch_either(const MxBackward &b, bool join, void *stream) {
     a.dx = b.dx;
     a.grid.nsplit = b.plan.nsplit;
     a.part = b.plan.nsplit > 1 ? b.part : nullptr;
-    if (b.rows) a.rows = *b.rows;
+    if (b.rows) {
+        a.rows = *b.rows;
+        a.grid.group = grouped_room(b.plan.tile);
+    }
     auto go = [&](auto e, auto grouped) {
         using E = decltype(e);
         constexpr bool G = decltype(grouped)::value;
@@ -582,7 +631,10 @@ MxPlan mx_backward_plan(int M, int n, int m) { return grad_plan(M, n, m); }
 MxPlan mx_grouped_backward_plan(int slots, int count, int n, int m) { return grad_plan_grouped(slots, count, n, m); }
 
 size_t mx_grouped_backward_parts(int slots, int count, int n, int m) {
-    return grouped_part_floats(mx_grouped_backward_plan(slots, count, n, m), slots, count, m);
+    size_t most = 0;
+    for (int t = 0; t < kGradCount && (n + 63) / 64 >= kCutSteps; ++t)
+        most = std::max(most, grouped_part_floats({t, kMostParts}, slots, count, m));
+    return most;
 }
 
 void mx_backward_tile(const MxPlan &p, int32_t *rows, int32_t *cols) {

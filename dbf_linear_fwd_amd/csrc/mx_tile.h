@@ -67,7 +67,8 @@ __device__ __forceinline__ int xcd_index(int b, int G) {
 // Tiles of an output and how workgroups go through them.
 struct TileGrid {
     int nbm, nbn, nsplit;  // tile rows and columns, K parts
-    int group;             // tile rows that consecutive workgroups go through first
+    int group;             // tile rows that consecutive workgroups go through first; of rows in groups: a
+                           // round's workgroups (GroupedWork)
 };
 
 // Output tile of position `tile`: bands of `group` tile rows, column by
@@ -97,16 +98,18 @@ struct RowPlaces {
     }
 };
 
-// The row tiles of a product, as a wave sees them.
+// The row tiles of a product, as a wave sees them (RowTile says their order).
 struct RowTiles {
-    int total = 0;                          // those of no group included
-    int grouped = 0, upto, tiles, lo, hi;   // without a table: lane e has group e
+    int work = 0, total = 0;                  // of the groups; those of no group too
+    int large_all = 0, large, upto, small_upto, lo, hi;  // without a table: lane e has group e
 };
 template <int BM>
 __device__ __forceinline__ RowTiles scan_rows(const MxRows &a) {
     RowTiles t;
     if (a.table) {
-        t.total = a.table[0].group;
+        const RowTile r = a.table[0];
+        t.work = r.group;
+        t.total = r.first;
         return t;
     }
     const int lane = threadIdx.x & 63;
@@ -114,12 +117,15 @@ __device__ __forceinline__ RowTiles scan_rows(const MxRows &a) {
     if (lane < a.count) group_places(a.offsets, a.count, a.slots, lane, t.lo, t.hi);
     int lo, hi;
     group_places(a.offsets, a.count, a.slots, a.count, lo, hi);
-    t.tiles = (t.hi - t.lo + BM - 1) / BM;
-    t.upto = wave_scan(t.tiles, lane);
-    t.grouped = __builtin_amdgcn_readlane(t.upto, 63);
+    const int c = t.hi - t.lo, rest = c % BM;
+    t.large = c / BM + (rest > BM / 2);
+    t.upto = wave_scan(t.large, lane);
+    t.small_upto = wave_scan(rest > 0 && rest <= BM / 2, lane);
+    t.large_all = __builtin_amdgcn_readlane(t.upto, 63);
     // (never more than an order's groups make: the grid and the parts' memory are for so many)
-    t.total = __builtin_amdgcn_readfirstlane(min(t.grouped + (hi - lo + BM - 1) / BM,
-                                                 static_cast<int>(row_tiles_bound(a.slots, a.count, BM))));
+    const int most = static_cast<int>(row_tiles_bound(a.slots, a.count, BM));
+    t.work = min(t.large_all + __builtin_amdgcn_readlane(t.small_upto, 63), most);
+    t.total = __builtin_amdgcn_readfirstlane(min(t.work + (hi - lo + BM - 1) / BM, most));
     return t;
 }
 
@@ -135,15 +141,20 @@ __device__ __forceinline__ RowPlaces take_group(const MxRows &a, const RowTiles 
         M = r.rows;
     } else {
         int lo, hi, at;
-        if (bm < t.grouped) {
+        if (bm < t.large_all) {
             e = __builtin_ctzll(__ballot(t.upto > bm));
             lo = __builtin_amdgcn_readlane(t.lo, e);
             hi = __builtin_amdgcn_readlane(t.hi, e);
-            at = bm - __builtin_amdgcn_readlane(t.upto - t.tiles, e);
+            at = bm - __builtin_amdgcn_readlane(t.upto - t.large, e);
+        } else if (bm < t.work) {
+            e = __builtin_ctzll(__ballot(t.small_upto > bm - t.large_all));
+            lo = __builtin_amdgcn_readlane(t.lo, e);
+            hi = __builtin_amdgcn_readlane(t.hi, e);
+            at = (hi - lo) / BM;
         } else {
             e = a.count;
             group_places(a.offsets, a.count, a.slots, e, lo, hi);
-            at = bm - t.grouped;
+            at = bm - t.work;
         }
         p.first = __builtin_amdgcn_readfirstlane(lo + at * BM);
         M = __builtin_amdgcn_readfirstlane(min(BM, hi - (lo + at * BM)));
@@ -155,6 +166,62 @@ __device__ __forceinline__ RowPlaces take_group(const MxRows &a, const RowTiles 
     w.colmax += at * a.colmax_stride;
     return p;
 }
+
+// What workgroup b of a grouped product does.  The groups' tiles go over the
+// CUs in rounds of `room` workgroups; those of the last round that would not
+// fill it are cut into up to nsplit parts of K (4 steps at least).  An XCD
+// (b % 8) keeps to its eighth of the columns where they divide, so that its
+// part of the weights stays in its L2 for all row tiles, and every XCD has
+// the same work.  Tiles of no group come last.
+struct GroupedWork {
+    int bm = -1, bn = 0;             // bm < 0: nothing
+    int split = 0, nsplit = 1;
+    int cut = 0, at = 0;             // tiles that are cut, and the place of this one among them
+};
+__device__ __forceinline__ void place_tile(int p, int nbn, GroupedWork &w) {
+    if (nbn % 8 == 0) {
+        const int per = nbn / 8, q = p >> 3;
+        w.bm = q / per;
+        w.bn = (p & 7) * per + q - w.bm * per;
+    } else {
+        w.bm = p / nbn;
+        w.bn = p - w.bm * nbn;
+    }
+}
+// The tiles that are cut, from `head` on, and into how many parts.
+__device__ __forceinline__ void cut_tiles(int tiles, int steps, int room, int most, int &head, int &parts) {
+    head = tiles / room * room;
+    const int cut = tiles - head;
+    parts = cut > 0 ? min(min(room / cut, most), steps / 4) : 1;
+    if (parts < 2) {
+        parts = 1;
+        head = tiles;
+    }
+}
+__device__ __forceinline__ GroupedWork grouped_work(const RowTiles &t, int nbn, int steps, int room, int most, int b) {
+    GroupedWork w;
+    int head, parts;
+    const int tiles = t.work * nbn;
+    cut_tiles(tiles, steps, room, most, head, parts);
+    w.cut = tiles - head;
+    if (b < head) {
+        place_tile(b, nbn, w);
+    } else if (b < head + w.cut * parts) {
+        w.split = (b - head) / w.cut;
+        w.at = b - head - w.split * w.cut;
+        w.nsplit = parts;
+        place_tile(head + w.at, nbn, w);
+    } else {
+        const int i = b - (head + w.cut * parts);
+        if (i < (t.total - t.work) * nbn) {
+            w.bm = t.work + i / nbn;
+            w.bn = i % nbn;
+        }
+    }
+    return w;
+}
+// Workgroups of a grid for row tiles of BM, and tiles whose parts need memory.
+inline int64_t grouped_grid(int64_t row_tiles, int nbn, int room) { return row_tiles * nbn + room; }
 
 // Row tiles of `bm` places to reckon with where `count` groups share `slots`
 // rows: the sizes are on the device, so they are taken to be spread as routers
@@ -171,9 +238,7 @@ inline int64_t grouped_row_tiles(int slots, int count, int bm) {
 struct GroupedCost {
     float light0, light, full0, full;
 };
-inline float grouped_time(const GroupedCost &c, int steps, float per_cu, bool alone) {
-    // (the largest tile has a CU to itself: whole rounds, until there are many)
-    if (alone && per_cu > 1.0f && per_cu < 4.0f) per_cu = std::ceil(per_cu - 0.05f);
+inline float grouped_time(const GroupedCost &c, int steps, float per_cu) {
     return std::max(c.light0 + steps * c.light, per_cu * (c.full0 + steps * c.full));
 }
 

@@ -197,35 +197,46 @@ __global__ __launch_bounds__(kThreads) void sort_scan_kernel(int32_t *counts, in
     }
 }
 
-// The row tiles of a grouped product, those of no group last.
+// The row tiles of a grouped product, in the order that RowTile says.
 __global__ __launch_bounds__(kThreads) void row_tiles_kernel(const int32_t *offsets, int count, int slots, int tile,
                                                              RowTile *table, int bound) {
-    __shared__ int start[kMaxGroups + 1], low[kMaxGroups + 1], high[kMaxGroups + 1];
+    __shared__ int large_at[kMaxGroups + 1], small_at[kMaxGroups + 1], low[kMaxGroups + 1], high[kMaxGroups + 1];
     __shared__ int tmp[kWaves];
-    int before = 0;
+    int larges = 0, smalls = 0;
     for (int e0 = 0; e0 <= count; e0 += kThreads) {
         const int e = e0 + threadIdx.x;
         int lo = 0, hi = 0;
         if (e <= count) group_places(offsets, count, slots, e, lo, hi);
-        const int tiles = (hi - lo + tile - 1) / tile;
+        const int c = e < count ? hi - lo : 0, rest = c % tile;
         int total;
-        const int at = before + block_scan(tiles, tmp, total);
-        before += total;
+        const int l = larges + block_scan(c / tile + (rest > tile / 2), tmp, total);
+        larges += total;
+        const int s = smalls + block_scan(rest > 0 && rest <= tile / 2, tmp, total);
+        smalls += total;
         if (e <= count) {
-            start[e] = at;
+            large_at[e] = l;
+            small_at[e] = s;
             low[e] = lo;
             high[e] = hi;
         }
     }
     __syncthreads();
-    const int all = min(before, bound);
-    if (threadIdx.x == 0) table[0] = RowTile{all, 0, 0, 0};
+    const int none_lo = low[count], nones = (high[count] - none_lo + tile - 1) / tile;
+    const int work = min(larges + smalls, bound), all = min(work + nones, bound);
+    if (threadIdx.x == 0) table[0] = RowTile{work, all, 0, 0};
     for (int t = threadIdx.x; t < all; t += kThreads) {
-        int e = 0;  // the last group that starts at or before t
-        for (int step = 1024; step > 0; step >>= 1)
-            if (e + step <= count && start[e + step] <= t) e += step;
-        const int first = low[e] + (t - start[e]) * tile;
-        table[1 + t] = RowTile{e, first, min(tile, high[e] - first), 0};
+        RowTile r{count, none_lo + (t - work) * tile, 0, 0};
+        if (t < work) {
+            const bool large = t < larges;
+            const int *at = large ? large_at : small_at, i = large ? t : t - larges;
+            int e = 0;  // the last group that starts at or before i
+            for (int step = 1024; step > 0; step >>= 1)
+                if (e + step < count && at[e + step] <= i) e += step;
+            r.group = e;
+            r.first = low[e] + (large ? i - at[e] : (high[e] - low[e]) / tile) * tile;
+        }
+        r.rows = min(tile, high[r.group] - r.first);
+        table[1 + t] = r;
     }
 }
 

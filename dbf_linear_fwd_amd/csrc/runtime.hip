@@ -1102,19 +1102,6 @@ extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, voi
 // ---------------------------------------------------------------------------
 // Experts: 4-bit block weights of one size, each for the rows of one group.
 
-// Floats of K-part sums of any call of up to max_rows places.
-static size_t experts_part_floats(int32_t count, int32_t n, int32_t m, int32_t max_rows) {
-    const int32_t blocks = round_up(m, 128) / 32;
-    size_t most = 0;
-    for (int64_t slots = 1; slots <= max_rows && slots <= 65536; slots += slots < 256 ? 1 : 32) {
-        const int32_t s = static_cast<int32_t>(slots);
-        most = std::max(most, dbf::mx_grouped_backward_parts(s, count, n, m));
-        for (int32_t t : {DBF_TYPE_E4M3, DBF_TYPE_E2M1})
-            most = std::max(most, dbf::mx_grouped_parts(s, count, n, blocks, t));
-    }
-    return most;
-}
-
 extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, const void *codes, const uint8_t *scales,
                                          int32_t act_type, int32_t max_rows, hipStream_t stream, dbf_handle_t *out) {
     if (out) *out = nullptr;
@@ -1145,7 +1132,8 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     const size_t xs_bytes = static_cast<size_t>(max_rows) * blocks;
     const size_t tile_bytes =
         count <= dbf::kScanGroups ? 0 : (dbf::row_tiles_bound(max_rows, count, 32) + 1) * sizeof(dbf::RowTile);
-    const size_t parts = experts_part_floats(count, n, m, max_rows);
+    const size_t parts = std::max(dbf::mx_grouped_parts(max_rows, count, n, static_cast<int32_t>(blocks)),
+                                  dbf::mx_grouped_backward_parts(max_rows, count, n, m));
     dbf_status_t st = hipGetDevice(&h->device) == hipSuccess ? DBF_OK : DBF_ERR_HIP;
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_codes), count * each * 16);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_scales), count * each);
