@@ -424,7 +424,7 @@ __device__ __forceinline__ bool find_chunk(const OuterArgs &a, int index, RowTil
         int lo = 0, hi = 0;
         if (e0 + lane < a.count) group_places(a.offsets, a.count, a.rows, e0 + lane, lo, hi);
         const int n = (hi - lo + a.chunk - 1) / a.chunk, many = n > 1 ? n : 0;
-        const int upto = before + wave_scan(n, lane), sev = several + wave_scan(many, lane);
+        const int upto = before + wave_scan(n), sev = several + wave_scan(many);
         const uint64_t past = __ballot(upto > index);
         if (past) {
             const int at = __builtin_ctzll(past), i = index - __builtin_amdgcn_readlane(upto - n, at);
@@ -596,7 +596,7 @@ __global__ __launch_bounds__(kJoinThreads) void outer_join_kernel(const OuterArg
         int l = 0, h = 0;
         if (e0 + lane < group) group_places(a.offsets, a.count, a.rows, e0 + lane, l, h);
         const int k = (h - l + a.chunk - 1) / a.chunk;
-        first += __builtin_amdgcn_readlane(wave_scan(k > 1 ? k : 0, lane), 63);
+        first += __builtin_amdgcn_readlane(wave_scan(k > 1 ? k : 0), 63);
     }
     const size_t each = static_cast<size_t>(a.rank) * sd.cols;
     const size_t at = (static_cast<size_t>(block) * kJoinThreads + threadIdx.x) * 4;

@@ -321,7 +321,7 @@ struct MxPlan {
 constexpr int kScanGroups = 64;
 // The order of row tiles: those of more than half a tile first, group after
 // group, then the others, then those of no group.  A table's first entry holds
-// the number of the former two kinds (group) and of all (first).
+// the number of the former two kinds (group), of all (first) and of the first kind (rows).
 struct RowTile {
     int32_t group, first, rows, zero;
 };
@@ -329,6 +329,7 @@ struct MxRows {
     const int32_t *order = nullptr, *offsets = nullptr;
     const RowTile *table = nullptr;  // null: up to kScanGroups groups
     int count = 0, slots = 0, per = 0, in_rows = 0, scatter = 0;
+    int tiled = 0;  // block scales of the input by place, in 32-row tiles like a weight's (launch_mx_place_scales)
     size_t code_stride = 0, scale_stride = 0, colmax_stride = 0;  // from a group's weight to the next
 };
 // Row tiles of `tile` places that groups of `slots` places can make at most.
@@ -344,7 +345,7 @@ int launch_row_tiles(const int32_t *offsets, int count, int slots, int tile, Row
 // at least mx_product_parts() floats for the sums of K parts.  Where the plan
 // has K parts, launch_mx_product_join is the second launch.  rows (null: one
 // group of M rows): M = slots, w the first group's weight, and xscales in
-// padded rows like xcodes.
+// padded rows like xcodes, or by place (MxRows::tiled).
 struct MxProduct {
     const void *xcodes = nullptr;
     const uint8_t *xscales = nullptr;
@@ -367,6 +368,9 @@ void mx_product_tile(const MxPlan &p, int32_t *rows, int32_t *cols);
 size_t mx_product_parts(int M, int n, int blocks, int x_type);
 // Padded scale rows into 32-row tiles: round_up(M, 32) * blocks bytes.
 int launch_mx_tile_scales(const uint8_t *xs, int M, int blocks, uint8_t *out, void *stream);
+// Padded scale rows of a grouped product's input into 32-place tiles:
+// round_up(slots, 32) * blocks bytes.
+int launch_mx_place_scales(const uint8_t *xs, const MxRows &rows, int blocks, uint8_t *out, void *stream);
 int launch_mx_product(const MxProduct &p, void *stream);
 int launch_mx_product_join(const MxProduct &p, void *stream);
 // dx (M x m) = dy (M x n) w, both f16 or bf16 (type).  zeros: 16 zero bytes

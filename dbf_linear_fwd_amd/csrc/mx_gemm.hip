@@ -149,6 +149,16 @@ __global__ __launch_bounds__(256) void mx_tile_scales_kernel(const uint32_t *__r
     out[idx] = row < M ? xs[row * steps + k] : 0u;
 }
 
+// The same for rows in groups, by place.
+__global__ __launch_bounds__(256) void mx_place_scales_kernel(const uint32_t *__restrict__ xs, const MxRows rows, int steps,
+                                                              uint32_t *__restrict__ out) {
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t q = idx >> 5, t = q / steps;
+    const int64_t place = t * 32 + (idx & 31);
+    if (t * 32 >= rows.slots) return;
+    if (place < rows.slots) out[idx] = xs[RowPlaces{}.in(rows, static_cast<int>(place)) * steps + (q - t * steps)];
+}
+
 struct MxGemmArgs {
     const uint8_t *xc, *xs;  // codes in padded rows; scales in 32-row tiles
     int M;
@@ -227,8 +237,13 @@ __global__ __launch_bounds__(C::Threads) void mx_gemm_kernel(MxGemmArgs a) {
         inc4[q - C::D16] = 128;
         if constexpr (G)
             if (x) {
-                src[q] = a.xs + (static_cast<size_t>(place.in(a.rows, min(r, a.M - 1))) * steps + k0) * 4;
-                inc4[q - C::D16] = 4;
+                const int at = place.first + min(r, a.M - 1);
+                if (a.rows.tiled) {
+                    src[q] = a.xs + (static_cast<size_t>(at >> 5) * steps + k0) * 128 + (at & 31) * 4;
+                } else {
+                    src[q] = a.xs + (static_cast<size_t>(place.in(a.rows, at - place.first)) * steps + k0) * 4;
+                    inc4[q - C::D16] = 4;
+                }
             }
     }
     // load q of the stage in slot `slot`
@@ -374,7 +389,7 @@ __global__ __launch_bounds__(64) void mx_finish_kernel(MxGemmArgs a) {
         cut_tiles(all, a.w.blocks >> 2, a.grid.group, a.grid.nsplit, head, parts);
         if (tile >= all - head) return;
         GroupedWork w;
-        place_tile(head + tile, a.grid.nbn, w);
+        place_tile(head + tile, a.grid.nbn, tiles.few, w);
         const RowPlaces place = take_group<C::BM>(a.rows, tiles, w.bm, a.w, a.M);
         add_parts<C>(part_at<C>(a.part, 0, all - head, tile, wave, lane), Each * (all - head), parts, acc);
         store_tile<C, E>(lds, acc, a.y, a.M, a.w.n, 0, w.bn * C::BN, wave, lane, [&](int r) { return place.out(a.rows, r); });
@@ -617,6 +632,15 @@ int launch_mx_tile_scales(const uint8_t *xs, int M, int blocks, uint8_t *out, vo
     const int64_t threads = static_cast<int64_t>((M + 31) / 32) * 32 * steps;
     launch_kernel(mx_tile_scales_kernel, dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0,
                   static_cast<hipStream_t>(stream), reinterpret_cast<const uint32_t *>(xs), M, steps,
+                  reinterpret_cast<uint32_t *>(out));
+    return static_cast<int>(hipGetLastError());
+}
+
+int launch_mx_place_scales(const uint8_t *xs, const MxRows &rows, int blocks, uint8_t *out, void *stream) {
+    const int steps = blocks / 4;
+    const int64_t threads = static_cast<int64_t>((rows.slots + 31) / 32) * 32 * steps;
+    launch_kernel(mx_place_scales_kernel, dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0,
+                  static_cast<hipStream_t>(stream), reinterpret_cast<const uint32_t *>(xs), rows, steps,
                   reinterpret_cast<uint32_t *>(out));
     return static_cast<int>(hipGetLastError());
 }

@@ -442,7 +442,7 @@ __global__ __launch_bounds__(64) void mx_grad_finish_kernel(MxGradArgs a) {
         cut_tiles(all, (a.w.n + C::BK - 1) / C::BK, a.grid.group, a.grid.nsplit, head, parts);
         if (tile >= all - head) return;
         GroupedWork w;
-        place_tile(head + tile, a.grid.nbn, w);
+        place_tile(head + tile, a.grid.nbn, tiles.few, w);
         const RowPlaces place = take_group<C::BM>(a.rows, tiles, w.bm, a.w, a.M);
         add_parts<C>(part_at<C>(a.part, 0, all - head, tile, wave, lane), Each * (all - head), parts, acc);
         scale_columns<C, E>(acc, a.w, w.bn * C::BN, wave % C::WN);

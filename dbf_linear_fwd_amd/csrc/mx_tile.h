@@ -101,6 +101,7 @@ struct RowPlaces {
 // The row tiles of a product, as a wave sees them (RowTile says their order).
 struct RowTiles {
     int work = 0, total = 0;                  // of the groups; those of no group too
+    bool few = false;                         // no tile is more than half full
     int large_all = 0, large, upto, small_upto, lo, hi;  // without a table: lane e has group e
 };
 template <int BM>
@@ -110,6 +111,7 @@ __device__ __forceinline__ RowTiles scan_rows(const MxRows &a) {
         const RowTile r = a.table[0];
         t.work = r.group;
         t.total = r.first;
+        t.few = r.rows == 0;
         return t;
     }
     const int lane = threadIdx.x & 63;
@@ -119,9 +121,10 @@ __device__ __forceinline__ RowTiles scan_rows(const MxRows &a) {
     group_places(a.offsets, a.count, a.slots, a.count, lo, hi);
     const int c = t.hi - t.lo, rest = c % BM;
     t.large = c / BM + (rest > BM / 2);
-    t.upto = wave_scan(t.large, lane);
-    t.small_upto = wave_scan(rest > 0 && rest <= BM / 2, lane);
+    t.upto = wave_scan(t.large);
+    t.small_upto = wave_scan(rest > 0 && rest <= BM / 2);
     t.large_all = __builtin_amdgcn_readlane(t.upto, 63);
+    t.few = t.large_all == 0;
     // (never more than an order's groups make: the grid and the parts' memory are for so many)
     const int most = static_cast<int>(row_tiles_bound(a.slots, a.count, BM));
     t.work = min(t.large_all + __builtin_amdgcn_readlane(t.small_upto, 63), most);
@@ -172,14 +175,16 @@ __device__ __forceinline__ RowPlaces take_group(const MxRows &a, const RowTiles 
 // fill it are cut into up to nsplit parts of K (4 steps at least).  An XCD
 // (b % 8) keeps to its eighth of the columns where they divide, so that its
 // part of the weights stays in its L2 for all row tiles, and every XCD has
-// the same work.  Tiles of no group come last.
+// the same work; where groups have few rows, and every tile has a weight of its
+// own, neighbouring workgroups take neighbouring columns (128 rows of 64 groups,
+// 4096 x 1024: 26 instead of 28 us).  Tiles of no group come last.
 struct GroupedWork {
     int bm = -1, bn = 0;             // bm < 0: nothing
     int split = 0, nsplit = 1;
     int cut = 0, at = 0;             // tiles that are cut, and the place of this one among them
 };
-__device__ __forceinline__ void place_tile(int p, int nbn, GroupedWork &w) {
-    if (nbn % 8 == 0) {
+__device__ __forceinline__ void place_tile(int p, int nbn, bool few, GroupedWork &w) {
+    if (nbn % 8 == 0 && !few) {
         const int per = nbn / 8, q = p >> 3;
         w.bm = q / per;
         w.bn = (p & 7) * per + q - w.bm * per;
@@ -205,12 +210,12 @@ __device__ __forceinline__ GroupedWork grouped_work(const RowTiles &t, int nbn, 
     cut_tiles(tiles, steps, room, most, head, parts);
     w.cut = tiles - head;
     if (b < head) {
-        place_tile(b, nbn, w);
+        place_tile(b, nbn, t.few, w);
     } else if (b < head + w.cut * parts) {
         w.split = (b - head) / w.cut;
         w.at = b - head - w.split * w.cut;
         w.nsplit = parts;
-        place_tile(head + w.at, nbn, w);
+        place_tile(head + w.at, nbn, t.few, w);
     } else {
         const int i = b - (head + w.cut * parts);
         if (i < (t.total - t.work) * nbn) {

@@ -59,7 +59,7 @@ __device__ __forceinline__ void wave_fence() {
 // Exclusive sum over the workgroup's threads; total is everyone's.
 __device__ __forceinline__ int block_scan(int v, int *tmp, int &total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int incl = wave_scan(v, lane);
+    const int incl = wave_scan(v);
     if (lane == 63) tmp[wave] = incl;
     __syncthreads();
     int before = 0;
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(kThreads) void row_tiles_kernel(const int32_t *offs
     __syncthreads();
     const int none_lo = low[count], nones = (high[count] - none_lo + tile - 1) / tile;
     const int work = min(larges + smalls, bound), all = min(work + nones, bound);
-    if (threadIdx.x == 0) table[0] = RowTile{work, all, 0, 0};
+    if (threadIdx.x == 0) table[0] = RowTile{work, all, larges, 0};
     for (int t = threadIdx.x; t < all; t += kThreads) {
         RowTile r{count, none_lo + (t - work) * tile, 0, 0};
         if (t < work) {

@@ -14,13 +14,15 @@ __device__ __forceinline__ void group_places(const int32_t *offsets, int count, 
     hi = e < count ? min(max(offsets[e + 1], lo), slots) : slots;
 }
 
-// Sum of v over the lanes up to this one.
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int up = __shfl_up(v, o);
-        if (lane >= o) v += up;
-    }
+// Sum of v over the lanes up to this one: in rows of 16 lanes by row shifts,
+// then the rows' last lanes into the rows behind (no LDS, as a shuffle takes).
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);  // row_shr:1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, true);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, true);  // row_bcast:31 into rows 2 and 3
     return v;
 }
 
@@ -36,7 +38,7 @@ __device__ __forceinline__ bool find_row_tile(const int32_t *offsets, int count,
         int lo = 0, hi = 0;
         if (e0 + lane <= count) group_places(offsets, count, slots, e0 + lane, lo, hi);
         const int tiles = (hi - lo + tile - 1) / tile;
-        const int upto = before + wave_scan(tiles, lane);
+        const int upto = before + wave_scan(tiles);
         const uint64_t past = __ballot(upto > index);
         if (past) {
             const int at = __builtin_ctzll(past);

@@ -70,6 +70,7 @@ struct dbf_layer {
     // one after the other, and the row tiles of a call's product (more than kScanGroups)
     int32_t experts = 0;
     dbf::RowTile *row_tiles = nullptr;
+    uint8_t *place_scales = nullptr;
     size_t packed_bytes = 0, scale_bytes = 0, workspace_bytes = 0;
     // backward (dbf_pack_ex with DBF_PACK_BACKWARD): the transposed layer
     // Wᵀ = diag(b) Bᵀ diag(mid) Aᵀ diag(a), and fp32 intermediates of the
@@ -141,6 +142,7 @@ void release(dbf_layer *h) {
     (void)hipFree(h->mx_xcodes);
     (void)hipFree(h->mx_xscales);
     (void)hipFree(h->row_tiles);
+    (void)hipFree(h->place_scales);
     release(h->bwd);
     for (auto &p : h->pending) {
         (void)hipEventDestroy(p.start);
@@ -1102,6 +1104,7 @@ extern "C" dbf_status_t dbf_mx_backward_data(dbf_handle_t h, const void *dy, voi
 // ---------------------------------------------------------------------------
 // Experts: 4-bit block weights of one size, each for the rows of one group.
 
+constexpr int32_t kPlaceScales = 256;
 extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, const void *codes, const uint8_t *scales,
                                          int32_t act_type, int32_t max_rows, hipStream_t stream, dbf_handle_t *out) {
     if (out) *out = nullptr;
@@ -1129,7 +1132,8 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     const size_t blocks = static_cast<size_t>(m_pad) / 32, each = static_cast<size_t>(n_pad) * blocks;
     const size_t max_bytes = blocks + 16;  // (blocks: a multiple of 4)
     const size_t xc_bytes = static_cast<size_t>(max_rows) * dbf_mx_code_bytes(m, act_type);
-    const size_t xs_bytes = static_cast<size_t>(max_rows) * blocks;
+    const size_t xs_bytes = static_cast<size_t>(round_up(max_rows, 32)) * blocks;
+    const size_t ps_bytes = max_rows >= kPlaceScales ? xs_bytes : 0;
     const size_t tile_bytes =
         count <= dbf::kScanGroups ? 0 : (dbf::row_tiles_bound(max_rows, count, 32) + 1) * sizeof(dbf::RowTile);
     const size_t parts = std::max(dbf::mx_grouped_parts(max_rows, count, n, static_cast<int32_t>(blocks)),
@@ -1140,6 +1144,7 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_colmax), count * max_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xcodes), xc_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xscales), xs_bytes);
+    if (st == DBF_OK && ps_bytes > 0) st = dev_alloc(reinterpret_cast<void **>(&h->place_scales), ps_bytes);
     if (st == DBF_OK && tile_bytes > 0) st = dev_alloc(reinterpret_cast<void **>(&h->row_tiles), tile_bytes);
     if (st == DBF_OK && parts > 0) st = dev_alloc(reinterpret_cast<void **>(&h->split), sizeof(float) * parts);
     if (st == DBF_OK) h->split_cap = parts;
@@ -1159,7 +1164,7 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     }
     h->packed_bytes = count * each * 16;
     h->scale_bytes = count * (each + max_bytes);
-    h->workspace_bytes = xc_bytes + xs_bytes + tile_bytes + sizeof(float) * parts;
+    h->workspace_bytes = xc_bytes + xs_bytes + ps_bytes + tile_bytes + sizeof(float) * parts;
     *out = h;
     return DBF_OK;
 }
@@ -1205,12 +1210,21 @@ extern "C" dbf_status_t dbf_experts_forward(dbf_handle_t h, const void *x, int32
     if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
     if (cur != h->device) return DBF_ERR_INVALID_ARG;
     const int act = real ? h->mx_act : x_type;
+    const int blocks = h->m_pad / 32;
     if (real) {
+        // (rows by place already: their scales as the product reads them)
+        rows.tiled = gather == 0;
         st = timed_launch(h, "mx_quantize", stream, [&] {
-            return dbf::launch_mx_quantize(x, x_type, rows.in_rows, h->m, act, h->mx_xcodes, h->mx_xscales, false, stream);
+            return dbf::launch_mx_quantize(x, x_type, rows.in_rows, h->m, act, h->mx_xcodes, h->mx_xscales, rows.tiled, stream);
         });
         x = h->mx_xcodes;
         x_scales = h->mx_xscales;
+    }
+    if (st == DBF_OK && !rows.tiled && slots >= kPlaceScales) {
+        st = timed_launch(h, "mx_place_scales", stream,
+                          [&] { return dbf::launch_mx_place_scales(x_scales, rows, blocks, h->place_scales, stream); });
+        x_scales = h->place_scales;
+        rows.tiled = 1;
     }
     dbf::MxProduct p;
     p.xcodes = x;
