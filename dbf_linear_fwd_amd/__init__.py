@@ -915,11 +915,21 @@ class Adapters:
         self.A, self.B, self.scale = A, B, scale
         self.count, self.rank, self.m = A.shape
         self.n = B.shape[1]
+        self._sizes: Dict[tuple, int] = {}
 
-    def _check(self, t, width, what):
-        if (t.dtype != self.A.dtype or t.dim() != 2 or t.shape[1] != width or not t.is_contiguous()
+    def _check(self, t, rows, width, what):
+        if (t.dtype != self.A.dtype or t.dim() != 2 or t.shape != (rows, width) or not t.is_contiguous()
                 or t.device != self.A.device):
-            raise ValueError(f"{what} must be a contiguous tensor of shape (rows, {width}) in A's type on its device")
+            raise ValueError(f"{what} must be a contiguous tensor of shape ({rows}, {width}) in A's type on its device")
+
+    def _workspace(self, of, rows):
+        """Bytes that a call on so many rows needs (asked once for calls of the same size)."""
+        known = self._sizes.get((of, rows))
+        if known is None:
+            if len(self._sizes) > 256:
+                self._sizes.clear()
+            known = self._sizes[of, rows] = getattr(lib(), of)(rows, self.n, self.m, self.rank, self.count)
+        return known
 
     def _low(self, t, rows):
         import torch
@@ -930,20 +940,16 @@ class Adapters:
         """(y, t) for rows x and the layer's results base; out may be base itself (see dbf_adapter_forward in
         include/dbf.h)."""
         import torch
-        self._check(x, self.m, "x")
-        self._check(base, self.n, "base")
         rows = x.shape[0]
-        if base.shape[0] != rows:
-            raise ValueError("x and base must have the same rows")
+        self._check(x, rows, self.m, "x")
+        self._check(base, rows, self.n, "base")
         _check_groups(groups, self.count, rows, x.device)
         if out is None:
             out = torch.empty_like(base)
         else:
-            self._check(out, self.n, "out")
-            if out.shape[0] != rows:
-                raise ValueError("out must have x's rows")
+            self._check(out, rows, self.n, "out")
         t = x.new_empty((rows, self.rank), dtype=torch.float32)
-        nbytes = lib().dbf_adapter_workspace(rows, self.n, self.m, self.rank, self.count)
+        nbytes = self._workspace("dbf_adapter_workspace", rows)
         ws = x.new_empty(max(nbytes, 16), dtype=torch.uint8)
         _call("dbf_adapter_forward", x, x.data_ptr(), base.data_ptr(), self.A.data_ptr(), self.B.data_ptr(),
               None if self.scale is None else self.scale.data_ptr(), _type_of(x.dtype), groups.order.data_ptr(),
@@ -957,23 +963,19 @@ class Adapters:
         """(dx', dA, dB) at rows x with the forward's t for the upstream gradient dy: dx' = dx + scale (dy B) A with
         the layer's own input gradient dx (None: zeros); dA and dB are float32.  out (for dx') may be dx itself."""
         import torch
-        self._check(dy, self.n, "dy")
-        self._check(x, self.m, "x")
         rows = x.shape[0]
-        if dy.shape[0] != rows:
-            raise ValueError("x and dy must have the same rows")
+        self._check(dy, rows, self.n, "dy")
+        self._check(x, rows, self.m, "x")
         self._low(t, rows)
         _check_groups(groups, self.count, rows, x.device)
         for a, what in ((dx, "dx"), (out, "out")):
             if a is not None:
-                self._check(a, self.m, what)
-                if a.shape[0] != rows:
-                    raise ValueError(f"{what} must have x's rows")
+                self._check(a, rows, self.m, what)
         if out is None:
             out = torch.empty_like(x)
         dA = x.new_empty(self.A.shape, dtype=torch.float32)
         dB = x.new_empty(self.B.shape, dtype=torch.float32)
-        nbytes = lib().dbf_adapter_backward_workspace(rows, self.n, self.m, self.rank, self.count)
+        nbytes = self._workspace("dbf_adapter_backward_workspace", rows)
         ws = x.new_empty(max(nbytes, 16), dtype=torch.uint8)
         _call("dbf_adapter_backward", x, dy.data_ptr(), x.data_ptr(), t.data_ptr(),
               None if dx is None else dx.data_ptr(), self.A.data_ptr(), self.B.data_ptr(),

@@ -306,14 +306,21 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
             if (!none) {
                 const float *src = a.in + static_cast<size_t>(at) * RP + j;
                 const size_t plane = static_cast<size_t>(a.rows) * RP;
-#pragma unroll 4
-                for (int p = 0; p < a.parts; ++p, src += plane) {
-                    const f32x4 lo = reinterpret_cast<const f32x4 *>(src)[0], hi = reinterpret_cast<const f32x4 *>(src)[1];
+                // (few rows: a wait for every eight parts, the others have each other)
+                constexpr int U = MT == 1 ? 8 : 4;
+                for (int p0 = 0; p0 < a.parts; p0 += U, src += U * plane) {
+                    f32x4 q[U][2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        v[k] += lo[k];
-                        v[4 + k] += hi[k];
-                    }
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            q[u][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                            if (p0 + u < a.parts) q[u][h] = reinterpret_cast<const f32x4 *>(src + u * plane)[h];
+                        }
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] += q[u][k >> 2][k & 3];
                 }
             }
             if (a.low && block == 0) {
@@ -473,23 +480,14 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
         for (int j = 0; j < 8; ++j) {
             const int r = rowid[32 * s + 8 * g + j];
             const float *src = sd.p + static_cast<size_t>(r < 0 ? 0 : r) * a.rank + rk;
-            bool vec = false;
-            if constexpr (RT > 1) vec = VEC && a.rank % RT == 0;
 #pragma unroll
             for (int i = 0; i < RT; ++i) p[j][i] = 0.0f;
             if (r < 0) continue;
-            if (vec) {
-                if (rk < a.rank) {
-                    if constexpr (RT == 2) {
-                        const float2 v = *reinterpret_cast<const float2 *>(src);
-                        p[j][0] = v.x;
-                        p[j][1] = v.y;
-                    } else if constexpr (RT == 4) {
-                        const f32x4 v = *reinterpret_cast<const f32x4 *>(src);
+            if (RT > 1 && rk + RT <= a.rank) {
+                typedef float vec __attribute__((ext_vector_type(RT), aligned(4)));
+                const vec v = *reinterpret_cast<const vec *>(src);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) p[j][i] = v[i];
-                    }
-                }
+                for (int i = 0; i < RT; ++i) p[j][i] = v[i];
             } else {
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
@@ -545,17 +543,20 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
         }
     }
     // lane (c, g): rank c RT + j, column 8 (4 g + v) + i; the waves' sums in order
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < min(kWaves, steps); ++w) {  // (the others have no rows)
         if (wave == w) {
 #pragma unroll
             for (int j = 0; j < RT; ++j)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float &d = sums[c * RT + j][32 * g + 8 * v + i];
-                        const float x = ldexpf(acc[i][j][v], -shift);
-                        d = w == 0 ? x : d + x;
+                    for (int h = 0; h < 2; ++h) {
+                        f32x4 *d = reinterpret_cast<f32x4 *>(&sums[c * RT + j][32 * g + 8 * v + 4 * h]);
+                        f32x4 x;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = E::code == DBF_TYPE_F16 ? ldexpf(acc[4 * h + i][j][v], -shift) : acc[4 * h + i][j][v];
+                        *d = w == 0 ? x : *d + x;
                     }
         }
         __syncthreads();
@@ -627,11 +628,14 @@ int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ?
 // share the weight's operands), as many as registers and LDS allow.
 constexpr int shrink_most(int rt) { return rt == 1 ? 4 : rt <= 4 ? 2 : 1; }
 constexpr int expand_most(int rt) { return rt == 8 ? 2 : 4; }
-bool full_groups(int rows, int count) { return rows / (rows < count ? rows : count) >= 32; }
+// (and there is enough of them for every CU: rows times the width)
+bool full_groups(int rows, int count, int width) {
+    return rows / (rows < count ? rows : count) >= 32 && static_cast<int64_t>(rows) * width >= 1 << 22;
+}
 
 // K parts of a shrink: about two workgroups per CU, two steps of 32 for a wave at least.
 int shrink_parts(int rows, int count, int K, int rank) {
-    const int64_t tiles = grouped_row_tiles(rows, count, full_groups(rows, count) ? 16 * shrink_most(rank_tiles(rank)) : 16);
+    const int64_t tiles = grouped_row_tiles(rows, count, full_groups(rows, count, K) ? 16 * shrink_most(rank_tiles(rank)) : 16);
     const int64_t steps = (K + 31) / 32, want = (512 + tiles - 1) / tiles, most = std::max<int64_t>(1, steps / (2 * kWaves));
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, kMaxParts})));
 }
@@ -676,7 +680,7 @@ void launch_shrink(const ShrinkArgs &a, hipStream_t s) {
             if (vec) launch_kernel(shrink_kernel<E, LEAD, MT, RT, true>, grid, dim3(kThreads), 0, s, a);
             else launch_kernel(shrink_kernel<E, LEAD, MT, RT, false>, grid, dim3(kThreads), 0, s, a);
         };
-        if (!full_groups(a.rows, a.count)) go(Tag<1>{});
+        if (!full_groups(a.rows, a.count, a.K)) go(Tag<1>{});
         else go(Tag<Big>{});
     });
 }
@@ -696,7 +700,7 @@ void launch_expand(ExpandArgs &a, hipStream_t s) {
             if (vec) launch_kernel(expand_kernel<E, LEAD, MT, RT, true>, grid, dim3(kThreads), 0, s, a);
             else launch_kernel(expand_kernel<E, LEAD, MT, RT, false>, grid, dim3(kThreads), 0, s, a);
         };
-        if (!full_groups(a.rows, a.count)) go(Tag<1>{});
+        if (!full_groups(a.rows, a.count, a.cols)) go(Tag<1>{});
         else go(Tag<Big>{});
     });
 }

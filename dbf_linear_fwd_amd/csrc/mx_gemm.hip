@@ -461,18 +461,18 @@ MxPlan mx_plan(int M, int n, int steps, bool x8) {
     return best;
 }
 
-// The same for rows in groups, e4m3 and e2m1.  Against every tile and 1, 2 and 4
-// parts at 164 sizes (2 to 128 groups of 640 to 14336 by 512 to 14336, 1 to 16384
-// rows, unevenly spread) the choice is 3 % from the best on average; the plan
-// for one weight was 12 %: 4096 rows of 64 groups, 4096 x 1024, 62 instead of 47 us.
-constexpr float kWorthCutting = 12.0f;
+// The same for rows in groups, e4m3 and e2m1.  Against every tile, cut and not,
+// at 328 sizes (2 to 128 groups of 640 to 14336 by 512 to 14336, 1 to 16384 rows,
+// unevenly spread, both formats) the choice is 3 % from the best on average; by
+// the costs of one weight it was 12 %: 4096 rows of 64 groups, 4096 x 1024, 62
+// instead of 47 us.
 constexpr GroupedCost kGrouped[kTileCount][2] = {
-    {{4.1f, 0.98f, 4.4f, 1.68f}, {3.4f, 0.64f, 4.4f, 1.20f}},
-    {{3.3f, 0.53f, 4.9f, 0.94f}, {3.2f, 0.37f, 5.3f, 0.71f}},
-    {{2.1f, 0.32f, 0.4f, 0.55f}, {1.9f, 0.26f, 0.7f, 0.42f}},
-    {{1.8f, 0.24f, 1.0f, 0.33f}, {1.6f, 0.21f, 1.2f, 0.26f}},
-    {{1.7f, 0.20f, 0.4f, 0.23f}, {1.5f, 0.16f, 0.5f, 0.17f}},
-    {{1.7f, 0.16f, 1.1f, 0.13f}, {1.4f, 0.15f, 1.1f, 0.12f}},
+    {{5.10f, 0.52f, 3.90f, 1.40f}, {4.79f, 0.38f, 4.82f, 1.02f}},
+    {{4.75f, 0.50f, 7.12f, 0.81f}, {4.39f, 0.35f, 7.18f, 0.61f}},
+    {{3.01f, 0.29f, 1.64f, 0.45f}, {2.68f, 0.23f, 1.94f, 0.32f}},
+    {{2.38f, 0.21f, 1.94f, 0.28f}, {2.20f, 0.19f, 2.17f, 0.21f}},
+    {{2.18f, 0.17f, 0.94f, 0.19f}, {1.80f, 0.14f, 1.05f, 0.13f}},
+    {{2.18f, 0.14f, 1.61f, 0.12f}, {1.73f, 0.13f, 1.53f, 0.11f}},
 };
 // Workgroups of a tile that the GPU holds at a time: a round.
 constexpr int grouped_room(int tile) { return tile == 0 ? kCus : 2 * kCus; }
@@ -482,21 +482,16 @@ MxPlan mx_plan_grouped(int slots, int count, int n, int steps, bool x8) {
     float least = 0.0f;
     for (int t = 0; t < kTileCount; ++t) {
         const TileCost &c = kTiles[t];
-        const GroupedCost &cost = kGrouped[t][x8 ? 0 : 1];
         const int64_t tiles = grouped_row_tiles(slots, count, c.bm) * ((n + c.bn - 1) / c.bn);
-        const float per_cu = static_cast<float>(tiles) / kCus;
-        // cut where a round is long against the join
-        const bool cut = steps >= kCutSteps && grouped_time(cost, steps, 0.0f) > kWorthCutting;
-        float us = grouped_time(cost, steps, t == 0 && !cut ? std::ceil(per_cu) : per_cu);
-        if (cut) {
-            const int parts = static_cast<int>(std::min<int64_t>({kMostParts, steps / 4, std::max<int64_t>(1, grouped_room(t) / tiles)}));
-            if (parts > 1) us = grouped_time(cost, (steps + parts - 1) / parts, per_cu * parts);
-            us += 3.0f;
-        }
-        if (least == 0.0f || us < least) {
-            least = us;
-            best.tile = t;
-            best.nsplit = cut ? kMostParts : 1;
+        for (bool cut : {false, true}) {
+            if (cut && steps < kCutSteps) continue;
+            const float us = grouped_estimate(kGrouped[t][x8 ? 0 : 1], tiles, steps, grouped_room(t), t == 0, kMostParts,
+                                              c.bm, c.bn, cut);
+            if (least == 0.0f || us < least) {
+                least = us;
+                best.tile = t;
+                best.nsplit = cut ? kMostParts : 1;
+            }
         }
     }
     return best;

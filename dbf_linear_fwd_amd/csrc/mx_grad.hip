@@ -507,37 +507,30 @@ MxPlan grad_plan(int M, int n, int m) {
     return best;
 }
 
-// The same for rows in groups.  Against every tile and 1, 2 and 4 parts at 164
-// sizes the choice is 2 % from the best on average.
+// The same for rows in groups.  Against every tile, cut and not, at 164 sizes
+// the choice is 3 % from the best on average.
 constexpr GroupedCost kGrouped[kGradCount] = {
-    {6.2f, 1.20f, 6.0f, 1.69f},
-    {3.5f, 0.56f, 2.1f, 0.56f},
-    {2.8f, 0.43f, 1.1f, 0.29f},
+    {5.38f, 0.93f, 4.36f, 1.51f},
+    {3.50f, 0.56f, 2.42f, 0.54f},
+    {2.58f, 0.44f, 1.16f, 0.28f},
 };
 constexpr int grouped_room(int tile) { return tile == 0 ? kCus : 2 * kCus; }
 constexpr int kMostParts = 12, kCutSteps = 8;
-constexpr float kWorthCutting = 12.0f;
 MxPlan grad_plan_grouped(int slots, int count, int n, int m) {
     MxPlan best;
     float least = 0.0f;
     const int steps = (n + 63) / 64;
     for (int t = 0; t < kGradCount; ++t) {
         const GradCost &c = kGrad[t];
-        const GroupedCost &cost = kGrouped[t];
         const int64_t tiles = grouped_row_tiles(slots, count, c.bm) * ((m + c.bn - 1) / c.bn);
-        const float per_cu = static_cast<float>(tiles) / kCus;
-        // cut where a round is long against the join
-        const bool cut = steps >= kCutSteps && grouped_time(cost, steps, 0.0f) > kWorthCutting;
-        float us = grouped_time(cost, steps, t == 0 && !cut ? std::ceil(per_cu) : per_cu);
-        if (cut) {
-            const int parts = static_cast<int>(std::min<int64_t>({kMostParts, steps / 4, std::max<int64_t>(1, grouped_room(t) / tiles)}));
-            if (parts > 1) us = grouped_time(cost, (steps + parts - 1) / parts, per_cu * parts);
-            us += 3.0f;
-        }
-        if (least == 0.0f || us < least) {
-            least = us;
-            best.tile = t;
-            best.nsplit = cut ? kMostParts : 1;
+        for (bool cut : {false, true}) {
+            if (cut && steps < kCutSteps) continue;
+            const float us = grouped_estimate(kGrouped[t], tiles, steps, grouped_room(t), t == 0, kMostParts, c.bm, c.bn, cut);
+            if (least == 0.0f || us < least) {
+                least = us;
+                best.tile = t;
+                best.nsplit = cut ? kMostParts : 1;
+            }
         }
     }
     return best;

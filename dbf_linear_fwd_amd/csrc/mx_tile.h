@@ -242,9 +242,22 @@ inline int64_t grouped_row_tiles(int slots, int count, int bm) {
 // rows of its own, and many starts overlap on a CU.
 struct GroupedCost {
     float light0, light, full0, full;
+    float time(int steps, float per_cu) const { return std::max(light0 + steps * light, per_cu * (full0 + steps * full)); }
 };
-inline float grouped_time(const GroupedCost &c, int steps, float per_cu) {
-    return std::max(c.light0 + steps * c.light, per_cu * (c.full0 + steps * c.full));
+// Estimated time of `tiles` tiles of bm x bn, `room` to a round (alone: one to
+// a CU), with or without the last round's cut into up to `most` parts; a join
+// costs its launch and the traffic of the parts.
+inline float grouped_estimate(const GroupedCost &c, int64_t tiles, int steps, int room, bool alone, int most, int bm, int bn,
+                              bool cut) {
+    constexpr float kCus = 256.0f;
+    const int64_t head = tiles / room * room, rest = tiles - head;
+    const int parts = rest > 0 ? static_cast<int>(std::min<int64_t>({most, steps / 4, room / rest})) : 1;
+    if (!cut || parts < 2) {
+        const float per_cu = tiles / kCus;
+        return c.time(steps, alone && per_cu < 8.0f ? std::ceil(per_cu) : per_cu) + (cut ? 3.0f : 0.0f);
+    }
+    return head / kCus * (c.full0 + steps * c.full) + c.time((steps + parts - 1) / parts, rest * parts / kCus) + 3.0f +
+           static_cast<float>(rest * parts) * bm * bn * 8.0f * 2e-7f;
 }
 
 // A wave's results to y.  A 32 x 32 result has one row of y per lane, its

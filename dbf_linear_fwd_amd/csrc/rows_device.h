@@ -10,8 +10,9 @@ namespace dbf {
 
 // Places [lo, hi) of group e (e = count: of no group), whatever stands in offsets.
 __device__ __forceinline__ void group_places(const int32_t *offsets, int count, int slots, int e, int &lo, int &hi) {
-    lo = min(max(offsets[e], 0), slots);
-    hi = e < count ? min(max(offsets[e + 1], lo), slots) : slots;
+    const int first = offsets[e], next = offsets[min(e + 1, count)];  // (two loads at once)
+    lo = min(max(first, 0), slots);
+    hi = e < count ? min(max(next, lo), slots) : slots;
 }
 
 // Sum of v over the lanes up to this one: in rows of 16 lanes by row shifts,
