@@ -973,6 +973,8 @@ class Adapters:
                 self._check(a, rows, self.m, what)
         if out is None:
             out = torch.empty_like(x)
+        elif out is x or out is dy:
+            raise ValueError("out must not be x or dy")
         dA = x.new_empty(self.A.shape, dtype=torch.float32)
         dB = x.new_empty(self.B.shape, dtype=torch.float32)
         nbytes = self._workspace("dbf_adapter_backward_workspace", rows)

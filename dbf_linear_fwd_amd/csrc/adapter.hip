@@ -736,9 +736,9 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 dbf_status_t check_sizes(int32_t type, int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count) {
     if (rows < 0 || n < 1 || m < 1 || rank < 1 || count < 1) return DBF_ERR_INVALID_ARG;
     if (type != DBF_TYPE_F16 && type != DBF_TYPE_BF16) return DBF_ERR_INVALID_ARG;
-    // (the last: threads of the gradients' join)
+    // (a launch holds less than 2^32 threads)
     const int64_t wide = std::max(n, m);
-    if (rank > kMaxRank || count > kMaxGroups || wide > (1 << 20) || rows > (1 << 24) || rows * wide > int64_t(1) << 40 ||
+    if (rank > kMaxRank || count > kMaxGroups || wide > (1 << 18) || rows > (1 << 24) || rows * wide > int64_t(1) << 36 ||
         int64_t(count) * rank * wide > int64_t(1) << 32)
         return DBF_ERR_SHAPE;
     return DBF_OK;
@@ -815,6 +815,7 @@ extern "C" dbf_status_t dbf_adapter_backward(const void *dy, const void *x, cons
     if (!aligned(dA, 16) || !aligned(dB, 16) || !aligned(offsets, 4) || !offsets) return DBF_ERR_INVALID_ARG;
     if (rows > 0) {
         if (!dy || !B || !order || !workspace || (dB && !t) || (dA && !x) || (dx_out && !A)) return DBF_ERR_INVALID_ARG;
+        if (dx_out && (dx_out == dy || dx_out == x)) return DBF_ERR_INVALID_ARG;  // (read after it is written)
         for (const void *p : {dy, x, dx, A, B, static_cast<const void *>(dx_out), static_cast<const void *>(workspace)})
             if (!aligned(p, 16)) return DBF_ERR_INVALID_ARG;
         if (!aligned(order, 4) || !aligned(scale, 4) || !aligned(t, 16) ||

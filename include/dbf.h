@@ -559,7 +559,7 @@ dbf_status_t dbf_group_rows(const void *index, int32_t index_bits, int32_t rows,
  * places (slots) of a call.  The handle takes dbf_experts_forward,
  * dbf_experts_backward_data, dbf_get_info (n, m of one weight), timing and
  * dbf_free; the other entry points return DBF_ERR_UNSUPPORTED.
- * count <= 1024, max_rows <= 2^24 (DBF_ERR_SHAPE above).
+ * count <= 1024, n, m <= 2^20, max_rows <= 2^24 (DBF_ERR_SHAPE above).
  *
  * dbf_experts_forward -- for each place s < slots, of group e,
  *   y[out(s)][o] = rne( Σ_l xq[in(s)][l] W_e[o][l] ).
@@ -572,8 +572,9 @@ dbf_status_t dbf_group_rows(const void *index, int32_t index_bits, int32_t rows,
  *            written: those of rows of no group with zeros.
  *   order    may be NULL where gather and scatter are 0.
  * Rows are quantised once, however many experts they go to.  A row's result
- * has the numerics of dbf_mx_forward; how its sum is cut into parts depends on
- * slots, count, n and m, not on how the rows are spread over the groups.  y
+ * has the numerics of dbf_mx_forward; into how many parts its sum is cut depends
+ * on the groups' sizes (so its last bits may differ between batches, as those
+ * of a layer do between batch sizes; equal calls give equal bits).  y
  * overlaps nothing.  Calls on one handle must be ordered.
  *
  * dbf_experts_backward_data -- dx[out(s)][l] = rne( Σ_o dy[in(s)][o] W_e[o][l] ),
@@ -604,7 +605,7 @@ dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy, int32_t t
  * Sums are fp32; t enters the second product in two 16-bit parts (f16: 22 bits
  * of the row's largest, bf16: 16 bits of each), a rounding of 2^-17 of t at most where
  * y's own is 2^-9 (2^-22 and 2^-12).  Sums are in a fixed order (no atomics).
- * 1 <= rank <= 128, count <= 1024, n, m <= 2^20, rows <= 2^24, rows * max(n, m) <= 2^40,
+ * 1 <= rank <= 128, count <= 1024, n, m <= 2^18, rows <= 2^24, rows * max(n, m) <= 2^36,
  * count * rank * max(n, m) <= 2^32 (DBF_ERR_SHAPE above).
  * Pointers 16-byte aligned (order, offsets, scale: 4).  rows = 0 returns
  * DBF_OK without launching.  The current HIP device must hold the buffers.
@@ -615,7 +616,8 @@ dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy, int32_t t
  *               NULL: 0; rows of no group: dx[r]),
  *   dA_a = Σ_r u[r] x[r]ᵀ,  dB_a = scale_a Σ_r dy[r] t[r]ᵀ   over the rows of group a
  *               (fp32, of A's and B's shapes; zeros for a group without rows).
- * dx_out, dA or dB may be NULL (not computed); dx_out may be dx itself.  t as the
+ * dx_out, dA or dB may be NULL (not computed); dx_out may be dx itself (not x
+ * or dy: DBF_ERR_INVALID_ARG).  t as the
  * forward gave it (needed for dB), x needed for dA.  u and t enter the
  * gradients' products in three bf16 parts (24 bits), or in two f16 parts
  * (22 bits of the group's largest).  Sums are in a fixed order.  rows = 0 writes

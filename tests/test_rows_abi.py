@@ -51,7 +51,7 @@ def test_experts_refusals():
     assert f(out=None) == E and f(codes=None) == E and f(scales=None) == E and f(codes=ODD) == E and f(scales=ODD) == E
     for bad in ({"count": 0}, {"n": 0}, {"m": -1}, {"rows": 0}, {"act": F16}):
         assert f(**bad) == E
-    for big in ({"count": 1025}, {"n": (1 << 30) + 1}, {"m": (1 << 30) + 1}, {"rows": (1 << 24) + 1},
+    for big in ({"count": 1025}, {"n": (1 << 20) + 1}, {"m": (1 << 20) + 1}, {"rows": (1 << 24) + 1},
                 {"n": 1 << 20, "m": 1 << 20}, {"m": 1 << 20, "rows": 1 << 20}, {"n": 1 << 20, "rows": 1 << 20}):
         assert f(**big) == SHAPE
     assert h.value is None
@@ -69,8 +69,9 @@ def _adapter(**k):
 
 
 def _adapter_back(**k):
-    a = dict(dy=P, x=P, t=P, dx=P, A=P, B=P, scale=P, type=F16, order=P, offsets=P, rows=5, n=8, m=16, rank=4, count=2,
-             out=P, dA=P, dB=P, ws=P, nbytes=BIG)
+    Q = ctypes.c_void_p(16384)
+    a = dict(dy=P, x=P, t=P, dx=Q, A=P, B=P, scale=P, type=F16, order=P, offsets=P, rows=5, n=8, m=16, rank=4, count=2,
+             out=Q, dA=P, dB=P, ws=P, nbytes=BIG)
     a.update(k)
     return dbf.lib().dbf_adapter_backward(a["dy"], a["x"], a["t"], a["dx"], a["A"], a["B"], a["scale"], a["type"],
                                           a["order"], a["offsets"], a["rows"], a["n"], a["m"], a["rank"], a["count"],
@@ -78,9 +79,9 @@ def _adapter_back(**k):
 
 
 SIZES = [({"rows": -1}, E), ({"n": 0}, E), ({"m": 0}, E), ({"rank": 0}, E), ({"count": 0}, E), ({"type": F32}, E),
-         ({"type": E4M3}, E), ({"rank": 129}, SHAPE), ({"count": 1025}, SHAPE), ({"n": (1 << 20) + 1}, SHAPE),
-         ({"m": (1 << 20) + 1}, SHAPE), ({"rows": (1 << 24) + 1}, SHAPE),
-         ({"rows": 1 << 24, "n": 1 << 17}, SHAPE), ({"count": 1024, "rank": 128, "m": 1 << 16}, SHAPE)]
+         ({"type": E4M3}, E), ({"rank": 129}, SHAPE), ({"count": 1025}, SHAPE), ({"n": (1 << 18) + 1}, SHAPE),
+         ({"m": (1 << 18) + 1}, SHAPE), ({"rows": (1 << 24) + 1}, SHAPE),
+         ({"rows": 1 << 24, "n": 1 << 13}, SHAPE), ({"count": 1024, "rank": 128, "m": 1 << 16}, SHAPE)]
 
 
 @pytest.mark.parametrize("bad,status", SIZES)
@@ -109,6 +110,8 @@ def test_adapter_backward_refusals():
     need = L.dbf_adapter_backward_workspace(5, 8, 16, 4, 2)
     assert need > 0 and _adapter_back(nbytes=need - 1) == E
     assert _adapter_back(out=None, dA=None, dB=None) == OK  # nothing to compute
+    other = ctypes.c_void_p(8192)
+    assert _adapter_back(x=other, out=other) == E and _adapter_back(dy=other, out=other) == E
     assert _adapter_back(rows=0, dA=None, dB=None) == OK
     assert L.dbf_adapter_backward_workspace(0, 8, 16, 4, 2) == 0
 
