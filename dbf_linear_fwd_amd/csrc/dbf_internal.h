@@ -384,7 +384,11 @@ struct MxBackward {
     size_t part_cap = 0;
     MxPlan plan;
     const MxRows *rows = nullptr;  // as in MxProduct
+    int ld = 0;                    // of rows in groups: elements from a row of dy to the next
 };
+// Rows of n elements, in a product's places, to rows of ld elements (a multiple
+// of eight; zeros behind the n) in the grouped order.
+int launch_mx_pad_rows(const void *x, const MxRows &rows, int n, int ld, void *out, void *stream);
 MxPlan mx_backward_plan(int M, int n, int m);
 MxPlan mx_grouped_backward_plan(int slots, int count, int n, int m);
 size_t mx_grouped_backward_parts(int slots, int count, int n, int m);

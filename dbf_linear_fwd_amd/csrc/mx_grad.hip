@@ -61,7 +61,28 @@ struct MxGradArgs {
     TileGrid grid;
     float *part;
     MxRows rows;  // grouped products
+    int ld;       // their dy's row stride
 };
+
+// One lane per eight elements of an output row.
+__global__ __launch_bounds__(256) void mx_pad_rows_kernel(const uint16_t *x, const MxRows rows, int n, int ld, uint16_t *out) {
+    typedef u32v4 u32v4_any __attribute__((aligned(2)));
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int per = ld / 8;
+    const int64_t place = idx / per;
+    if (place >= rows.slots) return;
+    const int col = static_cast<int>(idx - place * per) * 8;
+    const uint16_t *src = x + static_cast<size_t>(RowPlaces{}.in(rows, static_cast<int>(place))) * n + col;
+    u32v4 v = {0u, 0u, 0u, 0u};
+    if (col + 8 <= n) {
+        v = *reinterpret_cast<const u32v4_any *>(src);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < n) v[i >> 1] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+    }
+    *reinterpret_cast<u32v4 *>(out + static_cast<size_t>(place) * ld + col) = v;
+}
 
 // The factor of a block's codes: 2^(s - smax + kShift).
 template <typename E>
@@ -177,7 +198,7 @@ __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
         col[q] = k0 * C::BK + at;
         if constexpr (G) {
             // Whole: the row's first step, the others by their number
-            src[q] = dy + static_cast<size_t>(place.in(a.rows, row)) * a.w.n + (Whole ? at : col[q]);
+            src[q] = dy + static_cast<size_t>(place.in(a.rows, row)) * a.ld + (Whole ? at : col[q]);
         } else {
             src[q] = dy + static_cast<size_t>(row) * a.w.n + col[q];
             off[q] = (static_cast<uint32_t>(row - m0) * a.w.n + at) * 2;
@@ -566,8 +587,8 @@ void launch_grad(MxGradArgs &a, bool join, hipStream_t s) {
     // (offsets inside a tile are 32 bits)
     if (a.w.n % C::BK == 0 && a.w.n <= 1 << 22 && a.w.blocks <= 1 << 22)
         go(std::integral_constant<GradRows, GradRows::Whole>{}, lds0);
-    else if (a.w.n % 8 == 0) go(std::integral_constant<GradRows, GradRows::Rows16>{}, lds1);
-    else go(std::integral_constant<GradRows, GradRows::Elements>{}, lds2);
+    else if (G || a.w.n % 8 == 0) go(std::integral_constant<GradRows, GradRows::Rows16>{}, lds1);  // (G: padded rows)
+    else if constexpr (!G) go(std::integral_constant<GradRows, GradRows::Elements>{}, lds2);
 }
 
 // Floats of the sums of a plan's K parts.
@@ -586,6 +607,7 @@ size_t grouped_part_floats(const MxPlan &p, int slots, int count, int m) {
 
 int launch_either(const MxBackward &b, bool join, void *stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (b.rows && b.ld % 8 != 0) return static_cast<int>(hipErrorInvalidValue);
     if (b.plan.nsplit > 1 && (!b.part || b.part_cap < (b.rows ? grouped_part_floats(b.plan, b.M, b.rows->count, b.w.m)
                                                               : part_floats(b.plan, b.M, b.w.m))))
         return static_cast<int>(hipErrorInvalidValue);
@@ -599,6 +621,7 @@ int launch_either(const MxBackward &b, bool join, void *stream) {
     a.part = b.plan.nsplit > 1 ? b.part : nullptr;
     if (b.rows) {
         a.rows = *b.rows;
+        a.ld = b.ld;
         a.grid.group = grouped_room(b.plan.tile);
     }
     auto go = [&](auto e, auto grouped) {
@@ -636,6 +659,14 @@ void mx_backward_tile(const MxPlan &p, int32_t *rows, int32_t *cols) {
 }
 
 size_t mx_backward_parts(int M, int n, int m) { return part_floats(mx_backward_plan(M, n, m), M, m); }
+
+int launch_mx_pad_rows(const void *x, const MxRows &rows, int n, int ld, void *out, void *stream) {
+    const int64_t threads = static_cast<int64_t>(rows.slots) * (ld / 8);
+    launch_kernel(mx_pad_rows_kernel, dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0,
+                  static_cast<hipStream_t>(stream), static_cast<const uint16_t *>(x), rows, n, ld,
+                  static_cast<uint16_t *>(out));
+    return static_cast<int>(hipGetLastError());
+}
 
 int launch_mx_backward(const MxBackward &b, void *stream) { return launch_either(b, false, stream); }
 

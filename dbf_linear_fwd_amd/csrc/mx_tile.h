@@ -292,26 +292,24 @@ __device__ __forceinline__ void store_tile(char *mine, const f32x16 (&acc)[C::MI
                 }
                 *reinterpret_cast<u32v2 *>(mine + l32 * Pitch + (f * 32 + 8 * q + 4 * g) * 2) = u32v2{p[0], p[1]};
             }
-        if (n % 8 == 0) {
-            constexpr int Per = Cols / 8, Rows = 64 / Per;  // lanes per row, rows per store
-            const int c = lane % Per * 8;
+        // (rows of any alignment: the memory takes unaligned stores; two bytes
+        // at a time, 5376 rows of ten groups, 5518 x 64, 98 us)
+        typedef u32v4 u32v4_any __attribute__((aligned(2)));
+        constexpr int Per = Cols / 8, Rows = 64 / Per;  // lanes per row, rows per store
+        const int c = lane % Per * 8;
 #pragma unroll
-            for (int j = 0; j < 32; j += Rows) {
-                const int r = j + lane / Per;
-                const u32v4 v = *reinterpret_cast<const u32v4 *>(mine + r * Pitch + c * 2);
-                if (r0 + r < M && c0 + c < n) {
-                    const int64_t at = row_of(r0 + r);
-                    if (at >= 0) *reinterpret_cast<u32v4 *>(y + static_cast<size_t>(at) * n + c0 + c) = v;
-                }
-            }
-        } else {
-            for (int j = lane; j < 32 * Cols; j += 64) {
-                const int r = j / Cols, c = j % Cols;
-                if (r0 + r < M && c0 + c < n) {
-                    const int64_t at = row_of(r0 + r);
-                    if (at >= 0)
-                        y[static_cast<size_t>(at) * n + c0 + c] =
-                            *reinterpret_cast<const uint16_t *>(mine + r * Pitch + c * 2);
+        for (int j = 0; j < 32; j += Rows) {
+            const int r = j + lane / Per;
+            const u32v4 v = *reinterpret_cast<const u32v4 *>(mine + r * Pitch + c * 2);
+            if (r0 + r < M && c0 + c < n) {
+                const int64_t at = row_of(r0 + r);
+                if (at < 0) continue;
+                uint16_t *dst = y + static_cast<size_t>(at) * n + c0 + c;
+                if (c0 + c + 8 <= n) {
+                    *reinterpret_cast<u32v4_any *>(dst) = v;
+                } else {
+                    for (int k = 0; k < n - c0 - c; ++k)
+                        dst[k] = *reinterpret_cast<const uint16_t *>(mine + r * Pitch + (c + k) * 2);
                 }
             }
         }

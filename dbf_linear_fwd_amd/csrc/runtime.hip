@@ -71,6 +71,7 @@ struct dbf_layer {
     int32_t experts = 0;
     dbf::RowTile *row_tiles = nullptr;
     uint8_t *place_scales = nullptr;
+    uint16_t *padded = nullptr;  // n not a multiple of eight: rows of a gradient, padded
     size_t packed_bytes = 0, scale_bytes = 0, workspace_bytes = 0;
     // backward (dbf_pack_ex with DBF_PACK_BACKWARD): the transposed layer
     // Wᵀ = diag(b) Bᵀ diag(mid) Aᵀ diag(a), and fp32 intermediates of the
@@ -143,6 +144,7 @@ void release(dbf_layer *h) {
     (void)hipFree(h->mx_xscales);
     (void)hipFree(h->row_tiles);
     (void)hipFree(h->place_scales);
+    (void)hipFree(h->padded);
     release(h->bwd);
     for (auto &p : h->pending) {
         (void)hipEventDestroy(p.start);
@@ -1140,6 +1142,7 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     const size_t xc_bytes = static_cast<size_t>(max_rows) * dbf_mx_code_bytes(m, act_type);
     const size_t xs_bytes = static_cast<size_t>(round_up(max_rows, 32)) * blocks;
     const size_t ps_bytes = place_scales_pay(max_rows, n, m, DBF_TYPE_E2M1) ? xs_bytes : 0;
+    const size_t pad_bytes = n % 8 == 0 ? 0 : static_cast<size_t>(max_rows) * round_up(n, 8) * sizeof(uint16_t);
     const size_t tile_bytes =
         count <= dbf::kScanGroups ? 0 : (dbf::row_tiles_bound(max_rows, count, 32) + 1) * sizeof(dbf::RowTile);
     const size_t parts = std::max(dbf::mx_grouped_parts(max_rows, count, n, static_cast<int32_t>(blocks)),
@@ -1151,6 +1154,7 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xcodes), xc_bytes);
     if (st == DBF_OK) st = dev_alloc(reinterpret_cast<void **>(&h->mx_xscales), xs_bytes);
     if (st == DBF_OK && ps_bytes > 0) st = dev_alloc(reinterpret_cast<void **>(&h->place_scales), ps_bytes);
+    if (st == DBF_OK && pad_bytes > 0) st = dev_alloc(reinterpret_cast<void **>(&h->padded), pad_bytes);
     if (st == DBF_OK && tile_bytes > 0) st = dev_alloc(reinterpret_cast<void **>(&h->row_tiles), tile_bytes);
     if (st == DBF_OK && parts > 0) st = dev_alloc(reinterpret_cast<void **>(&h->split), sizeof(float) * parts);
     if (st == DBF_OK) h->split_cap = parts;
@@ -1170,7 +1174,7 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     }
     h->packed_bytes = count * each * 16;
     h->scale_bytes = count * (each + max_bytes);
-    h->workspace_bytes = xc_bytes + xs_bytes + ps_bytes + tile_bytes + sizeof(float) * parts;
+    h->workspace_bytes = xc_bytes + xs_bytes + ps_bytes + pad_bytes + tile_bytes + sizeof(float) * parts;
     *out = h;
     return DBF_OK;
 }
@@ -1280,6 +1284,18 @@ extern "C" dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy
     b.part = h->split;
     b.part_cap = h->split_cap;
     b.plan = dbf::mx_grouped_backward_plan(slots, h->experts, h->n, h->m);
+    b.ld = h->n;
+    if (h->padded) {
+        // Rows of odd sizes through registers, two bytes at a time, take several
+        // times the product: 1920 rows of 12 groups, 6733 x 3648, 512 us.
+        b.ld = round_up(h->n, 8);
+        st = timed_launch(h, "mx_pad_rows", stream,
+                          [&] { return dbf::launch_mx_pad_rows(dy, rows, h->n, b.ld, h->padded, stream); });
+        if (st != DBF_OK) return st;
+        b.dy = h->padded;
+        rows.per = 0;  // (in the grouped order now)
+        rows.in_rows = slots;
+    }
     b.rows = &rows;
     int32_t bm = 0, bn = 0;
     dbf::mx_backward_tile(b.plan, &bm, &bn);
