@@ -423,10 +423,12 @@ struct OuterArgs {
 };
 
 // Chunk `index` of the groups' chunks; slot: its place among the chunks of
-// groups that have several, -1 for the only one of a group.
+// groups that have several, -1 for the only one of a group.  Behind the last
+// chunk the groups without rows, in order (rows = 0).
 __device__ __forceinline__ bool find_chunk(const OuterArgs &a, int index, RowTile &out, int &slot) {
     const int lane = threadIdx.x & 63;
     int before = 0, several = 0;
+    slot = -1;
     for (int e0 = 0; e0 < a.count; e0 += 64) {
         int lo = 0, hi = 0;
         if (e0 + lane < a.count) group_places(a.offsets, a.count, a.rows, e0 + lane, lo, hi);
@@ -444,10 +446,23 @@ __device__ __forceinline__ bool find_chunk(const OuterArgs &a, int index, RowTil
         before = __builtin_amdgcn_readlane(upto, 63);
         several = __builtin_amdgcn_readlane(sev, 63);
     }
+    for (int e0 = 0; e0 < a.count; e0 += 64) {
+        int lo = 0, hi = 1;
+        if (e0 + lane < a.count) group_places(a.offsets, a.count, a.rows, e0 + lane, lo, hi);
+        const int upto = before + wave_scan(lo == hi);
+        const uint64_t past = __ballot(upto > index);
+        if (past) {
+            out.group = e0 + __builtin_ctzll(past);
+            out.first = out.rows = 0;
+            return true;
+        }
+        before = __builtin_amdgcn_readlane(upto, 63);
+    }
     return false;
 }
 
 constexpr int kMaxChunk = 2048;
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 // A chunk's rows x 128 columns x 16 RT ranks per workgroup; the waves take 32
 // rows in turn.
@@ -458,20 +473,56 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
     __shared__ __attribute__((aligned(16))) float sums[RP][Pitch];
     __shared__ __attribute__((aligned(16))) int rowid[kMaxChunk];
     const int strips = a.side[0].strips + a.side[1].strips;
-    const int chunk = blockIdx.x / strips, st = blockIdx.x % strips;
+    // (the rank blocks of a strip are neighbours on one XCD, whose L2 has its rows)
+    const int rank_blocks = (a.rank + RP - 1) / RP, at = blockIdx.x % (8 * rank_blocks);
+    const int work = blockIdx.x / (8 * rank_blocks) * 8 + at % 8;
+    const int chunk = work / strips, st = work % strips;
     const bool second = st >= a.side[0].strips;
     const OuterSide &sd = a.side[second ? 1 : 0];
-    const int strip = second ? st - a.side[0].strips : st, jb = blockIdx.y * RP;
+    const int strip = second ? st - a.side[0].strips : st, jb = at / 8 * RP;
     RowTile rt;
     int slot;
     if (!find_chunk(a, chunk, rt, slot)) return;
     if (slot >= a.most) return;  // (offsets that are not of an order)
+    const size_t each = static_cast<size_t>(a.rank) * sd.cols;
+    const int col0 = strip * Cols, nr = min(RP, a.rank - jb), nc = min(Cols, sd.cols - col0);
+    float *out = slot < 0 ? sd.out + static_cast<size_t>(rt.group) * each : sd.part + static_cast<size_t>(slot) * each;
+    // four neighbours of the result to memory, the first `valid` of them
+    auto store4 = [](float *to, f32x4 v, int valid) {
+        if (valid >= 4) {
+            *reinterpret_cast<f32x4_any *>(to) = v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (k < valid) to[k] = v[k];
+        }
+    };
+    // get(rank, column, along) of the workgroup's block, four neighbours at a time
+    auto store_all = [&](auto get) {
+        if (sd.along) {
+            constexpr int Per = RP / 4;
+            for (int i = threadIdx.x; i < Cols * Per; i += kThreads) {
+                const int x = i / Per, j = i % Per * 4;
+                if (x < nc) store4(out + static_cast<size_t>(col0 + x) * a.rank + jb + j, get(j, x, true), nr - j);
+            }
+        } else {
+            constexpr int Per = Cols / 4;
+            for (int i = threadIdx.x; i < RP * Per; i += kThreads) {
+                const int j = i / Per, x = i % Per * 4;
+                if (j < nr) store4(out + static_cast<size_t>(jb + j) * sd.cols + col0 + x, get(j, x, false), nc - x);
+            }
+        }
+    };
+    if (rt.rows == 0) {
+        store_all([](int, int, bool) { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; });
+        return;
+    }
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int i = threadIdx.x; i < (rt.rows + 31) / 32 * 32; i += kThreads)
         rowid[i] = i < rt.rows ? min(max(a.order[rt.first + i], 0), a.rows - 1) : -1;
     __syncthreads();
-    const int steps = (rt.rows + 31) / 32, col0 = strip * Cols, col = col0 + 8 * c;
+    const int steps = (rt.rows + 31) / 32, col = col0 + 8 * c;
     const int rk = jb + c * RT;  // this lane's first rank
 
     // p of eight rows: ranks rk .. rk + RT - 1
@@ -562,26 +613,16 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
         __syncthreads();
     }
     const float scale = sd.scale ? sd.scale[rt.group] : 1.0f;
-    const size_t each = static_cast<size_t>(a.rank) * sd.cols;
-    float *out = slot < 0 ? sd.out + static_cast<size_t>(rt.group) * each : sd.part + static_cast<size_t>(slot) * each;
-    const int nr = min(RP, a.rank - jb), nc = min(Cols, sd.cols - col0);
-    if (sd.along) {
-        for (int i = threadIdx.x; i < nr * nc; i += kThreads) {
-            const int x = i / nr, j = i - x * nr;
-            out[static_cast<size_t>(col0 + x) * a.rank + jb + j] = sums[j][x] * scale;
-        }
-    } else {
-        for (int i = threadIdx.x; i < nr * nc; i += kThreads) {
-            const int j = i / nc, x = i - j * nc;
-            out[static_cast<size_t>(jb + j) * sd.cols + col0 + x] = sums[j][x] * scale;
-        }
-    }
+    store_all([&](int j, int x, bool along) {
+        f32x4 v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = (along ? sums[j + k][x] : sums[j][x + k]) * scale;
+        return v;
+    });
 }
 
-// The chunks of each group that has several, added in order; zeros for groups
-// without rows.
+// The chunks of each group that has several, added in order.
 constexpr int kJoinThreads = 64;
-typedef f32x4 f32x4_any __attribute__((aligned(4)));
 __global__ __launch_bounds__(kJoinThreads) void outer_join_kernel(const OuterArgs a, int blocks0) {
     const int group = blockIdx.y;
     const bool second = static_cast<int>(blockIdx.x) >= blocks0;
@@ -590,7 +631,7 @@ __global__ __launch_bounds__(kJoinThreads) void outer_join_kernel(const OuterArg
     int lo, hi;
     group_places(a.offsets, a.count, a.rows, group, lo, hi);
     const int n = (hi - lo + a.chunk - 1) / a.chunk;
-    if (n == 1) return;
+    if (n < 2) return;
     int first = 0;  // chunks of the groups with several before this one
     const int lane = threadIdx.x & 63;
     for (int e0 = 0; e0 < group; e0 += 64) {
@@ -646,8 +687,10 @@ size_t part_bytes(int rows, int count, int K, int rank) {
     return align16(sizeof(float) * static_cast<size_t>(shrink_parts(rows, count, K, rank)) * rows * 16 * rank_tiles(rank));
 }
 
-// Rows of a chunk: enough chunks to fill the GPU.
+// Rows of a chunk: enough chunks to fill the GPU; up to 512 rows no group has
+// several (a join's launch costs more than the waves' longer way).
 int outer_chunk(int rows, int n, int m) {
+    if (rows <= 512) return 512;
     const int64_t strips = (n + 127) / 128 + (m + 127) / 128;
     int chunk = kMaxChunk;
     while (chunk > 128 && (rows / chunk) * strips < 1024) chunk /= 2;
@@ -707,9 +750,13 @@ void launch_expand(ExpandArgs &a, hipStream_t s) {
 
 template <typename E>
 void launch_outer(const OuterArgs &a, hipStream_t s) {
-    const int rt = std::min(rank_tiles(a.rank), 4);
+    // (two tiles of 16 ranks at most: four leave registers for one workgroup
+    // per CU; 8192 rows, 4096 + 4096, rank 64: 163 us instead of 128 in all)
+    const int rt = std::min(rank_tiles(a.rank), 2);
     const int strips = a.side[0].strips + a.side[1].strips;
-    const dim3 grid(static_cast<uint32_t>(row_tiles_bound(a.rows, a.count, a.chunk) * strips), (a.rank + 16 * rt - 1) / (16 * rt));
+    // (chunks, and groups without rows)
+    const int64_t work = (static_cast<int64_t>(a.rows) / a.chunk + a.count) * strips;
+    const dim3 grid(static_cast<uint32_t>((work + 7) / 8 * 8 * ((a.rank + 16 * rt - 1) / (16 * rt))));
     bool vec = true;
     for (const OuterSide &sd : a.side)
         if (sd.strips > 0 && sd.cols % 8 != 0) vec = false;
@@ -719,8 +766,7 @@ void launch_outer(const OuterArgs &a, hipStream_t s) {
         else launch_kernel(outer_kernel<E, RT, false>, grid, dim3(kThreads), 0, s, a);
     };
     if (rt == 1) go(Tag<1>{});
-    else if (rt == 2) go(Tag<2>{});
-    else go(Tag<4>{});
+    else go(Tag<2>{});
 }
 
 void launch_outer_join(const OuterArgs &a, hipStream_t s) {
@@ -851,11 +897,9 @@ extern "C" dbf_status_t dbf_adapter_backward(const void *dy, const void *x, cons
                              reinterpret_cast<float *>(ws + plan.dA)};
         if (dB) o.side[1] = {t, static_cast<const uint16_t *>(dy), n, 1, (n + 127) / 128, scale, dB,
                              reinterpret_cast<float *>(ws + plan.dB)};
-        if (rows > 0) {
-            if (type == DBF_TYPE_F16) launch_outer<F16>(o, stream);
-            else launch_outer<BF16>(o, stream);
-        }
-        launch_outer_join(o, stream);
+        if (type == DBF_TYPE_F16) launch_outer<F16>(o, stream);
+        else launch_outer<BF16>(o, stream);
+        if (rows > o.chunk) launch_outer_join(o, stream);
     }
     return hipGetLastError() == hipSuccess ? DBF_OK : DBF_ERR_HIP;
 }
