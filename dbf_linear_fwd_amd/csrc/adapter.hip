@@ -227,16 +227,27 @@ struct ExpandArgs {
     int per;                    // 64-column chunks of a wave
 };
 
+// Waves of a workgroup: more share a large tile's t (2048 rows, rank 64, n 14336:
+// 59 us with four in both products, 56 with eight).
+constexpr int expand_waves(int mt) { return mt == 1 ? 4 : 8; }
+
 template <typename E, bool LEAD, int MT, int RT, bool VEC>
-__global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
+__global__ __launch_bounds__(64 * expand_waves(MT)) void expand_kernel(const ExpandArgs a) {
+    constexpr int Waves = expand_waves(MT), Threads = 64 * Waves;
     constexpr int RP = 16 * RT, Rows = 16 * MT, Units = RP / 8;
     constexpr int WF = RP < 32 ? 1 : RP / 32;  // 32-rank pieces
     constexpr int KS = RT;                     // instructions of two parts: 2 RP / 32
     constexpr int Pitch = RP + 8;
     __shared__ __attribute__((aligned(16))) uint16_t parts[2][Rows][Pitch];
     __shared__ int shifts[Rows];
+    // Sums of large tiles change lanes: eight lanes take a row's 128 bytes, whole
+    // lines of base and result (8192 rows, n 4096, rank 16: 59 us in both
+    // products, 56 so; at 64 ranks it costs registers and with them a workgroup
+    // per CU: 2048 rows, n 14336: 62 instead of 56).
+    constexpr bool Turn = MT > 1 && RT != 4;
+    __shared__ __attribute__((aligned(16))) float turn[Turn ? Waves : 1][Turn ? 16 : 1][Turn ? 68 : 1];
     RowTile rt;
-    const int blocks = (a.cols + 64 * kWaves * a.per - 1) / (64 * kWaves * a.per);
+    const int blocks = (a.cols + 64 * Waves * a.per - 1) / (64 * Waves * a.per);
     const int tile = blockIdx.x / blocks, block = blockIdx.x % blocks;
     if (!find_row_tile(a.offsets, a.count, a.rows, Rows, tile, rt)) return;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -244,12 +255,20 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
     const bool none = rt.group >= a.count;
     const int j0 = RP < 32 ? 8 * (g & 1) : 8 * g;  // this lane's ranks of a piece
 
-    int64_t row[MT];
+    // rows and columns of this lane's two pieces of 16 bytes of a 16 x 64 block
+    int row[MT][2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r = a.order[rt.first + min(16 * i + c, rt.rows - 1)];
-        row[i] = 16 * i + c < rt.rows && r >= 0 && r < a.rows ? r : -1;
-    }
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!Turn && h == 1) {
+                row[i][1] = row[i][0];
+                continue;
+            }
+            const int k = 16 * i + (Turn ? 8 * h + (lane >> 3) : c), r = a.order[rt.first + min(k, rt.rows - 1)];
+            row[i][h] = k < rt.rows && r >= 0 && r < a.rows ? r : -1;
+        }
+    auto piece = [&](int h) { return Turn ? 8 * (lane & 7) : 32 * h + 8 * g; };
     // Columns of a wave's chunk: operand 2 h + e of lane c has column 32 h + 2 c + e,
     // so that lane (c, g) gets columns 32 h + 8 g .. + 7 of row c: 16 bytes, and
     // 64 of a row in the lanes of one store.
@@ -260,10 +279,10 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int col = col0 + 32 * h + 8 * g;
+                const int col = col0 + piece(h);
                 base[m][h] = u32v4{0u, 0u, 0u, 0u};
-                if (a.base && row[m] >= 0)
-                    base[m][h] = load_row8<VEC>(a.base + static_cast<size_t>(row[m]) * a.cols + col, a.cols - col);
+                if (a.base && row[m][h] >= 0)
+                    base[m][h] = load_row8<VEC>(a.base + static_cast<size_t>(row[m][h]) * a.cols + col, a.cols - col);
             }
         if (none) return;
 #pragma unroll
@@ -290,7 +309,7 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
             }
         }
     };
-    auto column = [&](int it) { return ((block * a.per + it) * kWaves + wave) * 64; };
+    auto column = [&](int it) { return ((block * a.per + it) * Waves + wave) * 64; };
     const bool skip = !a.out || (none && a.base == a.out);
     if (!skip && column(0) < a.cols) load_chunk(column(0));  // (on its way while t is added up)
 
@@ -298,7 +317,7 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
     // the two 16-bit parts of scale * t into LDS.
     if (!none || (a.low && block == 0)) {
         const float scale = none || !a.scale ? 1.0f : a.scale[rt.group];
-        for (int i = threadIdx.x; i < rt.rows * Units; i += kThreads) {
+        for (int i = threadIdx.x; i < rt.rows * Units; i += Threads) {
             const int r = i / Units, j = i % Units * 8, at = rt.first + r;
             float v[8];
 #pragma unroll
@@ -372,6 +391,34 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
 #pragma unroll
                     for (int s = 0; s < KS; ++s) acc[i] = mma<E>(wf[s % WF][i], tf[s], acc[i]);
                 }
+                // columns 32 h + 8 g + 2 v + e of row c, in order
+                float d[2][8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        d[h][k] = acc[2 * h + (k & 1)][k >> 1];
+                        if constexpr (E::code == DBF_TYPE_F16) d[h][k] = ldexpf(d[h][k], shift);
+                    }
+                if constexpr (Turn) {
+                    float(&own)[16][68] = turn[wave];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            *reinterpret_cast<f32x4 *>(&own[c][32 * h + 8 * g + 4 * q]) =
+                                f32x4{d[h][4 * q], d[h][4 * q + 1], d[h][4 * q + 2], d[h][4 * q + 3]};
+                    wave_fence();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const f32x4 v = *reinterpret_cast<const f32x4 *>(&own[8 * h + (lane >> 3)][8 * (lane & 7) + 4 * q]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) d[h][4 * q + k] = v[k];
+                        }
+                    wave_fence();
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -379,19 +426,16 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(const ExpandArgs a) {
                         const uint32_t old = base[m][h][k];
                         uint32_t o = 0;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float d = acc[2 * h + e][k];
-                            if constexpr (E::code == DBF_TYPE_F16) d = ldexpf(d, shift);
-                            o |= static_cast<uint32_t>(E::put(E::get(static_cast<uint16_t>(old >> (16 * e))) + d)) << (16 * e);
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            o |= static_cast<uint32_t>(E::put(E::get(static_cast<uint16_t>(old >> (16 * e))) + d[h][2 * k + e])) << (16 * e);
                         base[m][h][k] = o;
                     }
             }
-            if (row[m] < 0) continue;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int col = col0 + 32 * h + 8 * g, valid = a.cols - col;
-                uint16_t *dst = a.out + static_cast<size_t>(row[m]) * a.cols + col;
+                if (row[m][h] < 0) continue;
+                const int col = col0 + piece(h), valid = a.cols - col;
+                uint16_t *dst = a.out + static_cast<size_t>(row[m][h]) * a.cols + col;
                 if (VEC ? valid > 0 : valid >= 8) {
                     *reinterpret_cast<u32v4_any *>(dst) = base[m][h];
                 } else if (!VEC) {
@@ -734,14 +778,14 @@ void launch_expand(ExpandArgs &a, hipStream_t s) {
         constexpr int RT = decltype(rt)::value, Big = expand_most(RT);
         const bool vec = a.cols % 8 == 0 && (LEAD || a.rank % 8 == 0);
         auto go = [&](auto mt) {
-            constexpr int MT = decltype(mt)::value;
+            constexpr int MT = decltype(mt)::value, Waves = expand_waves(MT), Threads = 64 * Waves;
             const int64_t tiles = row_tiles_bound(a.rows, a.count, 16 * MT);
-            const int64_t chunks = (static_cast<int64_t>(a.cols) + 64 * kWaves - 1) / (64 * kWaves);
+            const int64_t chunks = (static_cast<int64_t>(a.cols) + 64 * Waves - 1) / (64 * Waves);
             // (results of t alone: one workgroup per row tile)
             a.per = static_cast<int>(a.out ? std::min<int64_t>(chunks, std::max<int64_t>(1, tiles * chunks / 512)) : chunks);
             const dim3 grid(static_cast<uint32_t>(tiles * ((chunks + a.per - 1) / a.per)));
-            if (vec) launch_kernel(expand_kernel<E, LEAD, MT, RT, true>, grid, dim3(kThreads), 0, s, a);
-            else launch_kernel(expand_kernel<E, LEAD, MT, RT, false>, grid, dim3(kThreads), 0, s, a);
+            if (vec) launch_kernel(expand_kernel<E, LEAD, MT, RT, true>, grid, dim3(Threads), 0, s, a);
+            else launch_kernel(expand_kernel<E, LEAD, MT, RT, false>, grid, dim3(Threads), 0, s, a);
         };
         if (!full_groups(a.rows, a.count, a.cols)) go(Tag<1>{});
         else go(Tag<Big>{});

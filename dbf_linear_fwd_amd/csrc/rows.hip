@@ -49,13 +49,6 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits, uint64_t on) {
     return m;
 }
 
-// The lanes of a wave see what each other wrote to LDS (whose accesses are in
-// order for a wave: nothing is waited for).
-__device__ __forceinline__ void wave_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // Exclusive sum over the workgroup's threads; total is everyone's.
 __device__ __forceinline__ int block_scan(int v, int *tmp, int &total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;

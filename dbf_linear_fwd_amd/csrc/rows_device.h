@@ -15,6 +15,13 @@ __device__ __forceinline__ void group_places(const int32_t *offsets, int count, 
     hi = e < count ? min(max(next, lo), slots) : slots;
 }
 
+// The lanes of a wave see what each other wrote to LDS (whose accesses are in
+// order for a wave: nothing is waited for).
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Sum of v over the lanes up to this one: in rows of 16 lanes by row shifts,
 // then the rows' last lanes into the rows behind (no LDS, as a shuffle takes).
 __device__ __forceinline__ int wave_scan(int v) {
