@@ -940,7 +940,7 @@ class Adapters:
         """(y, t) for rows x and the layer's results base; out may be base itself (see dbf_adapter_forward in
         include/dbf.h)."""
         import torch
-        rows = x.shape[0]
+        rows = x.shape[0] if x.dim() == 2 else 0
         self._check(x, rows, self.m, "x")
         self._check(base, rows, self.n, "base")
         _check_groups(groups, self.count, rows, x.device)
@@ -963,7 +963,7 @@ class Adapters:
         """(dx', dA, dB) at rows x with the forward's t for the upstream gradient dy: dx' = dx + scale (dy B) A with
         the layer's own input gradient dx (None: zeros); dA and dB are float32.  out (for dx') may be dx itself."""
         import torch
-        rows = x.shape[0]
+        rows = x.shape[0] if x.dim() == 2 else 0
         self._check(dy, rows, self.n, "dy")
         self._check(x, rows, self.m, "x")
         self._low(t, rows)

@@ -351,8 +351,9 @@ __global__ __launch_bounds__(64 * expand_waves(MT)) void expand_kernel(const Exp
                         if (j + k < a.rank) a.low[static_cast<size_t>(to) * a.rank + j + k] = v[k] * by;
                 }
             }
+            // (ranks behind the last: 0 where an infinite x made them 0 * inf)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= scale;
+            for (int k = 0; k < 8; ++k) v[k] = j + k < a.rank ? v[k] * scale : 0.0f;
             if constexpr (E::code == DBF_TYPE_F16) {
                 float top = 0.0f;
 #pragma unroll

@@ -262,6 +262,35 @@ def test_rows_and_groups_do_not_meet(gpu, name):
     assert bool(dAb[index[7], :, 3].isnan().all()) and bool(dBb[index[7]].isnan().all())
 
 
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("rank", [3, 8, 16, 20, 40, 100])
+@pytest.mark.parametrize("rows", [4, 600])
+def test_infinities(gpu, rows, rank, name):
+    """An infinite x is what it is in the formula: infinities of the products' signs, NaN only where they meet."""
+    torch = _torch()
+    rng = np.random.default_rng(rank)
+    n, m = 72, 9000 if rows == 600 else 136
+    x, _ = to_dev(rng.uniform(0.5, 1, (rows, m)), name)
+    x[1, 5], x[2, 7] = float("inf"), float("-inf")
+    A, _ = to_dev(rng.uniform(0.5, 1, (1, rank, m)), name)
+    B = rng.uniform(0.5, 1, (1, n, rank)) * np.where(rng.random((1, n, 1)) < 0.5, -1, 1)
+    B[0, 0, 0] *= -1  # both signs in one sum: NaN
+    B, _ = to_dev(B, name)
+    base = torch.zeros(rows, n, dtype=T(name), device="cuda")
+    g = group(np.zeros(rows, int), 1)
+    y, t = dbf.Adapters(A, B)(x, base, g)
+    low = x.double() @ A[0].double().t()
+    ref = low @ B[0].double().t()
+    assert torch.equal(torch.nan_to_num(t, 0, 1, -1)[1:3], torch.nan_to_num(low, 0, 1, -1).float()[1:3])
+    assert torch.equal(y[1:3].isnan(), ref[1:3].isnan()) and bool(ref[1, 0].isnan())
+    assert torch.equal(torch.nan_to_num(y, 0, 1, -1)[1:3], torch.nan_to_num(ref, 0, 1, -1).to(T(name))[1:3])
+    dy = torch.zeros(rows, n, dtype=T(name), device="cuda")
+    dy[:] = B[0, :, 0]
+    dy[1, 3] = float("inf")
+    dx, _, _ = dbf.Adapters(A, B.abs()).backward(dy, x, torch.ones(rows, rank, device="cuda"), g)
+    assert bool((dx[1] == float("inf")).all()) and bool(torch.isfinite(dx[3].float()).all())
+
+
 def test_large_and_small_magnitudes(gpu):
     """f16 values whose t is far outside of f16's range, and gradients far below it."""
     torch = _torch()
