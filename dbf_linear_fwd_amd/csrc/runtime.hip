@@ -1121,7 +1121,8 @@ extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, co
     if (act_type != DBF_TYPE_E4M3 && act_type != DBF_TYPE_E2M1) return DBF_ERR_INVALID_ARG;
     // (a launch holds less than 2^32 threads)
     const int64_t lim = int64_t(1) << 20;
-    if (count > 1024 || n > lim || m > lim || max_rows > (1 << 24)) return DBF_ERR_SHAPE;
+    if (count > 1024 || n > lim || m > lim || max_rows > (1 << 24) || int64_t(count) * std::max(n, m) > (int64_t(1) << 29))
+        return DBF_ERR_SHAPE;
     const int32_t n_pad = round_up(n, 32), m_pad = round_up(m, 128);
     if (int64_t(n_pad) * m_pad > (int64_t(1) << 36) || int64_t(max_rows) * m_pad > (int64_t(1) << 31) ||
         int64_t(max_rows) * n > (int64_t(1) << 31))

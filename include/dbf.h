@@ -559,7 +559,8 @@ dbf_status_t dbf_group_rows(const void *index, int32_t index_bits, int32_t rows,
  * places (slots) of a call.  The handle takes dbf_experts_forward,
  * dbf_experts_backward_data, dbf_get_info (n, m of one weight), timing and
  * dbf_free; the other entry points return DBF_ERR_UNSUPPORTED.
- * count <= 1024, n, m <= 2^20, max_rows <= 2^24 (DBF_ERR_SHAPE above).
+ * count <= 1024, n, m <= 2^20, count * max(n, m) <= 2^29, n * m <= 2^36, max_rows <= 2^24,
+ * max_rows * max(n, m) <= 2^31 with m rounded up to 128 (DBF_ERR_SHAPE above).
  *
  * dbf_experts_forward -- for each place s < slots, of group e,
  *   y[out(s)][o] = rne( Σ_l xq[in(s)][l] W_e[o][l] ).

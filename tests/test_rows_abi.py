@@ -59,6 +59,14 @@ def test_experts_refusals():
     assert L.dbf_experts_backward_data(None, P, F16, P, P, 1, 0, 0, P, None) == E
 
 
+def test_experts_wide_and_many():
+    # a launch over every group's tiles stays below 2^32 threads
+    pack = dbf.lib().dbf_experts_pack
+    out = ctypes.c_void_p()
+    for count, n, m in ((1024, 1 << 20, 128), (1024, 128, 1 << 20), (513, 1 << 20, 128), (1024, (1 << 19) + 1, 128)):
+        assert pack(count, n, m, P, P, E4M3, 16, None, ctypes.byref(out)) == SHAPE and not out.value
+
+
 def _adapter(**k):
     a = dict(x=P, base=P, A=P, B=P, scale=P, type=F16, order=P, offsets=P, rows=5, n=8, m=16, rank=4, count=2, y=P, t=P,
              ws=P, nbytes=BIG)
