@@ -3,16 +3,22 @@
 //   t = x A_aᵀ          y  = base + s_a t B_aᵀ
 //   u = s_a dy B_a      dx' = dx + u A_a     dA_a = Σ u xᵀ    dB_a = s_a Σ dy tᵀ
 //
-// Three kernels on the 16x16x32 16-bit matrix-core instructions, operands from
+// Kernels on the 16x16x32 16-bit matrix-core instructions, operands from
 // memory straight into registers:
 //   shrink  rows x K -> rows x rank (t, u): K cut between the waves of a
 //           workgroup and into parts, whose fp32 sums go to memory;
-//   expand  rows x rank -> rows x columns (y, dx'): adds the parts of t, one
-//           wave for all of its row tile, and goes through the columns;
+//   expand  rows x rank -> rows x columns (y, dx'): a workgroup adds the parts
+//           of its row tile's t into LDS and goes through its columns;
 //   outer   the sums over a group's rows (dA, dB): the rows of a group in
-//           chunks, joined in order by a fourth kernel where a group has several.
-// The rank is small (16 to 64), so all of them are bound by the rows' memory
-// traffic: a product needs rank / 2 to rank operations per byte of x, dy or y.
+//           chunks, joined in order by outer_join where a group has several.
+// A product needs no more than 2 rank operations per element of x, dy or y, so
+// the rows' memory traffic is the bound, and with few rows the launches.
+// Measured (kernel trace; bytes as they have to be moved): 8192 rows, 4096 +
+// 4096, rank 16, bf16: shrink 14 us (67 MB, 4.9 TB/s), expand 30 (134 MB, 4.5),
+// outer 28 (134 MB, 4.8) and its join 5; 2048 rows, m 4096, n 14336, rank 64:
+// shrink 13 us, expand 37 (117 MB, 3.1 TB/s); 16 rows of 32 adapters, 4096 x
+// 4096, rank 16, f16: 3.4 and 5.2 us, 8.2 for both in a graph (in one launch,
+// every workgroup with all of its t: 9.1).
 //
 // Of an instruction a lane (c = lane % 16, g = lane / 16) supplies row c of each
 // operand, eight values of K from 8 g on, and gets results 4 g .. 4 g + 3 of
@@ -135,7 +141,11 @@ struct ShrinkArgs {
     float *out;                 // [parts][rows][16 RT], by place
 };
 
-// MT tiles of 16 rows, ranks c RT + i (i < RT) in lane c's operand i.
+// MT tiles of 16 rows, ranks c RT + i (i < RT) in lane c's operand i.  Of large
+// launches two thirds of the time are the first loads' way: a workgroup's few
+// steps (2048 rows, K 4096, rank 64: four of 32 columns per wave) are little
+// more than one wait.  More steps in flight change nothing there, twice the
+// workgroups cost 4 us in both products.
 template <typename E, bool LEAD, int MT, int RT, bool VEC>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(const ShrinkArgs a) {
     constexpr int RP = 16 * RT, Rows = 16 * MT, Pitch = RP + 4;
@@ -313,8 +323,9 @@ __global__ __launch_bounds__(64 * expand_waves(MT)) void expand_kernel(const Exp
     const bool skip = !a.out || (none && a.base == a.out);
     if (!skip && column(0) < a.cols) load_chunk(column(0));  // (on its way while t is added up)
 
-    // The tile's rows of t, once per workgroup: the parts added in order, and
-    // the two 16-bit parts of scale * t into LDS.
+    // The tile's rows of t, once per workgroup (by each wave for itself: 2048
+    // rows, rank 64, n 14336, 179 instead of 43 us): the parts added in order,
+    // and the two 16-bit parts of scale * t into LDS.
     if (!none || (a.low && block == 0)) {
         const float scale = none || !a.scale ? 1.0f : a.scale[rt.group];
         for (int i = threadIdx.x; i < rt.rows * Units; i += Threads) {

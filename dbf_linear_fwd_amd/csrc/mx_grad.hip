@@ -154,6 +154,9 @@ __device__ __forceinline__ void scale_columns(f32x16 (&acc)[C::MI][C::NI], const
 enum class GradRows { Whole, Rows16, Elements };
 
 // G: rows in groups (as in the forward's product).
+// 2048 tokens with 2 of 8 experts each, 14336 x 4096, bf16: 457 to 530 us in the
+// trace, 0.9 to 1.05 PFLOP/s, matrix cores busy 61 % at a clock that falls to
+// 1.7 GHz; one weight for 4096 rows takes 355 to 368.
 template <typename C, typename E, GradRows ROWS, bool G>
 __global__ __launch_bounds__(C::Threads) void mx_grad_kernel(MxGradArgs a) {
     constexpr bool Whole = ROWS == GradRows::Whole, Dma = ROWS != GradRows::Elements;
