@@ -149,7 +149,7 @@ struct ShrinkArgs {
 template <typename E, bool LEAD, int MT, int RT, bool VEC>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(const ShrinkArgs a) {
     constexpr int RP = 16 * RT, Rows = 16 * MT, Pitch = RP + 4;
-    __shared__ __attribute__((aligned(16))) float red[kWaves][Rows][Pitch];
+    __shared__ __attribute__((aligned(16))) float red[kWaves][16][Pitch];
     const int tile = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
     RowTile rt;
     if (!find_row_tile(a.offsets, a.count, a.rows, Rows, tile, rt) || rt.group >= a.count) return;
@@ -172,23 +172,25 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(const ShrinkArgs a) {
         for (int j = 0; j < RT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // U steps' operands are on their way at a time
     constexpr int U = MT + RT <= 3 ? 4 : MT + RT <= 6 ? 2 : 1;
-    for (int s0 = k0; s0 < k1; s0 += U) {
+    // XV: every lane has all of its eight columns or none; WV: its RT ranks
+    auto turn = [&](int s0, auto xv, auto wv) {
+        constexpr bool XV = decltype(xv)::value, WV = decltype(wv)::value;
         u32v4 xf[U][MT], wf[U][RT];
         uint32_t q[U][8][(RT + 1) / 2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = 32 * (s0 + u), left = s0 + u < k1 ? a.K - k - 8 * g : 0;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) xf[u][i] = load_row8<VEC>(xr[i] + k, left);
+            for (int i = 0; i < MT; ++i) xf[u][i] = load_row8<XV>(xr[i] + k, left);
             if constexpr (LEAD) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    load_n<RT, VEC>(w + static_cast<size_t>(k + 8 * g + j) * a.rank + c * RT, j < left ? a.rank - c * RT : 0, q[u][j]);
+                    load_n<RT, WV>(w + static_cast<size_t>(k + 8 * g + j) * a.rank + c * RT, j < left ? a.rank - c * RT : 0, q[u][j]);
             } else {
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
                     const int j = c * RT + i;
-                    wf[u][i] = load_row8<VEC>(w + static_cast<size_t>(j) * a.K + k + 8 * g, j < a.rank ? left : 0);
+                    wf[u][i] = load_row8<XV>(w + static_cast<size_t>(j) * a.K + k + 8 * g, j < a.rank ? left : 0);
                 }
             }
         }
@@ -203,22 +205,39 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(const ShrinkArgs a) {
 #pragma unroll
                 for (int j = 0; j < RT; ++j) acc[i][j] = mma<E>(wf[u][j], xf[u][i], acc[i][j]);
         }
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    for (int s0 = k0; s0 < k1; s0 += U) {
+        if (VEC) {
+            turn(s0, Yes{}, Yes{});
+        } else {
+            // (only the last columns of an odd width are looked at one by one: 1491
+            // rows, K 247, rank 128, 7 instead of 11 us)
+            const bool full = 32 * (s0 + U) <= a.K, ranks = !LEAD || a.rank % RT == 0;
+            if (full && ranks) turn(s0, Yes{}, Yes{});
+            else if (ranks) turn(s0, No{}, Yes{});
+            else turn(s0, No{}, No{});
+        }
     }
-    // lane (c, g): ranks (4 g + v) RT + i of row c
+    // lane (c, g): ranks (4 g + v) RT + i of row c; 16 rows at a time
+    float *out = a.out + (static_cast<size_t>(part) * a.rows + rt.first) * RP;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i) {
+        if (16 * i >= rt.rows) break;
+        if (i > 0) __syncthreads();
 #pragma unroll
         for (int j = 0; j < RT; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) red[wave][16 * i + c][(4 * g + v) * RT + j] = acc[i][j][v];
-    __syncthreads();
-    float *out = a.out + (static_cast<size_t>(part) * a.rows + rt.first) * RP;
-    for (int i = threadIdx.x; i < rt.rows * (RP / 4); i += kThreads) {
-        const int r = i / (RP / 4), j = i % (RP / 4) * 4;
-        f32x4 s = *reinterpret_cast<const f32x4 *>(&red[0][r][j]);
+            for (int v = 0; v < 4; ++v) red[wave][c][(4 * g + v) * RT + j] = acc[i][j][v];
+        __syncthreads();
+        for (int k = threadIdx.x; k < min(16, rt.rows - 16 * i) * (RP / 4); k += kThreads) {
+            const int r = k / (RP / 4), j = k % (RP / 4) * 4;
+            f32x4 s = *reinterpret_cast<const f32x4 *>(&red[0][r][j]);
 #pragma unroll
-        for (int v = 1; v < kWaves; ++v) s += *reinterpret_cast<const f32x4 *>(&red[v][r][j]);
-        *reinterpret_cast<f32x4 *>(out + static_cast<size_t>(r) * RP + j) = s;
+            for (int v = 1; v < kWaves; ++v) s += *reinterpret_cast<const f32x4 *>(&red[v][r][j]);
+            *reinterpret_cast<f32x4 *>(out + static_cast<size_t>(16 * i + r) * RP + j) = s;
+        }
     }
 }
 
@@ -284,7 +303,8 @@ __global__ __launch_bounds__(64 * expand_waves(MT)) void expand_kernel(const Exp
     // 64 of a row in the lanes of one store.
     const uint16_t *w = a.w + static_cast<size_t>(none ? 0 : rt.group) * a.rank * a.cols;
     u32v4 wf[WF][4], base[MT][2];
-    auto load_chunk = [&](int col0) {
+    auto load = [&](int col0, auto cv, auto wv) __attribute__((always_inline)) {
+        constexpr bool CV = decltype(cv)::value, WV = decltype(wv)::value;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -292,7 +312,7 @@ __global__ __launch_bounds__(64 * expand_waves(MT)) void expand_kernel(const Exp
                 const int col = col0 + piece(h);
                 base[m][h] = u32v4{0u, 0u, 0u, 0u};
                 if (a.base && row[m][h] >= 0)
-                    base[m][h] = load_row8<VEC>(a.base + static_cast<size_t>(row[m][h]) * a.cols + col, a.cols - col);
+                    base[m][h] = load_row8<CV>(a.base + static_cast<size_t>(row[m][h]) * a.cols + col, a.cols - col);
             }
         if (none) return;
 #pragma unroll
@@ -305,7 +325,7 @@ __global__ __launch_bounds__(64 * expand_waves(MT)) void expand_kernel(const Exp
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int rk = 32 * f + j0 + j;
-                        load_n<2, VEC>(w + static_cast<size_t>(rk) * a.cols + col, rk < a.rank ? a.cols - col : 0, q[j]);
+                        load_n<2, CV>(w + static_cast<size_t>(rk) * a.cols + col, rk < a.rank ? a.cols - col : 0, q[j]);
                     }
                     wf[f][2 * h] = pick_column<2>(q, 0);
                     wf[f][2 * h + 1] = pick_column<2>(q, 1);
@@ -314,9 +334,25 @@ __global__ __launch_bounds__(64 * expand_waves(MT)) void expand_kernel(const Exp
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int col = col0 + 32 * (i >> 1) + 2 * c + (i & 1), rk = 32 * f + j0;
-                    wf[f][i] = load_row8<VEC>(w + static_cast<size_t>(col) * a.rank + rk, col < a.cols ? a.rank - rk : 0);
+                    wf[f][i] = load_row8<WV>(w + static_cast<size_t>(col) * a.rank + rk, col < a.cols ? a.rank - rk : 0);
                 }
             }
+        }
+    };
+    auto load_chunk = [&](int col0) __attribute__((always_inline)) {
+        using Yes = std::true_type;
+        using No = std::false_type;
+        if constexpr (VEC || MT > 1) {
+            using All = std::bool_constant<VEC>;
+            load(col0, All{}, All{});
+        } else {
+            // (only the last columns of an odd width are looked at one by one; with
+            // several tiles both forms cost registers: 6272 rows, n 1137, 33
+            // instead of 28 us in both products)
+            const bool full = col0 + 64 <= a.cols, ranks = LEAD || a.rank % 8 == 0;
+            if (full && ranks) load(col0, Yes{}, Yes{});
+            else if (full) load(col0, Yes{}, No{});
+            else load(col0, No{}, No{});
         }
     };
     auto column = [&](int it) { return ((block * a.per + it) * Waves + wave) * 64; };
@@ -522,7 +558,7 @@ typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 // A chunk's rows x 128 columns x 16 RT ranks per workgroup; the waves take 32
 // rows in turn.
-template <typename E, int RT, bool VEC>
+template <typename E, int RT>
 __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
     constexpr int RP = 16 * RT, Cols = 128, Pitch = Cols + 4;
     constexpr int NP = E::code == DBF_TYPE_F16 ? 2 : 3;
@@ -622,7 +658,8 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = wave; s < steps; s += kWaves) {
+    auto turn = [&](int s, auto vec) {
+        constexpr bool VEC = decltype(vec)::value;
         uint32_t q[8][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -648,6 +685,13 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
 #pragma unroll
                 for (int n = 0; n < NP; ++n) acc[i][j] = mma<E>(qf, pf[j][n], acc[i][j]);
         }
+    };
+    // (only the last strip of an odd width looks at its columns one by one: 1491
+    // rows, 247 + 11288, rank 128, 47 instead of 109 us)
+    if (sd.cols % 8 == 0 || col0 + Cols <= sd.cols) {
+        for (int s = wave; s < steps; s += kWaves) turn(s, std::true_type{});
+    } else {
+        for (int s = wave; s < steps; s += kWaves) turn(s, std::false_type{});
     }
     // lane (c, g): rank c RT + j, column 8 (4 g + v) + i; the waves' sums in order
     for (int w = 0; w < min(kWaves, steps); ++w) {  // (the others have no rows)
@@ -722,8 +766,9 @@ __global__ __launch_bounds__(kJoinThreads) void outer_join_kernel(const OuterArg
 int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
 // 16-row tiles of a row tile: several where the groups fill them (their rows
-// share the weight's operands), as many as registers and LDS allow.
-constexpr int shrink_most(int rt) { return rt == 1 ? 4 : rt <= 4 ? 2 : 1; }
+// share the weight's operands), as many as registers and LDS allow (5400 rows, K
+// 3200, rank 128: a shrink with one tile 42 us, with two 25).
+constexpr int shrink_most(int rt) { return rt == 1 ? 4 : 2; }
 constexpr int expand_most(int rt) { return rt == 8 ? 2 : 4; }
 // (and there is enough of them for every CU: rows times the width)
 bool full_groups(int rows, int count, int width) {
@@ -743,13 +788,15 @@ size_t part_bytes(int rows, int count, int K, int rank) {
     return align16(sizeof(float) * static_cast<size_t>(shrink_parts(rows, count, K, rank)) * rows * 16 * rank_tiles(rank));
 }
 
-// Rows of a chunk: enough chunks to fill the GPU; up to 512 rows no group has
-// several (a join's launch costs more than the waves' longer way).
-int outer_chunk(int rows, int n, int m) {
+// Rows of a chunk: enough chunks to fill the GPU, beside the half of the groups
+// that may be short (1549 rows of 5 groups, 8128 + 12499, rank 32: by rows and
+// columns alone 113 us in all, by ranks and groups too 89); up to 512 rows no group has several (a join's launch costs
+// more than the waves' longer way).
+int outer_chunk(int rows, int n, int m, int rank, int count) {
     if (rows <= 512) return 512;
-    const int64_t strips = (n + 127) / 128 + (m + 127) / 128;
+    const int64_t blocks = ((n + 127) / 128 + (m + 127) / 128) * static_cast<int64_t>((rank + 31) / 32);
     int chunk = kMaxChunk;
-    while (chunk > 128 && (rows / chunk) * strips < 1024) chunk /= 2;
+    while (chunk > 128 && (rows / chunk + std::min(rows, count) / 2) * blocks < 1024) chunk /= 2;
     return chunk;
 }
 // Chunks of groups that have several: ceil(c / chunk) of more than chunk rows
@@ -813,13 +860,8 @@ void launch_outer(const OuterArgs &a, hipStream_t s) {
     // (chunks, and groups without rows)
     const int64_t work = (static_cast<int64_t>(a.rows) / a.chunk + a.count) * strips;
     const dim3 grid(static_cast<uint32_t>((work + 7) / 8 * 8 * ((a.rank + 16 * rt - 1) / (16 * rt))));
-    bool vec = true;
-    for (const OuterSide &sd : a.side)
-        if (sd.strips > 0 && sd.cols % 8 != 0) vec = false;
     auto go = [&](auto r) {
-        constexpr int RT = decltype(r)::value;
-        if (vec) launch_kernel(outer_kernel<E, RT, true>, grid, dim3(kThreads), 0, s, a);
-        else launch_kernel(outer_kernel<E, RT, false>, grid, dim3(kThreads), 0, s, a);
+        launch_kernel(outer_kernel<E, decltype(r)::value>, grid, dim3(kThreads), 0, s, a);
     };
     if (rt == 1) go(Tag<1>{});
     else go(Tag<2>{});
@@ -894,7 +936,7 @@ BackwardPlan backward_plan(int32_t rows, int32_t n, int32_t m, int32_t rank, int
     BackwardPlan p;
     p.u = part_bytes(rows, count, n, rank);
     p.dA = p.u + align16(sizeof(float) * static_cast<size_t>(rows) * rank);
-    const size_t slots = static_cast<size_t>(outer_slots(rows, outer_chunk(rows, n, m)));
+    const size_t slots = static_cast<size_t>(outer_slots(rows, outer_chunk(rows, n, m, rank, count)));
     p.dB = p.dA + align16(sizeof(float) * slots * rank * m);
     p.total = p.dB + align16(sizeof(float) * slots * rank * n);
     return p;
@@ -947,7 +989,7 @@ extern "C" dbf_status_t dbf_adapter_backward(const void *dy, const void *x, cons
         o.rows = rows;
         o.rank = rank;
         o.count = count;
-        o.chunk = rows > 0 ? outer_chunk(rows, n, m) : 128;
+        o.chunk = rows > 0 ? outer_chunk(rows, n, m, rank, count) : 128;
         o.most = rows > 0 ? static_cast<int>(outer_slots(rows, o.chunk)) : 0;
         if (dA) o.side[0] = {u, static_cast<const uint16_t *>(x), m, 0, (m + 127) / 128, nullptr, dA,
                              reinterpret_cast<float *>(ws + plan.dA)};
