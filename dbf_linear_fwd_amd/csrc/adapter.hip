@@ -28,8 +28,8 @@
 // and its halves are picked by byte permutes, four per operand.
 //
 // t and u stay fp32 in memory and become 16-bit operands in parts: f16 two
-// parts of t 2^k, k from the largest of the row (of a wave's rows in the
-// gradients), 22 bits and more; bf16 two parts (16 bits) where a 16-bit result
+// parts of t 2^k, k from the largest of the row (of a wave's rows so far in
+// the gradients), 22 bits and more; bf16 two parts (16 bits) where a 16-bit result
 // follows, three (24 bits) for the fp32 gradients.
 
 #include <algorithm>
@@ -127,6 +127,7 @@ __device__ __forceinline__ int f16_shift(float top) {
     (void)frexpf(top, &ex);
     return top > 0.0f ? 15 - ex : 0;
 }
+constexpr int kNoShift = 200;  // (more than any value's)
 __device__ __forceinline__ float finite_abs(float v) {
     const float a = fabsf(v);
     return a < __builtin_inff() ? a : 0.0f;  // (a NaN: 0)
@@ -558,8 +559,10 @@ typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 // A chunk's rows x 128 columns x 16 RT ranks per workgroup; the waves take 32
 // rows in turn.
+// (Registers for three workgroups per CU, which the compiler misses for f16 by
+// itself: 1408 rows of 42 groups, 10688 + 768, rank 128, 169 instead of 217 us in all.)
 template <typename E, int RT>
-__global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
+__global__ __launch_bounds__(kThreads, 3) void outer_kernel(const OuterArgs a) {
     constexpr int RP = 16 * RT, Cols = 128, Pitch = Cols + 4;
     constexpr int NP = E::code == DBF_TYPE_F16 ? 2 : 3;
     __shared__ __attribute__((aligned(16))) float sums[RP][Pitch];
@@ -638,21 +641,9 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
             }
         }
     };
-    int shift = 0;
-    if constexpr (E::code == DBF_TYPE_F16) {
-        float top = 0.0f;
-        for (int s = wave; s < steps; s += kWaves) {
-            float p[8][RT];
-            load_p(s, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int i = 0; i < RT; ++i) top = fmaxf(top, finite_abs(p[j][i]));
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-        shift = f16_shift(top);
-    }
+    // f16: p times 2^shift, from the largest of the wave's rows so far (sought in
+    // a pass of its own: 300 rows, 1000 + 1300, rank 24, 19 instead of 22 us in all)
+    int shift = E::code == DBF_TYPE_F16 ? kNoShift : 0;
     f32x4 acc[8][RT];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -668,6 +659,24 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const OuterArgs a) {
         }
         float p[8][RT];
         load_p(s, p);
+        if constexpr (E::code == DBF_TYPE_F16) {
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) top = fmaxf(top, finite_abs(p[j][i]));
+            top = wave_largest(top);
+            const int to = top > 0.0f ? f16_shift(top) : kNoShift;
+            if (to < shift) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < RT; ++j)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[i][j][v] = ldexpf(acc[i][j][v], to - shift);
+                shift = to;
+            }
+        }
         u32v4 pf[RT][NP];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {

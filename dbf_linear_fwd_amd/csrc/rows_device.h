@@ -34,6 +34,18 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
+// The largest of the lanes' values, none of them negative (their order is that of their bits).
+__device__ __forceinline__ float wave_largest(float x) {
+    int v = __builtin_bit_cast(int, x);
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, true));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, true));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(v, 63));
+}
+
 // Row tile `index` of the groups' tiles of `tile` places, group after group,
 // those of no group (group = count) last: false past the last.  A wave finds
 // it by itself, 64 groups at a time: two loads and a scan instead of a launch

@@ -314,6 +314,33 @@ def test_large_and_small_magnitudes(gpu):
     within(dA.double().cpu().numpy(), dAr, (n / 8 + 3 * rows / 8 + 60) * 2.0 ** -23 * dAr, "dA")
 
 
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("rows", [130, 2500])
+def test_rows_of_changing_magnitude(gpu, rows, order, name):
+    """dB of rows whose t goes from 0 and 2^-40 to 2^40: each wave's power of two follows the rows, in any order."""
+    _say(f"adapters: {rows} rows, t {order}, {name}")
+    torch = _torch()
+    rng = np.random.default_rng(rows)
+    count, n, m, rank = 2, 72, 40, 20
+    index = np.sort(rng.integers(0, count, rows))
+    power = np.linspace(-40, 40, rows)
+    power = power[::-1] if order == "falling" else rng.permutation(power) if order == "mixed" else power
+    tv = (rng.standard_normal((rows, rank)) * 2.0 ** power[:, None]).astype(np.float32)
+    tv[:40] = 0
+    dy, dyv = to_dev(rng.standard_normal((rows, n)), name)
+    x, _ = to_dev(rng.standard_normal((rows, m)), name)
+    A, _ = to_dev(rng.standard_normal((count, rank, m)), name)
+    B, _ = to_dev(rng.standard_normal((count, n, rank)), name)
+    _, _, dB = dbf.Adapters(A, B).backward(dy, x, torch.from_numpy(tv).cuda(), group(index, count))
+    v = tv.astype(np.float64)
+    loose = parts_error(v, index, name, True) + (3 * rows / 8 + 20) * 2.0 ** -24 * np.abs(v)
+    for a in range(count):
+        at = index == a
+        ref, tol = dyv[at].T @ v[at], np.abs(dyv[at]).T @ loose[at]
+        within(dB[a].double().cpu().numpy(), ref, tol + 2.0 ** -149, f"dB of {a}")
+
+
 def test_nothing_outside_the_results(gpu):
     torch = _torch()
     rng = np.random.default_rng(51)
