@@ -101,10 +101,13 @@ __device__ __forceinline__ u32v4 pick_column(const uint32_t (&q)[8][(N + 1) / 2]
 }
 
 // Two neighbouring values of part P (0, 1, 2) of v: rounded to 16 bits, the
-// rest of that rounded, the rest of that.
+// rest of that rounded, the rest of that.  (A finite v above bf16's largest
+// value has that one for its first part, and a rest that the second holds.)
 template <typename E>
 __device__ __forceinline__ uint16_t part_of(float v, int part) {
     uint16_t h = E::put(v);
+    if constexpr (E::code == DBF_TYPE_BF16)
+        if ((h & 0x7fff) == 0x7f80 && __builtin_isfinite(v)) --h;
     for (int p = 0; p < part; ++p) {
         const float top = E::get(h);
         v = __builtin_isfinite(top) ? v - top : 0.0f;
