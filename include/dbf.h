@@ -606,6 +606,8 @@ dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy, int32_t t
  * Sums are fp32; t enters the second product in two 16-bit parts (f16: 22 bits
  * of the row's largest, bf16: 16 bits of each), a rounding of 2^-17 of t at most where
  * y's own is 2^-9 (2^-22 and 2^-12).  Sums are in a fixed order (no atomics).
+ * Infinities and NaN of x, A and B give what the formulas say (a t that is 0 in
+ * 16 bits counts as 0 beside an infinite B: f16 below 2^-39 of the row's largest, bf16 below 2^-134).
  * 1 <= rank <= 128, count <= 1024, n, m <= 2^18, rows <= 2^24, rows * max(n, m) <= 2^36,
  * count * rank * max(n, m) <= 2^32 (DBF_ERR_SHAPE above).
  * Pointers 16-byte aligned (order, offsets, scale: 4).  rows = 0 returns
@@ -621,7 +623,8 @@ dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy, int32_t t
  * or dy: DBF_ERR_INVALID_ARG).  t as the
  * forward gave it (needed for dB), x needed for dA.  u and t enter the
  * gradients' products in three bf16 parts (24 bits), or in two f16 parts
- * (22 bits of the group's largest).  Sums are in a fixed order.  rows = 0 writes
+ * (22 bits of the group's largest).  Sums are in a fixed order.  Infinities and
+ * NaN are those of the formulas here too (in dx_out a u as t above).  rows = 0 writes
  * zeros to dA and dB.  Other rules as above.
  */
 size_t dbf_adapter_workspace(int32_t rows, int32_t n, int32_t m, int32_t rank, int32_t count);
