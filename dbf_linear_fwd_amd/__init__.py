@@ -111,6 +111,13 @@ def lib() -> ctypes.CDLL:
         raise RuntimeError(
             f"{_LIB_PATH} is missing: build it with `python -m dbf_linear_fwd_amd.build` "
             "(the DBF forward has no non-HIP implementation)")
+    # PyTorch brings a HIP runtime of its own.  Loaded first, it serves the
+    # library too; loaded after the library, the process has two, and calls on
+    # PyTorch's memory and streams fail.
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     L = ctypes.CDLL(_LIB_PATH)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     L.dbf_pack.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i32, ctypes.POINTER(vp)]
