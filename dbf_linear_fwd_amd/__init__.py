@@ -34,7 +34,7 @@ __all__ = [
     "dbf_factorize", "factorize", "dbf_linear_forward_noalloc", "dbf_bqq_pack_grouped",
     "DBF_TYPE_F16", "DBF_TYPE_BF16", "DBF_TYPE_F32", "DBF_TYPE_E4M3", "DBF_TYPE_E2M1", "MxTensor", "mx_quantize",
     "dbf_mx_pack", "dbf_mx_forward_plan", "dbf_mx_backward_plan", "rms_norm", "RmsNormOutput", "rms_norm_backward", "norm_forward_group",
-    "RowGroups", "group_rows", "dbf_experts_pack", "Experts", "Adapters", "AdapterOutput",
+    "RowGroups", "group_rows", "dbf_experts_pack", "dbf_experts_forward_plan", "dbf_experts_backward_plan", "Experts", "Adapters", "AdapterOutput",
 ]
 
 DBF_OK = 0
@@ -69,7 +69,7 @@ EXPORTED_SYMBOLS = (
     "dbf_mx_pack", "dbf_mx_forward", "dbf_mx_forward_group", "dbf_mx_backward_data", "dbf_mx_forward_plan",
     "dbf_mx_backward_plan", "dbf_rms_norm", "dbf_rms_norm_backward_workspace", "dbf_rms_norm_backward",
     "dbf_group_rows_workspace", "dbf_group_rows", "dbf_experts_pack", "dbf_experts_forward",
-    "dbf_experts_backward_data", "dbf_adapter_workspace", "dbf_adapter_forward", "dbf_adapter_backward_workspace",
+    "dbf_experts_backward_data", "dbf_experts_forward_plan", "dbf_experts_backward_plan", "dbf_adapter_workspace", "dbf_adapter_forward", "dbf_adapter_backward_workspace",
     "dbf_adapter_backward",
 )
 
@@ -179,6 +179,10 @@ def lib() -> ctypes.CDLL:
     L.dbf_experts_forward.restype = ctypes.c_int
     L.dbf_experts_backward_data.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp]
     L.dbf_experts_backward_data.restype = ctypes.c_int
+    L.dbf_experts_forward_plan.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
+    L.dbf_experts_forward_plan.restype = ctypes.c_int
+    L.dbf_experts_backward_plan.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i32)]
+    L.dbf_experts_backward_plan.restype = ctypes.c_int
     for name in ("dbf_adapter_workspace", "dbf_adapter_backward_workspace"):
         getattr(L, name).argtypes = [i32, i32, i32, i32, i32]
         getattr(L, name).restype = sz
@@ -789,6 +793,21 @@ def dbf_experts_pack(count: int, n: int, m: int, codes_ptr: int, scales_ptr: int
     _check(lib().dbf_experts_pack(count, n, m, codes_ptr, scales_ptr, act_type, max_rows, stream, ctypes.byref(h)),
            "dbf_experts_pack")
     return h.value
+
+
+def dbf_experts_forward_plan(count: int, n: int, m: int, slots: int, x_type: int):
+    """(tile rows, tile columns, most K parts, workgroups of a round, 1 for another launch before) of a product of
+    experts (see dbf_experts_forward_plan in include/dbf.h)."""
+    plan = (ctypes.c_int32 * 5)()
+    _check(lib().dbf_experts_forward_plan(count, n, m, slots, x_type, plan), "dbf_experts_forward_plan")
+    return tuple(plan)
+
+
+def dbf_experts_backward_plan(count: int, n: int, m: int, slots: int):
+    """The same of an input gradient."""
+    plan = (ctypes.c_int32 * 5)()
+    _check(lib().dbf_experts_backward_plan(count, n, m, slots, plan), "dbf_experts_backward_plan")
+    return tuple(plan)
 
 
 class Experts:

@@ -364,6 +364,9 @@ MxPlan mx_grouped_plan(int slots, int count, int n, int blocks, int x_type);
 // Floats of K-part sums of any call of up to `slots` rows.
 size_t mx_grouped_parts(int slots, int count, int n, int blocks);
 void mx_product_tile(const MxPlan &p, int32_t *rows, int32_t *cols);
+// Workgroups of a round (GroupedWork in mx_tile.h).
+int mx_grouped_round(const MxPlan &p);
+int mx_grouped_backward_round(const MxPlan &p);
 // Floats of K-part sums that the product of this shape uses (0: K whole).
 size_t mx_product_parts(int M, int n, int blocks, int x_type);
 // Padded scale rows into 32-row tiles: round_up(M, 32) * blocks bytes.

@@ -611,6 +611,8 @@ MxPlan mx_grouped_plan(int slots, int count, int n, int blocks, int x_type) {
     return mx_plan_grouped(slots, count, n, blocks / 4, x_type == DBF_TYPE_E4M3);
 }
 
+int mx_grouped_round(const MxPlan &p) { return grouped_room(p.tile); }
+
 size_t mx_grouped_parts(int slots, int count, int n, int blocks) {
     size_t most = 0;
     for (int t = 0; t < kTileCount && blocks / 4 >= kCutSteps; ++t)

@@ -649,6 +649,8 @@ MxPlan mx_backward_plan(int M, int n, int m) { return grad_plan(M, n, m); }
 
 MxPlan mx_grouped_backward_plan(int slots, int count, int n, int m) { return grad_plan_grouped(slots, count, n, m); }
 
+int mx_grouped_backward_round(const MxPlan &p) { return grouped_room(p.tile); }
+
 size_t mx_grouped_backward_parts(int slots, int count, int n, int m) {
     size_t most = 0;
     for (int t = 0; t < kGradCount && (n + 63) / 64 >= kCutSteps; ++t)

@@ -1112,21 +1112,27 @@ static bool place_scales_pay(int32_t slots, int32_t n, int32_t m, int32_t act) {
     return int64_t(slots) * n >= (int64_t(1) << (act == DBF_TYPE_E4M3 ? 36 : 35)) / m;
 }
 
+static dbf_status_t experts_sizes(int32_t count, int32_t n, int32_t m, int32_t max_rows) {
+    if (count < 1 || n < 1 || m < 1 || max_rows < 1) return DBF_ERR_INVALID_ARG;
+    // (a launch holds less than 2^32 threads)
+    const int64_t lim = int64_t(1) << 20;
+    if (count > 1024 || n > lim || m > lim || max_rows > (1 << 24) || int64_t(count) * std::max(n, m) > (int64_t(1) << 29))
+        return DBF_ERR_SHAPE;
+    const int64_t n_pad = round_up(n, 32), m_pad = round_up(m, 128);
+    if (n_pad * m_pad > (int64_t(1) << 36) || max_rows * m_pad > (int64_t(1) << 31) || int64_t(max_rows) * n > (int64_t(1) << 31))
+        return DBF_ERR_SHAPE;
+    return DBF_OK;
+}
+
 extern "C" dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, const void *codes, const uint8_t *scales,
                                          int32_t act_type, int32_t max_rows, hipStream_t stream, dbf_handle_t *out) {
     if (out) *out = nullptr;
     if (!out || !codes || !scales || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u))
         return DBF_ERR_INVALID_ARG;
-    if (count < 1 || n < 1 || m < 1 || max_rows < 1) return DBF_ERR_INVALID_ARG;
     if (act_type != DBF_TYPE_E4M3 && act_type != DBF_TYPE_E2M1) return DBF_ERR_INVALID_ARG;
-    // (a launch holds less than 2^32 threads)
-    const int64_t lim = int64_t(1) << 20;
-    if (count > 1024 || n > lim || m > lim || max_rows > (1 << 24) || int64_t(count) * std::max(n, m) > (int64_t(1) << 29))
-        return DBF_ERR_SHAPE;
+    const dbf_status_t sizes = experts_sizes(count, n, m, max_rows);
+    if (sizes != DBF_OK) return sizes;
     const int32_t n_pad = round_up(n, 32), m_pad = round_up(m, 128);
-    if (int64_t(n_pad) * m_pad > (int64_t(1) << 36) || int64_t(max_rows) * m_pad > (int64_t(1) << 31) ||
-        int64_t(max_rows) * n > (int64_t(1) << 31))
-        return DBF_ERR_SHAPE;
     g_alloc_calls = 0;
     dbf_layer *h = new (std::nothrow) dbf_layer();
     if (!h) return DBF_ERR_OOM;
@@ -1308,6 +1314,31 @@ extern "C" dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy
     if (st == DBF_OK && b.plan.nsplit > 1)
         st = timed_launch(h, "mx_backward_join", stream, [&] { return dbf::launch_mx_backward_join(b, stream); });
     return st;
+}
+
+extern "C" dbf_status_t dbf_experts_forward_plan(int32_t count, int32_t n, int32_t m, int32_t slots, int32_t x_type,
+                                                 int32_t plan[5]) {
+    if (!plan || (x_type != DBF_TYPE_E4M3 && x_type != DBF_TYPE_E2M1)) return DBF_ERR_INVALID_ARG;
+    const dbf_status_t st = experts_sizes(count, n, m, slots);
+    if (st != DBF_OK) return st;
+    const dbf::MxPlan p = dbf::mx_grouped_plan(slots, count, n, round_up(m, 128) / 32, x_type);
+    dbf::mx_product_tile(p, &plan[0], &plan[1]);
+    plan[2] = p.nsplit;
+    plan[3] = dbf::mx_grouped_round(p);
+    plan[4] = place_scales_pay(slots, n, m, x_type);
+    return DBF_OK;
+}
+
+extern "C" dbf_status_t dbf_experts_backward_plan(int32_t count, int32_t n, int32_t m, int32_t slots, int32_t plan[5]) {
+    if (!plan) return DBF_ERR_INVALID_ARG;
+    const dbf_status_t st = experts_sizes(count, n, m, slots);
+    if (st != DBF_OK) return st;
+    const dbf::MxPlan p = dbf::mx_grouped_backward_plan(slots, count, n, m);
+    dbf::mx_backward_tile(p, &plan[0], &plan[1]);
+    plan[2] = p.nsplit;
+    plan[3] = dbf::mx_grouped_backward_round(p);
+    plan[4] = n % 8 != 0;
+    return DBF_OK;
 }
 
 extern "C" dbf_status_t dbf_mx_forward_plan(int32_t batch, int32_t n, int32_t m, int32_t x_type, int32_t plan[3]) {

@@ -592,6 +592,23 @@ dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy, int32_t t
                                        void *dx, hipStream_t stream);
 
 /*
+ * dbf_experts_forward_plan, dbf_experts_backward_plan -- how a call on `slots`
+ * places runs: plan[0] x plan[1] results (places of one group x output
+ * columns) to a workgroup, plan[3] workgroups to a round.  The R tiles that
+ * fill no round are cut along the sum, on the device, into the smallest of
+ * plan[2], plan[3] / R and a quarter of its steps (128 columns of x, 64 of dy)
+ * where that is 2 or more, and a second launch adds the parts (plan[2] 1: none
+ * is cut).  plan[4] 1: another launch puts the rows where the product reads
+ * them (forward: block scales by place, unless the call quantises rows that
+ * are by place already; gradient: n no multiple of eight).  More than 64
+ * experts have one more launch, for the row tiles.
+ * x_type: the blocks that the product takes, DBF_TYPE_E4M3 or DBF_TYPE_E2M1.
+ * Host-only.  Errors: as dbf_experts_pack for such sizes (slots: max_rows).
+ */
+dbf_status_t dbf_experts_forward_plan(int32_t count, int32_t n, int32_t m, int32_t slots, int32_t x_type, int32_t plan[5]);
+dbf_status_t dbf_experts_backward_plan(int32_t count, int32_t n, int32_t m, int32_t slots, int32_t plan[5]);
+
+/*
  * dbf_adapter_forward -- low-rank adapters beside a layer: for row r of group a,
  *   t[r] = A_a x[r]  (fp32),   y[r] = rne( base[r] + scale_a B_a t[r] ),
  * for rows of no group t[r] = 0 and y[r] = base[r].
