@@ -1026,6 +1026,8 @@ extern "C" dbf_status_t dbf_adapter_forward(const void *x, const void *base, con
     if (!order || !offsets || !aligned(order, 4) || !aligned(offsets, 4) || !aligned(scale, 4) || !aligned(t, 16) ||
         workspace_bytes < part_bytes(rows, count, m, rank))
         return DBF_ERR_INVALID_ARG;
+    const size_t y_bytes = static_cast<size_t>(rows) * n * sizeof(uint16_t);
+    if (y != base && share_bytes(y, y_bytes, base, y_bytes)) return DBF_ERR_INVALID_ARG;  // (other rows are read later)
     const ShrinkArgs s{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(A), order, offsets, rows, m, rank,
                        count, shrink_parts(rows, count, m, rank), static_cast<float *>(workspace)};
     ExpandArgs e{s.out, static_cast<const uint16_t *>(B), scale, order, offsets, rows, n, rank, count, s.parts,
@@ -1073,7 +1075,12 @@ extern "C" dbf_status_t dbf_adapter_backward(const void *dy, const void *x, cons
     if (!aligned(dA, 16) || !aligned(dB, 16) || !aligned(offsets, 4) || !offsets) return DBF_ERR_INVALID_ARG;
     if (rows > 0) {
         if (!dy || !B || !order || !workspace || (dB && !t) || (dA && !x) || (dx_out && !A)) return DBF_ERR_INVALID_ARG;
-        if (dx_out && (dx_out == dy || dx_out == x)) return DBF_ERR_INVALID_ARG;  // (read after it is written)
+        // (dy, x and other rows of dx are read after it is written)
+        const size_t x_bytes = static_cast<size_t>(rows) * m * sizeof(uint16_t);
+        if (dx_out && (share_bytes(dx_out, x_bytes, dy, static_cast<size_t>(rows) * n * sizeof(uint16_t)) ||
+                       (x && share_bytes(dx_out, x_bytes, x, x_bytes)) ||
+                       (dx && dx_out != dx && share_bytes(dx_out, x_bytes, dx, x_bytes))))
+            return DBF_ERR_INVALID_ARG;
         for (const void *p : {dy, x, dx, A, B, static_cast<const void *>(dx_out), static_cast<const void *>(workspace)})
             if (!aligned(p, 16)) return DBF_ERR_INVALID_ARG;
         if (!aligned(order, 4) || !aligned(scale, 4) || !aligned(t, 16) ||

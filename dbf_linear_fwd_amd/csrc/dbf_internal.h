@@ -303,6 +303,12 @@ int launch_mx_dequantize(const void *codes, const uint8_t *scales, int fmt, int 
 int launch_mx_layout(const void *codes, const uint8_t *scales, int n, int m, uint8_t *out_codes, uint8_t *out_scales,
                      uint8_t *colmax, void *stream);
 
+// Whether two ranges of bytes share one.
+inline bool share_bytes(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q + b_bytes && q < p + a_bytes;
+}
+
 // How a tiled product runs: which of its tiles, and in how many K parts (more
 // than one: the product's launch leaves fp32 sums, and a join follows it).  Of
 // rows in groups, whose number of tiles is on the device, nsplit is the most

@@ -1223,6 +1223,11 @@ extern "C" dbf_status_t dbf_experts_forward(dbf_handle_t h, const void *x, int32
     if (!x || !aligned16(x) || !y || !aligned16(y)) return DBF_ERR_INVALID_ARG;
     if (real ? x_scales != nullptr : (!x_scales || (reinterpret_cast<uintptr_t>(x_scales) & 3u)))
         return DBF_ERR_INVALID_ARG;
+    // (ready blocks are read while results are written; 16-bit rows are quantised before)
+    const size_t y_bytes = static_cast<size_t>(slots) * h->n * sizeof(uint16_t), in_rows = rows.in_rows;
+    if (!real && (dbf::share_bytes(y, y_bytes, x, in_rows * dbf_mx_code_bytes(h->m, x_type)) ||
+                  dbf::share_bytes(y, y_bytes, x_scales, in_rows * dbf_mx_scale_bytes(h->m))))
+        return DBF_ERR_INVALID_ARG;
     int cur = -1;
     if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
     if (cur != h->device) return DBF_ERR_INVALID_ARG;
@@ -1278,6 +1283,9 @@ extern "C" dbf_status_t dbf_experts_backward_data(dbf_handle_t h, const void *dy
     dbf_status_t st = experts_rows(h, order, offsets, slots, gather, scatter, &rows);
     if (st != DBF_OK || slots == 0) return st;
     if (!dy || !aligned16(dy) || !dx || !aligned16(dx)) return DBF_ERR_INVALID_ARG;
+    if (dbf::share_bytes(dx, static_cast<size_t>(slots) * h->m * sizeof(uint16_t), dy,
+                         static_cast<size_t>(rows.in_rows) * h->n * sizeof(uint16_t)))
+        return DBF_ERR_INVALID_ARG;  // (read while it is written)
     int cur = -1;
     if (hipGetDevice(&cur) != hipSuccess) return DBF_ERR_HIP;
     if (cur != h->device) return DBF_ERR_INVALID_ARG;

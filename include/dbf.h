@@ -576,11 +576,11 @@ dbf_status_t dbf_group_rows(const void *index, int32_t index_bits, int32_t rows,
  * has the numerics of dbf_mx_forward; into how many parts its sum is cut depends
  * on the groups' sizes (so its last bits may differ between batches, as those
  * of a layer do between batch sizes; equal calls give equal bits).  y
- * overlaps nothing.  Calls on one handle must be ordered.
+ * overlaps nothing (DBF_ERR_INVALID_ARG over ready blocks).  Calls on one handle must be ordered.
  *
  * dbf_experts_backward_data -- dx[out(s)][l] = rne( Σ_o dy[in(s)][o] W_e[o][l] ),
  * the gradient of each place's input, as dbf_mx_backward_data computes it;
- * gather, scatter and the rest as above.
+ * gather, scatter and the rest as above (dx over dy: DBF_ERR_INVALID_ARG).
  */
 dbf_status_t dbf_experts_pack(int32_t count, int32_t n, int32_t m, const void *codes, const uint8_t *scales,
                               int32_t act_type, int32_t max_rows, hipStream_t stream, dbf_handle_t *out);
@@ -613,7 +613,8 @@ dbf_status_t dbf_experts_backward_plan(int32_t count, int32_t n, int32_t m, int3
  *   t[r] = A_a x[r]  (fp32),   y[r] = rne( base[r] + scale_a B_a t[r] ),
  * for rows of no group t[r] = 0 and y[r] = base[r].
  *   x       rows x m, base and y rows x n (base: the layer's result), of `type`
- *           (f16 or bf16).  y may be base itself.
+ *           (f16 or bf16).  y may be base itself (DBF_ERR_INVALID_ARG where it
+ *           shares a part of it).
  *   A, B    count x rank x m and count x n x rank, of `type`.
  *   scale   count values, fp32, or NULL (1).
  *   order, offsets  the grouped order of the rows (dbf_group_rows).
@@ -636,8 +637,8 @@ dbf_status_t dbf_experts_backward_plan(int32_t count, int32_t n, int32_t m, int3
  *               NULL: 0; rows of no group: dx[r]),
  *   dA_a = Σ_r u[r] x[r]ᵀ,  dB_a = scale_a Σ_r dy[r] t[r]ᵀ   over the rows of group a
  *               (fp32, of A's and B's shapes; zeros for a group without rows).
- * dx_out, dA or dB may be NULL (not computed); dx_out may be dx itself (not x
- * or dy: DBF_ERR_INVALID_ARG).  t as the
+ * dx_out, dA or dB may be NULL (not computed); dx_out may be dx itself (over x,
+ * dy or a part of dx: DBF_ERR_INVALID_ARG).  t as the
  * forward gave it (needed for dB), x needed for dA.  u and t enter the
  * gradients' products in three bf16 parts (24 bits), or in two f16 parts
  * (22 bits of the group's largest).  Sums are in a fixed order.  Infinities and
