@@ -815,7 +815,9 @@ class Experts:
 
     W is an e2m1 MxTensor of count * n rows, one weight after the other;
     max_rows is the most places (tokens times experts of a token) of a call.
-    `groups` (of `group_rows`) assigns each place to an expert.
+    `groups` (of `group_rows`) assigns each place to an expert.  Calls on one
+    object, forward and backward alike, share its workspace: on several
+    streams they must be ordered, or each stream has an object of its own.
     """
 
     def __init__(self, W: MxTensor, count: int, max_rows: int, act: str = "e4m3"):

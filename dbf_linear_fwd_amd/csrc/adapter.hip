@@ -14,10 +14,10 @@
 // A product needs no more than 2 rank operations per element of x, dy or y, so
 // the rows' memory traffic is the bound, and with few rows the launches.
 // Measured (kernel trace; bytes as they have to be moved): 8192 rows, 4096 +
-// 4096, rank 16, bf16: shrink 14 us (67 MB, 4.9 TB/s), expand 30 (134 MB, 4.5),
-// outer 28 (134 MB, 4.8) and its join 5; 2048 rows, m 4096, n 14336, rank 64:
+// 4096, rank 16, bf16: shrink 14 us (67 MB, 4.7 TB/s), expand 28 (134 MB, 4.7),
+// outer 29 (134 MB, 4.7) and its join 5; 2048 rows, m 4096, n 14336, rank 64:
 // shrink 13 us, expand 37 (117 MB, 3.1 TB/s); 16 rows of 32 adapters, 4096 x
-// 4096, rank 16, f16: 3.4 and 5.2 us, 8.2 for both in a graph (in one launch,
+// 4096, rank 16, f16: 3.4 and 5.3 us, 8.2 for both in a graph (in one launch,
 // every workgroup with all of its t: 9.1).
 //
 // Of an instruction a lane (c = lane % 16, g = lane / 16) supplies row c of each
@@ -29,8 +29,8 @@
 //
 // t and u stay fp32 in memory and become 16-bit operands in parts: f16 two
 // parts of t 2^k, k from the largest of the row (of a wave's rows so far in
-// the gradients), 22 bits and more; bf16 two parts (16 bits) where a 16-bit result
-// follows, three (24 bits) for the fp32 gradients.
+// the gradients), 2^-23 of each value or 2^-39 of that largest; bf16 two parts
+// (2^-17) where a 16-bit result follows, three (24 bits) for the fp32 gradients.
 
 #include <algorithm>
 

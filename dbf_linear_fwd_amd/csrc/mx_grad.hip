@@ -532,7 +532,8 @@ MxPlan grad_plan(int M, int n, int m) {
 }
 
 // The same for rows in groups.  Against every tile, cut and not, at 164 sizes
-// the choice is 3 % from the best on average.
+// the choice is 3 % from the best on average, half of them within 1 %, at worst
+// 50 % (64 rows of 64 groups, 4096 x 1024).
 constexpr GroupedCost kGrouped[kGradCount] = {
     {5.38f, 0.93f, 4.36f, 1.51f},
     {3.50f, 0.56f, 2.42f, 0.54f},

@@ -621,9 +621,9 @@ dbf_status_t dbf_experts_backward_plan(int32_t count, int32_t n, int32_t m, int3
  *   t       out, rows x rank fp32 (the backward pass takes it), or NULL.
  *   workspace  dbf_adapter_workspace(rows, n, m, rank, count) bytes, 16-byte
  *           aligned.
- * Sums are fp32; t enters the second product in two 16-bit parts (f16: 22 bits
- * of the row's largest, bf16: 16 bits of each), a rounding of 2^-17 of t at most where
- * y's own is 2^-9 (2^-22 and 2^-12).  Sums are in a fixed order (no atomics).
+ * Sums are fp32; scale * t enters the second product in two 16-bit parts, off by
+ * 2^-17 of each value at most (bf16; f16: 2^-23, or 2^-39 of the row's largest)
+ * where y's own rounding is 2^-8 (2^-11).  Sums are in a fixed order (no atomics).
  * Infinities and NaN of x, A and B give what the formulas say (a t that is 0 in
  * 16 bits counts as 0 beside an infinite B: f16 below 2^-39 of the row's largest, bf16 below 2^-134).
  * 1 <= rank <= 128, count <= 1024, n, m <= 2^18, rows <= 2^24, rows * max(n, m) <= 2^36,
@@ -639,9 +639,9 @@ dbf_status_t dbf_experts_backward_plan(int32_t count, int32_t n, int32_t m, int3
  *               (fp32, of A's and B's shapes; zeros for a group without rows).
  * dx_out, dA or dB may be NULL (not computed); dx_out may be dx itself (over x,
  * dy or a part of dx: DBF_ERR_INVALID_ARG).  t as the
- * forward gave it (needed for dB), x needed for dA.  u and t enter the
- * gradients' products in three bf16 parts (24 bits), or in two f16 parts
- * (22 bits of the group's largest).  Sums are in a fixed order.  Infinities and
+ * forward gave it (needed for dB), x needed for dA.  u enters dx' as t enters y;
+ * u and t enter the gradients' products in three bf16 parts (24 bits), or in two
+ * f16 parts (2^-23 of each value, or 2^-39 of the group's largest).  Sums are in a fixed order.  Infinities and
  * NaN are those of the formulas here too (in dx_out a u as t above).  rows = 0 writes
  * zeros to dA and dB.  Other rules as above.
  */
