@@ -116,7 +116,7 @@ def lib() -> ctypes.CDLL:
     # PyTorch's memory and streams fail.
     try:
         import torch  # noqa: F401
-    except ImportError:
+    except (ImportError, OSError):  # (none, or one that does not load here)
         pass
     L = ctypes.CDLL(_LIB_PATH)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
