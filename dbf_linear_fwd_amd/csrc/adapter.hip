@@ -294,8 +294,9 @@ struct ExpandArgs {
 // 59 us with four in both products, 56 with eight).
 constexpr int expand_waves(int mt) { return mt == 1 ? 4 : 8; }
 
-// (Up to 32 ranks registers for four waves per SIMD, which the rare way of
-// infinite sums would take.)
+// (Up to 32 ranks registers for four waves per SIMD, which the rare way of infinite
+// sums would take: 1088 rows of 4 groups, n 2696, m 2368, rank 8, 10.7 instead of
+// 12.6 us in both products.)
 template <typename E, bool LEAD, int MT, int RT, bool VEC>
 __global__ __launch_bounds__(64 * expand_waves(MT), RT <= 2 ? 4 : 1) void expand_kernel(const ExpandArgs a) {
     constexpr int Waves = expand_waves(MT), Threads = 64 * Waves;
